@@ -17,7 +17,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfa_gb300.so")
 
 FULL, SLIDING = 0, 1
-KV_BF16, KV_INT8, KV_FP8 = 0, 1, 2
+KV_BF16, KV_INT8, KV_FP8, KV_FP4 = 0, 1, 2, 3
 KV_OWN, KV_AUTO = -1, -2
 DEV_ERR_PAGE, DEV_ERR_SLOT, DEV_ERR_BOUND, DEV_ERR_TIMEOUT, DEV_ERR_WORKSPACE, DEV_ERR_RANGE = 1, 2, 4, 8, 16, 32
 MAX_CACHES = 4096
@@ -58,6 +58,7 @@ def _load() -> ctypes.CDLL:
         "fa_cache_bind_slab": (i32, [vp, i32, vp, vp, vp, vp]),
         "fa_kv_bytes_per_token": (sz, [vp, i32]),
         "fa_kv_store": (i32, [vp, i32, vp, vp, vp, i32, vp]),
+        "fa_kv_load": (i32, [vp, i32, vp, i32, vp, vp, vp]),
         "fa_decode_workspace_bytes": (sz, [vp, i32, i32, i32]),
         "fa_extend_workspace_bytes": (sz, []),
         "fa_cache_bind_extend_workspace": (i32, [vp, vp, sz]),
@@ -107,6 +108,16 @@ def _s(stream):
 def _ptrs(ts):
     """A host array of device pointers (NULL for None), kept alive by the caller."""
     return (ctypes.c_void_p * len(ts))(*[None if t is None else t.data_ptr() for t in ts])
+
+
+def _need(what, t, dtype, numel=None):
+    """Refuse a tensor the kernels would misread: not on the current device,
+    another type, not dense, or (numel given) another size."""
+    if t.dtype != dtype or not t.is_contiguous() or not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise FAError(ERR_INVALID_ARG, f"{what} must be a dense {dtype} tensor on the current CUDA device, not "
+                                       f"{t.dtype}, strides {tuple(t.stride())}, on {t.device}")
+    if numel is not None and t.numel() != numel:
+        raise FAError(ERR_INVALID_ARG, f"{what} holds {t.numel()} elements, not {numel}")
 
 
 def _i32s(xs):
@@ -167,6 +178,11 @@ class Cache:
             return self.window_pages
         return self.num_pages
 
+    def _layer(self, layer: int) -> dict:
+        if not 0 <= layer < len(self.layers):
+            raise FAError(ERR_INVALID_ARG, f"layer {layer} out of range [0, {len(self.layers)})")
+        return self.layers[layer]
+
     def source(self, layer: int) -> int:
         out = ctypes.c_int32()
         _check(_lib.fa_cache_layer_source(self._h, layer, ctypes.byref(out)))
@@ -181,19 +197,27 @@ class Cache:
         return int(_lib.fa_kv_bytes_per_token(self._h, kind))
 
     def bind(self, layer: int, k, v, k_scale=None, v_scale=None) -> None:
+        if self.kv_dtype == KV_FP4 and None not in (k, v, k_scale, v_scale):
+            kv, sc = self.slab_bytes(layer)
+            for name, t, dt, n in (("k", k, torch.uint8, kv), ("v", v, torch.uint8, kv),
+                                   ("k_scale", k_scale, torch.float32, sc // 4), ("v_scale", v_scale, torch.float32, sc // 4)):
+                _need(name, t, dt, n if kv else None)   # a shared layer's refusal is the library's
         _check(_lib.fa_cache_bind_slab(self._h, layer, _p(k), _p(v), _p(k_scale), _p(v_scale)))
         self._slabs[layer] = (k, v, k_scale, v_scale)
 
     def allocate(self, device="cuda") -> dict:
         """Allocate (torch) and bind a slab for every owning layer; returns
-        {layer: (k, v, k_scale, v_scale)} with k, v shaped [num_pages][Hkv][page_size][D]."""
+        {layer: (k, v, k_scale, v_scale)} with k, v shaped [num_pages][Hkv][page_size][D]
+        (fp4: [num_pages][Hkv][page_size][D * 9 / 16] bytes)."""
         out = {}
         for i, d in enumerate(self.layers):
             if self.source(i) != i:
                 continue
-            shape = (self.layer_pages(i), d["num_kv_heads"], self.page_size, d["head_dim"])
-            # fp8 e4m3 codes are held as raw bytes (uint8 bit patterns)
-            dt = {KV_BF16: torch.bfloat16, KV_INT8: torch.int8, KV_FP8: torch.uint8}[self.kv_dtype]
+            # fp8 e4m3 codes are held as raw bytes (uint8 bit patterns); an fp4
+            # row as D / 2 bytes of codes and D / 16 bytes of block scales
+            width = d["head_dim"] * 9 // 16 if self.kv_dtype == KV_FP4 else d["head_dim"]
+            shape = (self.layer_pages(i), d["num_kv_heads"], self.page_size, width)
+            dt = {KV_BF16: torch.bfloat16, KV_INT8: torch.int8, KV_FP8: torch.uint8, KV_FP4: torch.uint8}[self.kv_dtype]
             k = torch.empty(shape, dtype=dt, device=device)
             v = torch.empty(shape, dtype=dt, device=device)
             ks = vs = None
@@ -208,9 +232,30 @@ class Cache:
         """(k, v, k_scale, v_scale) tensors the layer reads (its source's for a shared layer)."""
         return self._slabs[self.source(layer)]
 
+    def _rows(self, layer: int, k, v, slot_mapping) -> None:
+        """fp4 caches: refuse rows or slots the store would misread."""
+        d = self._layer(layer)
+        _need("slot_mapping", slot_mapping, torch.int32)
+        for name, t in (("k", k), ("v", v)):
+            _need(name, t, torch.bfloat16, slot_mapping.numel() * d["num_kv_heads"] * d["head_dim"])
+
     def store(self, layer: int, k, v, slot_mapping, stream=None) -> None:
+        if self.kv_dtype == KV_FP4 and self.source(layer) == layer:
+            self._rows(layer, k, v, slot_mapping)
         _check(_lib.fa_kv_store(self._h, layer, _p(k), _p(v), _p(slot_mapping), int(slot_mapping.numel()),
                                 _s(stream)))
+
+    def load(self, layer: int, slot_mapping, k=None, v=None, stream=None) -> None:
+        """fa_kv_load: read the rows at the slots back into k, v (bf16
+        [T][Hkv][D]; either may be None), from a slab of any format; a negative
+        slot leaves its rows as they were."""
+        d = self._layer(layer)
+        _need("slot_mapping", slot_mapping, torch.int32)
+        T = int(slot_mapping.numel())
+        for name, t in (("k", k), ("v", v)):
+            if t is not None:
+                _need(name, t, torch.bfloat16, T * d["num_kv_heads"] * d["head_dim"])
+        _check(_lib.fa_kv_load(self._h, layer, _p(slot_mapping), T, _p(k), _p(v), _s(stream)))
 
     def store_layers(self, layers, ks, vs, slot_mappings, stream=None) -> None:
         """fa_kv_store_layers: the stores of several layers in one launch

@@ -64,9 +64,13 @@ static void give_err_slot(int i) {
   g_slot_used[i] = false;
 }
 
-// int8 and fp8 slabs: one code byte per element plus an fp32 scale per row
+// int8, fp8 and fp4 slabs: codes plus an fp32 scale per row
 static bool quantised(int kv_dtype) { return kv_dtype != FA_KV_BF16; }
-static size_t elem_bytes(int kv_dtype) { return quantised(kv_dtype) ? 1 : 2; }
+static size_t elem_bytes(int kv_dtype) { return quantised(kv_dtype) ? 1 : 2; }   // not fp4
+// bytes of a slab row of D values, without its fp32 scale
+static size_t slab_row_bytes(int kv_dtype, int D) {
+  return kv_dtype == FA_KV_FP4 ? D / 2 + D / 16 : elem_bytes(kv_dtype) * D;
+}
 
 // ----------------------------------------------------------------- planning
 DecodePlan plan_decode(const fa_cache* c, int layer, int B, int max_seq_len, long long max_cta) {
@@ -165,6 +169,23 @@ static fa_status encode_tile_map(CUtensorMap* tm, void* base, int D, int kv_dtyp
                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled (tile map) failed (CUresult %d)", (int)r);
+  return FA_OK;
+}
+
+// fp4 slab rows [rows][D * 9 / 16 bytes] as a 2-D byte map: a box (32 bytes, 16
+// rows) lands as 16 rows x 32 B, 32-byte swizzled (the 16-byte unit index XORed
+// with bit 2 of the row).  A box at the last 16 bytes of a row reads zeros past it.
+static fa_status encode_fp4_map(CUtensorMap* tm, void* base, int D, uint64_t rows) {
+  auto enc = get_encoder();
+  if (!enc) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t rb = slab_row_bytes(FA_KV_FP4, D);
+  cuuint64_t dims[2] = {rb, rows};
+  cuuint64_t strides[1] = {rb};
+  cuuint32_t box[2] = {32, static_cast<cuuint32_t>(kTile)};
+  cuuint32_t es[2] = {1, 1};
+  CUresult r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled (fp4 rows) failed (CUresult %d)", (int)r);
   return FA_OK;
 }
 
@@ -272,7 +293,7 @@ fa_status fa_cache_create(const fa_layer_desc* layers, int32_t n_layers, int32_t
   if (num_pages <= 0) return fail(FA_ERR_INVALID_ARG, "num_pages must be positive");
   if (page_size <= 0 || page_size % kTile != 0 || page_size > 256)
     return fail(FA_ERR_UNSUPPORTED, "page_size %d: must be a multiple of %d, at most 256", page_size, kTile);
-  if (kv_dtype != FA_KV_BF16 && kv_dtype != FA_KV_INT8 && kv_dtype != FA_KV_FP8)
+  if (kv_dtype != FA_KV_BF16 && kv_dtype != FA_KV_INT8 && kv_dtype != FA_KV_FP8 && kv_dtype != FA_KV_FP4)
     return fail(FA_ERR_UNSUPPORTED, "kv_dtype %d unsupported", kv_dtype);
   fa_cache* c = new (std::nothrow) fa_cache();
   if (!c) return fail(FA_ERR_INVALID_ARG, "out of host memory");
@@ -380,7 +401,7 @@ fa_status fa_cache_slab_bytes(const fa_cache* c, int32_t layer, size_t* kv_bytes
     return ok();
   }
   const size_t rows = static_cast<size_t>(layer_pages(c, layer)) * L.d.num_kv_heads * c->page_size;
-  *kv_bytes = rows * L.d.head_dim * elem_bytes(c->kv_dtype);
+  *kv_bytes = rows * slab_row_bytes(c->kv_dtype, L.d.head_dim);
   *scale_bytes = quantised(c->kv_dtype) ? rows * sizeof(float) : 0;
   return ok();
 }
@@ -395,18 +416,25 @@ fa_status fa_cache_bind_slab(fa_cache* c, int32_t layer, void* k, void* v, float
   if (!k || !v) return fail(FA_ERR_INVALID_ARG, "layer %d: k and v must be non-NULL", layer);
   if (!aligned16(k) || !aligned16(v)) return fail(FA_ERR_INVALID_ARG, "layer %d: k, v must be 16-byte aligned", layer);
   if (quantised(c->kv_dtype)) {
-    if (!k_scale || !v_scale) return fail(FA_ERR_INVALID_ARG, "layer %d: the 8-bit formats need k_scale and v_scale", layer);
+    if (!k_scale || !v_scale) return fail(FA_ERR_INVALID_ARG, "layer %d: the 8- and 4-bit formats need k_scale and v_scale", layer);
     if (!aligned16(k_scale) || !aligned16(v_scale))
       return fail(FA_ERR_INVALID_ARG, "layer %d: scales must be 16-byte aligned", layer);
   }
   Slab& s = c->slabs[layer];
   const uint64_t rows = static_cast<uint64_t>(layer_pages(c, layer)) * L.d.num_kv_heads * c->page_size;
-  st = encode_slab_map(&s.tm_k, k, L.d.head_dim, c->kv_dtype, rows);
-  if (st) return st;
-  st = encode_slab_map(&s.tm_v, v, L.d.head_dim, c->kv_dtype, rows);
-  if (st) return st;
-  if ((st = encode_tile_map(&s.tm_kt, k, L.d.head_dim, c->kv_dtype, rows))) return st;
-  if ((st = encode_tile_map(&s.tm_vt, v, L.d.head_dim, c->kv_dtype, rows))) return st;
+  if (c->kv_dtype == FA_KV_FP4) {
+    if ((st = encode_fp4_map(&s.tm_k, k, L.d.head_dim, rows))) return st;
+    if ((st = encode_fp4_map(&s.tm_v, v, L.d.head_dim, rows))) return st;
+    s.tm_kt = s.tm_k;   // unused in fp4; keeps the kernel parameters defined
+    s.tm_vt = s.tm_v;
+  } else {
+    st = encode_slab_map(&s.tm_k, k, L.d.head_dim, c->kv_dtype, rows);
+    if (st) return st;
+    st = encode_slab_map(&s.tm_v, v, L.d.head_dim, c->kv_dtype, rows);
+    if (st) return st;
+    if ((st = encode_tile_map(&s.tm_kt, k, L.d.head_dim, c->kv_dtype, rows))) return st;
+    if ((st = encode_tile_map(&s.tm_vt, v, L.d.head_dim, c->kv_dtype, rows))) return st;
+  }
   if (quantised(c->kv_dtype)) {
     if ((st = encode_scale_map(&s.tm_ks, k_scale, rows))) return st;
     if ((st = encode_scale_map(&s.tm_vs, v_scale, rows))) return st;
@@ -432,7 +460,7 @@ size_t fa_kv_bytes_per_token(const fa_cache* c, int32_t kind) {
   for (size_t i = 0; i < c->layers.size(); ++i) {
     const Layer& L = c->layers[i];
     if (L.owner != static_cast<int>(i) || L.d.kind != kind) continue;
-    const size_t row = quantised(c->kv_dtype) ? L.d.head_dim + sizeof(float) : 2 * L.d.head_dim;
+    const size_t row = slab_row_bytes(c->kv_dtype, L.d.head_dim) + (quantised(c->kv_dtype) ? sizeof(float) : 0);
     total += 2 * L.d.num_kv_heads * row;
   }
   return total;
@@ -457,6 +485,27 @@ fa_status fa_kv_store(fa_cache* c, int32_t layer, const void* k, const void* v, 
               c->page_size, layer_pages(c, layer), c->kv_dtype, (c->flags & FA_FLAG_EARLY_METADATA) ? 1 : 0, err};
   ce = launch_store(a, static_cast<cudaStream_t>(stream));
   if (ce != cudaSuccess) return fail(FA_ERR_CUDA, "store launch: %s", cudaGetErrorString(ce));
+  return ok();
+}
+
+fa_status fa_kv_load(fa_cache* c, int32_t layer, const int32_t* slot_mapping, int32_t T, void* k, void* v,
+                     void* stream) {
+  fa_status st = check_layer(c, layer);
+  if (st) return st;
+  if (T < 0) return fail(FA_ERR_INVALID_ARG, "T must be >= 0");
+  if (T == 0) return ok();
+  const Slab* s = nullptr;
+  if ((st = check_bound(c, layer, &s))) return st;
+  if (!slot_mapping || (!k && !v)) return fail(FA_ERR_INVALID_ARG, "slot_mapping and one of k, v must be non-NULL");
+  if (!aligned16(k) || !aligned16(v)) return fail(FA_ERR_INVALID_ARG, "k, v must be 16-byte aligned");
+  cudaError_t ce;
+  unsigned int* err = device_error_word(c, &ce);
+  if (!err) return fail(FA_ERR_CUDA, "device error word: %s", cudaGetErrorString(ce));
+  const Layer& L = c->layers[layer];
+  LoadArgs a{slot_mapping, s->k, s->v, s->k_scale, s->v_scale, k, v, T, L.d.num_kv_heads, L.d.head_dim, c->page_size,
+             layer_pages(c, layer), c->kv_dtype, (c->flags & FA_FLAG_EARLY_METADATA) ? 1 : 0, err};
+  ce = launch_load(a, static_cast<cudaStream_t>(stream));
+  if (ce != cudaSuccess) return fail(FA_ERR_CUDA, "load launch: %s", cudaGetErrorString(ce));
   return ok();
 }
 
@@ -593,6 +642,7 @@ static fa_status decode_call(fa_cache* c, int32_t layer, const void* q, const vo
   if (max_pages_per_seq < (max_seq_len + c->page_size - 1) / c->page_size)
     return fail(FA_ERR_INVALID_ARG, "max_pages_per_seq %d cannot hold max_seq_len %d", max_pages_per_seq,
                 max_seq_len);
+  if (c->kv_dtype == FA_KV_FP4) return fail(FA_ERR_UNSUPPORTED, "fp4 slabs: attention is not served");
   DecodePlan p = plan_decode(c, layer, B, max_seq_len);
   if (workspace_bytes < p.ws_bytes || (p.ws_bytes && !workspace))
     return fail(FA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, p.ws_bytes);
@@ -664,6 +714,7 @@ fa_status fa_paged_decode_attn_layers(fa_cache* c, int32_t n, const int32_t* lay
     if (!aligned16(q[i]) || !aligned16(out[i])) return fail(FA_ERR_INVALID_ARG, "q, out of layer %d must be 16-byte aligned", layers[i]);
   }
   if (B == 0) return ok();
+  if (c->kv_dtype == FA_KV_FP4) return fail(FA_ERR_UNSUPPORTED, "fp4 slabs: attention is not served");
   const size_t need = fa_decode_layers_workspace_bytes(c, n, layers, B, max_seq_len);
   if (workspace_bytes < need || (need && !workspace))
     return fail(FA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
@@ -744,6 +795,7 @@ fa_status fa_paged_extend_attn(fa_cache* c, int32_t layer, const void* q, const 
   cudaError_t ce;
   unsigned int* err = device_error_word(c, &ce);
   if (!err) return fail(FA_ERR_CUDA, "device error word: %s", cudaGetErrorString(ce));
+  if (c->kv_dtype == FA_KV_FP4) return fail(FA_ERR_UNSUPPORTED, "fp4 slabs: attention is not served");
   ExtendArgs a{};
   a.q = q;
   a.k_ext = k_ext;
@@ -808,6 +860,7 @@ fa_status fa_paged_decode_multi_attn(fa_cache* c, int32_t layer, const void* q, 
   cudaError_t ce;
   unsigned int* err = device_error_word(c, &ce);
   if (!err) return fail(FA_ERR_CUDA, "device error word: %s", cudaGetErrorString(ce));
+  if (c->kv_dtype == FA_KV_FP4) return fail(FA_ERR_UNSUPPORTED, "fp4 slabs: attention is not served");
   ExtendArgs a{};
   a.q = q;
   a.qo_indptr = qo_indptr;

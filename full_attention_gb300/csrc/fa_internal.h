@@ -32,7 +32,9 @@ struct Slab {
   // boxes of tm_k / tm_v side by side (one copy per tile).
   CUtensorMap tm_kt;
   CUtensorMap tm_vt;
-  // int8 format: 2-D maps over the fp32 scales, one 16-float box per tile.
+  // fp4 format: tm_k and tm_v (and tm_kt, tm_vt, unused) are 2-D maps over
+  // the row bytes (codes, then block scales), boxes of 32 bytes x 16 rows.
+  // Quantised formats: 2-D maps over the fp32 scales, one 16-float box per tile.
   CUtensorMap tm_ks;
   CUtensorMap tm_vs;
 };
@@ -127,6 +129,19 @@ struct StoreArgs {
 cudaError_t launch_store(const StoreArgs& a, cudaStream_t s);
 // The stores of several layers in one launch (n <= kMaxLayersPerLaunch; any head_dim mix).
 cudaError_t launch_store_layers(const StoreArgs* a, int n, cudaStream_t s);
+
+struct LoadArgs {
+  const int32_t* slots;
+  const void* k_slab;
+  const void* v_slab;
+  const float* k_scale;
+  const float* v_scale;
+  void* k;   // either may be null
+  void* v;
+  int T, Hkv, D, page_size, num_pages, kv_dtype, early_metadata;
+  unsigned int* err;
+};
+cudaError_t launch_load(const LoadArgs& a, cudaStream_t s);
 
 struct DecodeArgs {
   const void* q;

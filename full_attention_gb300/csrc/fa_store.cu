@@ -6,7 +6,11 @@
 // and stores.  The 8-bit per-token-head formats quantise the row on the way:
 // a = max|x| (fp32, warp-shuffle reduction); int8: s = a / 127, c = rint(x / s)
 // clamped to [-127, 127]; fp8: s = a / 448, c = the e4m3 value nearest x / s,
-// saturating at 448; every division IEEE round-to-nearest.
+// saturating at 448; every division IEEE round-to-nearest.  The microscaled
+// 4-bit format is in fa_row.cuh (row_store_fp4).
+//
+// The reverse, fa_kv_load, reads rows back as bf16 with the same assignment of
+// rows to warps and values to lanes.
 #include <algorithm>
 #include <cstdio>
 #include <mutex>
@@ -88,7 +92,6 @@ __device__ __forceinline__ void store_rows(const StoreArgs& a, int warp, int lan
     if (r0 + i < rows)
       row_load<D>(r[i], static_cast<const __nv_bfloat16*>(((r0 + i) & 1) ? a.v : a.k) +
                             static_cast<size_t>((r0 + i) >> 1) * D, lane);
-  constexpr size_t elem = KV == FA_KV_BF16 ? 2 : 1;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int row = r0 + i;
@@ -101,7 +104,7 @@ __device__ __forceinline__ void store_rows(const StoreArgs& a, int warp, int lan
     const int h = (row >> 1) % a.Hkv;
     const size_t dst = (static_cast<size_t>(page) * a.Hkv + h) * a.page_size + off;
     const int which = row & 1;
-    row_store<D, KV>(r[i], static_cast<uint8_t*>(which ? a.v_slab : a.k_slab) + dst * D * elem,
+    row_store<D, KV>(r[i], static_cast<uint8_t*>(which ? a.v_slab : a.k_slab) + dst * kRowBytes<D, KV>,
                      KV == FA_KV_BF16 ? nullptr : (which ? a.v_scale : a.k_scale) + dst, lane);
   }
 }
@@ -149,6 +152,7 @@ cudaError_t launch_store_layers(const StoreArgs* a, int n, cudaStream_t s) {
   const dim3 g(static_cast<unsigned>(grid), static_cast<unsigned>(n)), b(block);
   if (a[0].kv_dtype == FA_KV_INT8) return launch_pdl(store_layers_kernel<FA_KV_INT8>, g, b, 0, s, m);
   if (a[0].kv_dtype == FA_KV_FP8) return launch_pdl(store_layers_kernel<FA_KV_FP8>, g, b, 0, s, m);
+  if (a[0].kv_dtype == FA_KV_FP4) return launch_pdl(store_layers_kernel<FA_KV_FP4>, g, b, 0, s, m);
   return launch_pdl(store_layers_kernel<FA_KV_BF16>, g, b, 0, s, m);
 }
 
@@ -164,8 +168,69 @@ cudaError_t launch_store(const StoreArgs& a, cudaStream_t s) {
   if (a.kv_dtype == FA_KV_FP8)
     return a.D == 256 ? launch_pdl(store_kernel<256, FA_KV_FP8>, g, b, 0, s, a)
                       : launch_pdl(store_kernel<512, FA_KV_FP8>, g, b, 0, s, a);
+  if (a.kv_dtype == FA_KV_FP4)
+    return a.D == 256 ? launch_pdl(store_kernel<256, FA_KV_FP4>, g, b, 0, s, a)
+                      : launch_pdl(store_kernel<512, FA_KV_FP4>, g, b, 0, s, a);
   return a.D == 256 ? launch_pdl(store_kernel<256, FA_KV_BF16>, g, b, 0, s, a)
                     : launch_pdl(store_kernel<512, FA_KV_BF16>, g, b, 0, s, a);
+}
+
+// The reverse of store_rows: R consecutive rows of the output per warp, row
+// (t * Hkv + h) * sides + side, with sides = 2 (K, then V) or 1 (only one of
+// them is wanted).  Slots, then every row's raw bytes, then the rows out.
+template <int D, int KV>
+__global__ void __launch_bounds__(256) load_kernel(LoadArgs a) {
+  constexpr int R = StoreShape<D>::R;
+  if (!a.early_metadata) griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int sides = a.k && a.v ? 2 : 1, only = a.k ? 0 : 1;
+  const long long rows = static_cast<long long>(a.T) * a.Hkv * sides;
+  const long long r0 = ((static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5) * R;
+  if (r0 >= rows) return;
+  int slot[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) slot[i] = (r0 + i < rows) ? __ldg(a.slots + (r0 + i) / (a.Hkv * sides)) : -1;
+  griddep_wait();   // the slab's rows may belong to the previous kernel
+  RawRow<D, KV> raw[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    if (slot[i] < 0) continue;   // a padding token: its rows stay as they are
+    const int page = slot[i] / a.page_size, off = slot[i] % a.page_size;
+    if (page >= a.num_pages) {
+      if (lane == 0) atomicOr(a.err, FA_DEV_ERR_SLOT);
+      slot[i] = -1;
+      continue;
+    }
+    const int q = static_cast<int>((r0 + i) % (a.Hkv * sides));
+    const int which = sides == 2 ? (q & 1) : only;
+    const size_t src = (static_cast<size_t>(page) * a.Hkv + q / sides) * a.page_size + off;
+    raw_load<D, KV>(raw[i], static_cast<const uint8_t*>(which ? a.v_slab : a.k_slab) + src * kRowBytes<D, KV>,
+                    KV == FA_KV_BF16 ? nullptr : (which ? a.v_scale : a.k_scale) + src, lane);
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    if (slot[i] < 0) continue;
+    const long long row = r0 + i;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(sides == 2 ? ((row & 1) ? a.v : a.k) : only ? a.v : a.k);
+    raw_to_bf16<D, KV>(raw[i], dst + static_cast<size_t>(row / sides) * D, lane);
+  }
+}
+
+cudaError_t launch_load(const LoadArgs& a, cudaStream_t s) {
+  const int R = a.D == 256 ? StoreShape<256>::R : StoreShape<512>::R;
+  const long long rows = static_cast<long long>(a.T) * a.Hkv * (a.k && a.v ? 2 : 1);
+  const int block = 256;
+  const long long grid = ((rows + R - 1) / R * 32 + block - 1) / block;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const dim3 g(static_cast<unsigned>(grid)), b(block);
+  auto run = [&](auto k256, auto k512) {
+    return a.D == 256 ? launch_pdl(k256, g, b, 0, s, a) : launch_pdl(k512, g, b, 0, s, a);
+  };
+  if (a.kv_dtype == FA_KV_INT8) return run(load_kernel<256, FA_KV_INT8>, load_kernel<512, FA_KV_INT8>);
+  if (a.kv_dtype == FA_KV_FP8) return run(load_kernel<256, FA_KV_FP8>, load_kernel<512, FA_KV_FP8>);
+  if (a.kv_dtype == FA_KV_FP4) return run(load_kernel<256, FA_KV_FP4>, load_kernel<512, FA_KV_FP4>);
+  return run(load_kernel<256, FA_KV_BF16>, load_kernel<512, FA_KV_BF16>);
 }
 
 }  // namespace fa

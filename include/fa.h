@@ -53,6 +53,11 @@
  *                 k_scale, v_scale: float [num_pages][Hkv][page_size]
  *   fp8 slab      K, V: uint8 [num_pages][Hkv][page_size][D]  (e4m3 codes)
  *                 k_scale, v_scale: float [num_pages][Hkv][page_size]
+ *   fp4 slab      K, V: uint8 [num_pages][Hkv][page_size][D * 9 / 16]: a row is
+ *                 D / 2 bytes of e2m1 codes (element 2 i in the low half of
+ *                 byte i, element 2 i + 1 in the high half), then D / 16
+ *                 bytes of e4m3 block scales
+ *                 k_scale, v_scale: float [num_pages][Hkv][page_size]
  *   slot          page * page_size + offset; logical position p of sequence b
  *                 lives in page block_table[b][p / page_size], offset
  *                 p % page_size.
@@ -88,8 +93,22 @@ typedef enum {
  * reading its source's scales) hold one code byte per element and one fp32
  * scale per (token, KV head), separately for K and V; the value is
  * code * scale.  fp8 codes are e4m3 (the OCP 8-bit floating point E4M3
- * encoding without infinities, largest finite magnitude 448). */
-typedef enum { FA_KV_BF16 = 0, FA_KV_INT8 = 1, FA_KV_FP8 = 2 } fa_kv_dtype;
+ * encoding without infinities, largest finite magnitude 448).
+ *
+ * fp4 (this library's, no counterpart on the pages): microscaled 4-bit codes.
+ * A row (one token, one KV head, K or V) of D values x has the scale
+ *   s = 2^e, e the smallest integer >= -116 with max|x| <= 2688 * 2^e
+ * (2688 = 6 * 448, the largest code times the largest block scale), each block
+ * of 16 consecutive values the e4m3 scale b nearest to (the block's max|x|) /
+ * (6 s), ties to the even mantissa, and each value the e2m1 code nearest to
+ * x / (s b), ties to the even code, magnitudes above 6 saturating, the sign
+ * kept.  e2m1 codes 0 .. 7 stand for 0, 0.5, 1, 1.5, 2, 3, 4, 6, codes 8 .. 15
+ * for their negatives.  A block whose scale is 0 keeps zeros.  The value of a
+ * code is code * b * s: 6 significant bits, so reading a row back into bf16
+ * rounds nothing.  A NaN element is stored as 0, a magnitude above 2^127 (the
+ * infinities included) as 2^127.  A token costs 2 * (D * 9 / 16 + 4) bytes per
+ * KV head: 3.5 times less than bf16. */
+typedef enum { FA_KV_BF16 = 0, FA_KV_INT8 = 1, FA_KV_FP8 = 2, FA_KV_FP4 = 3 } fa_kv_dtype;
 typedef enum { FA_FULL = 0, FA_SLIDING = 1 } fa_layer_kind;
 
 /* kv_source values besides an explicit earlier layer index */
@@ -104,7 +123,7 @@ typedef enum { FA_FULL = 0, FA_SLIDING = 1 } fa_layer_kind;
 #define FA_DEV_ERR_WORKSPACE 0x10u /* decode or extend-split workspace counters
                                       were not zero                                 */
 #define FA_DEV_ERR_RANGE 0x20u     /* a value out of the kernels' range: an f16
-                                      operand saturated (8-bit formats: a q, or
+                                      operand saturated (8- and 4-bit formats: a q, or
                                       an extend k_ext / v_ext, magnitude of 65520
                                       or more), or an extend score with
                                       |sm_scale * q.k| * log2(e) of 32767 or
@@ -211,14 +230,14 @@ FA_API fa_status fa_cache_set_window_pool(fa_cache* cache, int32_t window_pages)
 FA_API fa_status fa_cache_layer_source(const fa_cache* cache, int32_t layer, int32_t* slab_owner);
 
 /* Bytes the caller must allocate for one of K or V of an owning layer
- * (num_pages * Hkv * page_size * D * elem) and for one of k_scale or v_scale
- * (0 in bf16).  A shared layer reports 0 and 0.  Host only. */
+ * (num_pages * Hkv * page_size rows of 2 D bytes in bf16, D in the 8-bit
+ * formats, D * 9 / 16 in fp4) and for one of k_scale or v_scale (0 in bf16).  A shared layer reports 0 and 0.  Host only. */
 FA_API fa_status fa_cache_slab_bytes(const fa_cache* cache, int32_t layer, size_t* kv_bytes,
                               size_t* scale_bytes);
 
 /* Bind caller-owned device buffers as the slab of an owning layer (k, v in the
- * layout above; k_scale, v_scale required in the 8-bit formats, ignored in
- * bf16).  Binding a shared layer returns FA_ERR_INVALID_ARG: it reads its
+ * layout above; k_scale, v_scale required in the 8- and 4-bit formats, ignored
+ * in bf16).  Binding a shared layer returns FA_ERR_INVALID_ARG: it reads its
  * source's slab.  Rebinding replaces the previous pointers.  Encodes the TMA
  * descriptors the kernels use and clears the cache's device error word on
  * the current device (synchronously: do not call it during stream capture),
@@ -228,7 +247,8 @@ FA_API fa_status fa_cache_bind_slab(fa_cache* cache, int32_t layer, void* k, voi
                              float* v_scale);
 
 /* Bytes one token costs across the slabs of the owning layers of `kind`
- * (fa_layer_kind): per owning layer and KV head 2 * (D * elem + scale bytes).
+ * (fa_layer_kind): per owning layer and KV head 2 * (the row's bytes + 4 of scale,
+ * no scale in bf16).
  * Shared layers cost nothing ("FreeToken PR #898", description bullet on
  * kv_cache_group_specs; its "End to end" section prints these unit_bytes).
  * Host only. */
@@ -247,11 +267,27 @@ FA_API size_t fa_kv_bytes_per_token(const fa_cache* cache, int32_t kind);
  * gives s = 0 and all-zero codes.  fp8 format: the same with s = a / 448
  * and codes the e4m3 value nearest to the fp32 quotient x / s (ties to the
  * even mantissa, magnitudes above 448 saturating to 448, sign kept); a = 0
- * gives s = 0 and all-zero codes.
+ * gives s = 0 and all-zero codes.  fp4 format: as defined at fa_kv_dtype, every
+ * rounding decided exactly.
  * A KV-shared layer stores nothing: FA_OK, no launch.  T == 0: FA_OK, no
  * launch. */
 FA_API fa_status fa_kv_store(fa_cache* cache, int32_t layer, const void* k, const void* v,
                       const int32_t* slot_mapping, int32_t T, void* stream);
+
+/* Read rows back: the inverse of fa_kv_store, for every slab format.  Token t's
+ * K and V rows of every KV head are read from slot slot_mapping[t] of the
+ * layer's slab (a KV-shared layer reads its source's) into k[t], v[t].
+ * k, v: bf16 [T][Hkv][D] (device, written); either may be NULL to read only
+ * the other.  slot_mapping: int32 [T] (device); a negative slot leaves its
+ * rows of k and v as they were, as does a slot >= num_pages * page_size, which
+ * sets FA_DEV_ERR_SLOT.  Several tokens may read one slot.
+ * bf16: a bit-exact copy.  int8, fp8: the fp32 product code * scale rounded
+ * to bf16 (to nearest, ties to even).  fp4: the exact value (6 significant
+ * bits; nothing is rounded).  T == 0: FA_OK, no launch.  No counterpart on
+ * the pages: a cache's rows leave it through this call (to move a sequence to
+ * a cache of another format or page size, or to inspect it). */
+FA_API fa_status fa_kv_load(fa_cache* cache, int32_t layer, const int32_t* slot_mapping, int32_t T, void* k,
+                     void* v, void* stream);
 
 /* Workspace bytes fa_paged_decode_attn needs for this layer, batch and bound
  * on the sequence lengths: one arrival counter per (sequence, KV head, group
@@ -273,7 +309,7 @@ FA_API size_t fa_decode_workspace_bytes(const fa_cache* cache, int32_t layer, in
  * FA_DEV_ERR_BOUND and are cut at the bound).
  * out: bf16 [B][Hq][D].  lse: optional float [B][Hq], natural-log
  * sum-exp of the scaled scores.  seq_lens[b] <= 0 gives out = 0 and
- * lse = -inf.  Over 8-bit slabs q is converted to f16 for the tensor cores:
+ * lse = -inf.  Over 8- and 4-bit slabs q is converted to f16 for the tensor cores:
  * an element of magnitude 65536 or more saturates to +-65504 and sets
  * FA_DEV_ERR_RANGE.  workspace: device scratch of at least
  * fa_decode_workspace_bytes(cache, layer, B, max_seq_len) bytes (may be NULL
@@ -301,7 +337,7 @@ FA_API fa_status fa_paged_decode_attn(fa_cache* cache, int32_t layer, const void
  * position seq_lens[b] - 1 (negative: not stored; past the pool: not stored,
  * FA_DEV_ERR_SLOT).  The slot must be the one the block table gives for that
  * position, as with the two separate calls.  Rows are stored in the slab's
- * format (bf16 copy, or the 8-bit quantisation of fa_kv_store, bit for bit)
+ * format (bf16 copy, or the quantisation of fa_kv_store, bit for bit)
  * by the CTA that reads the tile holding that position, before it reads it;
  * sequences with seq_lens[b] <= 0 still get their row stored.  For a shared
  * layer k_new, v_new and slot_mapping are ignored (may be NULL) and the call
@@ -389,10 +425,11 @@ FA_API fa_status fa_paged_decode_attn_noalloc(fa_cache* cache, int32_t layer, co
  * capacity parameter).  Sequence b has prefix_lens[b] = P_b tokens already
  * in the cache and n_b = qo_indptr[b+1] - qo_indptr[b] new tokens; new token
  * i sits at position P_b + i and attends to prefix positions (from the slab;
- * in the 8-bit formats code * scale) and chunk positions P_b + j, j <= i
+ * in the 8- and 4-bit formats the code's value) and chunk positions P_b + j, j <= i
  * (from k_ext / v_ext, bf16, never quantised), under the layer's mask.  Over
- * 8-bit slabs every tensor-core operand is f16 with fp32 accumulation: q,
- * the chunk k, v, the prefix codes (exact in f16), and the softmax weights
+ * 8- and 4-bit slabs every tensor-core operand is f16 with fp32 accumulation: q,
+ * the chunk k, v, the prefix codes (exact in f16; fp4: times their block scales,
+ * exact too), and the softmax weights
  * times the keys' V scales; the K scales multiply the fp32 scores.  Range: a
  * q, k_ext or v_ext element of magnitude 65536 or more (bf16 has nothing
  * between 65280 and 65536, f16 nothing past 65504) saturates to +-65504 and
@@ -434,7 +471,7 @@ FA_API fa_status fa_paged_extend_attn(fa_cache* cache, int32_t layer, const void
  * lengths including the new tokens, <= max_seq_len; a length below n_b sets
  * FA_DEV_ERR_BOUND), block_table: int32 [B][max_pages_per_seq].  out: bf16
  * [num_tokens][Hq][D]; lse: optional float [num_tokens][Hq].  Every slab
- * format (8-bit codes and scales applied as in extend); Hq / Hkv must divide 128. */
+ * format (codes and scales applied as in extend); Hq / Hkv must divide 128. */
 FA_API fa_status fa_paged_decode_multi_attn(fa_cache* cache, int32_t layer, const void* q, const int32_t* qo_indptr,
                                             const int32_t* seq_lens, const int32_t* block_table,
                                             int32_t max_pages_per_seq, int32_t B, int32_t num_tokens,

@@ -18,7 +18,8 @@ It computes the plain definitions, slowly and obviously:
 Conventions (the same ones the C boundary documents):
 
 * bf16 values travel as numpy ``uint16`` bit patterns; int8 codes as ``int8``;
-  fp8 e4m3 codes as ``uint8`` bit patterns.
+  fp8 e4m3 codes as ``uint8`` bit patterns; fp4 rows (e2m1 codes, two a byte,
+  then e4m3 block scales) as ``uint8``, wrapped in ``Fp4Slab`` for attention.
 * slab layout ``[num_pages][Hkv][page_size][D]``; scales ``[num_pages][Hkv][page_size]``.
 * a slot is ``page * page_size + offset``; a negative slot is skipped.
 * query head ``j`` reads KV head ``j // (Hq / Hkv)`` (contiguous groups).
@@ -40,6 +41,7 @@ KV_AUTO = -2
 KV_BF16 = 0
 KV_INT8 = 1
 KV_FP8 = 2
+KV_FP4 = 3
 
 
 # ---------------------------------------------------------------------------
@@ -126,6 +128,8 @@ def kv_bytes_per_token(layers, kind: int, kv_dtype: int) -> int:
             continue
         if kv_dtype == KV_BF16:
             per_row = 2 * L["head_dim"]
+        elif kv_dtype == KV_FP4:
+            per_row = L["head_dim"] // 2 + L["head_dim"] // 16 + 4
         else:
             per_row = L["head_dim"] + 4
         total += 2 * L["num_kv_heads"] * per_row
@@ -260,6 +264,67 @@ def store_fp8(codes_k, codes_v, scale_k, scale_v, k, v, slot_mapping, page_size:
                      page_size)
 
 
+# fp4: microscaled 4-bit rows (include/fa.h, fa_kv_dtype).  In float64, where
+# every quotient compared with a border between two codes is exact enough to
+# fall on its side, and exactly on it where it is a tie.
+
+E2M1_MAGS = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def _nearest_even(mags, a):
+    """Index of the member of the ascending array nearest to each a >= 0, a tie
+    going to the even index, past the last member the last."""
+    lo = np.clip(np.searchsorted(mags, a, side="right") - 1, 0, len(mags) - 1)
+    hi = np.minimum(lo + 1, len(mags) - 1)
+    d_lo, d_hi = a - mags[lo], mags[hi] - a
+    return np.where((hi > lo) & ((d_hi < d_lo) | ((d_hi == d_lo) & (lo % 2 == 1))), hi, lo)
+
+
+def quantize_fp4(x_bits):
+    """fp4 rows of x[..., D] (bf16 bits): (rows uint8 [..., D * 9 / 16], scale
+    float32 [...]).  NaN counts as 0, a magnitude above 2^127 as 2^127; the row
+    scale is 2^e, e the smallest integer >= -116 with max|x| <= 2688 * 2^e; each
+    block of 16 has the e4m3 scale nearest to its max|x| / (6 * 2^e), each value
+    the e2m1 code nearest to x / (2^e * block scale)."""
+    x = bf16_to_f64(x_bits)
+    neg = np.signbit(x) & ~np.isnan(x)
+    mag = np.minimum(np.where(np.isnan(x), 0.0, np.abs(x)), 2.0 ** 127)
+    a = np.max(mag, axis=-1)
+    m, p = np.frexp(a)                                   # a = m * 2^p, m in [0.5, 1); 2688 = 0.65625 * 2^12
+    e = np.where(a > 0, np.maximum(np.where(m <= 0.65625, p - 12, p - 11), -116), -116)
+    y = np.ldexp(mag, -e[..., None])                     # exact
+    y = y.reshape(y.shape[:-1] + (-1, 16))
+    sb = _nearest_even(e4m3_value(np.arange(0x7F, dtype=np.uint8)), np.max(y, axis=-1) / 6.0).astype(np.uint8)
+    b = e4m3_value(sb)[..., None]
+    q = np.where(b > 0, y / np.where(b > 0, b, 1.0), 0.0)
+    code = _nearest_even(E2M1_MAGS, q).astype(np.uint8).reshape(mag.shape) | (neg.astype(np.uint8) << 3)
+    rows = np.concatenate([code[..., 0::2] | (code[..., 1::2] << 4), sb], axis=-1)
+    return rows.astype(np.uint8), np.ldexp(np.float32(1.0), e).astype(np.float32)
+
+
+def fp4_value(rows, scale) -> np.ndarray:
+    """float64 values [..., D] of fp4 rows [..., D * 9 / 16] and their scales."""
+    rows = np.asarray(rows, np.uint8)
+    D = rows.shape[-1] * 16 // 9
+    b = rows[..., : D // 2]
+    code = np.stack([b & 15, b >> 4], axis=-1).reshape(b.shape[:-1] + (D,))
+    v = np.where(code & 8, -1.0, 1.0) * E2M1_MAGS[code & 7]
+    return v * np.repeat(e4m3_value(rows[..., D // 2:]), 16, axis=-1) * np.asarray(scale, np.float64)[..., None]
+
+
+class Fp4Slab:
+    """An fp4 slab [num_pages][Hkv][ps][D * 9 / 16] for the attention functions."""
+
+    def __init__(self, rows):
+        self.rows = rows
+
+
+def store_fp4(rows_k, rows_v, scale_k, scale_v, k, v, slot_mapping, page_size: int) -> None:
+    """Quantise and write rows like store_bf16, into fp4 slabs (uint8)
+    [num_pages][Hkv][ps][D * 9 / 16] and fp32 scale arrays [num_pages][Hkv][ps]."""
+    _store_quantised(quantize_fp4, rows_k, rows_v, scale_k, scale_v, k, v, slot_mapping, page_size)
+
+
 # ---------------------------------------------------------------------------
 # attention over the logically gathered KV
 # ---------------------------------------------------------------------------
@@ -281,12 +346,15 @@ def gather_rows(slab, scales, block_table_row, positions, h: int, page_size: int
     """Logical rows at `positions` of KV head h, as float64 [n][D]: page =
     block_table_row[pos // page_size], offset = pos % page_size.  bf16 slabs
     (uint16) are widened exactly; int8 slabs (int8) and fp8 slabs (uint8 e4m3
-    bit patterns) are dequantised as value(code) * scale."""
+    bit patterns) are dequantised as value(code) * scale, fp4 slabs (Fp4Slab) as
+    code * block scale * scale."""
     positions = np.asarray(positions, dtype=np.int64)
     pages = np.asarray(block_table_row, dtype=np.int64)[positions // page_size]
     if np.any(pages < 0):
         raise IndexError("visible position maps to an unassigned page")
     offs = positions % page_size
+    if isinstance(slab, Fp4Slab):
+        return fp4_value(slab.rows[pages, h, offs, :], scales[pages, h, offs])
     rows = slab[pages, h, offs, :]
     if slab.dtype == np.uint16:
         return bf16_to_f64(rows)

@@ -31,6 +31,7 @@ KV_AUTO = -2  # shared layer: source = last earlier owning layer of its kind
 KV_BF16 = 0
 KV_INT8 = 1
 KV_FP8 = 2
+KV_FP4 = 3
 
 
 def layer(kind: int, head_dim: int, hq: int, hkv: int, window: int = 0,
