@@ -260,9 +260,25 @@ class Cache:
     def store_layers(self, layers, ks, vs, slot_mappings, stream=None) -> None:
         """fa_kv_store_layers: the stores of several layers in one launch
         (shared layers are skipped)."""
+        if self.kv_dtype == KV_FP4:
+            for i, k, v, s in zip(layers, ks, vs, slot_mappings):
+                if self.source(i) == i:
+                    self._rows(i, k, v, s)
+                    _need("slot_mappings", s, torch.int32, slot_mappings[0].numel())
         T = int(slot_mappings[0].numel())
         _check(_lib.fa_kv_store_layers(self._h, len(layers), _i32s(layers), _ptrs(ks), _ptrs(vs),
                                        _ptrs(slot_mappings), T, _s(stream)))
+
+    def _decode_args(self, layer: int, q, block_table, seq_lens, out, lse) -> None:
+        """fp4 caches: refuse tensors the decode kernel would misread."""
+        d, B = self._layer(layer), int(q.shape[0])
+        n = B * d["num_q_heads"]
+        _need("q", q, torch.bfloat16, n * d["head_dim"])
+        _need("out", out, torch.bfloat16, n * d["head_dim"])
+        _need("seq_lens", seq_lens, torch.int32, B)
+        _need("block_table", block_table, torch.int32, B * block_table.shape[1])
+        if lse is not None:
+            _need("lse", lse, torch.float32, n)
 
     def decode_layers_workspace_bytes(self, layers, batch: int, max_seq_len: int) -> int:
         return int(_lib.fa_decode_layers_workspace_bytes(self._h, len(layers), _i32s(layers), batch, max_seq_len))
@@ -271,6 +287,9 @@ class Cache:
                       workspace=None, stream=None) -> None:
         """fa_paged_decode_attn_layers: decode several layers of one head_dim
         in one launch (the current rows must already be stored)."""
+        if self.kv_dtype == KV_FP4:
+            for n, i in enumerate(layers):
+                self._decode_args(i, qs[n], block_tables[n], seq_lens, outs[n], None if lses is None else lses[n])
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         _check(_lib.fa_paged_decode_attn_layers(self._h, len(layers), _i32s(layers), _ptrs(qs), _ptrs(block_tables),
                                                 int(block_tables[0].shape[1]), _p(seq_lens), int(qs[0].shape[0]),
@@ -291,6 +310,8 @@ class Cache:
 
     def decode(self, layer: int, q, block_table, seq_lens, max_seq_len: int, out, lse=None, workspace=None,
                stream=None) -> None:
+        if self.kv_dtype == KV_FP4:
+            self._decode_args(layer, q, block_table, seq_lens, out, lse)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         _check(_lib.fa_paged_decode_attn(self._h, layer, _p(q), _p(block_table), int(block_table.shape[1]),
                                          _p(seq_lens), int(q.shape[0]), int(max_seq_len), _p(out), _p(lse),
@@ -300,6 +321,10 @@ class Cache:
                      out, lse=None, workspace=None, stream=None) -> None:
         """fa_paged_decode_store_attn: store the current token's k, v rows and
         decode in one launch (owning layers; a shared layer only decodes)."""
+        if self.kv_dtype == KV_FP4:
+            self._decode_args(layer, q, block_table, seq_lens, out, lse)
+            if self.source(layer) == layer:
+                self._rows(layer, k_new, v_new, slot_mapping)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         _check(_lib.fa_paged_decode_store_attn(self._h, layer, _p(q), _p(k_new), _p(v_new), _p(slot_mapping),
                                                _p(block_table), int(block_table.shape[1]), _p(seq_lens),
@@ -310,6 +335,8 @@ class Cache:
                        stream=None) -> None:
         """fa_paged_decode_attn_noalloc: decode with the library's fixed scratch
         (no device allocation); calls must not overlap on the GPU."""
+        if self.kv_dtype == KV_FP4:
+            self._decode_args(layer, q, block_table, seq_lens, out, lse)
         _check(_lib.fa_paged_decode_attn_noalloc(self._h, layer, _p(q), _p(block_table), int(block_table.shape[1]),
                                                  _p(seq_lens), int(q.shape[0]), int(max_seq_len), _p(out), _p(lse),
                                                  _s(stream)))

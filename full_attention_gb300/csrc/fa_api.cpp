@@ -89,6 +89,9 @@ DecodePlan plan_decode(const fa_cache* c, int layer, int B, int max_seq_len, lon
   // a pipeline step moves 32 KB of K and V; a CTA gets at least 4 steps
   const int tile_bytes = 2 * kTile * d.head_dim * static_cast<int>(elem_bytes(c->kv_dtype));
   p.min_tiles = 4 * (32768 / tile_bytes);
+  // fp4: a CTA gets at least two steps (of 64 keys at head_dim 512, 128 at 256)
+  const bool fp4 = c->kv_dtype == FA_KV_FP4;
+  if (fp4) p.min_tiles = d.head_dim == 512 ? 8 : 16;
   const long long t_bound = static_cast<long long>(p.units) * tiles;
   const long long slots = max_cta > 0 ? max_cta : 2LL * sm_count();   // two resident CTAs per SM
   long long n = (t_bound + p.min_tiles - 1) / p.min_tiles;
@@ -98,7 +101,7 @@ DecodePlan plan_decode(const fa_cache* c, int layer, int B, int max_seq_len, lon
   if (p.ncta > 1) {
     const size_t rows = static_cast<size_t>(p.ncta + p.units) * 8;   // partial slots x heads
     p.off_ml = (static_cast<size_t>(p.units) * 4 + 255) / 256 * 256;
-    p.off_o = p.off_ml + (rows * 2 * sizeof(float) + 255) / 256 * 256;
+    p.off_o = p.off_ml + (rows * (fp4 ? 4 : 2) * sizeof(float) + 255) / 256 * 256;
     p.ws_bytes = p.off_o + rows * d.head_dim * sizeof(float);
   }
   return p;
@@ -642,7 +645,6 @@ static fa_status decode_call(fa_cache* c, int32_t layer, const void* q, const vo
   if (max_pages_per_seq < (max_seq_len + c->page_size - 1) / c->page_size)
     return fail(FA_ERR_INVALID_ARG, "max_pages_per_seq %d cannot hold max_seq_len %d", max_pages_per_seq,
                 max_seq_len);
-  if (c->kv_dtype == FA_KV_FP4) return fail(FA_ERR_UNSUPPORTED, "fp4 slabs: attention is not served");
   DecodePlan p = plan_decode(c, layer, B, max_seq_len);
   if (workspace_bytes < p.ws_bytes || (p.ws_bytes && !workspace))
     return fail(FA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, p.ws_bytes);
@@ -714,7 +716,6 @@ fa_status fa_paged_decode_attn_layers(fa_cache* c, int32_t n, const int32_t* lay
     if (!aligned16(q[i]) || !aligned16(out[i])) return fail(FA_ERR_INVALID_ARG, "q, out of layer %d must be 16-byte aligned", layers[i]);
   }
   if (B == 0) return ok();
-  if (c->kv_dtype == FA_KV_FP4) return fail(FA_ERR_UNSUPPORTED, "fp4 slabs: attention is not served");
   const size_t need = fa_decode_layers_workspace_bytes(c, n, layers, B, max_seq_len);
   if (workspace_bytes < need || (need && !workspace))
     return fail(FA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);

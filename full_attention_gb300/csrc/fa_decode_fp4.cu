@@ -1,0 +1,676 @@
+// Paged decode attention over microscaled 4-bit slabs (FA_KV_FP4).
+//
+// Per unit (sequence, KV head, chunk of up to 8 query heads) with visible rows
+// j, in the log2 domain:
+//   s_j = sm_scale log2(e) * ks_j * (q . kc_j),      kc_j = code * block scale
+//   o   = sum_j 2^(s_j + e_j - M) vc_j * 2^M / L,    L = sum_j 2^(s_j - m) * 2^m
+// where ks_j and 2^e_j are the rows' fp32 scales (powers of two) and kc, vc are
+// exact f16 numbers.  The base M tracks the largest s_j + e_j, not the largest
+// score, so a row whose values are tiny against its neighbours' cannot push
+// their weights out of f16's range, nor an all-zero V row (e = -116) under a
+// sink token's weight; L keeps a base of its own.
+//
+// What bounds it: HBM (a row is 148 bytes at head_dim 256, 292 at 512), then
+// the conversion: every code passes through one e2m1 -> f16 conversion and one
+// f16 product with its block's scale before a matrix instruction can take it,
+// about 2.1 instructions a code pair with the loads.
+//
+// Work decomposition: the shares of fa_decode.cuh.  A step is 64 keys at
+// head_dim 512 and 128 at 256 (18 KB of K, as much of V): wide enough that one
+// barrier between the consumer warps per step is cheap.
+//   warp 4      producer: per step one bulk copy per 16-row tile of K and of V
+//               (a tile's rows are contiguous) and of their row scales, into a
+//               ring of five slots, K and V alternating;
+//   warps 0-3   S^T = K Q^T, each warp whole tiles over the full head_dim
+//               (keys on the MMA's M side, the 8 heads on N), the softmax
+//               weights of its own tiles against the tile's own base M_w,
+//               rounded up to an integer, into shared memory as f16; barrier;
+//               then O^T += V^T P^T, each warp a quarter of the columns, the
+//               weights of tile w times 2^(M_w - M), a power of two.
+// Rows are 144 or 288 bytes apart in shared memory, so the fragment loads (one
+// 4-byte word of 8 codes a lane at 256, 8 bytes at 512) hit 32 different banks
+// without any swizzle; at 512 the MMA's key index r stands for tile row
+// key_row(r) to that end.  The MMA contraction over head_dim may run in any
+// order, so a lane's codes are taken in the order they are stored, and Q
+// likewise.
+#include "fa_decode.cuh"
+
+namespace fa {
+
+template <int D>
+struct F4Cfg {
+  static constexpr int NW = D / 256;                   // words of 8 codes a lane loads at a time
+  static constexpr int ROWB = kRowBytes<D, FA_KV_FP4>; // 144, 288
+  static constexpr int TILE_BYTES = kTile * ROWB;
+  static constexpr int NCW = 4;                        // consumer warps
+  static constexpr int TPW = D == 256 ? 2 : 1;         // tiles per consumer warp and step
+  static constexpr int NT = NCW * TPW;                 // tiles per step
+  static constexpr int SC_BYTES = NT * kTile * 4;      // one step's K (or V) row scales
+  static constexpr int SLOT = NT * TILE_BYTES + 2 * SC_BYTES;   // rows; in K slots also both row scales
+  static constexpr int NSLOT = 5;
+  static constexpr int NTHR = (NCW + 1) * 32;
+  static constexpr int NJ = 8;                         // loads of NW words a lane makes per row
+  static constexpr int MT = D / 4 / 16;                // m16 tiles of O^T per warp
+  static constexpr int P_HEAD = 48;                    // bytes per head of a tile's weights (16 f16 + padding)
+  static constexpr int P_TILE = 8 * P_HEAD;
+  static constexpr int OFF_P = NSLOT * SLOT;           // [2][NT] tiles of weights
+  static constexpr int OFF_MW = OFF_P + 2 * NT * P_TILE;   // [2][8 heads][NT] tile bases
+  static constexpr int OFF_ML = OFF_MW + 2 * 8 * NT * 4;   // [NCW][8] (m, l)
+  static constexpr int OFF_W = OFF_ML + NCW * 8 * 8;       // merge weights [64][8], then [8] factors and [8] lse
+  static constexpr int OFF_BAR = OFF_W + (64 * 8 + 16) * 4;
+  static constexpr int SMEM = OFF_BAR + 2 * NSLOT * 8;
+  static_assert(SLOT % 128 == 0, "slot alignment");
+  static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
+};
+
+// Tile row that MMA key index r stands for.  Rows 288 bytes apart start 8 banks
+// apart: with this order both the S loads (lanes' rows r = 0..7) and the PV
+// loads (rows r = 2t, and so on) start in four banks 8 apart.
+template <int D>
+__device__ __forceinline__ int key_row(int r) {
+  if constexpr (D == 256) return r;
+  else return (r & 8) | ((r & 1) << 2) | ((r >> 1) & 3);
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The f16 block scales (broadcast to both halves) of the lane's words j = 2 i
+// and 2 i + 1 of a row whose D / 16 scale bytes are sw.
+template <int D>
+__device__ __forceinline__ void block_scales(const uint32_t (&sw)[D / 64], int i, int tig, uint32_t& s0, uint32_t& s1) {
+  uint32_t two;
+  if constexpr (D == 256) {   // words 4 j + tig: block 2 j + tig / 2
+    const uint32_t h = tig >> 1;
+    two = __byte_perm(sw[i], 0, h | ((2 + h) << 4));
+  } else {                    // words 8 j + 2 tig, + 1: block 4 j + tig
+    two = __byte_perm(sw[2 * i], sw[2 * i + 1], tig | ((4 + tig) << 4));
+  }
+  const uint32_t h = e4m3x2_to_f16x2(two & 0xffffu);
+  s0 = __byte_perm(h, 0, 0x1010);
+  s1 = __byte_perm(h, 0, 0x3232);
+}
+
+template <int N>
+__device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 1) {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (N == 2) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    w[0] = x.x;
+    w[1] = x.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const uint4 x = *reinterpret_cast<const uint4*>(p + 4 * i);
+      w[i] = x.x;
+      w[i + 1] = x.y;
+      w[i + 2] = x.z;
+      w[i + 3] = x.w;
+    }
+  }
+}
+
+// Merge the partial rows of unit u that CTAs cf..cl left (this CTA arrived
+// last), in CTA order.  Run by the 128 consumer threads; wbuf holds 64 * 8 + 16
+// floats.
+template <int D>
+__device__ void merge_unit_fp4(const DecK& p, int u, const Unit& x, int nh, int head0, int cf, int cl, float* wbuf) {
+  constexpr int CH = 64;
+  constexpr int ITEMS = 8 * (D / 4) / 128;
+  const int tid = threadIdx.x, nct = cl - cf + 1;
+  const float4* ml = reinterpret_cast<const float4*>(p.ml_part) + (static_cast<size_t>(cf) + u) * 8;
+  float* fin = wbuf + CH * 8;   // [8] 2^(M - m) / L, [8] lse
+  const int h = tid >> 4, k = tid & 15;
+  float M = -INFINITY, m = -INFINITY, L = 0.f;
+  for (int c = k; c < nct; c += 16) {
+    const float4 v = __ldcg(ml + c * 8 + h);
+    M = fmaxf(M, v.x);
+    const float mn = fmaxf(m, v.y);
+    if (mn > -INFINITY) L = L * ex2(m - mn) + v.z * ex2(v.y - mn);
+    else L += v.z;   // NaN scores only
+    m = mn;
+  }
+#pragma unroll
+  for (int o = 8; o; o >>= 1) {
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float mo = __shfl_xor_sync(0xffffffffu, m, o), Lo = __shfl_xor_sync(0xffffffffu, L, o);
+    const float mn = fmaxf(m, mo);
+    L = mn > -INFINITY ? L * ex2(m - mn) + Lo * ex2(mo - mn) : L + Lo;
+    m = mn;
+  }
+  if (k == 0) {
+    fin[h] = M > -INFINITY ? ex2(M - m) / L : 1.0f / L;
+    fin[8 + h] = (m + __log2f(L)) * 0.69314718055994531f;
+  }
+  float4 acc[ITEMS];
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c0 = 0; c0 < nct; c0 += CH) {
+    const int n = min(CH, nct - c0);
+    named_bar_sync(1, 128);
+    for (int c = k; c < n; c += 16) {
+      const float Mc = __ldcg(&ml[(c0 + c) * 8 + h].x);
+      wbuf[c * 8 + h] = Mc > -INFINITY ? ex2(Mc - M) : 0.f;
+    }
+    named_bar_sync(1, 128);
+#pragma unroll 4
+    for (int c = 0; c < n; ++c) {
+      const float* src = p.o_part + (static_cast<size_t>(cf + c0 + c) + u) * 8 * D;
+      float4 o[ITEMS];
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i) o[i] = __ldcg(reinterpret_cast<const float4*>(src) + tid + i * 128);
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i) {
+        const float w = wbuf[c * 8 + (tid + i * 128) / (D / 4)];
+        acc[i].x += w * o[i].x;
+        acc[i].y += w * o[i].y;
+        acc[i].z += w * o[i].z;
+        acc[i].w += w * o[i].w;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const int idx = tid + i * 128, hh = idx / (D / 4), d = (idx % (D / 4)) * 4;
+    if (hh >= nh) continue;
+    const float f = fin[hh];
+    *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(x.b) * p.Hq + head0 + hh) * D + d) =
+        make_uint2(pack_bf16x2(acc[i].x * f, acc[i].y * f), pack_bf16x2(acc[i].z * f, acc[i].w * f));
+  }
+  if (p.lse && tid < nh) p.lse[static_cast<size_t>(x.b) * p.Hq + head0 + tid] = fin[8 + tid];
+  named_bar_sync(1, 128);   // the scratch is free again
+}
+
+template <int D>
+__device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, const int grid) {
+  using C = F4Cfg<D>;
+  constexpr int KV = FA_KV_FP4;
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* empty = full + C::NSLOT;
+  __shared__ int abort_flag, sh_last;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gid = lane >> 2, tig = lane & 3;
+
+  if (!p.early_metadata) griddep_wait();
+  griddep_launch_dependents();
+
+  Share sh;
+  if (!cut_share(p, cta, grid, sh)) {
+    if (sh.ncta == 0 && cta == 0) {   // nothing visible anywhere: only empty outputs to write
+      griddep_wait();
+      zero_empty_units<D, KV>(p, 0, 1, threadIdx.x, blockDim.x);
+    }
+    return;
+  }
+  const int ncta = sh.ncta, kper = sh.kper, T = sh.T;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::NSLOT; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], C::NCW);
+    }
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  finish_share(cta, sh);
+  const int u0 = sh.u0, p0 = sh.p0;
+  const long long s_beg = sh.s_beg, s_end = sh.s_end;
+
+  if (warp == C::NCW) {
+    // ------------------------------------------------------------ producer
+    int e = 0;   // slots filled
+    bool ok = true, first = true;
+    long long P = p0;
+    for (int u = u0; ok && P < s_end; ++u) {
+      const Unit x = unit_of(p, u);
+      if (x.n > 0) {
+        const int ta = x.t_first + static_cast<int>(max(s_beg, P) - P);
+        const int tz = x.t_first + static_cast<int>(min(s_end, P + x.n) - P);
+        const int32_t* bt = p.block_table + static_cast<size_t>(x.b) * p.max_pages_per_seq;
+        // the CTA that reads the unit's last tile (it holds position L - 1)
+        // stores the current token's rows first, so its own copy sees them
+        const bool store_here = p.slots != nullptr && tz == x.t_first + x.n;
+        RowRegs<D> rk, rv;
+        for (int k0 = ta; ok && k0 < tz; k0 += 32) {
+          int pid = -1;
+          if (k0 + lane < tz) {
+            pid = __ldg(bt + (k0 + lane) / p.tiles_per_page);
+            if (pid < 0 || pid >= p.num_pages) {
+              atomicOr(p.err, FA_DEV_ERR_PAGE);
+              pid = -1;
+            }
+          }
+          if (first) griddep_wait();   // from here on the slab is read
+          first = false;
+          if (k0 == ta && store_here) {
+            const size_t src = (static_cast<size_t>(x.b) * p.Hkv + x.h) * D;
+            row_load<D>(rk, p.k_new + src, lane);
+            row_load<D>(rv, p.v_new + src, lane);
+          }
+          for (int k = k0; k < min(k0 + 32, tz); k += C::NT) {
+            const int ntl = min(C::NT, tz - k);
+            if (store_here && k + ntl >= tz) {
+              store_current<D, KV>(p, rk, rv, x.h, __ldg(p.slots + x.b), lane);
+              // each lane orders its generic writes before the async-proxy
+              // read of the tile that holds them
+              fence_proxy_async_global();
+              __syncwarp();
+            }
+            const int pg = __shfl_sync(0xffffffffu, pid, (k - k0 + lane) & 31);
+            const bool mine = lane < ntl;
+            const unsigned bad = __ballot_sync(0xffffffffu, mine && pg < 0);
+            const int nbad = __popc(bad);
+            const int tile = k + lane;
+            const size_t row0 = mine && pg >= 0
+                                    ? (static_cast<size_t>(pg) * p.Hkv + x.h) * p.page_size + (tile % p.tiles_per_page) * kTile
+                                    : 0;
+#pragma unroll
+            for (int side = 0; side < 2; ++side, ++e) {
+              const int st = e % C::NSLOT;
+              uint8_t* dst = smem + st * C::SLOT;
+              bool w = true;
+              if (lane == 0) w = mbar_wait(&empty[st], ((e / C::NSLOT) & 1) ^ 1);
+              ok = __shfl_sync(0xffffffffu, w, 0) && ok;
+              if (!ok) break;
+              if (bad) {   // tiles without a page (reported) read as zeros
+                for (int t = 0; t < ntl; ++t)
+                  if (bad >> t & 1) {
+                    for (int i = lane; i < C::TILE_BYTES / 16; i += 32)
+                      reinterpret_cast<uint4*>(dst + t * C::TILE_BYTES)[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (side == 0 && lane < kTile) {
+                      float* sc = reinterpret_cast<float*>(dst + C::NT * C::TILE_BYTES);
+                      sc[t * kTile + lane] = 1.0f;
+                      sc[(C::NT + t) * kTile + lane] = 1.0f;
+                    }
+                  }
+                fence_proxy_async_smem();   // before later copies into the slot
+                __syncwarp();
+              }
+              if (lane == 0)
+                mbar_arrive_expect_tx(&full[st], (ntl - nbad) * (C::TILE_BYTES + (side == 0 ? 2 * kTile * 4 : 0)));
+              __syncwarp();
+              if (mine && pg >= 0) {
+                bulk_load(dst + lane * C::TILE_BYTES, (side ? p.vb : p.kb) + row0 * C::ROWB, C::TILE_BYTES, &full[st]);
+                if (side == 0) {
+                  uint8_t* sc = dst + C::NT * C::TILE_BYTES;
+                  bulk_load(sc + lane * kTile * 4, p.ksb + row0, kTile * 4, &full[st]);
+                  bulk_load(sc + C::SC_BYTES + lane * kTile * 4, p.vsb + row0, kTile * 4, &full[st]);
+                }
+              }
+              __syncwarp();
+            }
+            if (!ok) break;
+          }
+        }
+      }
+      P += x.n;
+    }
+    if (lane == 0) {
+      if (!ok) atomicOr(p.err, FA_DEV_ERR_TIMEOUT);
+      // drain: no bulk copy may still be landing when the CTA exits
+      for (int i = max(0, e - C::NSLOT); i < e; ++i)
+        if (!mbar_wait(&full[i % C::NSLOT], (i / C::NSLOT) & 1)) atomicOr(p.err, FA_DEV_ERR_TIMEOUT);
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  griddep_wait();
+  zero_empty_units<D, KV>(p, cta, ncta, threadIdx.x, C::NCW * 32);
+  constexpr float P_OFF = 8.0f;      // weights reach 2^8 against their own tile's base
+  constexpr float SLACK = 4.0f;      // M follows a tile's base only past 2^4 (weights stay below 2^12)
+  int e = 0, step = 0;
+  long long P = p0;
+  for (int u = u0; P < s_end; ++u) {
+    const Unit x = unit_of(p, u);
+    if (x.n == 0) continue;   // an empty unit advances nothing
+    const int ta = x.t_first + static_cast<int>(max(s_beg, P) - P);
+    const int tz = x.t_first + static_cast<int>(min(s_end, P + x.n) - P);
+    const int nh = min(8, p.g - x.c * 8), head0 = x.h * p.g + x.c * 8;
+    const int qpos = x.L - 1, lo = x.lo;
+    const bool hv = gid < nh;
+
+    // queries: Q^T fragments (B operand) as f16, in the order the codes are
+    // stored; zero for padded heads
+    uint32_t qf[C::NJ][4 * C::NW];
+    {
+      uint32_t qbig = 0;
+      const __nv_bfloat16* qrow = p.q + (static_cast<size_t>(x.b) * p.Hq + head0 + (hv ? gid : 0)) * D;
+#pragma unroll
+      for (int j = 0; j < C::NJ; ++j)
+#pragma unroll
+        for (int w = 0; w < C::NW; ++w) {
+          const uint4 v = hv ? __ldcg(reinterpret_cast<const uint4*>(qrow) + (4 * j + tig) * C::NW + w)
+                             : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t vv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            qbig |= bf16x2_past_f16(vv[i]);
+            qf[j][4 * w + i] = pack_f16x2_sat(__uint_as_float(vv[i] << 16), __uint_as_float(vv[i] & 0xffff0000u));
+          }
+        }
+      if (__any_sync(0xffffffffu, qbig != 0) && lane == 0) atomicOr(p.err, FA_DEV_ERR_RANGE);
+    }
+
+    float o[C::MT][4];
+#pragma unroll
+    for (int i = 0; i < C::MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+    float M = -INFINITY;                          // O's base, head gid
+    float ml[2] = {-INFINITY, -INFINITY}, ll[2] = {0.f, 0.f};   // this lane's keys: max, sum (heads 2 tig, 2 tig + 1)
+
+    for (int tile0 = ta; tile0 < tz; tile0 += C::NT, ++step) {
+      const int ntl = min(C::NT, tz - tile0);
+      const int buf = step & 1;
+      uint8_t* pbuf = smem + C::OFF_P + buf * C::NT * C::P_TILE;
+      float* mw = reinterpret_cast<float*>(smem + C::OFF_MW) + buf * 8 * C::NT;
+      const int kst = e % C::NSLOT;
+      const bool kok = __all_sync(0xffffffffu, mbar_wait(&full[kst], (e / C::NSLOT) & 1));
+      if (!kok && lane == 0) {
+        abort_flag = 1;
+        atomicOr(p.err, FA_DEV_ERR_TIMEOUT);
+      }
+      ++e;
+      const uint8_t* kslot = smem + kst * C::SLOT;
+      const float* scl = reinterpret_cast<const float*>(kslot + C::NT * C::TILE_BYTES);
+#pragma unroll
+      for (int tw = 0; tw < C::TPW; ++tw) {
+        const int tile = warp + tw * C::NCW;
+        float mt[2] = {-INFINITY, -INFINITY};
+        if (kok && tile < ntl) {
+          // ---- S^T of this tile: keys gid, gid + 8 (as MMA rows), heads 2 tig, 2 tig + 1
+          const uint8_t* ra = kslot + tile * C::TILE_BYTES + key_row<D>(gid) * C::ROWB;
+          const uint8_t* rb = kslot + tile * C::TILE_BYTES + key_row<D>(gid + 8) * C::ROWB;
+          uint32_t sa[D / 64], sb[D / 64];
+          lds_words(ra + D / 2, sa);
+          lds_words(rb + D / 2, sb);
+          float acc[2][4] = {};
+#pragma unroll
+          for (int i = 0; i < C::NJ / 2; ++i) {
+            uint32_t fa_[2], fb_[2];
+            block_scales<D>(sa, i, tig, fa_[0], fa_[1]);
+            block_scales<D>(sb, i, tig, fb_[0], fb_[1]);
+#pragma unroll
+            for (int jj = 0; jj < 2; ++jj) {
+              const int j = 2 * i + jj;
+              uint32_t wa[C::NW], wb[C::NW];
+              lds_words(ra + (4 * j + tig) * 4 * C::NW, wa);
+              lds_words(rb + (4 * j + tig) * 4 * C::NW, wb);
+#pragma unroll
+              for (int w = 0; w < C::NW; ++w) {
+                uint32_t ha[4], hb[4];
+                e2m1x8_to_f16(wa[w], ha);
+                e2m1x8_to_f16(wb[w], hb);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  ha[c] = hmul2(ha[c], fa_[jj]);
+                  hb[c] = hmul2(hb[c], fb_[jj]);
+                }
+                mma_f16(acc[0], ha[0], hb[0], ha[1], hb[1], qf[j][4 * w], qf[j][4 * w + 1]);
+                mma_f16(acc[1], ha[2], hb[2], ha[3], hb[3], qf[j][4 * w + 2], qf[j][4 * w + 3]);
+              }
+            }
+          }
+          // ---- scores, weights against the tile's own base
+          const int key[2] = {tile * kTile + key_row<D>(gid), tile * kTile + key_row<D>(gid + 8)};
+          float s[2][2], se[2][2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int pos = tile0 * kTile + key[r];
+            const bool vis = pos >= lo && pos <= qpos;
+            const float ks = scl[key[r]] * p.scale_log2;
+            const float ve = static_cast<float>(static_cast<int>(__float_as_uint(scl[C::NT * kTile + key[r]]) >> 23) - 127);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              s[r][h] = vis ? (acc[0][2 * r + h] + acc[1][2 * r + h]) * ks : -INFINITY;
+              se[r][h] = s[r][h] + ve;
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float mn = fmaxf(ml[h], fmaxf(s[0][h], s[1][h]));
+            const float mg = mn == -INFINITY ? 0.f : mn;
+            ll[h] = ll[h] * ex2(ml[h] - mg) + (ex2(s[0][h] - mg) + ex2(s[1][h] - mg));
+            ml[h] = mn;
+            float v = fmaxf(se[0][h], se[1][h]);
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+            mt[h] = ceilf(v);
+            const float base = mt[h] == -INFINITY ? 0.f : mt[h] - P_OFF;
+            uint8_t* ph = pbuf + tile * C::P_TILE + (2 * tig + h) * C::P_HEAD + gid * 2;
+            *reinterpret_cast<__half*>(ph) = __float2half_rn(ex2(se[0][h] - base));
+            *reinterpret_cast<__half*>(ph + 16) = __float2half_rn(ex2(se[1][h] - base));
+          }
+        }
+        if (gid == 0) {   // a tile past the segment leaves -inf
+          mw[(2 * tig) * C::NT + tile] = mt[0];
+          mw[(2 * tig + 1) * C::NT + tile] = mt[1];
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[kst]);
+      named_bar_sync(1, C::NCW * 32);   // every tile's weights and base are there
+      if (*reinterpret_cast<volatile int*>(&abort_flag)) return;
+
+      // ---- O's base
+      float f[C::NT];
+      {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < C::NT; i += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(mw + gid * C::NT + i);
+          f[i] = v.x;
+          f[i + 1] = v.y;
+          f[i + 2] = v.z;
+          f[i + 3] = v.w;
+          mx = fmaxf(mx, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
+        }
+        const bool grow = mx > M + SLACK;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float r = grow ? ex2(M - mx) : 1.0f;   // 0 where O is still empty (M = -inf)
+          if (grow) M = mx;
+          const float rA = __shfl_sync(0xffffffffu, r, 8 * tig), rB = __shfl_sync(0xffffffffu, r, 8 * tig + 4);
+#pragma unroll
+          for (int i = 0; i < C::MT; ++i) {
+            o[i][0] *= rA;
+            o[i][1] *= rB;
+            o[i][2] *= rA;
+            o[i][3] *= rB;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < C::NT; ++i) f[i] = f[i] == -INFINITY ? 0.f : ex2(f[i] - M);
+      }
+
+      const int vst = e % C::NSLOT;
+      const bool vok = __all_sync(0xffffffffu, mbar_wait(&full[vst], (e / C::NSLOT) & 1));
+      if (!vok && lane == 0) {   // everyone leaves at the next barrier
+        abort_flag = 1;
+        atomicOr(p.err, FA_DEV_ERR_TIMEOUT);
+      }
+      ++e;
+      uint8_t* vslot = smem + vst * C::SLOT;
+      constexpr int SB = D / 64;   // this warp's block scales per row (bytes)
+      if (vok && (tile0 * kTile < lo || (tile0 + ntl) * kTile - 1 > qpos)) {
+        // masked keys have weight 0, but their rows may hold anything (block
+        // scales of NaN included): zero this warp's block scales of those rows
+        for (int r = lane; r < ntl * kTile; r += 32) {
+          const int pos = tile0 * kTile + r;
+          if (pos < lo || pos > qpos) {
+            uint32_t* z = reinterpret_cast<uint32_t*>(vslot + r * C::ROWB + D / 2 + warp * SB);
+            z[0] = 0u;
+            if constexpr (SB == 8) z[1] = 0u;
+          }
+        }
+        fence_proxy_async_smem();   // before the copy that refills the slot
+        __syncwarp();
+      }
+      // ---- O^T += V^T P^T over this warp's columns
+      if (vok) {
+#pragma unroll
+        for (int t = 0; t < C::NT; ++t) {
+          if (t >= ntl) break;
+          const uint8_t* vt = vslot + t * C::TILE_BYTES;
+          const uint32_t* pw = reinterpret_cast<const uint32_t*>(pbuf + t * C::P_TILE + gid * C::P_HEAD);
+          const __half2 fh = __float2half2_rn(f[t]);
+          const uint32_t fu = *reinterpret_cast<const uint32_t*>(&fh);
+          const uint32_t b0 = hmul2(pw[tig], fu), b1 = hmul2(pw[tig + 4], fu);
+          uint32_t w[4][C::NW], sc[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {   // keys 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9
+            const uint8_t* row = vt + key_row<D>(2 * tig + (r & 1) + (r >> 1) * 8) * C::ROWB;
+            lds_words(row + (8 * warp + gid) * 4 * C::NW, w[r]);
+            sc[r] = row[D / 2 + warp * SB + (D == 256 ? gid >> 1 : gid)];
+          }
+          const uint32_t s01 = e4m3x2_to_f16x2(sc[0] | (sc[1] << 8)), s23 = e4m3x2_to_f16x2(sc[2] | (sc[3] << 8));
+#pragma unroll
+          for (int q = 0; q < C::NW; ++q) {
+            // code pairs of two keys at one column: even columns, odd columns
+            constexpr uint32_t LOW = 0x0f0f0f0fu;
+            uint32_t e01[4], d01[4], e23[4], d23[4];
+            e2m1x8_to_f16((w[0][q] & LOW) | ((w[1][q] << 4) & ~LOW), e01);
+            e2m1x8_to_f16(((w[0][q] >> 4) & LOW) | (w[1][q] & ~LOW), d01);
+            e2m1x8_to_f16((w[2][q] & LOW) | ((w[3][q] << 4) & ~LOW), e23);
+            e2m1x8_to_f16(((w[2][q] >> 4) & LOW) | (w[3][q] & ~LOW), d23);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mma_f16(o[4 * q + i], hmul2(e01[i], s01), hmul2(d01[i], s01), hmul2(e23[i], s23), hmul2(d23[i], s23), b0, b1);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[vst]);
+    }
+
+    // -------------------------------------------------------- segment epilogue
+    // the denominator: lanes of a head, then the warps, in a fixed order
+    float2* mls = reinterpret_cast<float2*>(smem + C::OFF_ML);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int of = 4; of < 32; of <<= 1) {
+        const float mo = __shfl_xor_sync(0xffffffffu, ml[h], of), lo_ = __shfl_xor_sync(0xffffffffu, ll[h], of);
+        const float mn = fmaxf(ml[h], mo);
+        const float mg = mn == -INFINITY ? 0.f : mn;
+        ll[h] = ll[h] * ex2(ml[h] - mg) + lo_ * ex2(mo - mg);
+        ml[h] = mn;
+      }
+      if (gid == 0) mls[warp * 8 + 2 * tig + h] = make_float2(ml[h], ll[h]);
+    }
+    named_bar_sync(1, C::NCW * 32);
+    if (*reinterpret_cast<volatile int*>(&abort_flag)) return;
+    float m = -INFINITY, l = 0.f;   // of head gid
+#pragma unroll
+    for (int w = 0; w < C::NCW; ++w) m = fmaxf(m, mls[w * 8 + gid].x);
+#pragma unroll
+    for (int w = 0; w < C::NCW; ++w) {
+      const float2 v = mls[w * 8 + gid];
+      l += v.y * ex2(v.x - (m == -INFINITY ? 0.f : m));
+    }
+    const float Mo = M - P_OFF;
+    const int c_first = kper ? u * kper : cta_of(P, ncta, T);
+    const int c_last = kper ? c_first + kper - 1 : cta_of(P + x.n - 1, ncta, T);
+    const int d0 = (8 * warp + gid) * 8 * C::NW;   // this lane's columns: 8 NW from d0 on
+    if (c_first == c_last) {
+      const float r = Mo > -INFINITY ? ex2(Mo - m) / l : 1.0f / l;
+      const float r2[2] = {__shfl_sync(0xffffffffu, r, 8 * tig), __shfl_sync(0xffffffffu, r, 8 * tig + 4)};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (2 * tig + h >= nh) continue;
+        uint4* dst = reinterpret_cast<uint4*>(p.out + (static_cast<size_t>(x.b) * p.Hq + head0 + 2 * tig + h) * D + d0);
+#pragma unroll
+        for (int q = 0; q < C::NW; ++q) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(o[4 * q + i][h] * r2[h], o[4 * q + i][2 + h] * r2[h]);
+          dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      if (p.lse && warp == 0 && tig == 0 && hv)
+        p.lse[static_cast<size_t>(x.b) * p.Hq + head0 + gid] = (m + __log2f(l)) * 0.69314718055994531f;
+    } else {
+      const size_t slot = static_cast<size_t>(cta) + u;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float4* dst = reinterpret_cast<float4*>(p.o_part + (slot * 8 + 2 * tig + h) * D + d0);
+#pragma unroll
+        for (int i = 0; i < C::MT / 2; ++i)
+          dst[i] = make_float4(o[2 * i][h], o[2 * i][2 + h], o[2 * i + 1][h], o[2 * i + 1][2 + h]);
+      }
+      if (warp == 0 && tig == 0) reinterpret_cast<float4*>(p.ml_part)[slot * 8 + gid] = make_float4(Mo, m, l, 0.f);
+      // arrive; the last of the unit's CTAs merges every partial row.  The
+      // barrier orders the CTA's partial writes before thread 0's
+      // release/acquire add, which publishes them and, for the last arrival,
+      // makes the other CTAs' rows visible.
+      named_bar_sync(1, C::NCW * 32);
+      if (threadIdx.x == 0) {
+        const int nct = c_last - c_first + 1;
+        const int old = atom_add_acq_rel_gpu(p.counters + u, 1);
+        int last = 0;
+        if (old == nct - 1) {
+          last = 1;
+          atomicExch(p.counters + u, 0);   // leave the counter zero for the next call
+        } else if (old >= nct) {
+          atomicOr(p.err, FA_DEV_ERR_WORKSPACE);
+        }
+        sh_last = last;
+      }
+      named_bar_sync(1, C::NCW * 32);
+      if (sh_last) merge_unit_fp4<D>(p, u, x, nh, head0, c_first, c_last, reinterpret_cast<float*>(smem + C::OFF_W));
+    }
+    P += x.n;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(F4Cfg<D>::NTHR, 2) decode_fp4_kernel(const __grid_constant__ DecK p) {
+  decode_fp4_body<D>(p, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
+}
+
+// Several layers in one launch: the CTAs of layer i are [cta0[i], cta0[i + 1]).
+struct F4Layers {
+  DecK k[kMaxLayersPerLaunch];
+  int cta0[kMaxLayersPerLaunch + 1];
+  int n;
+};
+
+template <int D>
+__global__ void __launch_bounds__(F4Cfg<D>::NTHR, 2) decode_fp4_layers_kernel(const __grid_constant__ F4Layers m) {
+  const int b = static_cast<int>(blockIdx.x);
+  int li = 0;
+  while (li + 1 < m.n && b >= m.cta0[li + 1]) ++li;
+  decode_fp4_body<D>(m.k[li], b - m.cta0[li], m.cta0[li + 1] - m.cta0[li]);
+}
+
+template <int D>
+static cudaError_t launch_fp4(const DecodeArgs* a, int n, cudaStream_t s) {
+  using C = F4Cfg<D>;
+  cudaError_t e;
+  if (n == 1) {
+    static unsigned int done = 0;
+    e = set_smem_once(reinterpret_cast<const void*>(decode_fp4_kernel<D>), C::SMEM, &done);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(decode_fp4_kernel<D>, dim3(a->plan.ncta), dim3(C::NTHR), C::SMEM, s, make_deck(*a));
+  }
+  static unsigned int done = 0;
+  e = set_smem_once(reinterpret_cast<const void*>(decode_fp4_layers_kernel<D>), C::SMEM, &done);
+  if (e != cudaSuccess) return e;
+  F4Layers m{};
+  m.n = n;
+  for (int i = 0; i < n; ++i) {
+    m.k[i] = make_deck(a[i]);
+    m.cta0[i + 1] = m.cta0[i] + a[i].plan.ncta;
+  }
+  return launch_pdl(decode_fp4_layers_kernel<D>, dim3(m.cta0[n]), dim3(C::NTHR), C::SMEM, s, m);
+}
+
+cudaError_t launch_decode_fp4(const DecodeArgs* a, int n, cudaStream_t s) {
+  return a[0].D == 256 ? launch_fp4<256>(a, n, s) : launch_fp4<512>(a, n, s);
+}
+
+}  // namespace fa

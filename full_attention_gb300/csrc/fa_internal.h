@@ -171,6 +171,9 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s);
 // Several layers of one head_dim and KV format in one launch (n <= kMaxLayersPerLaunch).
 cudaError_t launch_decode_layers(const DecodeArgs* a, int n, cudaStream_t s);
 
+// The same over fp4 slabs (fa_decode_fp4.cu); n = 1 for a single layer.
+cudaError_t launch_decode_fp4(const DecodeArgs* a, int n, cudaStream_t s);
+
 struct ExtendArgs {
   const void* q;
   const void* k_ext;
