@@ -73,6 +73,9 @@ static size_t slab_row_bytes(int kv_dtype, int D) {
 }
 
 // ----------------------------------------------------------------- planning
+// CTAs of a decode launch the device holds at once: two per SM, three in fp4.
+static long long decode_slots(const fa_cache* c) { return (c->kv_dtype == FA_KV_FP4 ? 3LL : 2LL) * sm_count(); }
+
 DecodePlan plan_decode(const fa_cache* c, int layer, int B, int max_seq_len, long long max_cta) {
   DecodePlan p;
   const fa_layer_desc& d = c->layers[layer].d;
@@ -89,18 +92,19 @@ DecodePlan plan_decode(const fa_cache* c, int layer, int B, int max_seq_len, lon
   // a pipeline step moves 32 KB of K and V; a CTA gets at least 4 steps
   const int tile_bytes = 2 * kTile * d.head_dim * static_cast<int>(elem_bytes(c->kv_dtype));
   p.min_tiles = 4 * (32768 / tile_bytes);
-  // fp4: a CTA gets at least two steps (of 64 keys at head_dim 512, 128 at 256)
+  // fp4: a CTA gets at least two steps of 64 keys
   const bool fp4 = c->kv_dtype == FA_KV_FP4;
-  if (fp4) p.min_tiles = d.head_dim == 512 ? 8 : 16;
+  if (fp4) p.min_tiles = 8;
   const long long t_bound = static_cast<long long>(p.units) * tiles;
-  const long long slots = max_cta > 0 ? max_cta : 2LL * sm_count();   // two resident CTAs per SM
+  const long long slots = max_cta > 0 ? max_cta : decode_slots(c);
   long long n = (t_bound + p.min_tiles - 1) / p.min_tiles;
   if (n > slots) n = slots;
   if (n < 1) n = 1;
   p.ncta = static_cast<int>(n);
   if (p.ncta > 1) {
     const size_t rows = static_cast<size_t>(p.ncta + p.units) * 8;   // partial slots x heads
-    p.off_ml = (static_cast<size_t>(p.units) * 4 + 255) / 256 * 256;
+    // arrival counters: one per unit; fp4: one per partial slot
+    p.off_ml = (static_cast<size_t>(p.units + (fp4 ? p.ncta : 0)) * 4 + 255) / 256 * 256;
     p.off_o = p.off_ml + (rows * (fp4 ? 4 : 2) * sizeof(float) + 255) / 256 * 256;
     p.ws_bytes = p.off_o + rows * d.head_dim * sizeof(float);
   }
@@ -562,7 +566,7 @@ static void plan_decode_layers(const fa_cache* c, int n, const int32_t* layers, 
     tb[i] = static_cast<long long>(p[i].units) * p[i].max_tiles;
     tot += tb[i];
   }
-  const long long slots = 2LL * sm_count();
+  const long long slots = decode_slots(c);
   for (int i = 0; i < n; ++i) {
     long long share = tot > 0 ? slots * tb[i] / tot : 1;
     if (share < 1) share = 1;

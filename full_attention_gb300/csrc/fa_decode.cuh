@@ -22,7 +22,8 @@ struct DecK {
   const int32_t* slots;
   __nv_bfloat16* out;
   float* lse;
-  int* counters;    // [U] arrival count per unit (null: no workspace, one CTA); zero between calls
+  int* counters;    // [U] arrival count per unit (fp4: [ncta + U], per group of partials; null: no
+                    // workspace, one CTA); zero between calls
   float* ml_part;   // [(ncta + U) * 8][2] (fp4: [4])
   float* o_part;    // [(ncta + U) * 8][D]
   unsigned int* err;
@@ -211,6 +212,104 @@ __device__ __forceinline__ void finish_share(int cta, Share& s) {
     s.s_beg = s.p0 + static_cast<long long>(r) * w.n0 / s.kper;
     s.s_end = s.p0 + static_cast<long long>(r + 1) * w.n0 / s.kper;
   }
+}
+
+// floor(c * T / n) for c <= n, in 32 bits: with T = q n + r it is c q + floor(c r / n).
+__device__ __forceinline__ uint32_t share_begin(uint32_t c, uint32_t n, uint32_t q, uint32_t r) {
+  return c * q + (r ? c * r / n : 0u);
+}
+
+// The same cut for up to kWarpUnits units, found by every warp for itself from
+// shuffles: no block barrier, one round of loads, and 32-bit divisions only (a
+// 64-bit one costs some 0.3 us on the way to the first copy).  Returns false
+// where cut_share does; a true share is complete (no finish_share).
+constexpr int kWarpUnits = 256;
+__device__ __forceinline__ bool cut_share_warp(const DecK& p, int cta, int grid, Share& s) {
+  constexpr int PER = kWarpUnits / 32;
+  const int lane = threadIdx.x & 31;
+  const int per = (p.units + 31) / 32;   // units of a lane: [lane * per, ...)
+  const int hc = p.Hkv * p.chunks;
+  int n[PER], sum = 0, mn = INT_MAX, mx = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    n[i] = 0;
+    if (i >= per) continue;
+    const int u = lane * per + i;
+    if (u < p.units) {
+      const int L = __ldg(p.seq_lens + (hc == 1 ? u : static_cast<int>(static_cast<uint32_t>(u) / hc)));
+      if (cta == 0 && threadIdx.x < 32 && L > p.max_seq_len) atomicOr(p.err, FA_DEV_ERR_BOUND);
+      const int len = min(L, p.max_seq_len);
+      if (len > 0) {
+        const uint32_t lo = p.kind == FA_SLIDING ? max(0, len - p.window) : 0;
+        n[i] = static_cast<uint32_t>(len - 1) / kTile + 1 - lo / kTile;
+      }
+      mn = min(mn, n[i]);
+      mx = max(mx, n[i]);
+      sum += n[i];
+    }
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += t;
+  }
+  const int T = __shfl_sync(0xffffffffu, incl, 31);
+  mn = __reduce_min_sync(0xffffffffu, mn);
+  mx = __reduce_max_sync(0xffffffffu, mx);
+  int ncta = (T == 0) ? 0 : min(grid, max(1, static_cast<int>(static_cast<uint32_t>(T + p.min_tiles - 1) / p.min_tiles)));
+  int kper = 0;
+  if (ncta > 0 && p.units <= static_cast<int>(blockDim.x) && mn >= 1 && mx - mn <= max(1, mn >> 3)) {
+    const int k = min(static_cast<int>(static_cast<uint32_t>(ncta) / p.units), mn);
+    if (k >= 1 && 20 * k * p.units >= 17 * ncta) {
+      kper = k;
+      ncta = k * p.units;
+    }
+  }
+  s.T = T;
+  s.ncta = ncta;
+  s.kper = kper;
+  if (cta >= ncta) return false;
+  const int ucta = kper ? static_cast<uint32_t>(cta) / kper : 0;
+  const uint32_t q = static_cast<uint32_t>(T) / ncta, r = T - q * ncta;
+  const int s_beg = share_begin(cta, ncta, q, r);
+  // the unit that holds tile s_beg, or the unit of this CTA's part
+  int u0 = -1, p0 = 0, n0 = 0, P = incl - sum;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (i >= per) continue;
+    const int u = lane * per + i;
+    if (kper ? u == ucta : n[i] > 0 && P <= s_beg && s_beg < P + n[i]) {
+      u0 = u;
+      p0 = P;
+      n0 = n[i];
+    }
+    P += n[i];
+  }
+  const int src = __ffs(__ballot_sync(0xffffffffu, u0 >= 0)) - 1;
+  s.u0 = __shfl_sync(0xffffffffu, u0, src);
+  s.p0 = __shfl_sync(0xffffffffu, p0, src);
+  n0 = __shfl_sync(0xffffffffu, n0, src);
+  if (kper) {   // part i of unit u0
+    const uint32_t i = cta - ucta * kper, uq = static_cast<uint32_t>(n0) / kper, ur = n0 - uq * kper;
+    s.s_beg = s.p0 + share_begin(i, kper, uq, ur);
+    s.s_end = s.p0 + share_begin(i + 1, kper, uq, ur);
+  } else {
+    s.s_beg = s_beg;
+    s.s_end = share_begin(cta + 1, ncta, q, r);
+  }
+  return true;
+}
+
+// The CTA that owns tile g of T cut over n: cta_of without its 64-bit division.
+// The quotient is estimated in fp32 and put right against share_begin.
+__device__ __forceinline__ int cta_of_fast(uint32_t g, uint32_t n, uint32_t T) {
+  const uint32_t q = T / n, r = T - q * n;
+  int c = static_cast<int>(__fdividef(static_cast<float>(g) * static_cast<float>(n), static_cast<float>(T)));
+  c = max(0, min(c, static_cast<int>(n) - 1));
+  while (c > 0 && share_begin(c, n, q, r) > g) --c;
+  while (c + 1 < static_cast<int>(n) && share_begin(c + 1, n, q, r) <= g) ++c;
+  return c;
 }
 
 // The current token's K and V rows of (sequence b, KV head h) into slot `slot`

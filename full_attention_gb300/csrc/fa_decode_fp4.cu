@@ -43,25 +43,43 @@ struct F4Cfg {
   static constexpr int ROWB = kRowBytes<D, FA_KV_FP4>; // 144, 288
   static constexpr int TILE_BYTES = kTile * ROWB;
   static constexpr int NCW = 4;                        // consumer warps
-  static constexpr int TPW = D == 256 ? 2 : 1;         // tiles per consumer warp and step
-  static constexpr int NT = NCW * TPW;                 // tiles per step
+  static constexpr int NT = NCW;                       // tiles per step
   static constexpr int SC_BYTES = NT * kTile * 4;      // one step's K (or V) row scales
   static constexpr int SLOT = NT * TILE_BYTES + 2 * SC_BYTES;   // rows; in K slots also both row scales
-  static constexpr int NSLOT = 5;
+  static constexpr int NSLOT = D == 256 ? 6 : 3;
+  static constexpr int CTAS = 3;                       // per SM
   static constexpr int NTHR = (NCW + 1) * 32;
   static constexpr int NJ = 8;                         // loads of NW words a lane makes per row
   static constexpr int MT = D / 4 / 16;                // m16 tiles of O^T per warp
   static constexpr int P_HEAD = 48;                    // bytes per head of a tile's weights (16 f16 + padding)
   static constexpr int P_TILE = 8 * P_HEAD;
-  static constexpr int OFF_P = NSLOT * SLOT;           // [2][NT] tiles of weights
+  static constexpr int OFF_Q = NSLOT * SLOT;           // Q^T fragments [NJ][NW][32 lanes] of 16 bytes
+  static constexpr int OFF_P = OFF_Q + 8 * D * 2;      // [2][NT] tiles of weights
   static constexpr int OFF_MW = OFF_P + 2 * NT * P_TILE;   // [2][8 heads][NT] tile bases
-  static constexpr int OFF_ML = OFF_MW + 2 * 8 * NT * 4;   // [NCW][8] (m, l)
-  static constexpr int OFF_W = OFF_ML + NCW * 8 * 8;       // merge weights [64][8], then [8] factors and [8] lse
-  static constexpr int OFF_BAR = OFF_W + (64 * 8 + 16) * 4;
+  static constexpr int OFF_FLAG = OFF_MW + 2 * 8 * NT * 4; // [2][NT] the tile's base is its own
+  static constexpr int OFF_ML = OFF_FLAG + 2 * NT * 4;     // [NCW][8] (m, l)
+  static constexpr int OFF_W = OFF_ML + NCW * 8 * 8;       // merge weights [4][8], then [8] (M, m, L, 0)
+  static constexpr int OFF_BAR = OFF_W + (4 * 8 + 4 * 8) * 4;
   static constexpr int SMEM = OFF_BAR + 2 * NSLOT * 8;
   static_assert(SLOT % 128 == 0, "slot alignment");
-  static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
+  static_assert(CTAS * (SMEM + 1024 + 256) <= 228 * 1024, "CTAs per SM");
 };
+
+// "No score yet": finite, so that differences against it are never NaN.
+constexpr float kNoScore = -3.402823466e38f;
+
+// unit_of without divisions where each sequence is one unit.
+__device__ __forceinline__ Unit unit_at(const DecK& p, int u) {
+  if (p.Hkv * p.chunks != 1) return unit_of(p, u);
+  Unit x;
+  x.b = u;
+  x.h = x.c = 0;
+  x.L = min(__ldg(p.seq_lens + u), p.max_seq_len);
+  x.lo = (p.kind == FA_SLIDING) ? max(0, x.L - p.window) : 0;
+  x.t_first = x.lo / kTile;
+  x.n = x.L > 0 ? (x.L - 1) / kTile + 1 - x.t_first : 0;
+  return x;
+}
 
 // Tile row that MMA key index r stands for.  Rows 288 bytes apart start 8 banks
 // apart: with this order both the S loads (lanes' rows r = 0..7) and the PV
@@ -113,75 +131,107 @@ __device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
   }
 }
 
-// Merge the partial rows of unit u that CTAs cf..cl left (this CTA arrived
-// last), in CTA order.  Run by the 128 consumer threads; wbuf holds 64 * 8 + 16
-// floats.
+// Combine the partial rows of unit u that its nct CTAs cf .. leave, as a tree of
+// groups of four in CTA order: the last CTA of a group to arrive merges the
+// group's partials and goes on to the next level, the others are done.  (One
+// CTA merging all of a long sequence's partials alone, 57 of 16 KB with 8
+// sequences on 152 SMs, took 32 us after the last byte had been read; four
+// levels of at most four take 2 us each, most of them before that.)  The
+// order of the sums depends on the tree only, so results do not depend on who
+// arrives last.  Run by the 128 consumer threads once the CTA's own partial is
+// written; i is its index in the unit, wbuf 4 * 8 + 32 floats.
 template <int D>
-__device__ void merge_unit_fp4(const DecK& p, int u, const Unit& x, int nh, int head0, int cf, int cl, float* wbuf) {
-  constexpr int CH = 64;
-  constexpr int ITEMS = 8 * (D / 4) / 128;
-  const int tid = threadIdx.x, nct = cl - cf + 1;
-  const float4* ml = reinterpret_cast<const float4*>(p.ml_part) + (static_cast<size_t>(cf) + u) * 8;
-  float* fin = wbuf + CH * 8;   // [8] 2^(M - m) / L, [8] lse
-  const int h = tid >> 4, k = tid & 15;
-  float M = -INFINITY, m = -INFINITY, L = 0.f;
-  for (int c = k; c < nct; c += 16) {
-    const float4 v = __ldcg(ml + c * 8 + h);
-    M = fmaxf(M, v.x);
-    const float mn = fmaxf(m, v.y);
-    if (mn > -INFINITY) L = L * ex2(m - mn) + v.z * ex2(v.y - mn);
-    else L += v.z;   // NaN scores only
-    m = mn;
-  }
-#pragma unroll
-  for (int o = 8; o; o >>= 1) {
-    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float mo = __shfl_xor_sync(0xffffffffu, m, o), Lo = __shfl_xor_sync(0xffffffffu, L, o);
-    const float mn = fmaxf(m, mo);
-    L = mn > -INFINITY ? L * ex2(m - mn) + Lo * ex2(mo - mn) : L + Lo;
-    m = mn;
-  }
-  if (k == 0) {
-    fin[h] = M > -INFINITY ? ex2(M - m) / L : 1.0f / L;
-    fin[8 + h] = (m + __log2f(L)) * 0.69314718055994531f;
-  }
-  float4 acc[ITEMS];
-#pragma unroll
-  for (int i = 0; i < ITEMS; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c0 = 0; c0 < nct; c0 += CH) {
-    const int n = min(CH, nct - c0);
+__device__ void merge_tree(const DecK& p, int u, const Unit& x, int nh, int head0, int cf, int nct, int i, float* wbuf,
+                           int* sh_last) {
+  constexpr int ITEMS = 8 * (D / 4) / 128;   // float4 pieces of a partial per thread
+  constexpr int HPI = 8 / ITEMS;             // heads a round of 128 pieces covers
+  const int tid = threadIdx.x;
+  int n = nct, st = 1;
+  for (int level = 0;; ++level, i >>= 2, st *= 4) {
+    const int first = i & ~3, cnt = min(4, n - first);
+    const size_t base = static_cast<size_t>(cf) + u + static_cast<size_t>(first) * st;   // slot of the group's first partial
+    n = (n + 3) >> 2;
+    if (cnt == 1) continue;   // alone in its group (others exist: n > 1): the partial stands for the group
+    // arrive: the barrier orders the CTA's partial writes before thread 0's
+    // release/acquire add, which publishes them and, for the last arrival,
+    // makes the other CTAs' rows visible.  A group's counter lies in its own
+    // slots: at level l its partials are 4^l slots apart, and the offset l
+    // (past 3, l + 1) keeps the levels' counters apart.
     named_bar_sync(1, 128);
-    for (int c = k; c < n; c += 16) {
-      const float Mc = __ldcg(&ml[(c0 + c) * 8 + h].x);
-      wbuf[c * 8 + h] = Mc > -INFINITY ? ex2(Mc - M) : 0.f;
+    if (tid == 0) {
+      int* c = p.counters + base + level + (level > 3 ? 1 : 0);
+      const int old = atom_add_acq_rel_gpu(c, 1);
+      if (old == cnt - 1) atomicExch(c, 0);   // zero for the next call
+      else if (old >= cnt) atomicOr(p.err, FA_DEV_ERR_WORKSPACE);
+      *sh_last = old == cnt - 1;
     }
     named_bar_sync(1, 128);
-#pragma unroll 4
-    for (int c = 0; c < n; ++c) {
-      const float* src = p.o_part + (static_cast<size_t>(cf + c0 + c) + u) * 8 * D;
-      float4 o[ITEMS];
+    if (!*sh_last) return;
+    float4 acc[ITEMS], nx[ITEMS];
+    auto fetch = [&](int k, float4 (&v)[ITEMS]) {
+      const float4* src = reinterpret_cast<const float4*>(p.o_part + (base + static_cast<size_t>(k) * st) * 8 * D) + tid;
 #pragma unroll
-      for (int i = 0; i < ITEMS; ++i) o[i] = __ldcg(reinterpret_cast<const float4*>(src) + tid + i * 128);
+      for (int j = 0; j < ITEMS; ++j)
+        v[j] = j * HPI < nh ? __ldcg(src + j * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    fetch(0, acc);
+    fetch(1, nx);
+    if (tid < 32) {   // lane: partial k = tid / 8, head tid % 8
+      const int k = tid >> 3;
+      float4 v = make_float4(kNoScore, kNoScore, 0.f, 0.f);
+      if (k < cnt) v = __ldcg(reinterpret_cast<const float4*>(p.ml_part) + (base + static_cast<size_t>(k) * st) * 8 + (tid & 7));
+      float M = v.x, m = v.y;
+      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 8));
+      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+      float L = v.z * ex2(v.y - m);
+      L += __shfl_xor_sync(0xffffffffu, L, 8);
+      L += __shfl_xor_sync(0xffffffffu, L, 16);
+      wbuf[tid] = ex2(v.x - M);
+      if (k == 0) *reinterpret_cast<float4*>(wbuf + 32 + 4 * tid) = make_float4(M, m, L, 0.f);
+    }
+    named_bar_sync(1, 128);
+    auto add = [&](int k, const float4 (&v)[ITEMS], bool set) {
 #pragma unroll
-      for (int i = 0; i < ITEMS; ++i) {
-        const float w = wbuf[c * 8 + (tid + i * 128) / (D / 4)];
-        acc[i].x += w * o[i].x;
-        acc[i].y += w * o[i].y;
-        acc[i].z += w * o[i].z;
-        acc[i].w += w * o[i].w;
+      for (int j = 0; j < ITEMS; ++j) {
+        const float w = wbuf[k * 8 + j * HPI + tid / (128 / HPI)];
+        acc[j].x = w * v[j].x + (set ? 0.f : acc[j].x);
+        acc[j].y = w * v[j].y + (set ? 0.f : acc[j].y);
+        acc[j].z = w * v[j].z + (set ? 0.f : acc[j].z);
+        acc[j].w = w * v[j].w + (set ? 0.f : acc[j].w);
       }
-    }
-  }
+    };
+    add(0, acc, true);
+    for (int k = 1; k < cnt; ++k) {
+      float4 v[ITEMS];
 #pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    const int idx = tid + i * 128, hh = idx / (D / 4), d = (idx % (D / 4)) * 4;
-    if (hh >= nh) continue;
-    const float f = fin[hh];
-    *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(x.b) * p.Hq + head0 + hh) * D + d) =
-        make_uint2(pack_bf16x2(acc[i].x * f, acc[i].y * f), pack_bf16x2(acc[i].z * f, acc[i].w * f));
+      for (int j = 0; j < ITEMS; ++j) v[j] = nx[j];
+      if (k + 1 < cnt) fetch(k + 1, nx);
+      add(k, v, false);
+    }
+    if (n == 1) {
+#pragma unroll
+      for (int j = 0; j < ITEMS; ++j) {
+        const int hh = j * HPI + tid / (128 / HPI), d = (tid % (128 / HPI)) * 4;
+        if (hh >= nh) continue;
+        const float4 fm = *reinterpret_cast<const float4*>(wbuf + 32 + 4 * hh);
+        const float f = ex2(fm.x - fm.y) / fm.z;
+        *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(x.b) * p.Hq + head0 + hh) * D + d) =
+            make_uint2(pack_bf16x2(acc[j].x * f, acc[j].y * f), pack_bf16x2(acc[j].z * f, acc[j].w * f));
+      }
+      if (p.lse && tid < nh) {
+        const float4 fm = *reinterpret_cast<const float4*>(wbuf + 32 + 4 * tid);
+        p.lse[static_cast<size_t>(x.b) * p.Hq + head0 + tid] = (fm.y + __log2f(fm.z)) * 0.69314718055994531f;
+      }
+      named_bar_sync(1, 128);   // the scratch is free again
+      return;
+    }
+    float4* dst = reinterpret_cast<float4*>(p.o_part + base * 8 * D) + tid;
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j) dst[j * 128] = acc[j];
+    if (tid < 8) reinterpret_cast<float4*>(p.ml_part)[base * 8 + tid] = *reinterpret_cast<const float4*>(wbuf + 32 + 4 * tid);
   }
-  if (p.lse && tid < nh) p.lse[static_cast<size_t>(x.b) * p.Hq + head0 + tid] = fin[8 + tid];
-  named_bar_sync(1, 128);   // the scratch is free again
 }
 
 template <int D>
@@ -200,7 +250,8 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
   griddep_launch_dependents();
 
   Share sh;
-  if (!cut_share(p, cta, grid, sh)) {
+  const bool small = p.units <= kWarpUnits;
+  if (!(small ? cut_share_warp(p, cta, grid, sh) : cut_share(p, cta, grid, sh))) {
     if (sh.ncta == 0 && cta == 0) {   // nothing visible anywhere: only empty outputs to write
       griddep_wait();
       zero_empty_units<D, KV>(p, 0, 1, threadIdx.x, blockDim.x);
@@ -217,20 +268,21 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
     fence_mbar_init();
   }
   __syncthreads();
-  finish_share(cta, sh);
+  if (!small) finish_share(cta, sh);
   const int u0 = sh.u0, p0 = sh.p0;
-  const long long s_beg = sh.s_beg, s_end = sh.s_end;
+  const int s_beg = static_cast<int>(sh.s_beg), s_end = static_cast<int>(sh.s_end);   // T fits an int
 
   if (warp == C::NCW) {
     // ------------------------------------------------------------ producer
     int e = 0;   // slots filled
     bool ok = true, first = true;
-    long long P = p0;
+    const bool one = p.tiles_per_page == 1;   // the usual page of 16: no division
+    int P = p0;
     for (int u = u0; ok && P < s_end; ++u) {
-      const Unit x = unit_of(p, u);
+      const Unit x = unit_at(p, u);
       if (x.n > 0) {
-        const int ta = x.t_first + static_cast<int>(max(s_beg, P) - P);
-        const int tz = x.t_first + static_cast<int>(min(s_end, P + x.n) - P);
+        const int ta = x.t_first + max(s_beg, P) - P;
+        const int tz = x.t_first + min(s_end, P + x.n) - P;
         const int32_t* bt = p.block_table + static_cast<size_t>(x.b) * p.max_pages_per_seq;
         // the CTA that reads the unit's last tile (it holds position L - 1)
         // stores the current token's rows first, so its own copy sees them
@@ -239,7 +291,7 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
         for (int k0 = ta; ok && k0 < tz; k0 += 32) {
           int pid = -1;
           if (k0 + lane < tz) {
-            pid = __ldg(bt + (k0 + lane) / p.tiles_per_page);
+            pid = __ldg(bt + (one ? k0 + lane : static_cast<uint32_t>(k0 + lane) / p.tiles_per_page));
             if (pid < 0 || pid >= p.num_pages) {
               atomicOr(p.err, FA_DEV_ERR_PAGE);
               pid = -1;
@@ -267,7 +319,8 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
             const int nbad = __popc(bad);
             const int tile = k + lane;
             const size_t row0 = mine && pg >= 0
-                                    ? (static_cast<size_t>(pg) * p.Hkv + x.h) * p.page_size + (tile % p.tiles_per_page) * kTile
+                                    ? (static_cast<size_t>(pg) * p.Hkv + x.h) * p.page_size +
+                                          (one ? 0 : static_cast<uint32_t>(tile) % p.tiles_per_page) * kTile
                                     : 0;
 #pragma unroll
             for (int side = 0; side < 2; ++side, ++e) {
@@ -322,181 +375,187 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
   // -------------------------------------------------------------- consumers
   griddep_wait();
   zero_empty_units<D, KV>(p, cta, ncta, threadIdx.x, C::NCW * 32);
-  constexpr float P_OFF = 8.0f;      // weights reach 2^8 against their own tile's base
-  constexpr float SLACK = 4.0f;      // M follows a tile's base only past 2^4 (weights stay below 2^12)
+  constexpr float P_OFF = 4.0f;    // weights reach 2^P_OFF against a base of their own tile's,
+  constexpr float SLACK = 8.0f;    // and 2^(P_OFF + SLACK) against O's base before it is raised
   int e = 0, step = 0;
-  long long P = p0;
+  int P = p0;
   for (int u = u0; P < s_end; ++u) {
-    const Unit x = unit_of(p, u);
+    const Unit x = unit_at(p, u);
     if (x.n == 0) continue;   // an empty unit advances nothing
-    const int ta = x.t_first + static_cast<int>(max(s_beg, P) - P);
-    const int tz = x.t_first + static_cast<int>(min(s_end, P + x.n) - P);
+    const int ta = x.t_first + max(s_beg, P) - P;
+    const int tz = x.t_first + min(s_end, P + x.n) - P;
     const int nh = min(8, p.g - x.c * 8), head0 = x.h * p.g + x.c * 8;
     const int qpos = x.L - 1, lo = x.lo;
     const bool hv = gid < nh;
 
     // queries: Q^T fragments (B operand) as f16, in the order the codes are
-    // stored; zero for padded heads
-    uint32_t qf[C::NJ][4 * C::NW];
+    // stored, zero for padded heads; the warps share the conversion.  (Every
+    // warp has left the previous segment's QK phase: the epilogue's barrier.)
     {
       uint32_t qbig = 0;
       const __nv_bfloat16* qrow = p.q + (static_cast<size_t>(x.b) * p.Hq + head0 + (hv ? gid : 0)) * D;
 #pragma unroll
-      for (int j = 0; j < C::NJ; ++j)
+      for (int jj = 0; jj < C::NJ * C::NW / 4; ++jj) {
+        const int jw = warp * (C::NJ * C::NW / 4) + jj, j = jw / C::NW, w = jw % C::NW;
+        const uint4 v = hv ? __ldcg(reinterpret_cast<const uint4*>(qrow) + (4 * j + tig) * C::NW + w)
+                           : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t vv[4] = {v.x, v.y, v.z, v.w};
+        uint32_t f[4];
 #pragma unroll
-        for (int w = 0; w < C::NW; ++w) {
-          const uint4 v = hv ? __ldcg(reinterpret_cast<const uint4*>(qrow) + (4 * j + tig) * C::NW + w)
-                             : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t vv[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            qbig |= bf16x2_past_f16(vv[i]);
-            qf[j][4 * w + i] = pack_f16x2_sat(__uint_as_float(vv[i] << 16), __uint_as_float(vv[i] & 0xffff0000u));
-          }
+        for (int i = 0; i < 4; ++i) {
+          qbig |= bf16x2_past_f16(vv[i]);
+          f[i] = pack_f16x2_sat(__uint_as_float(vv[i] << 16), __uint_as_float(vv[i] & 0xffff0000u));
         }
+        *reinterpret_cast<uint4*>(smem + C::OFF_Q + (jw * 32 + lane) * 16) = make_uint4(f[0], f[1], f[2], f[3]);
+      }
       if (__any_sync(0xffffffffu, qbig != 0) && lane == 0) atomicOr(p.err, FA_DEV_ERR_RANGE);
+      named_bar_sync(1, C::NCW * 32);
     }
 
     float o[C::MT][4];
 #pragma unroll
     for (int i = 0; i < C::MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-    float M = -INFINITY;                          // O's base, head gid
-    float ml[2] = {-INFINITY, -INFINITY}, ll[2] = {0.f, 0.f};   // this lane's keys: max, sum (heads 2 tig, 2 tig + 1)
+    float M = kNoScore;                            // O's base, head gid
+    float Mh[2] = {kNoScore, kNoScore};            // the same, heads 2 tig, 2 tig + 1
+    float ml[2] = {kNoScore, kNoScore}, ll[2] = {0.f, 0.f};   // this lane's keys: base and sum of the denominator
 
     for (int tile0 = ta; tile0 < tz; tile0 += C::NT, ++step) {
       const int ntl = min(C::NT, tz - tile0);
       const int buf = step & 1;
       uint8_t* pbuf = smem + C::OFF_P + buf * C::NT * C::P_TILE;
       float* mw = reinterpret_cast<float*>(smem + C::OFF_MW) + buf * 8 * C::NT;
+      int* flag = reinterpret_cast<int*>(smem + C::OFF_FLAG) + buf * C::NT;
       const int kst = e % C::NSLOT;
-      const bool kok = __all_sync(0xffffffffu, mbar_wait(&full[kst], (e / C::NSLOT) & 1));
-      if (!kok && lane == 0) {
-        abort_flag = 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[kst], (e / C::NSLOT) & 1)) && lane == 0) {
+        abort_flag = 1;   // everyone leaves at the barrier below
         atomicOr(p.err, FA_DEV_ERR_TIMEOUT);
       }
       ++e;
       const uint8_t* kslot = smem + kst * C::SLOT;
       const float* scl = reinterpret_cast<const float*>(kslot + C::NT * C::TILE_BYTES);
+      if (warp < ntl) {
+        // ---- S^T of this warp's tile: keys gid, gid + 8 (as MMA rows), heads 2 tig, 2 tig + 1
+        const uint8_t* ra = kslot + warp * C::TILE_BYTES + key_row<D>(gid) * C::ROWB;
+        const uint8_t* rb = ra + 8 * C::ROWB;   // key_row(gid + 8) = key_row(gid) + 8
+        uint32_t sa[D / 64], sb[D / 64];
+        lds_words(ra + D / 2, sa);
+        lds_words(rb + D / 2, sb);
+        float acc[2][4] = {};
 #pragma unroll
-      for (int tw = 0; tw < C::TPW; ++tw) {
-        const int tile = warp + tw * C::NCW;
-        float mt[2] = {-INFINITY, -INFINITY};
-        if (kok && tile < ntl) {
-          // ---- S^T of this tile: keys gid, gid + 8 (as MMA rows), heads 2 tig, 2 tig + 1
-          const uint8_t* ra = kslot + tile * C::TILE_BYTES + key_row<D>(gid) * C::ROWB;
-          const uint8_t* rb = kslot + tile * C::TILE_BYTES + key_row<D>(gid + 8) * C::ROWB;
-          uint32_t sa[D / 64], sb[D / 64];
-          lds_words(ra + D / 2, sa);
-          lds_words(rb + D / 2, sb);
-          float acc[2][4] = {};
+        for (int i = 0; i < C::NJ / 2; ++i) {
+          uint32_t fa_[2], fb_[2];
+          block_scales<D>(sa, i, tig, fa_[0], fa_[1]);
+          block_scales<D>(sb, i, tig, fb_[0], fb_[1]);
 #pragma unroll
-          for (int i = 0; i < C::NJ / 2; ++i) {
-            uint32_t fa_[2], fb_[2];
-            block_scales<D>(sa, i, tig, fa_[0], fa_[1]);
-            block_scales<D>(sb, i, tig, fb_[0], fb_[1]);
+          for (int jj = 0; jj < 2; ++jj) {
+            const int j = 2 * i + jj;
+            uint32_t wa[C::NW], wb[C::NW];
+            lds_words(ra + (4 * j + tig) * 4 * C::NW, wa);
+            lds_words(rb + (4 * j + tig) * 4 * C::NW, wb);
 #pragma unroll
-            for (int jj = 0; jj < 2; ++jj) {
-              const int j = 2 * i + jj;
-              uint32_t wa[C::NW], wb[C::NW];
-              lds_words(ra + (4 * j + tig) * 4 * C::NW, wa);
-              lds_words(rb + (4 * j + tig) * 4 * C::NW, wb);
+            for (int w = 0; w < C::NW; ++w) {
+              const uint4 qf = *reinterpret_cast<const uint4*>(smem + C::OFF_Q + ((j * C::NW + w) * 32 + lane) * 16);
+              uint32_t ha[4], hb[4];
+              e2m1x8_to_f16(wa[w], ha);
+              e2m1x8_to_f16(wb[w], hb);
 #pragma unroll
-              for (int w = 0; w < C::NW; ++w) {
-                uint32_t ha[4], hb[4];
-                e2m1x8_to_f16(wa[w], ha);
-                e2m1x8_to_f16(wb[w], hb);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                  ha[c] = hmul2(ha[c], fa_[jj]);
-                  hb[c] = hmul2(hb[c], fb_[jj]);
-                }
-                mma_f16(acc[0], ha[0], hb[0], ha[1], hb[1], qf[j][4 * w], qf[j][4 * w + 1]);
-                mma_f16(acc[1], ha[2], hb[2], ha[3], hb[3], qf[j][4 * w + 2], qf[j][4 * w + 3]);
+              for (int c = 0; c < 4; ++c) {
+                ha[c] = hmul2(ha[c], fa_[jj]);
+                hb[c] = hmul2(hb[c], fb_[jj]);
               }
+              mma_f16(acc[0], ha[0], hb[0], ha[1], hb[1], qf.x, qf.y);
+              mma_f16(acc[1], ha[2], hb[2], ha[3], hb[3], qf.z, qf.w);
             }
           }
-          // ---- scores, weights against the tile's own base
-          const int key[2] = {tile * kTile + key_row<D>(gid), tile * kTile + key_row<D>(gid + 8)};
-          float s[2][2], se[2][2];
+        }
+        // ---- scores and weights
+        const int key = warp * kTile + key_row<D>(gid);
+        float s[2][2], se[2][2];
+        bool grow = false;
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const int pos = tile0 * kTile + key[r];
-            const bool vis = pos >= lo && pos <= qpos;
-            const float ks = scl[key[r]] * p.scale_log2;
-            const float ve = static_cast<float>(static_cast<int>(__float_as_uint(scl[C::NT * kTile + key[r]]) >> 23) - 127);
+        for (int r = 0; r < 2; ++r) {
+          const int pos = tile0 * kTile + key + 8 * r;
+          const bool vis = pos >= lo && pos <= qpos;
+          const float ks = scl[key + 8 * r] * p.scale_log2;
+          const float ve =
+              static_cast<float>(static_cast<int>(__float_as_uint(scl[C::NT * kTile + key + 8 * r]) >> 23) - 127);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              s[r][h] = vis ? (acc[0][2 * r + h] + acc[1][2 * r + h]) * ks : -INFINITY;
-              se[r][h] = s[r][h] + ve;
-            }
+          for (int h = 0; h < 2; ++h) {
+            s[r][h] = vis ? (acc[0][2 * r + h] + acc[1][2 * r + h]) * ks : -INFINITY;
+            se[r][h] = s[r][h] + ve;
+            grow |= se[r][h] > Mh[h] + SLACK || s[r][h] > ml[h] + 30.0f;
           }
+        }
+        float base[2] = {Mh[0], Mh[1]};
+        grow = __any_sync(0xffffffffu, grow);
+        if (grow) {
+          // rare once O's base has settled: this tile's own base where it
+          // exceeds O's by more than the slack, and the denominators' bases
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float mn = fmaxf(ml[h], fmaxf(s[0][h], s[1][h]));
-            const float mg = mn == -INFINITY ? 0.f : mn;
-            ll[h] = ll[h] * ex2(ml[h] - mg) + (ex2(s[0][h] - mg) + ex2(s[1][h] - mg));
+            ll[h] *= ex2(ml[h] - mn);
             ml[h] = mn;
             float v = fmaxf(se[0][h], se[1][h]);
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-            mt[h] = ceilf(v);
-            const float base = mt[h] == -INFINITY ? 0.f : mt[h] - P_OFF;
-            uint8_t* ph = pbuf + tile * C::P_TILE + (2 * tig + h) * C::P_HEAD + gid * 2;
-            *reinterpret_cast<__half*>(ph) = __float2half_rn(ex2(se[0][h] - base));
-            *reinterpret_cast<__half*>(ph + 16) = __float2half_rn(ex2(se[1][h] - base));
+            if (v > Mh[h] + SLACK) base[h] = ceilf(v);
+            if (gid == 0) mw[(2 * tig + h) * C::NT + warp] = base[h];
           }
         }
-        if (gid == 0) {   // a tile past the segment leaves -inf
-          mw[(2 * tig) * C::NT + tile] = mt[0];
-          mw[(2 * tig + 1) * C::NT + tile] = mt[1];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          ll[h] += ex2(s[0][h] - ml[h]) + ex2(s[1][h] - ml[h]);
+          uint8_t* ph = pbuf + warp * C::P_TILE + (2 * tig + h) * C::P_HEAD + gid * 2;
+          *reinterpret_cast<__half*>(ph) = __float2half_rn(ex2(se[0][h] - base[h] + P_OFF));
+          *reinterpret_cast<__half*>(ph + 16) = __float2half_rn(ex2(se[1][h] - base[h] + P_OFF));
         }
+        if (lane == 0) flag[warp] = grow;
+      } else if (lane == 0) {
+        flag[warp] = 0;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[kst]);
       named_bar_sync(1, C::NCW * 32);   // every tile's weights and base are there
       if (*reinterpret_cast<volatile int*>(&abort_flag)) return;
 
-      // ---- O's base
-      float f[C::NT];
-      {
-        float mx = -INFINITY;
+      // ---- tiles with a base of their own: raise O's base to the largest, and
+      // bring every tile's weights to it (exact powers of two)
+      float f[C::NT] = {1.f, 1.f, 1.f, 1.f};
+      const int4 fl = *reinterpret_cast<const int4*>(flag);
+      if (fl.x | fl.y | fl.z | fl.w) {
+        const float4 v = *reinterpret_cast<const float4*>(mw + gid * C::NT);
+        f[0] = fl.x ? v.x : M;
+        f[1] = fl.y ? v.y : M;
+        f[2] = fl.z ? v.z : M;
+        f[3] = fl.w ? v.w : M;
+        const float Mn = fmaxf(M, fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])));
+        const float r = ex2(M - Mn);   // 0 where O is still empty
+        M = Mn;
 #pragma unroll
-        for (int i = 0; i < C::NT; i += 4) {
-          const float4 v = *reinterpret_cast<const float4*>(mw + gid * C::NT + i);
-          f[i] = v.x;
-          f[i + 1] = v.y;
-          f[i + 2] = v.z;
-          f[i + 3] = v.w;
-          mx = fmaxf(mx, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
+        for (int i = 0; i < C::NT; ++i) f[i] = ex2(f[i] - M);
+        const float rA = __shfl_sync(0xffffffffu, r, 8 * tig), rB = __shfl_sync(0xffffffffu, r, 8 * tig + 4);
+        Mh[0] = __shfl_sync(0xffffffffu, M, 8 * tig);
+        Mh[1] = __shfl_sync(0xffffffffu, M, 8 * tig + 4);
+#pragma unroll
+        for (int i = 0; i < C::MT; ++i) {
+          o[i][0] *= rA;
+          o[i][1] *= rB;
+          o[i][2] *= rA;
+          o[i][3] *= rB;
         }
-        const bool grow = mx > M + SLACK;
-        if (__any_sync(0xffffffffu, grow)) {
-          const float r = grow ? ex2(M - mx) : 1.0f;   // 0 where O is still empty (M = -inf)
-          if (grow) M = mx;
-          const float rA = __shfl_sync(0xffffffffu, r, 8 * tig), rB = __shfl_sync(0xffffffffu, r, 8 * tig + 4);
-#pragma unroll
-          for (int i = 0; i < C::MT; ++i) {
-            o[i][0] *= rA;
-            o[i][1] *= rB;
-            o[i][2] *= rA;
-            o[i][3] *= rB;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < C::NT; ++i) f[i] = f[i] == -INFINITY ? 0.f : ex2(f[i] - M);
       }
 
       const int vst = e % C::NSLOT;
-      const bool vok = __all_sync(0xffffffffu, mbar_wait(&full[vst], (e / C::NSLOT) & 1));
-      if (!vok && lane == 0) {   // everyone leaves at the next barrier
-        abort_flag = 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[vst], (e / C::NSLOT) & 1)) && lane == 0) {
+        abort_flag = 1;   // everyone leaves at the next barrier
         atomicOr(p.err, FA_DEV_ERR_TIMEOUT);
       }
       ++e;
       uint8_t* vslot = smem + vst * C::SLOT;
       constexpr int SB = D / 64;   // this warp's block scales per row (bytes)
-      if (vok && (tile0 * kTile < lo || (tile0 + ntl) * kTile - 1 > qpos)) {
+      if (tile0 * kTile < lo || (tile0 + ntl) * kTile - 1 > qpos) {
         // masked keys have weight 0, but their rows may hold anything (block
         // scales of NaN included): zero this warp's block scales of those rows
         for (int r = lane; r < ntl * kTile; r += 32) {
@@ -511,38 +570,38 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
         __syncwarp();
       }
       // ---- O^T += V^T P^T over this warp's columns
-      if (vok) {
+      auto pv_tile = [&](int t, float ft) {
+        const uint8_t* vt = vslot + t * C::TILE_BYTES;
+        const uint32_t* pw = reinterpret_cast<const uint32_t*>(pbuf + t * C::P_TILE + gid * C::P_HEAD);
+        const __half2 fh = __float2half2_rn(ft);
+        const uint32_t fu = *reinterpret_cast<const uint32_t*>(&fh);
+        const uint32_t b0 = hmul2(pw[tig], fu), b1 = hmul2(pw[tig + 4], fu);
+        uint32_t w[4][C::NW], sc[4];
 #pragma unroll
-        for (int t = 0; t < C::NT; ++t) {
-          if (t >= ntl) break;
-          const uint8_t* vt = vslot + t * C::TILE_BYTES;
-          const uint32_t* pw = reinterpret_cast<const uint32_t*>(pbuf + t * C::P_TILE + gid * C::P_HEAD);
-          const __half2 fh = __float2half2_rn(f[t]);
-          const uint32_t fu = *reinterpret_cast<const uint32_t*>(&fh);
-          const uint32_t b0 = hmul2(pw[tig], fu), b1 = hmul2(pw[tig + 4], fu);
-          uint32_t w[4][C::NW], sc[4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {   // keys 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9
-            const uint8_t* row = vt + key_row<D>(2 * tig + (r & 1) + (r >> 1) * 8) * C::ROWB;
-            lds_words(row + (8 * warp + gid) * 4 * C::NW, w[r]);
-            sc[r] = row[D / 2 + warp * SB + (D == 256 ? gid >> 1 : gid)];
-          }
-          const uint32_t s01 = e4m3x2_to_f16x2(sc[0] | (sc[1] << 8)), s23 = e4m3x2_to_f16x2(sc[2] | (sc[3] << 8));
-#pragma unroll
-          for (int q = 0; q < C::NW; ++q) {
-            // code pairs of two keys at one column: even columns, odd columns
-            constexpr uint32_t LOW = 0x0f0f0f0fu;
-            uint32_t e01[4], d01[4], e23[4], d23[4];
-            e2m1x8_to_f16((w[0][q] & LOW) | ((w[1][q] << 4) & ~LOW), e01);
-            e2m1x8_to_f16(((w[0][q] >> 4) & LOW) | (w[1][q] & ~LOW), d01);
-            e2m1x8_to_f16((w[2][q] & LOW) | ((w[3][q] << 4) & ~LOW), e23);
-            e2m1x8_to_f16(((w[2][q] >> 4) & LOW) | (w[3][q] & ~LOW), d23);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              mma_f16(o[4 * q + i], hmul2(e01[i], s01), hmul2(d01[i], s01), hmul2(e23[i], s23), hmul2(d23[i], s23), b0, b1);
-          }
+        for (int r = 0; r < 4; ++r) {   // keys 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9
+          const uint8_t* row = vt + key_row<D>(2 * tig + (r & 1) + (r >> 1) * 8) * C::ROWB;
+          lds_words(row + (8 * warp + gid) * 4 * C::NW, w[r]);
+          sc[r] = row[D / 2 + warp * SB + (D == 256 ? gid >> 1 : gid)];
         }
-      }
+        const uint32_t s01 = e4m3x2_to_f16x2(sc[0] | (sc[1] << 8)), s23 = e4m3x2_to_f16x2(sc[2] | (sc[3] << 8));
+#pragma unroll
+        for (int q = 0; q < C::NW; ++q) {
+          // code pairs of two keys at one column: even columns, odd columns
+          constexpr uint32_t LOW = 0x0f0f0f0fu;
+          uint32_t e01[4], d01[4], e23[4], d23[4];
+          e2m1x8_to_f16((w[0][q] & LOW) | ((w[1][q] << 4) & ~LOW), e01);
+          e2m1x8_to_f16(((w[0][q] >> 4) & LOW) | (w[1][q] & ~LOW), d01);
+          e2m1x8_to_f16((w[2][q] & LOW) | ((w[3][q] << 4) & ~LOW), e23);
+          e2m1x8_to_f16(((w[2][q] >> 4) & LOW) | (w[3][q] & ~LOW), d23);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mma_f16(o[4 * q + i], hmul2(e01[i], s01), hmul2(d01[i], s01), hmul2(e23[i], s23), hmul2(d23[i], s23), b0, b1);
+        }
+      };
+      pv_tile(0, f[0]);
+      if (ntl > 1) pv_tile(1, f[1]);
+      if (ntl > 2) pv_tile(2, f[2]);
+      if (ntl > 3) pv_tile(3, f[3]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[vst]);
     }
@@ -556,28 +615,27 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
       for (int of = 4; of < 32; of <<= 1) {
         const float mo = __shfl_xor_sync(0xffffffffu, ml[h], of), lo_ = __shfl_xor_sync(0xffffffffu, ll[h], of);
         const float mn = fmaxf(ml[h], mo);
-        const float mg = mn == -INFINITY ? 0.f : mn;
-        ll[h] = ll[h] * ex2(ml[h] - mg) + lo_ * ex2(mo - mg);
+        ll[h] = ll[h] * ex2(ml[h] - mn) + lo_ * ex2(mo - mn);
         ml[h] = mn;
       }
       if (gid == 0) mls[warp * 8 + 2 * tig + h] = make_float2(ml[h], ll[h]);
     }
     named_bar_sync(1, C::NCW * 32);
     if (*reinterpret_cast<volatile int*>(&abort_flag)) return;
-    float m = -INFINITY, l = 0.f;   // of head gid
+    float m = kNoScore, l = 0.f;   // of head gid
 #pragma unroll
     for (int w = 0; w < C::NCW; ++w) m = fmaxf(m, mls[w * 8 + gid].x);
 #pragma unroll
     for (int w = 0; w < C::NCW; ++w) {
       const float2 v = mls[w * 8 + gid];
-      l += v.y * ex2(v.x - (m == -INFINITY ? 0.f : m));
+      l += v.y * ex2(v.x - m);
     }
     const float Mo = M - P_OFF;
-    const int c_first = kper ? u * kper : cta_of(P, ncta, T);
-    const int c_last = kper ? c_first + kper - 1 : cta_of(P + x.n - 1, ncta, T);
+    const int c_first = kper ? u * kper : cta_of_fast(static_cast<uint32_t>(P), ncta, T);
+    const int c_last = kper ? c_first + kper - 1 : cta_of_fast(static_cast<uint32_t>(P + x.n - 1), ncta, T);
     const int d0 = (8 * warp + gid) * 8 * C::NW;   // this lane's columns: 8 NW from d0 on
     if (c_first == c_last) {
-      const float r = Mo > -INFINITY ? ex2(Mo - m) / l : 1.0f / l;
+      const float r = ex2(Mo - m) / l;
       const float r2[2] = {__shfl_sync(0xffffffffu, r, 8 * tig), __shfl_sync(0xffffffffu, r, 8 * tig + 4)};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -603,32 +661,15 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
           dst[i] = make_float4(o[2 * i][h], o[2 * i][2 + h], o[2 * i + 1][h], o[2 * i + 1][2 + h]);
       }
       if (warp == 0 && tig == 0) reinterpret_cast<float4*>(p.ml_part)[slot * 8 + gid] = make_float4(Mo, m, l, 0.f);
-      // arrive; the last of the unit's CTAs merges every partial row.  The
-      // barrier orders the CTA's partial writes before thread 0's
-      // release/acquire add, which publishes them and, for the last arrival,
-      // makes the other CTAs' rows visible.
-      named_bar_sync(1, C::NCW * 32);
-      if (threadIdx.x == 0) {
-        const int nct = c_last - c_first + 1;
-        const int old = atom_add_acq_rel_gpu(p.counters + u, 1);
-        int last = 0;
-        if (old == nct - 1) {
-          last = 1;
-          atomicExch(p.counters + u, 0);   // leave the counter zero for the next call
-        } else if (old >= nct) {
-          atomicOr(p.err, FA_DEV_ERR_WORKSPACE);
-        }
-        sh_last = last;
-      }
-      named_bar_sync(1, C::NCW * 32);
-      if (sh_last) merge_unit_fp4<D>(p, u, x, nh, head0, c_first, c_last, reinterpret_cast<float*>(smem + C::OFF_W));
+      merge_tree<D>(p, u, x, nh, head0, c_first, c_last - c_first + 1, cta - c_first,
+                    reinterpret_cast<float*>(smem + C::OFF_W), &sh_last);
     }
     P += x.n;
   }
 }
 
 template <int D>
-__global__ void __launch_bounds__(F4Cfg<D>::NTHR, 2) decode_fp4_kernel(const __grid_constant__ DecK p) {
+__global__ void __launch_bounds__(F4Cfg<D>::NTHR, F4Cfg<D>::CTAS) decode_fp4_kernel(const __grid_constant__ DecK p) {
   decode_fp4_body<D>(p, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
 }
 
@@ -640,7 +681,7 @@ struct F4Layers {
 };
 
 template <int D>
-__global__ void __launch_bounds__(F4Cfg<D>::NTHR, 2) decode_fp4_layers_kernel(const __grid_constant__ F4Layers m) {
+__global__ void __launch_bounds__(F4Cfg<D>::NTHR, F4Cfg<D>::CTAS) decode_fp4_layers_kernel(const __grid_constant__ F4Layers m) {
   const int b = static_cast<int>(blockIdx.x);
   int li = 0;
   while (li + 1 < m.n && b >= m.cta0[li + 1]) ++li;
