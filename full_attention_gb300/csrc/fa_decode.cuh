@@ -108,6 +108,7 @@ struct Share {
   long long s_beg, s_end;
   int T, ncta, kper;   // kper: CTAs per unit of the unit-aligned cut (0: concatenated cut)
   int u0, p0;
+  int cf, nct;         // the whole-unit cut: the unit's first CTA and its CTAs (nct 0: another cut)
 };
 struct ShareWork {   // shared memory of the cut
   int scan[8], mm[16];
@@ -219,17 +220,24 @@ __device__ __forceinline__ uint32_t share_begin(uint32_t c, uint32_t n, uint32_t
   return c * q + (r ? c * r / n : 0u);
 }
 
-// The same cut for up to kWarpUnits units, found by every warp for itself from
+// A cut for up to kWarpUnits units, found by every warp for itself from
 // shuffles: no block barrier, one round of loads, and 32-bit divisions only (a
-// 64-bit one costs some 0.3 us on the way to the first copy).  Returns false
-// where cut_share does; a true share is complete (no finish_share).
+// 64-bit one costs some 0.3 us on the way to the first copy).  Where it can,
+// it gives every CTA a part of one unit only: unit u is cut into ceil(n_u / Q)
+// equal parts, Q the smallest quota found for which the launch's CTAs
+// suffice.  A CTA that crosses from one unit to the next pays a second query
+// load, epilogue and merge in the middle of its stream, which costs more than
+// the uneven parts as long as Q stays below 3/2 of the even share; past that
+// (many units, few CTAs for each) the lists are laid end to end as in
+// cut_share.  Returns false where cut_share does; a true share is complete (no
+// finish_share).
 constexpr int kWarpUnits = 256;
 __device__ __forceinline__ bool cut_share_warp(const DecK& p, int cta, int grid, Share& s) {
   constexpr int PER = kWarpUnits / 32;
   const int lane = threadIdx.x & 31;
   const int per = (p.units + 31) / 32;   // units of a lane: [lane * per, ...)
   const int hc = p.Hkv * p.chunks;
-  int n[PER], sum = 0, mn = INT_MAX, mx = 0;
+  int n[PER], sum = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     n[i] = 0;
@@ -243,61 +251,94 @@ __device__ __forceinline__ bool cut_share_warp(const DecK& p, int cta, int grid,
         const uint32_t lo = p.kind == FA_SLIDING ? max(0, len - p.window) : 0;
         n[i] = static_cast<uint32_t>(len - 1) / kTile + 1 - lo / kTile;
       }
-      mn = min(mn, n[i]);
-      mx = max(mx, n[i]);
       sum += n[i];
     }
   }
-  int incl = sum;
+  auto scan = [&](int v) {   // inclusive, over the lanes
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += t;
-  }
-  const int T = __shfl_sync(0xffffffffu, incl, 31);
-  mn = __reduce_min_sync(0xffffffffu, mn);
-  mx = __reduce_max_sync(0xffffffffu, mx);
-  int ncta = (T == 0) ? 0 : min(grid, max(1, static_cast<int>(static_cast<uint32_t>(T + p.min_tiles - 1) / p.min_tiles)));
-  int kper = 0;
-  if (ncta > 0 && p.units <= static_cast<int>(blockDim.x) && mn >= 1 && mx - mn <= max(1, mn >> 3)) {
-    const int k = min(static_cast<int>(static_cast<uint32_t>(ncta) / p.units), mn);
-    if (k >= 1 && 20 * k * p.units >= 17 * ncta) {
-      kper = k;
-      ncta = k * p.units;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += t;
     }
-  }
+    return v;
+  };
+  const int incl = scan(sum);
+  const int T = __shfl_sync(0xffffffffu, incl, 31);
   s.T = T;
+  s.kper = s.nct = s.cf = 0;
+  s.ncta = 0;
+  if (T == 0) return false;
+  const uint32_t even = max((static_cast<uint32_t>(T) + grid - 1) / grid, static_cast<uint32_t>(p.min_tiles));
+  int k[PER], ks = 0, total = 0;
+  uint32_t Q = even;
+  while (true) {
+    const float rq = __frcp_rn(static_cast<float>(Q));
+    ks = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      k[i] = 0;
+      if (i >= per) continue;
+      // ceil(n / Q): the fp32 estimate is put right by one either way
+      const int m = n[i] + static_cast<int>(Q) - 1;
+      int c = static_cast<int>(static_cast<float>(m) * rq);
+      c -= c * static_cast<int>(Q) > m;
+      c += (c + 1) * static_cast<int>(Q) <= m;
+      k[i] = c;
+      ks += c;
+    }
+    total = __reduce_add_sync(0xffffffffu, ks);
+    if (total <= grid || 2 * Q >= 3 * even) break;
+    // in proportion, as far as the fractions of a part allow
+    Q = max(Q + 1, static_cast<uint32_t>(static_cast<float>(Q) * total / grid));
+  }
+  int u0 = -1, p0 = 0, P = incl - sum;
+  if (total <= grid) {
+    s.ncta = total;
+    if (cta >= total) return false;
+    int n0 = 0, k0 = 0, c0 = 0, K = scan(ks) - ks;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (i >= per) continue;
+      if (K <= cta && cta < K + k[i]) {
+        u0 = lane * per + i;
+        p0 = P;
+        n0 = n[i];
+        k0 = k[i];
+        c0 = K;
+      }
+      P += n[i];
+      K += k[i];
+    }
+    const int src = __ffs(__ballot_sync(0xffffffffu, u0 >= 0)) - 1;
+    s.u0 = __shfl_sync(0xffffffffu, u0, src);
+    s.p0 = __shfl_sync(0xffffffffu, p0, src);
+    s.cf = __shfl_sync(0xffffffffu, c0, src);
+    s.nct = __shfl_sync(0xffffffffu, k0, src);
+    n0 = __shfl_sync(0xffffffffu, n0, src);
+    const uint32_t i = cta - s.cf, uq = static_cast<uint32_t>(n0) / s.nct, ur = n0 - uq * s.nct;
+    s.s_beg = s.p0 + share_begin(i, s.nct, uq, ur);
+    s.s_end = s.p0 + share_begin(i + 1, s.nct, uq, ur);
+    return true;
+  }
+  const int ncta = min(grid, static_cast<int>((static_cast<uint32_t>(T) + p.min_tiles - 1) / p.min_tiles));
   s.ncta = ncta;
-  s.kper = kper;
   if (cta >= ncta) return false;
-  const int ucta = kper ? static_cast<uint32_t>(cta) / kper : 0;
   const uint32_t q = static_cast<uint32_t>(T) / ncta, r = T - q * ncta;
   const int s_beg = share_begin(cta, ncta, q, r);
-  // the unit that holds tile s_beg, or the unit of this CTA's part
-  int u0 = -1, p0 = 0, n0 = 0, P = incl - sum;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     if (i >= per) continue;
-    const int u = lane * per + i;
-    if (kper ? u == ucta : n[i] > 0 && P <= s_beg && s_beg < P + n[i]) {
-      u0 = u;
+    if (n[i] > 0 && P <= s_beg && s_beg < P + n[i]) {
+      u0 = lane * per + i;
       p0 = P;
-      n0 = n[i];
     }
     P += n[i];
   }
   const int src = __ffs(__ballot_sync(0xffffffffu, u0 >= 0)) - 1;
   s.u0 = __shfl_sync(0xffffffffu, u0, src);
   s.p0 = __shfl_sync(0xffffffffu, p0, src);
-  n0 = __shfl_sync(0xffffffffu, n0, src);
-  if (kper) {   // part i of unit u0
-    const uint32_t i = cta - ucta * kper, uq = static_cast<uint32_t>(n0) / kper, ur = n0 - uq * kper;
-    s.s_beg = s.p0 + share_begin(i, kper, uq, ur);
-    s.s_end = s.p0 + share_begin(i + 1, kper, uq, ur);
-  } else {
-    s.s_beg = s_beg;
-    s.s_end = share_begin(cta + 1, ncta, q, r);
-  }
+  s.s_beg = s_beg;
+  s.s_end = share_begin(cta + 1, ncta, q, r);
   return true;
 }
 

@@ -60,8 +60,9 @@ struct F4Cfg {
   static constexpr int OFF_ML = OFF_FLAG + 2 * NT * 4;     // [NCW][8] (m, l)
   static constexpr int OFF_W = OFF_ML + NCW * 8 * 8;       // merge weights [4][8], then [8] (M, m, L, 0)
   static constexpr int OFF_BAR = OFF_W + (4 * 8 + 4 * 8) * 4;
-  static constexpr int SMEM = OFF_BAR + 2 * NSLOT * 8;
+  static constexpr int SMEM = OFF_BAR + (2 * NSLOT + 1) * 8;
   static_assert(SLOT % 128 == 0, "slot alignment");
+  static_assert(NSLOT * SLOT >= 3 * 8 * D * 4, "the ring holds three partials");
   static_assert(CTAS * (SMEM + 1024 + 256) <= 228 * 1024, "CTAs per SM");
 };
 
@@ -82,12 +83,13 @@ __device__ __forceinline__ Unit unit_at(const DecK& p, int u) {
 }
 
 // Tile row that MMA key index r stands for.  Rows 288 bytes apart start 8 banks
-// apart: with this order both the S loads (lanes' rows r = 0..7) and the PV
-// loads (rows r = 2t, and so on) start in four banks 8 apart.
+// apart, so a half-warp's 8-byte loads are free of conflicts when its four rows
+// differ modulo 4: for S those of r = 0..3 (and 4..7), for PV those of r = 0, 2,
+// 4, 6 (and 1, 3, 5, 7).
 template <int D>
 __device__ __forceinline__ int key_row(int r) {
   if constexpr (D == 256) return r;
-  else return (r & 8) | ((r & 1) << 2) | ((r >> 1) & 3);
+  else return (r & 8) | ((r & 1) ? 4 | (((r >> 1) & 3) ^ 2) : (r >> 1) & 3);
 }
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
@@ -95,20 +97,25 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// The f16 block scales (broadcast to both halves) of the lane's words j = 2 i
-// and 2 i + 1 of a row whose D / 16 scale bytes are sw.
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, __half2 b) {
+  const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&a), b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The f16 block scales of the lane's words j = 2 i (low half) and 2 i + 1 (high
+// half) of a row whose block scales start at sc.
 template <int D>
-__device__ __forceinline__ void block_scales(const uint32_t (&sw)[D / 64], int i, int tig, uint32_t& s0, uint32_t& s1) {
+__device__ __forceinline__ __half2 block_scales(const uint8_t* sc, int i, int tig) {
   uint32_t two;
   if constexpr (D == 256) {   // words 4 j + tig: block 2 j + tig / 2
     const uint32_t h = tig >> 1;
-    two = __byte_perm(sw[i], 0, h | ((2 + h) << 4));
+    two = __byte_perm(*reinterpret_cast<const uint32_t*>(sc + 4 * i), 0, h | ((2 + h) << 4));
   } else {                    // words 8 j + 2 tig, + 1: block 4 j + tig
-    two = __byte_perm(sw[2 * i], sw[2 * i + 1], tig | ((4 + tig) << 4));
+    const uint2 w = *reinterpret_cast<const uint2*>(sc + 8 * i);
+    two = __byte_perm(w.x, w.y, tig | ((4 + tig) << 4));
   }
   const uint32_t h = e4m3x2_to_f16x2(two & 0xffffu);
-  s0 = __byte_perm(h, 0, 0x1010);
-  s1 = __byte_perm(h, 0, 0x3232);
+  return *reinterpret_cast<const __half2*>(&h);
 }
 
 template <int N>
@@ -142,7 +149,7 @@ __device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
 // written; i is its index in the unit, wbuf 4 * 8 + 32 floats.
 template <int D>
 __device__ void merge_tree(const DecK& p, int u, const Unit& x, int nh, int head0, int cf, int nct, int i, float* wbuf,
-                           int* sh_last) {
+                           volatile int* sh_last, uint8_t* ring, uint64_t* bar, uint32_t& phase) {
   constexpr int ITEMS = 8 * (D / 4) / 128;   // float4 pieces of a partial per thread
   constexpr int HPI = 8 / ITEMS;             // heads a round of 128 pieces covers
   const int tid = threadIdx.x;
@@ -167,15 +174,24 @@ __device__ void merge_tree(const DecK& p, int u, const Unit& x, int nh, int head
     }
     named_bar_sync(1, 128);
     if (!*sh_last) return;
-    float4 acc[ITEMS], nx[ITEMS];
-    auto fetch = [&](int k, float4 (&v)[ITEMS]) {
-      const float4* src = reinterpret_cast<const float4*>(p.o_part + (base + static_cast<size_t>(k) * st) * 8 * D) + tid;
-#pragma unroll
-      for (int j = 0; j < ITEMS; ++j)
-        v[j] = j * HPI < nh ? __ldcg(src + j * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
+    // the last partial by loads, the others (three at most) by bulk copies into
+    // the ring, idle by now, or one after the other by loads
+    constexpr int PART = 8 * D * 4;
+    if (ring && tid == 0) {
+      fence_proxy_async_global();   // the other CTAs' rows, seen through the acquire, for the bulk copies
+      fence_proxy_async_smem();     // the ring's generic reads and zeroed scales before them
+      mbar_arrive_expect_tx(bar, (cnt - 1) * nh * D * 4);
+      for (int k = 0; k < cnt - 1; ++k)
+        bulk_load(ring + k * PART, p.o_part + (base + static_cast<size_t>(k) * st) * 8 * D, nh * D * 4, bar);
+    }
+    // the group's last partial by loads, issued before its weight is known
+    float4 acc[ITEMS];
+    auto part = [&](int k) {
+      return reinterpret_cast<const float4*>(p.o_part + (base + static_cast<size_t>(k) * st) * 8 * D) + tid;
     };
-    fetch(0, acc);
-    fetch(1, nx);
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j)
+      acc[j] = j * HPI < nh ? __ldcg(part(cnt - 1) + j * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
     if (tid < 32) {   // lane: partial k = tid / 8, head tid % 8
       const int k = tid >> 3;
       float4 v = make_float4(kNoScore, kNoScore, 0.f, 0.f);
@@ -192,23 +208,41 @@ __device__ void merge_tree(const DecK& p, int u, const Unit& x, int nh, int head
       if (k == 0) *reinterpret_cast<float4*>(wbuf + 32 + 4 * tid) = make_float4(M, m, L, 0.f);
     }
     named_bar_sync(1, 128);
-    auto add = [&](int k, const float4 (&v)[ITEMS], bool set) {
+    auto weight = [&](int k, int j) { return wbuf[k * 8 + j * HPI + tid / (128 / HPI)]; };
 #pragma unroll
-      for (int j = 0; j < ITEMS; ++j) {
-        const float w = wbuf[k * 8 + j * HPI + tid / (128 / HPI)];
-        acc[j].x = w * v[j].x + (set ? 0.f : acc[j].x);
-        acc[j].y = w * v[j].y + (set ? 0.f : acc[j].y);
-        acc[j].z = w * v[j].z + (set ? 0.f : acc[j].z);
-        acc[j].w = w * v[j].w + (set ? 0.f : acc[j].w);
-      }
+    for (int j = 0; j < ITEMS; ++j) {
+      const float w = weight(cnt - 1, j);
+      acc[j].x *= w;
+      acc[j].y *= w;
+      acc[j].z *= w;
+      acc[j].w *= w;
+    }
+    auto add = [&](int k, int j, float4 v) {
+      const float w = weight(k, j);
+      acc[j].x += w * v.x;
+      acc[j].y += w * v.y;
+      acc[j].z += w * v.z;
+      acc[j].w += w * v.w;
     };
-    add(0, acc, true);
-    for (int k = 1; k < cnt; ++k) {
-      float4 v[ITEMS];
+    if (ring) {
+      if (!mbar_wait(bar, phase)) *sh_last = 2;
+      phase ^= 1;
+      named_bar_sync(1, 128);
+      if (*sh_last == 2) {   // a copy that did not land in time: everyone leaves
+        if (tid == 0) atomicOr(p.err, FA_DEV_ERR_TIMEOUT);
+        return;
+      }
+      for (int k = 0; k < cnt - 1; ++k) {
+        const float4* src = reinterpret_cast<const float4*>(ring + k * PART) + tid;
 #pragma unroll
-      for (int j = 0; j < ITEMS; ++j) v[j] = nx[j];
-      if (k + 1 < cnt) fetch(k + 1, nx);
-      add(k, v, false);
+        for (int j = 0; j < ITEMS; ++j)
+          if (j * HPI < nh) add(k, j, src[j * 128]);
+      }
+    } else {
+      for (int k = 0; k < cnt - 1; ++k)
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j)
+          if (j * HPI < nh) add(k, j, __ldcg(part(k) + j * 128));
     }
     if (n == 1) {
 #pragma unroll
@@ -241,6 +275,7 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
   extern __shared__ __align__(128) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* empty = full + C::NSLOT;
+  uint64_t* mbar_merge = empty + C::NSLOT;
   __shared__ int abort_flag, sh_last;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -258,12 +293,14 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
     }
     return;
   }
-  const int ncta = sh.ncta, kper = sh.kper, T = sh.T;
+  if (!small) sh.nct = 0;
+  const int ncta = sh.ncta, T = sh.T;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NSLOT; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], C::NCW);
     }
+    mbar_init(mbar_merge, 1);
     abort_flag = 0;
     fence_mbar_init();
   }
@@ -378,6 +415,7 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
   constexpr float P_OFF = 4.0f;    // weights reach 2^P_OFF against a base of their own tile's,
   constexpr float SLACK = 8.0f;    // and 2^(P_OFF + SLACK) against O's base before it is raised
   int e = 0, step = 0;
+  uint32_t merge_phase = 0;
   int P = p0;
   for (int u = u0; P < s_end; ++u) {
     const Unit x = unit_at(p, u);
@@ -437,18 +475,14 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
         // ---- S^T of this warp's tile: keys gid, gid + 8 (as MMA rows), heads 2 tig, 2 tig + 1
         const uint8_t* ra = kslot + warp * C::TILE_BYTES + key_row<D>(gid) * C::ROWB;
         const uint8_t* rb = ra + 8 * C::ROWB;   // key_row(gid + 8) = key_row(gid) + 8
-        uint32_t sa[D / 64], sb[D / 64];
-        lds_words(ra + D / 2, sa);
-        lds_words(rb + D / 2, sb);
         float acc[2][4] = {};
 #pragma unroll
         for (int i = 0; i < C::NJ / 2; ++i) {
-          uint32_t fa_[2], fb_[2];
-          block_scales<D>(sa, i, tig, fa_[0], fa_[1]);
-          block_scales<D>(sb, i, tig, fb_[0], fb_[1]);
+          const __half2 sca = block_scales<D>(ra + D / 2, i, tig), scb = block_scales<D>(rb + D / 2, i, tig);
 #pragma unroll
           for (int jj = 0; jj < 2; ++jj) {
             const int j = 2 * i + jj;
+            const __half2 fa_ = jj ? __high2half2(sca) : __low2half2(sca), fb_ = jj ? __high2half2(scb) : __low2half2(scb);
             uint32_t wa[C::NW], wb[C::NW];
             lds_words(ra + (4 * j + tig) * 4 * C::NW, wa);
             lds_words(rb + (4 * j + tig) * 4 * C::NW, wb);
@@ -460,8 +494,8 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
               e2m1x8_to_f16(wb[w], hb);
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
-                ha[c] = hmul2(ha[c], fa_[jj]);
-                hb[c] = hmul2(hb[c], fb_[jj]);
+                ha[c] = hmul2(ha[c], fa_);
+                hb[c] = hmul2(hb[c], fb_);
               }
               mma_f16(acc[0], ha[0], hb[0], ha[1], hb[1], qf.x, qf.y);
               mma_f16(acc[1], ha[2], hb[2], ha[3], hb[3], qf.z, qf.w);
@@ -598,10 +632,8 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
             mma_f16(o[4 * q + i], hmul2(e01[i], s01), hmul2(d01[i], s01), hmul2(e23[i], s23), hmul2(d23[i], s23), b0, b1);
         }
       };
-      pv_tile(0, f[0]);
-      if (ntl > 1) pv_tile(1, f[1]);
-      if (ntl > 2) pv_tile(2, f[2]);
-      if (ntl > 3) pv_tile(3, f[3]);
+#pragma unroll 2
+      for (int t = 0; t < ntl; ++t) pv_tile(t, t == 0 ? f[0] : t == 1 ? f[1] : t == 2 ? f[2] : f[3]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[vst]);
     }
@@ -631,10 +663,18 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
       l += v.y * ex2(v.x - m);
     }
     const float Mo = M - P_OFF;
-    const int c_first = kper ? u * kper : cta_of_fast(static_cast<uint32_t>(P), ncta, T);
-    const int c_last = kper ? c_first + kper - 1 : cta_of_fast(static_cast<uint32_t>(P + x.n - 1), ncta, T);
+    int c_first = sh.cf, nct = sh.nct;
+    if (nct == 0) {   // not the whole-unit cut
+      if (sh.kper) {
+        c_first = u * sh.kper;
+        nct = sh.kper;
+      } else {
+        c_first = cta_of_fast(static_cast<uint32_t>(P), ncta, T);
+        nct = cta_of_fast(static_cast<uint32_t>(P + x.n - 1), ncta, T) - c_first + 1;
+      }
+    }
     const int d0 = (8 * warp + gid) * 8 * C::NW;   // this lane's columns: 8 NW from d0 on
-    if (c_first == c_last) {
+    if (nct == 1) {
       const float r = ex2(Mo - m) / l;
       const float r2[2] = {__shfl_sync(0xffffffffu, r, 8 * tig), __shfl_sync(0xffffffffu, r, 8 * tig + 4)};
 #pragma unroll
@@ -661,8 +701,9 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
           dst[i] = make_float4(o[2 * i][h], o[2 * i][2 + h], o[2 * i + 1][h], o[2 * i + 1][2 + h]);
       }
       if (warp == 0 && tig == 0) reinterpret_cast<float4*>(p.ml_part)[slot * 8 + gid] = make_float4(Mo, m, l, 0.f);
-      merge_tree<D>(p, u, x, nh, head0, c_first, c_last - c_first + 1, cta - c_first,
-                    reinterpret_cast<float*>(smem + C::OFF_W), &sh_last);
+      merge_tree<D>(p, u, x, nh, head0, c_first, nct, cta - c_first,
+                    reinterpret_cast<float*>(smem + C::OFF_W), &sh_last, P + x.n >= s_end ? smem : nullptr, mbar_merge,
+                    merge_phase);
     }
     P += x.n;
   }
