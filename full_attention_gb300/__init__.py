@@ -341,6 +341,21 @@ class Cache:
                                                  _p(seq_lens), int(q.shape[0]), int(max_seq_len), _p(out), _p(lse),
                                                  _s(stream)))
 
+    def _extend_args(self, layer: int, q, indptr, lens, block_table, out, lse, k_ext=None, v_ext=None) -> None:
+        """fp4 caches: refuse tensors the extend kernel would misread."""
+        d, N, B = self._layer(layer), int(q.shape[0]), int(lens.numel())
+        _need("q", q, torch.bfloat16, N * d["num_q_heads"] * d["head_dim"])
+        _need("out", out, torch.bfloat16, q.numel())
+        _need("qo_indptr", indptr, torch.int32, B + 1)
+        _need("lengths", lens, torch.int32)
+        for name, t in (("k_ext", k_ext), ("v_ext", v_ext)):
+            if t is not None:
+                _need(name, t, torch.bfloat16, N * d["num_kv_heads"] * d["head_dim"])
+        if block_table is not None:
+            _need("block_table", block_table, torch.int32, B * block_table.shape[1])
+        if lse is not None:
+            _need("lse", lse, torch.float32, N * d["num_q_heads"])
+
     def decode_multi(self, layer: int, q, qo_indptr, seq_lens, block_table, max_q_len: int, max_seq_len: int, out,
                      lse=None, stream=None) -> None:
         """fa_paged_decode_multi_attn: several new tokens per sequence, their rows
@@ -351,6 +366,8 @@ class Cache:
 
     def extend(self, layer: int, q, k_ext, v_ext, qo_indptr, prefix_lens, block_table, max_q_len: int,
                max_prefix_len: int, out, lse=None, stream=None) -> None:
+        if self.kv_dtype == KV_FP4:
+            self._extend_args(layer, q, qo_indptr, prefix_lens, block_table, out, lse, k_ext, v_ext)
         maxp = int(block_table.shape[1]) if block_table is not None else 0
         _check(_lib.fa_paged_extend_attn(self._h, layer, _p(q), _p(k_ext), _p(v_ext), _p(qo_indptr),
                                          _p(prefix_lens), _p(block_table), maxp, int(prefix_lens.numel()),

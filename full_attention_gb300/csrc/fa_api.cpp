@@ -800,7 +800,6 @@ fa_status fa_paged_extend_attn(fa_cache* c, int32_t layer, const void* q, const 
   cudaError_t ce;
   unsigned int* err = device_error_word(c, &ce);
   if (!err) return fail(FA_ERR_CUDA, "device error word: %s", cudaGetErrorString(ce));
-  if (c->kv_dtype == FA_KV_FP4) return fail(FA_ERR_UNSUPPORTED, "fp4 slabs: attention is not served");
   ExtendArgs a{};
   a.q = q;
   a.k_ext = k_ext;
@@ -865,7 +864,6 @@ fa_status fa_paged_decode_multi_attn(fa_cache* c, int32_t layer, const void* q, 
   cudaError_t ce;
   unsigned int* err = device_error_word(c, &ce);
   if (!err) return fail(FA_ERR_CUDA, "device error word: %s", cudaGetErrorString(ce));
-  if (c->kv_dtype == FA_KV_FP4) return fail(FA_ERR_UNSUPPORTED, "fp4 slabs: attention is not served");
   ExtendArgs a{};
   a.q = q;
   a.qo_indptr = qo_indptr;

@@ -56,6 +56,10 @@
 // below 2^15 whatever the scales.  A q or chunk value f16 cannot hold
 // (magnitude 65520 or more) saturates to +-65504 and sets FA_DEV_ERR_RANGE;
 // stored prefix rows have no such limit.
+// fp4 slabs run the same path: a prefix slot's codes and block scales land as
+// boxes of 16 rows x 32 bytes (64 codes, or a row's block scales) in the slot's
+// upper half, each row group inside the rows that its own converting warp will
+// overwrite, and become the exact f16 products code * block scale.
 // Every wait is bounded; tensor memory is always freed.
 #include <algorithm>
 #include <cfloat>
@@ -64,6 +68,7 @@
 
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
+#include "fa_row.cuh"
 
 namespace fa {
 
@@ -97,6 +102,11 @@ struct ExtCfg {
   // 8-bit slabs: a prefix slot's raw codes (CPS x 64 rows x 64 codes) land
   // in the slot's upper half, in 128-byte lines of 128 codes
   static constexpr int CODE_OFF = SLOT / 2;
+  // fp4: row group g's boxes at CODE_OFF + g * 2048: CPS of 64 codes a row,
+  // and the block scales' behind them, or a block further where 2 KB are full
+  static constexpr bool F4 = KV == FA_KV_FP4;
+  static constexpr int F4_BOX = 16 * 32;
+  static constexpr int F4_SC_OFF = CODE_OFF + (CPS == 4 ? CHUNK : CPS * F4_BOX);
   static constexpr int NPW = 4;                 // producer warps
   // the rest of shared memory is a ring of slots; per tile KB K chunks and 4 V blocks pass through it
   static constexpr int NSLOT = (232448 - 1024 - Q_BYTES - BAR_BYTES - SCL_BYTES) / SLOT;
@@ -525,14 +535,51 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
     // the same rows: the warp reads all its codes, syncs, then writes.  Rows
     // that hold no visible key become zero.  Chunk rows (bf16) convert piece
     // by piece in place; rows past the chunk become zero.
-    auto convert = [&](const TileSrc& q) {
+    auto convert = [&](const TileSrc& q, int blk0) {
       const int sl = e % C::NSLOT;
       ok = __all_sync(0xffffffffu, mbar_wait(&land[sl], (e / C::NSLOT) & 1)) && ok;
       if (!ok) return;
       uint8_t* dst = ring + sl * C::SLOT;
-      const int rr = lane >> 1, cpart = lane & 1;
+      // (fp4: rows of a quarter-warp consecutive, which its 32-byte rows need
+      // to be free of bank conflicts)
+      const int rr = C::F4 ? lane & 15 : lane >> 1, cpart = C::F4 ? lane >> 4 : lane & 1;
       const int r = 16 * pw + rr;   // this warp's row group: pw
-      if (q.prefix) {
+      if (C::F4 && q.prefix) {
+        const int row0 = pw == 0 ? q.row0[0] : pw == 1 ? q.row0[1] : pw == 2 ? q.row0[2] : q.row0[3];
+        const bool v = row0 >= 0 && r < q.lim && r >= q.wlim;
+        // boxes of 16 rows x 32 bytes, 32-byte swizzled: row rr's 16-byte unit
+        // u lies at unit u ^ (rr / 4 & 1)
+        const int swz = (rr >> 2) & 1;
+        const uint8_t* cb = dst + C::CODE_OFF + pw * 2048 + rr * 32 + ((cpart ^ swz) << 4);
+        const uint8_t* sb = dst + C::F4_SC_OFF + pw * 2048 + rr * 32 + (swz << 4) + ((blk0 * 4) & 15);
+        uint4 w[C::CPS];
+        uint32_t sc[C::CPS];
+#pragma unroll
+        for (int h = 0; h < C::CPS; ++h) {
+          w[h] = v ? *reinterpret_cast<const uint4*>(cb + h * C::F4_BOX) : make_uint4(0u, 0u, 0u, 0u);
+          // the two blocks of 16 of this lane's half; a masked row's may be NaN
+          sc[h] = v ? *reinterpret_cast<const uint16_t*>(sb + h * 4 + cpart * 2) : 0u;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < C::CPS; ++h) {
+          const uint32_t hs = e4m3x2_to_f16x2(sc[h]);
+          const __half2 s2 = *reinterpret_cast<const __half2*>(&hs);
+          const uint32_t cw[4] = {w[h].x, w[h].y, w[h].z, w[h].w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const __half2 su = u < 2 ? __low2half2(s2) : __high2half2(s2);
+            uint32_t pk[4];
+            e2m1x8_to_f16(cw[u], pk);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&pk[k]), su);
+              pk[k] = *reinterpret_cast<const uint32_t*>(&x);
+            }
+            *reinterpret_cast<uint4*>(dst + h * C::CHUNK + sw128(r, cpart * 4 + u)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          }
+        }
+      } else if (!C::F4 && q.prefix) {
         const int row0 = pw == 0 ? q.row0[0] : pw == 1 ? q.row0[1] : pw == 2 ? q.row0[2] : q.row0[3];
         const bool v = row0 >= 0 && r < q.lim && r >= q.wlim;
         // every code this lane converts is read before any write (the writes
@@ -549,7 +596,7 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
 #pragma unroll
         for (int h = 0; h < C::CPS; ++h) {
           uint32_t pk[16];
-          codes32<KV>(w[h], pk);
+          codes32<C::F4 ? FA_KV_FP8 : KV>(w[h], pk);   // (fp4: above)
 #pragma unroll
           for (int u = 0; u < 4; ++u)
             *reinterpret_cast<uint4*>(dst + h * C::CHUNK + sw128(r, cpart * 4 + u)) =
@@ -605,13 +652,26 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
                 int tx = 0;
 #pragma unroll
                 for (int g = 0; g < 4; ++g)
-                  if (ts.row0[g] >= 0 && 16 * g < ts.lim && 16 * g + 16 > ts.wlim) tx += (C::CPS / 2) * 2048;
+                  if (ts.row0[g] >= 0 && 16 * g < ts.lim && 16 * g + 16 > ts.wlim)
+                    tx += C::F4 ? (C::CPS + 1) * C::F4_BOX : (C::CPS / 2) * 2048;
                 mbar_arrive_expect_tx(&land[sl], tx);
               } else {
                 mbar_arrive(&land[sl]);
               }
               __syncwarp();
-              if (lane < 4) {
+              if (C::F4 && lane < 4 * (C::CPS + 1)) {
+                // fp4: box b of row group g, one a lane; the last is the row's
+                // 32 bytes from the 16-byte line of the slot's block scales on
+                // (past the row's end it reads zeros)
+                const int g = lane & 3, b = lane >> 2;
+                const int rg = g == 0 ? ts.row0[0] : g == 1 ? ts.row0[1] : g == 2 ? ts.row0[2] : ts.row0[3];
+                if (rg >= 0 && 16 * g < ts.lim && 16 * g + 16 > ts.wlim) {
+                  const bool sc = b == C::CPS;
+                  tma_load_2d(dst + g * 2048 + (sc ? C::F4_SC_OFF : C::CODE_OFF + b * C::F4_BOX), is_v ? &tm_v : &tm_k,
+                              &land[sl], sc ? D / 2 + ((blk0 * 4) & ~15) : (blk0 + b) * 32, rg, pol);
+                }
+              }
+              if (!C::F4 && lane < 4) {
                 const int g = lane;
                 const int rg = g == 0 ? ts.row0[0] : g == 1 ? ts.row0[1] : g == 2 ? ts.row0[2] : ts.row0[3];
                 if (rg >= 0 && 16 * g < ts.lim && 16 * g + 16 > ts.wlim)
@@ -634,7 +694,7 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
           }
           __syncwarp();
         } else if (ok) {
-          convert(ts);
+          convert(ts, blk0);
         }
         ++e;
         return;
@@ -1316,6 +1376,8 @@ cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t s) {
     return a.D == 256 ? launch_extend_t<256, FA_KV_INT8>(a, k, s) : launch_extend_t<512, FA_KV_INT8>(a, k, s);
   if (a.kv_dtype == FA_KV_FP8)
     return a.D == 256 ? launch_extend_t<256, FA_KV_FP8>(a, k, s) : launch_extend_t<512, FA_KV_FP8>(a, k, s);
+  if (a.kv_dtype == FA_KV_FP4)
+    return a.D == 256 ? launch_extend_t<256, FA_KV_FP4>(a, k, s) : launch_extend_t<512, FA_KV_FP4>(a, k, s);
   return a.D == 256 ? launch_extend_t<256, FA_KV_BF16>(a, k, s) : launch_extend_t<512, FA_KV_BF16>(a, k, s);
 }
 

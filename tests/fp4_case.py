@@ -148,3 +148,108 @@ class DecodeCase4:
                 worst = np.max(np.abs(out[b, j] - o) / tol)
                 assert worst <= 1, (i, b, j, int(self.lens[b]), worst)
                 assert abs(lse[b, j] - s) <= 2.0 ** -9 + 2.0 ** -20 * abs(s), (i, b, j, lse[b, j], s)
+
+
+class ExtendCase4:
+    """Sequences of stored prefix rows and new tokens; with `stored` the new
+    tokens' rows are in the slab too (multi-token decode)."""
+
+    def __init__(self, layers, prefix, chunk, page_size=16, seed=0, stored=False, split=None, edit=None):
+        import full_attention_gb300 as fa
+        self.fa, self.layers, self.ps, self.stored = fa, layers, page_size, stored
+        self.prefix, self.chunk = np.asarray(prefix, np.int32), np.asarray(chunk, np.int32)
+        self.B = len(prefix)
+        total = self.prefix + self.chunk
+        plan = W.plan_pages(np.maximum(total if stored else self.prefix, 1), page_size, seed)
+        self.cache = fa.Cache(layers, plan.num_pages, page_size, fa.KV_FP4)
+        self.src = [self.cache.source(i) for i in range(len(layers))]
+        self.slabs = self.cache.allocate("cuda")
+        if split == "all":
+            self.cache.set_flags(fa.FLAG_EXTEND_SPLIT_ALL)
+        if split is not None:
+            self.ws = fa.workspace(fa.extend_workspace_bytes())
+            self.cache.bind_extend_workspace(self.ws)
+        self.indptr = np.concatenate([[0], np.cumsum(self.chunk)]).astype(np.int32)
+        self.N = int(self.indptr[-1])
+        self.q, self.ext, self.vals = {}, {}, {}
+        for i, d in enumerate(layers):
+            g = torch.Generator().manual_seed(seed * 77 + i)
+            self.q[i] = torch.randn((self.N, d["num_q_heads"], d["head_dim"]), generator=g).to(torch.bfloat16).cuda()
+            if self.src[i] != i:
+                continue
+            junk(self.slabs[i], seed + i)
+            H, D = d["num_kv_heads"], d["head_dim"]
+            pre = [rows_like_a_model(int(self.prefix.sum()), H, D, seed * 31 + 4 * i + s) for s in (0, 1)]
+            new = [rows_like_a_model(self.N, H, D, seed * 31 + 4 * i + 2 + s) for s in (0, 1)]
+            if edit is not None:
+                edit(i, *pre, *new)
+            at = np.concatenate([[0], np.cumsum(self.prefix)])
+            slots = [W.slots_for_positions(plan.block_table[b], np.arange(int(self.prefix[b])), page_size)
+                     for b in range(self.B)]
+            rows = [x for x in pre]
+            if stored:
+                slots += [W.slots_for_positions(plan.block_table[b], np.arange(int(self.prefix[b]), int(total[b])), page_size)
+                          for b in range(self.B)]
+                rows = [torch.cat([a, b]) for a, b in zip(pre, new)]
+            sl = torch.from_numpy(np.concatenate(slots).astype(np.int32)).cuda()
+            if sl.numel():
+                self.cache.store(i, rows[0].cuda(), rows[1].cuda(), sl)
+            self.ext[i] = [x.cuda() for x in new]
+            kept = [oracle.fp4_value(*oracle.quantize_fp4(bits(x))) if len(x) else np.zeros((0, H, D)) for x in pre]
+            fresh = [oracle.fp4_value(*oracle.quantize_fp4(bits(x))) if stored else oracle.bf16_to_f64(bits(x)) for x in new]
+            self.vals[i] = [[np.concatenate([k[at[b]: at[b + 1]], f[self.indptr[b]: self.indptr[b + 1]]])
+                             for k, f in zip(kept, fresh)] for b in range(self.B)]
+        self.bt = torch.from_numpy(plan.block_table).cuda()
+        self.indptr_dev = torch.from_numpy(self.indptr).cuda()
+        self.prefix_dev = torch.from_numpy(self.prefix).cuda()
+        self.lens_dev = torch.from_numpy(total.astype(np.int32)).cuda()
+        torch.cuda.synchronize()
+
+    def outs(self, i):
+        d = self.layers[i]
+        return (torch.full((self.N, d["num_q_heads"], d["head_dim"]), float("nan"), dtype=torch.bfloat16, device="cuda"),
+                torch.full((self.N, d["num_q_heads"]), float("nan"), device="cuda"))
+
+    def run(self, i):
+        out, lse = self.outs(i)
+        if self.stored:
+            self.cache.decode_multi(i, self.q[i], self.indptr_dev, self.lens_dev, self.bt, int(self.chunk.max()),
+                                    int((self.prefix + self.chunk).max()), out, lse)
+        else:
+            k, v = self.ext[self.src[i]]
+            self.cache.extend(i, self.q[i], k, v, self.indptr_dev, self.prefix_dev, self.bt, int(self.chunk.max()),
+                              int(self.prefix.max()), out, lse)
+        return out, lse
+
+    def check(self, i, out, lse, most=400):
+        """Every new token (past `most` of a sequence, an even sample that holds the first and the last)."""
+        d = self.layers[i]
+        g = d["num_q_heads"] // d["num_kv_heads"]
+        q = oracle.bf16_to_f64(bits(self.q[i]))
+        out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        assert np.isfinite(out).all() and np.isfinite(lse).all()
+        win = d["window"] if d["kind"] == W.SLIDING else 0
+        for b in range(self.B):
+            n, P = int(self.chunk[b]), int(self.prefix[b])
+            if n == 0:
+                continue
+            t = np.unique(np.linspace(0, n - 1, min(n, most)).astype(int))
+            K, V = self.vals[self.src[i]][b]
+            kpos = np.arange(P + n)
+            seen = kpos[None] <= P + t[:, None]
+            if win:
+                seen &= P + t[:, None] - kpos[None] < win
+            rows = self.indptr[b] + t
+            for j in range(d["num_q_heads"]):
+                k, v = K[:, j // g], V[:, j // g]
+                s = np.where(seen, d["sm_scale"] * (q[rows, j] @ k.T), -np.inf)
+                m = s.max(1, keepdims=True)
+                p = np.exp(s - m)
+                l = p.sum(1, keepdims=True)
+                p /= l
+                ref = p @ v
+                tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -8 * (p @ np.abs(v)) + 1e-30
+                worst = np.max(np.abs(out[rows, j] - ref) / tol)
+                assert worst <= 1, (i, b, j, worst)
+                r = (m + np.log(l))[:, 0]
+                assert np.all(np.abs(lse[rows, j] - r) <= 2.0 ** -9 + 2.0 ** -20 * np.abs(r)), (i, b, j)
