@@ -61,6 +61,7 @@ def _load() -> ctypes.CDLL:
         "fa_kv_load": (i32, [vp, i32, vp, i32, vp, vp, vp]),
         "fa_decode_workspace_bytes": (sz, [vp, i32, i32, i32]),
         "fa_extend_workspace_bytes": (sz, []),
+        "fa_extend_unpack_bytes": (sz, [vp, i32, i32, i32, i32]),
         "fa_cache_bind_extend_workspace": (i32, [vp, vp, sz]),
         "fa_paged_decode_attn": (i32, [vp, i32, vp, vp, i32, vp, i32, i32, vp, vp, vp, sz, vp]),
         "fa_paged_decode_store_attn": (i32, [vp, i32, vp, vp, vp, vp, vp, i32, vp, i32, i32, vp, vp, vp, sz, vp]),
@@ -298,6 +299,14 @@ class Cache:
 
     def decode_workspace_bytes(self, layer: int, batch: int, max_seq_len: int) -> int:
         return int(_lib.fa_decode_workspace_bytes(self._h, layer, batch, max_seq_len))
+
+    def extend_workspace_bytes(self, layer: int, batch: int, max_q_len: int, max_len: int) -> int:
+        """Bytes of an extend workspace for calls of up to these sizes (max_len: of the
+        prefixes, or in multi-token decode of the sequences):
+        fa_extend_workspace_bytes, and on an fp4 cache fa_extend_unpack_bytes more."""
+        self._layer(layer)
+        return extend_workspace_bytes() + int(_lib.fa_extend_unpack_bytes(self._h, layer, int(batch), int(max_q_len),
+                                                                          int(max_len)))
 
     def bind_extend_workspace(self, workspace) -> None:
         """fa_cache_bind_extend_workspace: let extend and multi-token decode

@@ -17,7 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfa_gb300.so")
-SOURCES = ["fa_api.cpp", "fa_store.cu", "fa_decode.cu", "fa_decode_fp4.cu", "fa_extend.cu"]
+SOURCES = ["fa_api.cpp", "fa_store.cu", "fa_decode.cu", "fa_decode_fp4.cu", "fa_extend.cu",
+           "fa_unpack.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -3,6 +3,8 @@
 // memory is allocated here; every device buffer belongs to the caller.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -754,13 +756,95 @@ static void set_split(const fa_cache* c, ExtendArgs& a) {
   a.split_mode = !c->split_ws ? 0 : (c->flags & FA_FLAG_EXTEND_SPLIT_ALL) ? 2 : 1;
 }
 
+namespace fa {
+// Where the unpacked fp4 rows of an extend or multi-token decode call lie in the
+// workspace: K rows, V rows, block table.  ring 0: nothing to unpack.
+struct UnpackLayout {
+  int ring = 0, table_pages = 0;
+  size_t off_v = 0, off_table = 0, bytes = 0;
+};
+static UnpackLayout unpack_layout(const fa_cache* c, int32_t layer, int32_t B, int32_t max_q_len, int32_t max_len) {
+  UnpackLayout u;
+  const fa_layer_desc& d = c->layers[layer].d;
+  if (c->kv_dtype != FA_KV_FP4 || B <= 0 || max_len <= 0 || max_q_len < 0) return u;
+  // a sliding layer's queries see W - 1 rows before the first of them and (in
+  // multi-token decode) their own, from a 16-row boundary on
+  const int64_t seen = d.kind == FA_SLIDING ? std::min<int64_t>(max_len, static_cast<int64_t>(d.window) + max_q_len + 15) : max_len;
+  const int64_t ring = (seen + kTile - 1) / kTile * kTile;
+  const int64_t rows = ring * B * d.num_kv_heads;
+  if (rows >= (1LL << 31) || static_cast<int64_t>(B) * d.num_kv_heads > 65535) return u;   // row indices are 32-bit
+  u.ring = static_cast<int>(ring);
+  u.table_pages = static_cast<int>((max_len + ring - 1) / ring);
+  auto up = [](size_t b) { return (b + 255) / 256 * 256; };
+  u.off_v = up(static_cast<size_t>(rows) * d.head_dim * 2);
+  u.off_table = 2 * u.off_v;
+  u.bytes = u.off_table + up(static_cast<size_t>(B) * u.table_pages * sizeof(int32_t));
+  return u;
+}
+
+// Whether unpacking shortens a call.  Converting inside the kernel costs each
+// job about 2.5 us per 64 keys at head_dim 512 and 0.6 at 256 over the bf16
+// kernel; unpacking moves 2.6 bytes per value of every visible row at some 5
+// TB/s, behind a launch.  Measured, converting inside against unpacked:
+// 8 x 4096 keys at 512, 2 KV heads, 4 queries 178 : 109 us, 256 queries 1218 :
+// 556; 64 x 4096 keys, 4 queries 341 : 265; at 256 with a window of 1024, 8 KV
+// heads, 8 sequences, 16 queries 36 : 44, 256 queries 111 : 84.
+static bool unpack_pays(const ExtendArgs& a, int ring) {
+  const double span = a.kind == FA_SLIDING ? std::min(ring, a.max_prefix_len) : a.max_prefix_len;
+  const int T = 128 / (a.Hq / a.Hkv);
+  const double jobs = static_cast<double>((a.max_q_len + T - 1) / T) * a.Hkv * (a.D / 256) * a.B;
+  const double waves = std::max(1.0, std::ceil(jobs / sm_count()));
+  const double saved_us = waves * span / 64 * (a.D == 512 ? 2.5 : 0.6);
+  const double cost_us = 1.5 + static_cast<double>(a.B) * a.Hkv * span * a.D * 2 * 2.6 / 5e6;
+  return saved_us > cost_us;
+}
+
+// fp4 with room in the workspace: unpack what the call can see and point its
+// arguments at the bf16 rows (maps are written to tm).  Leaves `a` as it is
+// where the call converts codes itself.
+static fa_status unpack_for_extend(const fa_cache* c, int32_t layer, ExtendArgs& a, CUtensorMap (&tm)[2], cudaStream_t stream) {
+  const Layer& L = c->layers[layer];
+  const UnpackLayout ul = unpack_layout(c, layer, a.B, a.max_q_len, a.max_prefix_len);
+  if (ul.ring == 0 || ul.bytes > c->unpack_bytes || !unpack_pays(a, ul.ring)) return FA_OK;
+  char* ws = static_cast<char*>(c->unpack_ws);
+  const UnpackArgs u{a.keys_in_pages ? a.seq_lens : a.prefix_lens, a.keys_in_pages ? a.qo_indptr : nullptr, a.block_table,
+                     a.k_slab, a.v_slab, a.k_scale, a.v_scale, ws, ws + ul.off_v,
+                     reinterpret_cast<int32_t*>(ws + ul.off_table), a.B, a.Hkv, a.D, a.kind == FA_SLIDING ? a.window : 0,
+                     a.page_size, a.num_pages, a.max_pages_per_seq, a.max_prefix_len, a.max_q_len, a.early_metadata,
+                     ul.ring, ul.table_pages, a.err};
+  const uint64_t rows = static_cast<uint64_t>(a.B) * L.d.num_kv_heads * ul.ring;
+  fa_status st;
+  if ((st = encode_slab_map(&tm[0], u.k, a.D, FA_KV_BF16, rows))) return st;
+  if ((st = encode_slab_map(&tm[1], u.v, a.D, FA_KV_BF16, rows))) return st;
+  const cudaError_t ce = launch_unpack(u, stream);
+  if (ce != cudaSuccess) return fail(FA_ERR_CUDA, "unpack launch: %s", cudaGetErrorString(ce));
+  a.k_slab = u.k;
+  a.v_slab = u.v;
+  a.tm_k = &tm[0];
+  a.tm_v = &tm[1];
+  a.kv_dtype = FA_KV_BF16;
+  a.page_size = ul.ring;
+  a.num_pages = a.B;
+  a.block_table = u.table;
+  a.max_pages_per_seq = ul.table_pages;
+  a.early_metadata = 0;   // the table comes from the kernel before
+  return FA_OK;
+}
+}  // namespace fa
+
+size_t fa_extend_unpack_bytes(const fa_cache* c, int32_t layer, int32_t B, int32_t max_q_len, int32_t max_len) {
+  if (check_layer(c, layer) != FA_OK) return 0;
+  return unpack_layout(c, layer, B, max_q_len, max_len).bytes;
+}
+
 size_t fa_extend_workspace_bytes(void) { return ext_split_layout(ext_split_cap()).bytes; }
 
 fa_status fa_cache_bind_extend_workspace(fa_cache* c, void* workspace, size_t bytes) {
   if (!c) return fail(FA_ERR_INVALID_ARG, "cache is NULL");
   if (!workspace) {
-    c->split_ws = nullptr;
+    c->split_ws = c->unpack_ws = nullptr;
     c->split_cap = 0;
+    c->unpack_bytes = 0;
     return ok();
   }
   if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(FA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
@@ -773,6 +857,9 @@ fa_status fa_cache_bind_extend_workspace(fa_cache* c, void* workspace, size_t by
   if (ce != cudaSuccess) return fail(FA_ERR_CUDA, "clearing the extend workspace: %s", cudaGetErrorString(ce));
   c->split_ws = workspace;
   c->split_cap = cap;
+  const size_t used = (ext_split_layout(cap).bytes + 255) / 256 * 256;
+  c->unpack_ws = bytes > used ? static_cast<char*>(workspace) + used : nullptr;
+  c->unpack_bytes = bytes > used ? bytes - used : 0;
   return ok();
 }
 
@@ -837,6 +924,8 @@ fa_status fa_paged_extend_attn(fa_cache* c, int32_t layer, const void* q, const 
   if ((st = encode_q_map(&a.tm_q, q, num_tokens, L.d.num_q_heads, L.d.head_dim, g))) return st;
   if ((st = encode_ext_map(&a.tm_kx, k_ext, num_tokens, L.d.num_kv_heads, L.d.head_dim))) return st;
   if ((st = encode_ext_map(&a.tm_vx, v_ext, num_tokens, L.d.num_kv_heads, L.d.head_dim))) return st;
+  CUtensorMap tm_unpacked[2];
+  if ((st = unpack_for_extend(c, layer, a, tm_unpacked, static_cast<cudaStream_t>(stream)))) return st;
   ce = launch_extend(a, static_cast<cudaStream_t>(stream));
   if (ce != cudaSuccess) return fail(FA_ERR_CUDA, "extend launch: %s", cudaGetErrorString(ce));
   return ok();
@@ -900,6 +989,8 @@ fa_status fa_paged_decode_multi_attn(fa_cache* c, int32_t layer, const void* q, 
   if ((st = encode_q_map(&a.tm_q, q, num_tokens, L.d.num_q_heads, L.d.head_dim, g))) return st;
   a.tm_kx = s->tm_k;   // no chunk rows in this mode: the chunk maps are never used
   a.tm_vx = s->tm_v;
+  CUtensorMap tm_unpacked[2];
+  if ((st = unpack_for_extend(c, layer, a, tm_unpacked, static_cast<cudaStream_t>(stream)))) return st;
   ce = launch_extend(a, static_cast<cudaStream_t>(stream));
   if (ce != cudaSuccess) return fail(FA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(ce));
   return ok();

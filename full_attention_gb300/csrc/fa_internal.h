@@ -57,6 +57,8 @@ struct fa_cache {
   int32_t err_slot = -1;   // this cache's device error word (index into the per-device array)
   void* split_ws = nullptr;   // extend split workspace (caller's memory), split_cap jobs
   int32_t split_cap = 0;
+  void* unpack_ws = nullptr;  // fp4: what the extend workspace holds past its split part
+  size_t unpack_bytes = 0;
 };
 
 namespace fa {
@@ -207,6 +209,24 @@ struct ExtendArgs {
   int split_cap, split_mode;
 };
 cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t s);
+
+// The fp4 rows of an extend or multi-token decode call as bf16 (fa_unpack.cu).
+struct UnpackArgs {
+  const int32_t* lens;        // prefix lengths, or with qo_indptr sequence lengths
+  const int32_t* qo_indptr;   // multi-token decode: the queries are the last tokens
+  const int32_t* block_table;
+  const void* k_slab;
+  const void* v_slab;
+  const float* k_scale;
+  const float* v_scale;
+  void* k;          // [B][Hkv][ring][D] bf16
+  void* v;
+  int32_t* table;   // [B][table_pages]
+  int B, Hkv, D, window, page_size, num_pages, max_pages_per_seq, max_len, max_q_len, early_metadata;
+  int ring, table_pages;
+  unsigned int* err;
+};
+cudaError_t launch_unpack(const UnpackArgs& a, cudaStream_t s);
 
 // Split workspace of extend for `cap` jobs: arrival counters, then per job
 // and CTA 128 rows of (base, rounded sum, unrounded sum, 0), then per job

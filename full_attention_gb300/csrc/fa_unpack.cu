@@ -1,0 +1,84 @@
+// The fp4 rows an extend or multi-token decode call can see, unpacked to bf16.
+//
+// An extend over a 4-bit slab multiplies every prefix key with every 128-row
+// block of queries.  Converting codes inside the kernel repeats the conversion
+// for each block and paces it (286 and 213 TFLOP/s on the two shapes below);
+// a value of the format has 6 significant bits, so a bf16 row holds it exactly,
+// and the bf16 kernel over unpacked rows does the same arithmetic without it.
+// This kernel writes them: a memory pass over the rows some query can see, 0.58
+// bytes in and 2 out per value, most of which the extend kernel then finds in
+// L2.
+//
+// The rows of sequence b and KV head h form a ring of `ring` rows (a multiple
+// of 16): position pos lies in row (b * Hkv + h) * ring + pos % ring.  To the
+// extend kernel that is a slab of pages of `ring` rows whose block table says b
+// for every page of sequence b; the table is written here too.
+#include "fa_internal.h"
+#include "fa_ptx.cuh"
+#include "fa_row.cuh"
+
+namespace fa {
+
+template <int D>
+__global__ void __launch_bounds__(256) unpack_kernel(UnpackArgs a) {
+  constexpr int R = D == 256 ? 8 : 4;   // rows a warp moves at a time, K and V alternating
+  if (!a.early_metadata) griddep_wait();
+  griddep_launch_dependents();
+  const int b = blockIdx.y / a.Hkv, h = blockIdx.y % a.Hkv;
+  const int lane = threadIdx.x & 31;
+  // rows [first, P): extend, the prefix; multi-token decode, the whole sequence,
+  // whose last n tokens are the queries
+  const int P = min(__ldg(a.lens + b), a.max_len);
+  const int n = a.qo_indptr ? min(max(__ldg(a.qo_indptr + b + 1) - __ldg(a.qo_indptr + b), 0), a.max_q_len) : 0;
+  if (blockIdx.x == 0 && h == 0) {
+    griddep_wait();   // the table may still be read by the previous call's kernel
+    for (int i = threadIdx.x; i < a.table_pages; i += blockDim.x) a.table[static_cast<size_t>(b) * a.table_pages + i] = b;
+  }
+  // the first query sees from P - W + 1 on; the extend kernel's tiles start on 16 rows
+  const int lo = a.window > 0 ? max(0, P - n - a.window + 1) & ~15 : 0;
+  const int pos0 = lo + (blockIdx.x * 8 + (threadIdx.x >> 5)) * (R / 2);
+  if (pos0 >= P) {
+    griddep_wait();   // the grid ends only after the kernel before it
+    return;
+  }
+  int row[R / 2];
+#pragma unroll
+  for (int i = 0; i < R / 2; ++i) {
+    row[i] = -1;
+    if (pos0 + i >= P) continue;
+    const int pg = (pos0 + i) / a.page_size;
+    const int pid = __ldg(a.block_table + static_cast<size_t>(b) * a.max_pages_per_seq + pg);
+    if (pid >= 0 && pid < a.num_pages) row[i] = (pid * a.Hkv + h) * a.page_size + (pos0 + i - pg * a.page_size);
+    else if (lane == 0) atomicOr(a.err, FA_DEV_ERR_PAGE);   // reads as zeros
+  }
+  griddep_wait();
+  RawRow<D, FA_KV_FP4> raw[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    if (row[i / 2] >= 0) {
+      const size_t r = row[i / 2];
+      raw_load<D, FA_KV_FP4>(raw[i], static_cast<const uint8_t*>((i & 1) ? a.v_slab : a.k_slab) + r * kRowBytes<D, FA_KV_FP4>,
+                             ((i & 1) ? a.v_scale : a.k_scale) + r, lane);
+    } else {
+      raw[i] = RawRow<D, FA_KV_FP4>{};
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int pos = pos0 + i / 2;
+    if (pos >= P) continue;
+    const size_t dst = (static_cast<size_t>(b) * a.Hkv + h) * a.ring + pos % a.ring;
+    raw_to_bf16<D, FA_KV_FP4>(raw[i], static_cast<__nv_bfloat16*>((i & 1) ? a.v : a.k) + dst * D, lane);
+  }
+}
+
+cudaError_t launch_unpack(const UnpackArgs& a, cudaStream_t s) {
+  const int per_block = 8 * (a.D == 256 ? 4 : 2);   // positions
+  const int span = a.ring < a.max_len ? a.ring : a.max_len;
+  const long long gy = static_cast<long long>(a.B) * a.Hkv;
+  if (gy > 65535) return cudaErrorInvalidConfiguration;   // the caller takes the direct path
+  const dim3 g(static_cast<unsigned>((span + per_block - 1) / per_block), static_cast<unsigned>(gy)), b(256);
+  return a.D == 256 ? launch_pdl(unpack_kernel<256>, g, b, 0, s, a) : launch_pdl(unpack_kernel<512>, g, b, 0, s, a);
+}
+
+}  // namespace fa

@@ -207,12 +207,28 @@ FA_API size_t fa_extend_workspace_bytes(void);
  * fa_extend_workspace_bytes() bytes holds fewer jobs).  The caller keeps
  * ownership; it must stay allocated while calls may use it, and calls on
  * the cache that use it must run in stream order (one stream, or streams
- * ordered by events): concurrent calls would share its slots.  Zeroes its
+ * ordered by events): concurrent calls would share its slots.  On an fp4
+ * cache the bytes past fa_extend_workspace_bytes() take the unpacked prefix
+ * (fa_extend_unpack_bytes).  Zeroes its
  * arrival counters (synchronous); each launch leaves them zero.  A launch
  * splits when the wave is at most half full and its length bounds promise
  * 8 key tiles (512 keys) or more per job.  NULL unbinds.  Errors: FA_ERR_INVALID_ARG
  * (misaligned), FA_ERR_WORKSPACE (too small for one job), FA_ERR_CUDA. */
 FA_API fa_status fa_cache_bind_extend_workspace(fa_cache* cache, void* workspace, size_t bytes);
+
+/* Bytes that an extend workspace holds beyond fa_extend_workspace_bytes() for
+ * extend and multi-token decode calls over an fp4 slab to run on bf16 rows: the
+ * rows of `layer` that B sequences' queries can see (max_len: the bound on the
+ * prefix, or in multi-token decode on the sequence; of a sliding layer the
+ * window's part), K and V, unpacked by the call (an fp4 value is exact in
+ * bf16), and a block table.  Bind a workspace of fa_extend_workspace_bytes()
+ * plus the largest of these of the layers and calls it serves: such calls then
+ * unpack once and run the bf16 kernel where that is faster (about twice on
+ * long chunks); q and the chunk have no f16 range there.  A call that needs
+ * more room than the workspace has, or has none bound, converts the codes
+ * inside the kernel.  0 in the other formats.  Host only. */
+FA_API size_t fa_extend_unpack_bytes(const fa_cache* cache, int32_t layer, int32_t B, int32_t max_q_len,
+                                     int32_t max_len);
 
 /* Give the sliding layers' slabs a page pool of their own (the pages' window
  * pool: "FreeToken PR #898", description, the window slots come from one

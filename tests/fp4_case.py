@@ -11,6 +11,12 @@ output may be off by:
   64, which also bounds the weights' relative error): together 2^-8 |out| +
   2^-8 * sum_j p_j |v_j|;
   lse: the score error, 2^-9, and a few fp32 roundings of its own size, 2^-20 |lse|.
+
+Where a workspace for unpacked rows is bound, extend may run the bf16 kernel: its
+weights p (1 + d) are rounded to bf16, |d| <= 2^-8, and divided by the sum of the
+rounded ones, which moves the output by at most sum_j p_j |d_j| |v_j - out| <=
+2^-8 (sum_j p_j |v_j| + |out|); with the output's own rounding and the score
+error, 2^-7 |out| + (2^-8 + 2^-9) sum_j p_j |v_j|.
 """
 import numpy as np
 import torch
@@ -157,6 +163,7 @@ class ExtendCase4:
     def __init__(self, layers, prefix, chunk, page_size=16, seed=0, stored=False, split=None, edit=None):
         import full_attention_gb300 as fa
         self.fa, self.layers, self.ps, self.stored = fa, layers, page_size, stored
+        self.unpacked = split is not None and "unpack" in split
         self.prefix, self.chunk = np.asarray(prefix, np.int32), np.asarray(chunk, np.int32)
         self.B = len(prefix)
         total = self.prefix + self.chunk
@@ -166,8 +173,14 @@ class ExtendCase4:
         self.slabs = self.cache.allocate("cuda")
         if split == "all":
             self.cache.set_flags(fa.FLAG_EXTEND_SPLIT_ALL)
-        if split is not None:
-            self.ws = fa.workspace(fa.extend_workspace_bytes())
+        if split is not None:   # "tail", "all": the split part only; "unpack": with room for the prefix as bf16 rows
+            n = fa.extend_workspace_bytes()
+            if "unpack" in split:
+                if "all" in split:
+                    self.cache.set_flags(fa.FLAG_EXTEND_SPLIT_ALL)
+                most = int((self.prefix + self.chunk).max())
+                n = max(self.cache.extend_workspace_bytes(i, self.B, int(self.chunk.max()), most) for i in range(len(layers)))
+            self.ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")   # NaN rows where nothing is unpacked
             self.cache.bind_extend_workspace(self.ws)
         self.indptr = np.concatenate([[0], np.cumsum(self.chunk)]).astype(np.int32)
         self.N = int(self.indptr[-1])
@@ -248,7 +261,8 @@ class ExtendCase4:
                 l = p.sum(1, keepdims=True)
                 p /= l
                 ref = p @ v
-                tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -8 * (p @ np.abs(v)) + 1e-30
+                a, w = (2.0 ** -7, 1.5 * 2.0 ** -8) if self.unpacked else (2.0 ** -8, 2.0 ** -8)
+                tol = a * np.abs(ref) + w * (p @ np.abs(v)) + 1e-30
                 worst = np.max(np.abs(out[rows, j] - ref) / tol)
                 assert worst <= 1, (i, b, j, worst)
                 r = (m + np.log(l))[:, 0]
