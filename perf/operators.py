@@ -209,7 +209,7 @@ def prepare(case, seed):
         if kind == "decode":
             st["ws"] = fa.workspace(st["cache"].decode_workspace_bytes(0, case["B"], st["max_len"]))
         if kind == "extend":
-            st["ws"] = fa.workspace(fa.extend_workspace_bytes())
+            st["ws"] = fa.workspace(st["cache"].extend_workspace_bytes(0, case["B"], st["max_new"], st["max_prefix"]))
             st["cache"].bind_extend_workspace(st["ws"])
     return st
 
