@@ -117,6 +117,21 @@ static cudaError_t launch_pdl(Kern kern, dim3 grid, dim3 block, size_t smem, cud
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// Division by an invariant: n / d for 0 <= n < 2^31 as one high product and a
+// shift (Granlund and Montgomery's method, the multiplier rounded up).
+struct FastDiv {
+  uint32_t mul, shift, d;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t div) : d(div) {
+    shift = 0;
+    while ((1ull << shift) < div) ++shift;   // ceil(log2 d)
+    mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << shift) - div)) / div + 1);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+#endif
+};
+
 struct StoreArgs {
   const void* k;
   const void* v;
@@ -127,6 +142,7 @@ struct StoreArgs {
   float* v_scale;
   int T, Hkv, D, page_size, num_pages, kv_dtype, early_metadata;
   unsigned int* err;
+  FastDiv by_page, by_rows;   // page_size; 2 Hkv (set by the launch, fp4)
 };
 cudaError_t launch_store(const StoreArgs& a, cudaStream_t s);
 // The stores of several layers in one launch (n <= kMaxLayersPerLaunch; any head_dim mix).
@@ -142,6 +158,7 @@ struct LoadArgs {
   void* v;
   int T, Hkv, D, page_size, num_pages, kv_dtype, early_metadata;
   unsigned int* err;
+  FastDiv by_page, by_rows;   // page_size; Hkv x sides (set by the launch)
 };
 cudaError_t launch_load(const LoadArgs& a, cudaStream_t s);
 

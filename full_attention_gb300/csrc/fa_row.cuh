@@ -156,23 +156,48 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
 // largest code times the block scale, rounded up, still fits bf16).
 constexpr uint32_t kFp4MaxBits = 0x7f00u;
 
-// The larger of two unsigned 16-bit halves, for both halves of a word.
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+// Two fp32 values in a register pair, for the packed fp32 arithmetic.
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t p, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 // The fp4 format (fa.h, fa_kv_dtype): the row scale 2^e, per block of 16 values
 // the e4m3 scale b nearest to amax_b / (6 * 2^e), per value the e2m1 code
-// nearest to x / (2^e b).  Every rounding is decided exactly with one fp32
-// product each:
+// nearest to x / (2^e b).  Every rounding is decided exactly without a division
+// per value:
 //  * amax_b * 2^-e is exact (a power of two); its product with fp32(1/6) equals
 //    the midpoint of two e4m3 values exactly when the quotient does (fp32(1/6)
 //    is off by 2^-25 relative, less than half a step of any midpoint, which has
 //    5 significant bits), and otherwise stays on its side (the quotient of an
 //    8-bit number by 6 is 2^-9 or more away from every midpoint, relatively);
-//  * x * (2^-e / b) is within 2^-23 of the quotient x / (2^e b), whose distance
-//    from a midpoint of the e2m1 values (at most 3 significant bits, times b's
-//    4) is 0 or at least 2^-9 relative: rounding the product to 12 significant
-//    bits puts an exact tie back on the midpoint and moves nothing across it.
-// A division per value instead costs 8 times the arithmetic of the row.
+//  * x * (2^-e / b), with the reciprocal rounded once, is within 2^-21 of the
+//    quotient where that is below 8, and rounding it to a multiple of 2^-12 (a
+//    fused product and sum with 2560, whose last place is 2^-12, and the sum
+//    undone) puts an exact tie between two e2m1 values, a multiple of 1/4, back
+//    on the midpoint and moves nothing across one: a quotient of 8 significant
+//    bits by 4 that is not on a midpoint is 2^-10 or more away from it.
+//    Quotients past 8 saturate either way.
+// The 8-bit formats divide each value instead and take twice as long.
 // Lane l holds values [i * 256 + 8 l, i * 256 + 8 l + 8) of the row; blocks are
 // lane pairs.
 template <int D>
@@ -183,10 +208,10 @@ __device__ __forceinline__ void row_store_fp4(const RowRegs<D>& r, uint8_t* dst,
     uint32_t row = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) m = max_u16x2(m, w[i][e] & 0x7fff7fffu);
-      m = max(m & 0xffffu, m >> 16);
+      auto h = [&](int e) { return *reinterpret_cast<const __nv_bfloat162*>(&w[i][e]); };
+      const __nv_bfloat162 m2 = __hmax2_nan(__hmax2_nan(__habs2(h(0)), __habs2(h(1))), __hmax2_nan(__habs2(h(2)), __habs2(h(3))));
+      const uint32_t b2 = *reinterpret_cast<const uint32_t*>(&m2);
+      const uint32_t m = max(b2 & 0xffffu, b2 >> 16);
       blk[i] = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
       row = max(row, blk[i]);
     }
@@ -226,13 +251,16 @@ __device__ __forceinline__ void row_store_fp4(const RowRegs<D>& r, uint8_t* dst,
     const uint32_t sb = __nv_cvt_float_to_fp8(__fmul_rn(ab, 1.0f / 6.0f), __NV_SATFINITE, __NV_E4M3);
     const float b = __half2float(__ushort_as_half(static_cast<unsigned short>(e4m3x2_to_f16x2(sb) & 0xffffu)));
     const float t = sb ? inv_s * __frcp_rn(b) : 0.0f;
+    const uint64_t t2 = pack_f32x2(t, t), c2 = pack_f32x2(2560.0f, 2560.0f), n2 = pack_f32x2(-2560.0f, -2560.0f);
     float q[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float x = __uint_as_float((k & 1) ? (w[i][k >> 1] & 0xffff0000u) : (w[i][k >> 1] << 16));
-      q[k] = __uint_as_float((__float_as_uint(__fmul_rn(x, t)) + 0x800u) & 0xfffff000u);
+    for (int k = 0; k < 4; ++k) {
+      const uint64_t x2 = pack_f32x2(__uint_as_float(w[i][k] << 16), __uint_as_float(w[i][k] & 0xffff0000u));
+      unpack_f32x2(add_f32x2(fma_f32x2(x2, t2, c2), n2), q[2 * k], q[2 * k + 1]);
     }
-    *reinterpret_cast<uint32_t*>(dst + i * 128 + lane * 4) = e2m1x8(q);
+    uint32_t c = e2m1x8(q);
+    c = (c & 0x77777777u) | (c & ((c | (c >> 1) | (c >> 2)) << 3) & 0x88888888u);   // no negative zeros
+    *reinterpret_cast<uint32_t*>(dst + i * 128 + lane * 4) = c;
     if (!(lane & 1)) dst[D / 2 + i * 16 + (lane >> 1)] = static_cast<uint8_t>(sb);
   }
   if (lane == 0) *scale = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
@@ -306,9 +334,12 @@ __device__ __forceinline__ void raw_to_bf16(const RawRow<D, KV>& r, __nv_bfloat1
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] = static_cast<float>(static_cast<int8_t>(r.c[i][k >> 2] >> (8 * (k & 3))));
       }
+      const uint64_t s2 = pack_f32x2(s, s);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(__fmul_rn(x[2 * k], s), __fmul_rn(x[2 * k + 1], s));
+        float lo, hi;
+        unpack_f32x2(mul_f32x2(pack_f32x2(x[2 * k], x[2 * k + 1]), s2), lo, hi);
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
         o[k] = *reinterpret_cast<const uint32_t*>(&v);
       }
     }

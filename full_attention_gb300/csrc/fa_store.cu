@@ -9,8 +9,7 @@
 // saturating at 448; every division IEEE round-to-nearest.  The microscaled
 // 4-bit format is in fa_row.cuh (row_store_fp4).
 //
-// The reverse, fa_kv_load, reads rows back as bf16 with the same assignment of
-// rows to warps and values to lanes.
+// The reverse, fa_kv_load, reads rows back as bf16.
 #include <algorithm>
 #include <cstdio>
 #include <mutex>
@@ -109,11 +108,53 @@ __device__ __forceinline__ void store_rows(const StoreArgs& a, int warp, int lan
   }
 }
 
+// fp4: the same with the warp's R rows those of R consecutive tokens for one
+// (KV head, K or V).  Tokens stored together mostly lie in consecutive slots, so
+// the warp's 144- or 288-byte rows and their scales are neighbours in the slab
+// and share their sectors.
+template <int D>
+__device__ __forceinline__ void store_rows_fp4(const StoreArgs& a, int warp, int lane) {
+  constexpr int R = StoreShape<D>::R;
+  const uint32_t per = 2 * a.Hkv;
+  const uint32_t tg = a.by_rows.div(warp), q = warp - tg * per;   // token group, 2 h + side
+  const int t0 = static_cast<int>(tg) * R;
+  if (t0 >= a.T) return;
+  const uint32_t h = q >> 1, which = q & 1;
+  int slot[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) slot[i] = (t0 + i < a.T) ? __ldg(a.slots + t0 + i) : -1;
+  griddep_wait();   // the rows (and the slab) may belong to the previous kernel
+  RowRegs<D> r[R];
+  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(which ? a.v : a.k) + (static_cast<size_t>(t0) * a.Hkv + h) * D;
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    if (t0 + i < a.T) row_load<D>(r[i], src + static_cast<size_t>(i) * a.Hkv * D, lane);
+  uint8_t* slab = static_cast<uint8_t*>(which ? a.v_slab : a.k_slab);
+  float* scale = which ? a.v_scale : a.k_scale;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    if (slot[i] < 0) continue;   // a padding token
+    const uint32_t page = a.by_page.div(slot[i]), off = slot[i] - page * a.page_size;
+    if (page >= static_cast<uint32_t>(a.num_pages)) {
+      if (lane == 0) atomicOr(a.err, FA_DEV_ERR_SLOT);
+      continue;
+    }
+    const size_t dst = (page * a.Hkv + h) * a.page_size + off;   // below 2^31 (fa_cache_create)
+    row_store_fp4<D>(r[i], slab + dst * kRowBytes<D, FA_KV_FP4>, scale + dst, lane);
+  }
+}
+
+template <int D, int KV>
+__device__ __forceinline__ void store_warp(const StoreArgs& a, int warp, int lane) {
+  if constexpr (KV == FA_KV_FP4) store_rows_fp4<D>(a, warp, lane);
+  else store_rows<D, KV>(a, warp, lane);
+}
+
 template <int D, int KV>
 __global__ void __launch_bounds__(256) store_kernel(StoreArgs a) {
   if (!a.early_metadata) griddep_wait();
   griddep_launch_dependents();
-  store_rows<D, KV>(a, (blockIdx.x * blockDim.x + threadIdx.x) >> 5, threadIdx.x & 31);
+  store_warp<D, KV>(a, (blockIdx.x * blockDim.x + threadIdx.x) >> 5, threadIdx.x & 31);
 }
 
 // Several layers' stores in one launch: blockIdx.y picks the layer.
@@ -127,15 +168,22 @@ __global__ void __launch_bounds__(256) store_layers_kernel(const __grid_constant
   if (!a.early_metadata) griddep_wait();
   griddep_launch_dependents();
   const int warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-  if (a.D == 256) store_rows<256, KV>(a, warp, lane);
-  else store_rows<512, KV>(a, warp, lane);
+  if (a.D == 256) store_warp<256, KV>(a, warp, lane);
+  else store_warp<512, KV>(a, warp, lane);
 }
 
 // Warps a store of T tokens needs.
 static long store_warps(const StoreArgs& a) {
   const long rows = static_cast<long>(a.T) * a.Hkv * 2;
   const int R = a.D == 256 ? StoreShape<256>::R : StoreShape<512>::R;
+  if (a.kv_dtype == FA_KV_FP4) return static_cast<long>((a.T + R - 1) / R) * a.Hkv * 2;
   return (rows + R - 1) / R;
+}
+
+static StoreArgs with_divs(StoreArgs a) {
+  a.by_page = FastDiv(a.page_size);
+  a.by_rows = FastDiv(2 * a.Hkv);
+  return a;
 }
 
 cudaError_t launch_store_layers(const StoreArgs* a, int n, cudaStream_t s) {
@@ -143,7 +191,7 @@ cudaError_t launch_store_layers(const StoreArgs* a, int n, cudaStream_t s) {
   StoreLayers m{};
   long warps = 0;
   for (int i = 0; i < n; ++i) {
-    m.a[i] = a[i];
+    m.a[i] = with_divs(a[i]);
     warps = std::max(warps, store_warps(a[i]));
   }
   const int block = 256;
@@ -156,7 +204,8 @@ cudaError_t launch_store_layers(const StoreArgs* a, int n, cudaStream_t s) {
   return launch_pdl(store_layers_kernel<FA_KV_BF16>, g, b, 0, s, m);
 }
 
-cudaError_t launch_store(const StoreArgs& a, cudaStream_t s) {
+cudaError_t launch_store(const StoreArgs& args, cudaStream_t s) {
+  const StoreArgs a = with_divs(args);
   const long warps = store_warps(a);
   const int block = 256;
   const long grid = (warps * 32 + block - 1) / block;
@@ -175,54 +224,59 @@ cudaError_t launch_store(const StoreArgs& a, cudaStream_t s) {
                     : launch_pdl(store_kernel<512, FA_KV_BF16>, g, b, 0, s, a);
 }
 
-// The reverse of store_rows: R consecutive rows of the output per warp, row
-// (t * Hkv + h) * sides + side, with sides = 2 (K, then V) or 1 (only one of
-// them is wanted).  Slots, then every row's raw bytes, then the rows out.
+// The reverse, any format: a warp's R rows are those of R consecutive tokens for
+// one (KV head, K or V).  Slots, then every row's raw bytes, then the rows out.
 template <int D, int KV>
 __global__ void __launch_bounds__(256) load_kernel(LoadArgs a) {
   constexpr int R = StoreShape<D>::R;
   if (!a.early_metadata) griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int sides = a.k && a.v ? 2 : 1, only = a.k ? 0 : 1;
-  const long long rows = static_cast<long long>(a.T) * a.Hkv * sides;
-  const long long r0 = ((static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5) * R;
-  if (r0 >= rows) return;
+  const uint32_t sides = a.k && a.v ? 2 : 1;
+  const uint32_t warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const uint32_t tg = a.by_rows.div(warp), q = warp - tg * a.by_rows.d;
+  const long long t0 = static_cast<long long>(tg) * R;
+  if (t0 >= a.T) {
+    griddep_wait();   // the grid ends only after the kernel before it
+    return;
+  }
+  const uint32_t h = sides == 2 ? q >> 1 : q;
+  const bool which = sides == 2 ? (q & 1) : a.v != nullptr;
   int slot[R];
 #pragma unroll
-  for (int i = 0; i < R; ++i) slot[i] = (r0 + i < rows) ? __ldg(a.slots + (r0 + i) / (a.Hkv * sides)) : -1;
+  for (int i = 0; i < R; ++i) slot[i] = (t0 + i < a.T) ? __ldg(a.slots + t0 + i) : -1;
   griddep_wait();   // the slab's rows may belong to the previous kernel
+  const uint8_t* slab = static_cast<const uint8_t*>(which ? a.v_slab : a.k_slab);
+  const float* scale = which ? a.v_scale : a.k_scale;
   RawRow<D, KV> raw[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     if (slot[i] < 0) continue;   // a padding token: its rows stay as they are
-    const int page = slot[i] / a.page_size, off = slot[i] % a.page_size;
-    if (page >= a.num_pages) {
+    const uint32_t page = a.by_page.div(slot[i]), off = slot[i] - page * a.page_size;
+    if (page >= static_cast<uint32_t>(a.num_pages)) {
       if (lane == 0) atomicOr(a.err, FA_DEV_ERR_SLOT);
       slot[i] = -1;
       continue;
     }
-    const int q = static_cast<int>((r0 + i) % (a.Hkv * sides));
-    const int which = sides == 2 ? (q & 1) : only;
-    const size_t src = (static_cast<size_t>(page) * a.Hkv + q / sides) * a.page_size + off;
-    raw_load<D, KV>(raw[i], static_cast<const uint8_t*>(which ? a.v_slab : a.k_slab) + src * kRowBytes<D, KV>,
-                    KV == FA_KV_BF16 ? nullptr : (which ? a.v_scale : a.k_scale) + src, lane);
+    const size_t src = (page * a.Hkv + h) * a.page_size + off;   // below 2^31 (fa_cache_create)
+    raw_load<D, KV>(raw[i], slab + src * kRowBytes<D, KV>, scale + src, lane);
   }
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(which ? a.v : a.k) + (static_cast<size_t>(t0) * a.Hkv + h) * D;
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    if (slot[i] < 0) continue;
-    const long long row = r0 + i;
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(sides == 2 ? ((row & 1) ? a.v : a.k) : only ? a.v : a.k);
-    raw_to_bf16<D, KV>(raw[i], dst + static_cast<size_t>(row / sides) * D, lane);
-  }
+  for (int i = 0; i < R; ++i)
+    if (slot[i] >= 0) raw_to_bf16<D, KV>(raw[i], dst + static_cast<size_t>(i) * a.Hkv * D, lane);
 }
 
-cudaError_t launch_load(const LoadArgs& a, cudaStream_t s) {
+cudaError_t launch_load(const LoadArgs& args, cudaStream_t s) {
+  LoadArgs a = args;
   const int R = a.D == 256 ? StoreShape<256>::R : StoreShape<512>::R;
-  const long long rows = static_cast<long long>(a.T) * a.Hkv * (a.k && a.v ? 2 : 1);
+  const int per = a.Hkv * (a.k && a.v ? 2 : 1);
+  a.by_page = FastDiv(a.page_size);
+  a.by_rows = FastDiv(per);
+  const long long warps = (static_cast<long long>(a.T) + R - 1) / R * per;
   const int block = 256;
-  const long long grid = ((rows + R - 1) / R * 32 + block - 1) / block;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const long long grid = (warps * 32 + block - 1) / block;
+  if (warps >= (1LL << 31) - 8) return cudaErrorInvalidValue;
   const dim3 g(static_cast<unsigned>(grid)), b(block);
   auto run = [&](auto k256, auto k512) {
     return a.D == 256 ? launch_pdl(k256, g, b, 0, s, a) : launch_pdl(k512, g, b, 0, s, a);

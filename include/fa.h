@@ -101,8 +101,8 @@ typedef enum {
  * (2688 = 6 * 448, the largest code times the largest block scale), each block
  * of 16 consecutive values the e4m3 scale b nearest to (the block's max|x|) /
  * (6 s), ties to the even mantissa, and each value the e2m1 code nearest to
- * x / (s b), ties to the even code, magnitudes above 6 saturating, the sign
- * kept.  e2m1 codes 0 .. 7 stand for 0, 0.5, 1, 1.5, 2, 3, 4, 6, codes 8 .. 15
+ * x / (s b), ties to the even code, magnitudes above 6 saturating; a value
+ * that rounds to zero is code 0.  e2m1 codes 0 .. 7 stand for 0, 0.5, 1, 1.5, 2, 3, 4, 6, codes 8 .. 15
  * for their negatives.  A block whose scale is 0 keeps zeros.  The value of a
  * code is code * b * s: 6 significant bits, so reading a row back into bf16
  * rounds nothing.  A NaN element is stored as 0, a magnitude above 2^127 (the

@@ -285,7 +285,8 @@ def quantize_fp4(x_bits):
     float32 [...]).  NaN counts as 0, a magnitude above 2^127 as 2^127; the row
     scale is 2^e, e the smallest integer >= -116 with max|x| <= 2688 * 2^e; each
     block of 16 has the e4m3 scale nearest to its max|x| / (6 * 2^e), each value
-    the e2m1 code nearest to x / (2^e * block scale)."""
+    the e2m1 code nearest to x / (2^e * block scale), a value that rounds to
+    zero code 0."""
     x = bf16_to_f64(x_bits)
     neg = np.signbit(x) & ~np.isnan(x)
     mag = np.minimum(np.where(np.isnan(x), 0.0, np.abs(x)), 2.0 ** 127)
@@ -297,7 +298,8 @@ def quantize_fp4(x_bits):
     sb = _nearest_even(e4m3_value(np.arange(0x7F, dtype=np.uint8)), np.max(y, axis=-1) / 6.0).astype(np.uint8)
     b = e4m3_value(sb)[..., None]
     q = np.where(b > 0, y / np.where(b > 0, b, 1.0), 0.0)
-    code = _nearest_even(E2M1_MAGS, q).astype(np.uint8).reshape(mag.shape) | (neg.astype(np.uint8) << 3)
+    code = _nearest_even(E2M1_MAGS, q).astype(np.uint8).reshape(mag.shape)
+    code = code | ((neg & (code > 0)).astype(np.uint8) << 3)
     rows = np.concatenate([code[..., 0::2] | (code[..., 1::2] << 4), sb], axis=-1)
     return rows.astype(np.uint8), np.ldexp(np.float32(1.0), e).astype(np.float32)
 

@@ -62,7 +62,7 @@ def test_oracle_matches_exact_rationals(D):
         c = np.stack([b & 15, b >> 4], -1).reshape(-1)
         assert F(float(scale[i])) == s
         assert (c & 7).tolist() == codes and got[i, D // 2:].tolist() == scales
-        assert ((c >> 3) == np.signbit(oracle.bf16_to_f64(x[i]))).all()
+        assert ((c >> 3) == (np.signbit(oracle.bf16_to_f64(x[i])) & (c != 0))).all()
         want = [(-1 if n else 1) * E2M1[k] * E4M3[scales[j // 16]] * s for j, (k, n) in enumerate(zip(codes, c >> 3))]
         assert [F(float(v)) for v in oracle.fp4_value(got[i:i + 1], scale[i:i + 1])[0]] == want
 
