@@ -84,6 +84,7 @@ def _load() -> ctypes.CDLL:
 
 
 _lib = _load()
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # absent in a CPU-only torch
 _live = weakref.WeakSet()   # every Cache not yet destroyed (for device_error())
 
 
@@ -97,13 +98,14 @@ def _check(status: int) -> None:
 
 
 def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _s(stream):
+    # the raw handle: building a torch Stream object costs more than the rest of a call's marshalling
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        return _raw_stream(torch._C._cuda_getDevice()) if _raw_stream else torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream
 
 
 def _ptrs(ts):
@@ -111,10 +113,15 @@ def _ptrs(ts):
     return (ctypes.c_void_p * len(ts))(*[None if t is None else t.data_ptr() for t in ts])
 
 
-def _need(what, t, dtype, numel=None):
-    """Refuse a tensor the kernels would misread: not on the current device,
-    another type, not dense, or (numel given) another size."""
-    if t.dtype != dtype or not t.is_contiguous() or not t.is_cuda or t.device.index != torch.cuda.current_device():
+def _device() -> int:
+    """The current device; -2, which no tensor is on, where no GPU can be reached."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -2
+
+
+def _need(what, t, dtype, numel, dev):
+    """Refuse a tensor the kernels would misread: not on device `dev`, another
+    type, not dense, or (numel not None) another size."""
+    if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != dev:
         raise FAError(ERR_INVALID_ARG, f"{what} must be a dense {dtype} tensor on the current CUDA device, not "
                                        f"{t.dtype}, strides {tuple(t.stride())}, on {t.device}")
     if numel is not None and t.numel() != numel:
@@ -184,6 +191,9 @@ class Cache:
             raise FAError(ERR_INVALID_ARG, f"layer {layer} out of range [0, {len(self.layers)})")
         return self.layers[layer]
 
+    def _owns(self, layer: int) -> bool:
+        return self._layer(layer).get("kv_source", KV_OWN) == KV_OWN
+
     def source(self, layer: int) -> int:
         out = ctypes.c_int32()
         _check(_lib.fa_cache_layer_source(self._h, layer, ctypes.byref(out)))
@@ -200,9 +210,10 @@ class Cache:
     def bind(self, layer: int, k, v, k_scale=None, v_scale=None) -> None:
         if self.kv_dtype == KV_FP4 and None not in (k, v, k_scale, v_scale):
             kv, sc = self.slab_bytes(layer)
+            dev = _device()
             for name, t, dt, n in (("k", k, torch.uint8, kv), ("v", v, torch.uint8, kv),
                                    ("k_scale", k_scale, torch.float32, sc // 4), ("v_scale", v_scale, torch.float32, sc // 4)):
-                _need(name, t, dt, n if kv else None)   # a shared layer's refusal is the library's
+                _need(name, t, dt, n if kv else None, dev)   # a shared layer's refusal is the library's
         _check(_lib.fa_cache_bind_slab(self._h, layer, _p(k), _p(v), _p(k_scale), _p(v_scale)))
         self._slabs[layer] = (k, v, k_scale, v_scale)
 
@@ -235,13 +246,14 @@ class Cache:
 
     def _rows(self, layer: int, k, v, slot_mapping) -> None:
         """fp4 caches: refuse rows or slots the store would misread."""
-        d = self._layer(layer)
-        _need("slot_mapping", slot_mapping, torch.int32)
-        for name, t in (("k", k), ("v", v)):
-            _need(name, t, torch.bfloat16, slot_mapping.numel() * d["num_kv_heads"] * d["head_dim"])
+        d, dev = self._layer(layer), _device()
+        _need("slot_mapping", slot_mapping, torch.int32, None, dev)
+        n = slot_mapping.numel() * d["num_kv_heads"] * d["head_dim"]
+        _need("k", k, torch.bfloat16, n, dev)
+        _need("v", v, torch.bfloat16, n, dev)
 
     def store(self, layer: int, k, v, slot_mapping, stream=None) -> None:
-        if self.kv_dtype == KV_FP4 and self.source(layer) == layer:
+        if self.kv_dtype == KV_FP4 and self._owns(layer):
             self._rows(layer, k, v, slot_mapping)
         _check(_lib.fa_kv_store(self._h, layer, _p(k), _p(v), _p(slot_mapping), int(slot_mapping.numel()),
                                 _s(stream)))
@@ -250,12 +262,14 @@ class Cache:
         """fa_kv_load: read the rows at the slots back into k, v (bf16
         [T][Hkv][D]; either may be None), from a slab of any format; a negative
         slot leaves its rows as they were."""
-        d = self._layer(layer)
-        _need("slot_mapping", slot_mapping, torch.int32)
-        T = int(slot_mapping.numel())
-        for name, t in (("k", k), ("v", v)):
-            if t is not None:
-                _need(name, t, torch.bfloat16, T * d["num_kv_heads"] * d["head_dim"])
+        d, dev = self._layer(layer), _device()
+        _need("slot_mapping", slot_mapping, torch.int32, None, dev)
+        T = slot_mapping.numel()
+        n = T * d["num_kv_heads"] * d["head_dim"]
+        if k is not None:
+            _need("k", k, torch.bfloat16, n, dev)
+        if v is not None:
+            _need("v", v, torch.bfloat16, n, dev)
         _check(_lib.fa_kv_load(self._h, layer, _p(slot_mapping), T, _p(k), _p(v), _s(stream)))
 
     def store_layers(self, layers, ks, vs, slot_mappings, stream=None) -> None:
@@ -265,21 +279,21 @@ class Cache:
             for i, k, v, s in zip(layers, ks, vs, slot_mappings):
                 if self.source(i) == i:
                     self._rows(i, k, v, s)
-                    _need("slot_mappings", s, torch.int32, slot_mappings[0].numel())
+                    _need("slot_mappings", s, torch.int32, slot_mappings[0].numel(), _device())
         T = int(slot_mappings[0].numel())
         _check(_lib.fa_kv_store_layers(self._h, len(layers), _i32s(layers), _ptrs(ks), _ptrs(vs),
                                        _ptrs(slot_mappings), T, _s(stream)))
 
     def _decode_args(self, layer: int, q, block_table, seq_lens, out, lse) -> None:
         """fp4 caches: refuse tensors the decode kernel would misread."""
-        d, B = self._layer(layer), int(q.shape[0])
+        d, B, dev = self._layer(layer), q.shape[0], _device()
         n = B * d["num_q_heads"]
-        _need("q", q, torch.bfloat16, n * d["head_dim"])
-        _need("out", out, torch.bfloat16, n * d["head_dim"])
-        _need("seq_lens", seq_lens, torch.int32, B)
-        _need("block_table", block_table, torch.int32, B * block_table.shape[1])
+        _need("q", q, torch.bfloat16, n * d["head_dim"], dev)
+        _need("out", out, torch.bfloat16, n * d["head_dim"], dev)
+        _need("seq_lens", seq_lens, torch.int32, B, dev)
+        _need("block_table", block_table, torch.int32, B * block_table.shape[1], dev)
         if lse is not None:
-            _need("lse", lse, torch.float32, n)
+            _need("lse", lse, torch.float32, n, dev)
 
     def decode_layers_workspace_bytes(self, layers, batch: int, max_seq_len: int) -> int:
         return int(_lib.fa_decode_layers_workspace_bytes(self._h, len(layers), _i32s(layers), batch, max_seq_len))
@@ -332,7 +346,7 @@ class Cache:
         decode in one launch (owning layers; a shared layer only decodes)."""
         if self.kv_dtype == KV_FP4:
             self._decode_args(layer, q, block_table, seq_lens, out, lse)
-            if self.source(layer) == layer:
+            if self._owns(layer):
                 self._rows(layer, k_new, v_new, slot_mapping)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         _check(_lib.fa_paged_decode_store_attn(self._h, layer, _p(q), _p(k_new), _p(v_new), _p(slot_mapping),
@@ -352,18 +366,18 @@ class Cache:
 
     def _extend_args(self, layer: int, q, indptr, lens, block_table, out, lse, k_ext=None, v_ext=None) -> None:
         """fp4 caches: refuse tensors the extend kernel would misread."""
-        d, N, B = self._layer(layer), int(q.shape[0]), int(lens.numel())
-        _need("q", q, torch.bfloat16, N * d["num_q_heads"] * d["head_dim"])
-        _need("out", out, torch.bfloat16, q.numel())
-        _need("qo_indptr", indptr, torch.int32, B + 1)
-        _need("lengths", lens, torch.int32)
+        d, N, B, dev = self._layer(layer), q.shape[0], lens.numel(), _device()
+        _need("q", q, torch.bfloat16, N * d["num_q_heads"] * d["head_dim"], dev)
+        _need("out", out, torch.bfloat16, q.numel(), dev)
+        _need("qo_indptr", indptr, torch.int32, B + 1, dev)
+        _need("lengths", lens, torch.int32, None, dev)
         for name, t in (("k_ext", k_ext), ("v_ext", v_ext)):
             if t is not None:
-                _need(name, t, torch.bfloat16, N * d["num_kv_heads"] * d["head_dim"])
+                _need(name, t, torch.bfloat16, N * d["num_kv_heads"] * d["head_dim"], dev)
         if block_table is not None:
-            _need("block_table", block_table, torch.int32, B * block_table.shape[1])
+            _need("block_table", block_table, torch.int32, B * block_table.shape[1], dev)
         if lse is not None:
-            _need("lse", lse, torch.float32, N * d["num_q_heads"])
+            _need("lse", lse, torch.float32, N * d["num_q_heads"], dev)
 
     def decode_multi(self, layer: int, q, qo_indptr, seq_lens, block_table, max_q_len: int, max_seq_len: int, out,
                      lse=None, stream=None) -> None:

@@ -463,6 +463,7 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
       uint8_t* pbuf = smem + C::OFF_P + buf * C::NT * C::P_TILE;
       float* mw = reinterpret_cast<float*>(smem + C::OFF_MW) + buf * 8 * C::NT;
       int* flag = reinterpret_cast<int*>(smem + C::OFF_FLAG) + buf * C::NT;
+      const bool edge = tile0 * kTile < lo || (tile0 + ntl) * kTile - 1 > qpos;   // some keys are masked
       const int kst = e % C::NSLOT;
       if (!__all_sync(0xffffffffu, mbar_wait(&full[kst], (e / C::NSLOT) & 1)) && lane == 0) {
         abort_flag = 1;   // everyone leaves at the barrier below
@@ -509,7 +510,7 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int pos = tile0 * kTile + key + 8 * r;
-          const bool vis = pos >= lo && pos <= qpos;
+          const bool vis = !edge || (pos >= lo && pos <= qpos);
           const float ks = scl[key + 8 * r] * p.scale_log2;
           const float ve =
               static_cast<float>(static_cast<int>(__float_as_uint(scl[C::NT * kTile + key + 8 * r]) >> 23) - 127);
@@ -589,7 +590,7 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
       ++e;
       uint8_t* vslot = smem + vst * C::SLOT;
       constexpr int SB = D / 64;   // this warp's block scales per row (bytes)
-      if (tile0 * kTile < lo || (tile0 + ntl) * kTile - 1 > qpos) {
+      if (edge) {
         // masked keys have weight 0, but their rows may hold anything (block
         // scales of NaN included): zero this warp's block scales of those rows
         for (int r = lane; r < ntl * kTile; r += 32) {
