@@ -277,6 +277,7 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
   uint64_t* empty = full + C::NSLOT;
   uint64_t* mbar_merge = empty + C::NSLOT;
   __shared__ int abort_flag, sh_last;
+  __shared__ Share share;   // what the epilogue needs of the cut, out of the registers meanwhile
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
@@ -294,7 +295,6 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
     return;
   }
   if (!small) sh.nct = 0;
-  const int ncta = sh.ncta, T = sh.T;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NSLOT; ++s) {
       mbar_init(&full[s], 1);
@@ -302,10 +302,14 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
     }
     mbar_init(mbar_merge, 1);
     abort_flag = 0;
+    if (small) share = sh;
     fence_mbar_init();
   }
   __syncthreads();
-  if (!small) finish_share(cta, sh);
+  if (!small) {
+    finish_share(cta, sh);
+    if (threadIdx.x == 0) share = sh;   // read after the barriers of the first step
+  }
   const int u0 = sh.u0, p0 = sh.p0;
   const int s_beg = static_cast<int>(sh.s_beg), s_end = static_cast<int>(sh.s_end);   // T fits an int
 
@@ -411,7 +415,7 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
 
   // -------------------------------------------------------------- consumers
   griddep_wait();
-  zero_empty_units<D, KV>(p, cta, ncta, threadIdx.x, C::NCW * 32);
+  zero_empty_units<D, KV>(p, cta, sh.ncta, threadIdx.x, C::NCW * 32);
   constexpr float P_OFF = 4.0f;    // weights reach 2^P_OFF against a base of their own tile's,
   constexpr float SLACK = 8.0f;    // and 2^(P_OFF + SLACK) against O's base before it is raised
   int e = 0, step = 0;
@@ -664,15 +668,10 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
       l += v.y * ex2(v.x - m);
     }
     const float Mo = M - P_OFF;
-    int c_first = sh.cf, nct = sh.nct;
+    int c_first = share.cf, nct = share.nct;
     if (nct == 0) {   // not the whole-unit cut
-      if (sh.kper) {
-        c_first = u * sh.kper;
-        nct = sh.kper;
-      } else {
-        c_first = cta_of_fast(static_cast<uint32_t>(P), ncta, T);
-        nct = cta_of_fast(static_cast<uint32_t>(P + x.n - 1), ncta, T) - c_first + 1;
-      }
+      c_first = cta_of_fast(static_cast<uint32_t>(P), share.ncta, share.T);
+      nct = cta_of_fast(static_cast<uint32_t>(P + x.n - 1), share.ncta, share.T) - c_first + 1;
     }
     const int d0 = (8 * warp + gid) * 8 * C::NW;   // this lane's columns: 8 NW from d0 on
     if (nct == 1) {
