@@ -220,41 +220,38 @@ __device__ __forceinline__ uint32_t share_begin(uint32_t c, uint32_t n, uint32_t
   return c * q + (r ? c * r / n : 0u);
 }
 
-// A cut for up to kWarpUnits units, found by every warp for itself from
-// shuffles: no block barrier, one round of loads, and 32-bit divisions only (a
-// 64-bit one costs some 0.3 us on the way to the first copy).  Where it can,
-// it gives every CTA a part of one unit only: unit u is cut into ceil(n_u / Q)
-// equal parts, Q the smallest quota found for which the launch's CTAs
-// suffice.  A CTA that crosses from one unit to the next pays a second query
+// A cut for up to kWarpSeqs sequences, found by every warp for itself from
+// shuffles: no block barrier, one round of loads up to 32 sequences, and 32-bit
+// divisions only (a 64-bit one costs some 0.3 us on the way to the first copy).
+// Where it can, it gives every CTA a part of one unit only: unit u is cut into
+// ceil(n_u / Q) equal parts, Q the smallest quota found for which the launch's
+// CTAs suffice.  A CTA that crosses from one unit to the next pays a second query
 // load, epilogue and merge in the middle of its stream, which costs more than
 // the uneven parts as long as Q stays below 3/2 of the even share; past that
 // (many units, few CTAs for each) the lists are laid end to end as in
 // cut_share.  Returns false where cut_share does; a true share is complete (no
 // finish_share).
-constexpr int kWarpUnits = 256;
+//
+// A sequence's units (KV head x chunk) are all alike, so a lane looks at
+// sequences only.  Past 32 of them the loops stay rolled and read the lengths
+// again (from L1): the whole kernel has to come through the instruction cache
+// once per launch, and unrolled copies cost short launches more than the loads.
+constexpr int kWarpSeqs = 256;
 __device__ __forceinline__ bool cut_share_warp(const DecK& p, int cta, int grid, Share& s) {
-  constexpr int PER = kWarpUnits / 32;
   const int lane = threadIdx.x & 31;
-  const int per = (p.units + 31) / 32;   // units of a lane: [lane * per, ...)
-  const int hc = p.Hkv * p.chunks;
-  int n[PER], sum = 0;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    n[i] = 0;
-    if (i >= per) continue;
-    const int u = lane * per + i;
-    if (u < p.units) {
-      const int L = __ldg(p.seq_lens + (hc == 1 ? u : static_cast<int>(static_cast<uint32_t>(u) / hc)));
-      if (cta == 0 && threadIdx.x < 32 && L > p.max_seq_len) atomicOr(p.err, FA_DEV_ERR_BOUND);
-      const int len = min(L, p.max_seq_len);
-      if (len > 0) {
-        const uint32_t lo = p.kind == FA_SLIDING ? max(0, len - p.window) : 0;
-        n[i] = static_cast<uint32_t>(len - 1) / kTile + 1 - lo / kTile;
-      }
-      sum += n[i];
-    }
-  }
-  auto scan = [&](int v) {   // inclusive, over the lanes
+  const int per = (p.B + 31) / 32;       // sequences of a lane: [lane * per, ...)
+  const int hc = p.Hkv * p.chunks;       // units of a sequence
+  bool past = false;
+  auto tiles = [&](int i) {              // of each unit of the lane's sequence i
+    const int b = lane * per + i;
+    int len = b < p.B ? __ldg(p.seq_lens + b) : 0;
+    past |= len > p.max_seq_len;
+    len = min(len, p.max_seq_len);
+    if (len <= 0) return 0;
+    const uint32_t lo = p.kind == FA_SLIDING ? max(0, len - p.window) : 0;
+    return static_cast<int>(static_cast<uint32_t>(len - 1) / kTile + 1 - lo / kTile);
+  };
+  auto scan = [&](int v) {               // inclusive, over the lanes
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int t = __shfl_up_sync(0xffffffffu, v, o);
@@ -262,6 +259,12 @@ __device__ __forceinline__ bool cut_share_warp(const DecK& p, int cta, int grid,
     }
     return v;
   };
+  const int n0 = tiles(0);
+  int sum = n0;
+#pragma unroll 1
+  for (int i = 1; i < per; ++i) sum += tiles(i);
+  if (past && cta == 0 && threadIdx.x < 32) atomicOr(p.err, FA_DEV_ERR_BOUND);
+  sum *= hc;
   const int incl = scan(sum);
   const int T = __shfl_sync(0xffffffffu, incl, 31);
   s.T = T;
@@ -269,82 +272,75 @@ __device__ __forceinline__ bool cut_share_warp(const DecK& p, int cta, int grid,
   s.ncta = 0;
   if (T == 0) return false;
   const uint32_t even = max((static_cast<uint32_t>(T) + grid - 1) / grid, static_cast<uint32_t>(p.min_tiles));
-  int k[PER], ks = 0, total = 0;
+  int ks = 0, total = 0;
   uint32_t Q = even;
+  float rq;
+  auto parts = [&](int n) {              // ceil(n / Q): the fp32 estimate is put right by one either way
+    const int m = n + static_cast<int>(Q) - 1;
+    int c = static_cast<int>(static_cast<float>(m) * rq);
+    c -= c * static_cast<int>(Q) > m;
+    c += (c + 1) * static_cast<int>(Q) <= m;
+    return c;
+  };
   while (true) {
-    const float rq = __frcp_rn(static_cast<float>(Q));
-    ks = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      k[i] = 0;
-      if (i >= per) continue;
-      // ceil(n / Q): the fp32 estimate is put right by one either way
-      const int m = n[i] + static_cast<int>(Q) - 1;
-      int c = static_cast<int>(static_cast<float>(m) * rq);
-      c -= c * static_cast<int>(Q) > m;
-      c += (c + 1) * static_cast<int>(Q) <= m;
-      k[i] = c;
-      ks += c;
-    }
+    rq = __frcp_rn(static_cast<float>(Q));
+    ks = parts(n0);
+#pragma unroll 1
+    for (int i = 1; i < per; ++i) ks += parts(tiles(i));
+    ks *= hc;
     total = __reduce_add_sync(0xffffffffu, ks);
     if (total <= grid || 2 * Q >= 3 * even) break;
     // in proportion, as far as the fractions of a part allow
     Q = max(Q + 1, static_cast<uint32_t>(static_cast<float>(Q) * total / grid));
   }
-  int u0 = -1, p0 = 0, P = incl - sum;
-  if (total <= grid) {
-    s.ncta = total;
-    if (cta >= total) return false;
-    int n0 = 0, k0 = 0, c0 = 0, K = scan(ks) - ks;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      if (i >= per) continue;
-      if (K <= cta && cta < K + k[i]) {
-        u0 = lane * per + i;
-        p0 = P;
-        n0 = n[i];
-        k0 = k[i];
-        c0 = K;
-      }
-      P += n[i];
-      K += k[i];
-    }
-    const int src = __ffs(__ballot_sync(0xffffffffu, u0 >= 0)) - 1;
-    s.u0 = __shfl_sync(0xffffffffu, u0, src);
-    s.p0 = __shfl_sync(0xffffffffu, p0, src);
-    s.cf = __shfl_sync(0xffffffffu, c0, src);
-    s.nct = __shfl_sync(0xffffffffu, k0, src);
-    n0 = __shfl_sync(0xffffffffu, n0, src);
-    const uint32_t i = cta - s.cf, uq = static_cast<uint32_t>(n0) / s.nct, ur = n0 - uq * s.nct;
-    s.s_beg = s.p0 + share_begin(i, s.nct, uq, ur);
-    s.s_end = s.p0 + share_begin(i + 1, s.nct, uq, ur);
-    return true;
-  }
-  const int ncta = min(grid, static_cast<int>((static_cast<uint32_t>(T) + p.min_tiles - 1) / p.min_tiles));
+  const bool whole = total <= grid;
+  const int ncta = whole ? total : min(grid, static_cast<int>((static_cast<uint32_t>(T) + p.min_tiles - 1) / p.min_tiles));
   s.ncta = ncta;
   if (cta >= ncta) return false;
   const uint32_t q = static_cast<uint32_t>(T) / ncta, r = T - q * ncta;
   const int s_beg = share_begin(cta, ncta, q, r);
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    if (i >= per) continue;
-    if (n[i] > 0 && P <= s_beg && s_beg < P + n[i]) {
-      u0 = lane * per + i;
+  int b0 = -1, p0 = 0, un = 0, k0 = 0, c0 = 0, P = incl - sum, K = scan(ks) - ks;
+#pragma unroll 1
+  for (int i = 0; i < per; ++i) {
+    const int n = i == 0 ? n0 : tiles(i), k = parts(n);
+    if (whole ? K <= cta && cta < K + k * hc : P <= s_beg && s_beg < P + n * hc) {
+      b0 = lane * per + i;
       p0 = P;
+      un = n;
+      k0 = k;
+      c0 = K;
     }
-    P += n[i];
+    P += n * hc;
+    K += k * hc;
   }
-  const int src = __ffs(__ballot_sync(0xffffffffu, u0 >= 0)) - 1;
-  s.u0 = __shfl_sync(0xffffffffu, u0, src);
-  s.p0 = __shfl_sync(0xffffffffu, p0, src);
-  s.s_beg = s_beg;
-  s.s_end = share_begin(cta + 1, ncta, q, r);
+  const int src = __ffs(__ballot_sync(0xffffffffu, b0 >= 0)) - 1;
+  b0 = __shfl_sync(0xffffffffu, b0, src);
+  p0 = __shfl_sync(0xffffffffu, p0, src);
+  un = __shfl_sync(0xffffffffu, un, src);
+  if (whole) {
+    c0 = __shfl_sync(0xffffffffu, c0, src);
+    k0 = __shfl_sync(0xffffffffu, k0, src);
+    const int j = static_cast<uint32_t>(cta - c0) / static_cast<uint32_t>(k0);   // unit in the sequence
+    s.u0 = b0 * hc + j;
+    s.p0 = p0 + j * un;
+    s.cf = c0 + j * k0;
+    s.nct = k0;
+    const uint32_t i = cta - s.cf, uq = static_cast<uint32_t>(un) / k0, ur = un - uq * k0;
+    s.s_beg = s.p0 + share_begin(i, k0, uq, ur);
+    s.s_end = s.p0 + share_begin(i + 1, k0, uq, ur);
+  } else {
+    const int j = static_cast<uint32_t>(s_beg - p0) / static_cast<uint32_t>(un);
+    s.u0 = b0 * hc + j;
+    s.p0 = p0 + j * un;
+    s.s_beg = s_beg;
+    s.s_end = share_begin(cta + 1, ncta, q, r);
+  }
   return true;
 }
 
 // The CTA that owns tile g of T cut over n: cta_of without its 64-bit division.
 // The quotient is estimated in fp32 and put right against share_begin.
-__device__ __forceinline__ int cta_of_fast(uint32_t g, uint32_t n, uint32_t T) {
+static __device__ __noinline__ int cta_of_fast(uint32_t g, uint32_t n, uint32_t T) {
   const uint32_t q = T / n, r = T - q * n;
   int c = static_cast<int>(__fdividef(static_cast<float>(g) * static_cast<float>(n), static_cast<float>(T)));
   c = max(0, min(c, static_cast<int>(n) - 1));

@@ -69,13 +69,25 @@ struct F4Cfg {
 // "No score yet": finite, so that differences against it are never NaN.
 constexpr float kNoScore = -3.402823466e38f;
 
-// unit_of without divisions where each sequence is one unit.
+// What runs once or rarely in a launch stays out of line: all of the code has to
+// come through the instruction cache, which short launches wait for.
+static __device__ __noinline__ int3 unit_place(int Hkv, int chunks, int u) {   // (sequence, KV head, chunk)
+  const uint32_t b = static_cast<uint32_t>(u) / (Hkv * chunks), r = u - b * (Hkv * chunks), h = r / chunks;
+  return make_int3(b, h, r - h * chunks);
+}
+static __device__ __noinline__ uint32_t div_u32(uint32_t n, uint32_t d) { return n / d; }
+
 __device__ __forceinline__ Unit unit_at(const DecK& p, int u) {
-  if (p.Hkv * p.chunks != 1) return unit_of(p, u);
   Unit x;
   x.b = u;
   x.h = x.c = 0;
-  x.L = min(__ldg(p.seq_lens + u), p.max_seq_len);
+  if (p.Hkv * p.chunks != 1) {
+    const int3 at = unit_place(p.Hkv, p.chunks, u);
+    x.b = at.x;
+    x.h = at.y;
+    x.c = at.z;
+  }
+  x.L = min(__ldg(p.seq_lens + x.b), p.max_seq_len);
   x.lo = (p.kind == FA_SLIDING) ? max(0, x.L - p.window) : 0;
   x.t_first = x.lo / kTile;
   x.n = x.L > 0 ? (x.L - 1) / kTile + 1 - x.t_first : 0;
@@ -268,10 +280,52 @@ __device__ void merge_tree(const DecK& p, int u, const Unit& x, int nh, int head
   }
 }
 
+// The block-wide cut, for more sequences than a warp's.
+static __device__ __noinline__ bool cut_share_block(const DecK& p, int cta, int grid, Share* out) {   // out: shared memory
+  Share s;
+  const bool any = cut_share(p, cta, grid, s);
+  if (any) {
+    __syncthreads();
+    finish_share(cta, s);
+  }
+  if (threadIdx.x == 0) {
+    s.nct = 0;
+    *out = s;
+  }
+  __syncthreads();
+  return any;
+}
+
+// The current token's rows of (sequence b, KV head h) into their slot (one warp).
+template <int D>
+__device__ __noinline__ void store_now(const DecK& p, int b, int h, int lane) {
+  RowRegs<D> rk, rv;
+  const size_t src = (static_cast<size_t>(b) * p.Hkv + h) * D;
+  row_load<D>(rk, p.k_new + src, lane);
+  row_load<D>(rv, p.v_new + src, lane);
+  store_current<D, FA_KV_FP4>(p, rk, rv, h, __ldg(p.slots + b), lane);
+}
+
+// Sequences of length <= 0 get out = 0 and lse = -inf, and their row is still
+// stored; CTA `cta` of `ncta` writes the units u with u % ncta == cta.
+template <int D>
+__device__ __noinline__ void empty_units(const DecK& p, int cta, int ncta, int tid, int nthr) {
+#pragma unroll 1
+  for (int u = cta; u < p.units; u += ncta) {
+    const Unit x = unit_at(p, u);
+    if (x.L > 0) continue;
+    if (p.slots && x.c == 0 && tid < 32) store_now<D>(p, x.b, x.h, tid);
+    const int nh = min(8, p.g - x.c * 8);
+    const size_t head = static_cast<size_t>(x.b) * p.Hq + x.h * p.g + x.c * 8;
+#pragma unroll 1
+    for (int i = tid; i < nh * D / 8; i += nthr) *(reinterpret_cast<uint4*>(p.out + head * D) + i) = make_uint4(0u, 0u, 0u, 0u);
+    if (p.lse && tid < nh) p.lse[head + tid] = -INFINITY;
+  }
+}
+
 template <int D>
 __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, const int grid) {
   using C = F4Cfg<D>;
-  constexpr int KV = FA_KV_FP4;
   extern __shared__ __align__(128) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* empty = full + C::NSLOT;
@@ -282,19 +336,6 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
 
-  if (!p.early_metadata) griddep_wait();
-  griddep_launch_dependents();
-
-  Share sh;
-  const bool small = p.units <= kWarpUnits;
-  if (!(small ? cut_share_warp(p, cta, grid, sh) : cut_share(p, cta, grid, sh))) {
-    if (sh.ncta == 0 && cta == 0) {   // nothing visible anywhere: only empty outputs to write
-      griddep_wait();
-      zero_empty_units<D, KV>(p, 0, 1, threadIdx.x, blockDim.x);
-    }
-    return;
-  }
-  if (!small) sh.nct = 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NSLOT; ++s) {
       mbar_init(&full[s], 1);
@@ -302,14 +343,29 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
     }
     mbar_init(mbar_merge, 1);
     abort_flag = 0;
-    if (small) share = sh;
     fence_mbar_init();
   }
-  __syncthreads();
-  if (!small) {
-    finish_share(cta, sh);
-    if (threadIdx.x == 0) share = sh;   // read after the barriers of the first step
+  if (!p.early_metadata) griddep_wait();
+  griddep_launch_dependents();
+
+  Share sh;
+  const bool small = p.B <= kWarpSeqs;
+  bool any;
+  if (small) {
+    any = cut_share_warp(p, cta, grid, sh);
+  } else {
+    any = cut_share_block(p, cta, grid, &share);
+    sh = share;
   }
+  if (!any) {
+    if (sh.ncta == 0 && cta == 0) {   // nothing visible anywhere: only empty outputs to write
+      griddep_wait();
+      empty_units<D>(p, 0, 1, threadIdx.x, blockDim.x);
+    }
+    return;
+  }
+  if (small && threadIdx.x == 0) share = sh;
+  __syncthreads();
   const int u0 = sh.u0, p0 = sh.p0;
   const int s_beg = static_cast<int>(sh.s_beg), s_end = static_cast<int>(sh.s_end);   // T fits an int
 
@@ -328,11 +384,10 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
         // the CTA that reads the unit's last tile (it holds position L - 1)
         // stores the current token's rows first, so its own copy sees them
         const bool store_here = p.slots != nullptr && tz == x.t_first + x.n;
-        RowRegs<D> rk, rv;
         for (int k0 = ta; ok && k0 < tz; k0 += 32) {
           int pid = -1;
           if (k0 + lane < tz) {
-            pid = __ldg(bt + (one ? k0 + lane : static_cast<uint32_t>(k0 + lane) / p.tiles_per_page));
+            pid = __ldg(bt + (one ? k0 + lane : div_u32(k0 + lane, p.tiles_per_page)));
             if (pid < 0 || pid >= p.num_pages) {
               atomicOr(p.err, FA_DEV_ERR_PAGE);
               pid = -1;
@@ -340,15 +395,10 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
           }
           if (first) griddep_wait();   // from here on the slab is read
           first = false;
-          if (k0 == ta && store_here) {
-            const size_t src = (static_cast<size_t>(x.b) * p.Hkv + x.h) * D;
-            row_load<D>(rk, p.k_new + src, lane);
-            row_load<D>(rv, p.v_new + src, lane);
-          }
           for (int k = k0; k < min(k0 + 32, tz); k += C::NT) {
             const int ntl = min(C::NT, tz - k);
             if (store_here && k + ntl >= tz) {
-              store_current<D, KV>(p, rk, rv, x.h, __ldg(p.slots + x.b), lane);
+              store_now<D>(p, x.b, x.h, lane);
               // each lane orders its generic writes before the async-proxy
               // read of the tile that holds them
               fence_proxy_async_global();
@@ -361,9 +411,9 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
             const int tile = k + lane;
             const size_t row0 = mine && pg >= 0
                                     ? (static_cast<size_t>(pg) * p.Hkv + x.h) * p.page_size +
-                                          (one ? 0 : static_cast<uint32_t>(tile) % p.tiles_per_page) * kTile
+                                          (one ? 0 : tile - div_u32(tile, p.tiles_per_page) * p.tiles_per_page) * kTile
                                     : 0;
-#pragma unroll
+#pragma unroll 1
             for (int side = 0; side < 2; ++side, ++e) {
               const int st = e % C::NSLOT;
               uint8_t* dst = smem + st * C::SLOT;
@@ -415,7 +465,7 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
 
   // -------------------------------------------------------------- consumers
   griddep_wait();
-  zero_empty_units<D, KV>(p, cta, sh.ncta, threadIdx.x, C::NCW * 32);
+  empty_units<D>(p, cta, sh.ncta, threadIdx.x, C::NCW * 32);
   constexpr float P_OFF = 4.0f;    // weights reach 2^P_OFF against a base of their own tile's,
   constexpr float SLACK = 8.0f;    // and 2^(P_OFF + SLACK) against O's base before it is raised
   int e = 0, step = 0;
