@@ -75,7 +75,8 @@ static size_t slab_row_bytes(int kv_dtype, int D) {
 }
 
 // ----------------------------------------------------------------- planning
-// CTAs of a decode launch the device holds at once: two per SM, three in fp4.
+// Shares of a decode launch the device works on at once: two per SM (a CTA
+// each), three in fp4 (one CTA).
 static long long decode_slots(const fa_cache* c) { return (c->kv_dtype == FA_KV_FP4 ? 3LL : 2LL) * sm_count(); }
 
 DecodePlan plan_decode(const fa_cache* c, int layer, int B, int max_seq_len, long long max_cta) {
@@ -103,6 +104,7 @@ DecodePlan plan_decode(const fa_cache* c, int layer, int B, int max_seq_len, lon
   if (n > slots) n = slots;
   if (n < 1) n = 1;
   p.ncta = static_cast<int>(n);
+  if (fp4) p.blocks = static_cast<int>(std::min(n, std::max(1LL, slots / 3)));
   if (p.ncta > 1) {
     const size_t rows = static_cast<size_t>(p.ncta + p.units) * 8;   // partial slots x heads
     // arrival counters: one per unit; fp4: one per partial slot
@@ -571,8 +573,9 @@ static void plan_decode_layers(const fa_cache* c, int n, const int32_t* layers, 
   const long long slots = decode_slots(c);
   for (int i = 0; i < n; ++i) {
     long long share = tot > 0 ? slots * tb[i] / tot : 1;
+    if (c->kv_dtype == FA_KV_FP4) share = std::max(share / 3, 1LL) * 3;   // whole CTAs
     if (share < 1) share = 1;
-    if (share < p[i].ncta) p[i] = plan_decode(c, layers[i], B, max_seq_len, share);
+    if (share < p[i].ncta || c->kv_dtype == FA_KV_FP4) p[i] = plan_decode(c, layers[i], B, max_seq_len, share);
   }
 }
 }  // namespace fa

@@ -29,6 +29,7 @@ struct DecK {
   unsigned int* err;
   int B, Hq, Hkv, g, chunks, kind, window, page_size, tiles_per_page, num_pages, max_pages_per_seq;
   int max_seq_len, units, min_tiles, early_metadata;
+  int shares;         // fp4: shares the work may be cut into
   float scale_log2;   // sm_scale * log2(e)
 };
 
@@ -108,7 +109,6 @@ struct Share {
   long long s_beg, s_end;
   int T, ncta, kper;   // kper: CTAs per unit of the unit-aligned cut (0: concatenated cut)
   int u0, p0;
-  int cf, nct;         // the whole-unit cut: the unit's first CTA and its CTAs (nct 0: another cut)
 };
 struct ShareWork {   // shared memory of the cut
   int scan[8], mm[16];
@@ -215,140 +215,6 @@ __device__ __forceinline__ void finish_share(int cta, Share& s) {
   }
 }
 
-// floor(c * T / n) for c <= n, in 32 bits: with T = q n + r it is c q + floor(c r / n).
-__device__ __forceinline__ uint32_t share_begin(uint32_t c, uint32_t n, uint32_t q, uint32_t r) {
-  return c * q + (r ? c * r / n : 0u);
-}
-
-// A cut for up to kWarpSeqs sequences, found by every warp for itself from
-// shuffles: no block barrier, one round of loads up to 32 sequences, and 32-bit
-// divisions only (a 64-bit one costs some 0.3 us on the way to the first copy).
-// Where it can, it gives every CTA a part of one unit only: unit u is cut into
-// ceil(n_u / Q) equal parts, Q the smallest quota found for which the launch's
-// CTAs suffice.  A CTA that crosses from one unit to the next pays a second query
-// load, epilogue and merge in the middle of its stream, which costs more than
-// the uneven parts as long as Q stays below 3/2 of the even share; past that
-// (many units, few CTAs for each) the lists are laid end to end as in
-// cut_share.  Returns false where cut_share does; a true share is complete (no
-// finish_share).
-//
-// A sequence's units (KV head x chunk) are all alike, so a lane looks at
-// sequences only.  Past 32 of them the loops stay rolled and read the lengths
-// again (from L1): the whole kernel has to come through the instruction cache
-// once per launch, and unrolled copies cost short launches more than the loads.
-constexpr int kWarpSeqs = 256;
-__device__ __forceinline__ bool cut_share_warp(const DecK& p, int cta, int grid, Share& s) {
-  const int lane = threadIdx.x & 31;
-  const int per = (p.B + 31) / 32;       // sequences of a lane: [lane * per, ...)
-  const int hc = p.Hkv * p.chunks;       // units of a sequence
-  bool past = false;
-  auto tiles = [&](int i) {              // of each unit of the lane's sequence i
-    const int b = lane * per + i;
-    int len = b < p.B ? __ldg(p.seq_lens + b) : 0;
-    past |= len > p.max_seq_len;
-    len = min(len, p.max_seq_len);
-    if (len <= 0) return 0;
-    const uint32_t lo = p.kind == FA_SLIDING ? max(0, len - p.window) : 0;
-    return static_cast<int>(static_cast<uint32_t>(len - 1) / kTile + 1 - lo / kTile);
-  };
-  auto scan = [&](int v) {               // inclusive, over the lanes
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += t;
-    }
-    return v;
-  };
-  const int n0 = tiles(0);
-  int sum = n0;
-#pragma unroll 1
-  for (int i = 1; i < per; ++i) sum += tiles(i);
-  if (past && cta == 0 && threadIdx.x < 32) atomicOr(p.err, FA_DEV_ERR_BOUND);
-  sum *= hc;
-  const int incl = scan(sum);
-  const int T = __shfl_sync(0xffffffffu, incl, 31);
-  s.T = T;
-  s.kper = s.nct = s.cf = 0;
-  s.ncta = 0;
-  if (T == 0) return false;
-  const uint32_t even = max((static_cast<uint32_t>(T) + grid - 1) / grid, static_cast<uint32_t>(p.min_tiles));
-  int ks = 0, total = 0;
-  uint32_t Q = even;
-  float rq;
-  auto parts = [&](int n) {              // ceil(n / Q): the fp32 estimate is put right by one either way
-    const int m = n + static_cast<int>(Q) - 1;
-    int c = static_cast<int>(static_cast<float>(m) * rq);
-    c -= c * static_cast<int>(Q) > m;
-    c += (c + 1) * static_cast<int>(Q) <= m;
-    return c;
-  };
-  while (true) {
-    rq = __frcp_rn(static_cast<float>(Q));
-    ks = parts(n0);
-#pragma unroll 1
-    for (int i = 1; i < per; ++i) ks += parts(tiles(i));
-    ks *= hc;
-    total = __reduce_add_sync(0xffffffffu, ks);
-    if (total <= grid || 2 * Q >= 3 * even) break;
-    // in proportion, as far as the fractions of a part allow
-    Q = max(Q + 1, static_cast<uint32_t>(static_cast<float>(Q) * total / grid));
-  }
-  const bool whole = total <= grid;
-  const int ncta = whole ? total : min(grid, static_cast<int>((static_cast<uint32_t>(T) + p.min_tiles - 1) / p.min_tiles));
-  s.ncta = ncta;
-  if (cta >= ncta) return false;
-  const uint32_t q = static_cast<uint32_t>(T) / ncta, r = T - q * ncta;
-  const int s_beg = share_begin(cta, ncta, q, r);
-  int b0 = -1, p0 = 0, un = 0, k0 = 0, c0 = 0, P = incl - sum, K = scan(ks) - ks;
-#pragma unroll 1
-  for (int i = 0; i < per; ++i) {
-    const int n = i == 0 ? n0 : tiles(i), k = parts(n);
-    if (whole ? K <= cta && cta < K + k * hc : P <= s_beg && s_beg < P + n * hc) {
-      b0 = lane * per + i;
-      p0 = P;
-      un = n;
-      k0 = k;
-      c0 = K;
-    }
-    P += n * hc;
-    K += k * hc;
-  }
-  const int src = __ffs(__ballot_sync(0xffffffffu, b0 >= 0)) - 1;
-  b0 = __shfl_sync(0xffffffffu, b0, src);
-  p0 = __shfl_sync(0xffffffffu, p0, src);
-  un = __shfl_sync(0xffffffffu, un, src);
-  if (whole) {
-    c0 = __shfl_sync(0xffffffffu, c0, src);
-    k0 = __shfl_sync(0xffffffffu, k0, src);
-    const int j = static_cast<uint32_t>(cta - c0) / static_cast<uint32_t>(k0);   // unit in the sequence
-    s.u0 = b0 * hc + j;
-    s.p0 = p0 + j * un;
-    s.cf = c0 + j * k0;
-    s.nct = k0;
-    const uint32_t i = cta - s.cf, uq = static_cast<uint32_t>(un) / k0, ur = un - uq * k0;
-    s.s_beg = s.p0 + share_begin(i, k0, uq, ur);
-    s.s_end = s.p0 + share_begin(i + 1, k0, uq, ur);
-  } else {
-    const int j = static_cast<uint32_t>(s_beg - p0) / static_cast<uint32_t>(un);
-    s.u0 = b0 * hc + j;
-    s.p0 = p0 + j * un;
-    s.s_beg = s_beg;
-    s.s_end = share_begin(cta + 1, ncta, q, r);
-  }
-  return true;
-}
-
-// The CTA that owns tile g of T cut over n: cta_of without its 64-bit division.
-// The quotient is estimated in fp32 and put right against share_begin.
-static __device__ __noinline__ int cta_of_fast(uint32_t g, uint32_t n, uint32_t T) {
-  const uint32_t q = T / n, r = T - q * n;
-  int c = static_cast<int>(__fdividef(static_cast<float>(g) * static_cast<float>(n), static_cast<float>(T)));
-  c = max(0, min(c, static_cast<int>(n) - 1));
-  while (c > 0 && share_begin(c, n, q, r) > g) --c;
-  while (c + 1 < static_cast<int>(n) && share_begin(c + 1, n, q, r) <= g) ++c;
-  return c;
-}
-
 // The current token's K and V rows of (sequence b, KV head h) into slot `slot`
 // (one warp; slot < 0 skips, a slot past the pool is reported).
 template <int D, int KV>
@@ -424,6 +290,7 @@ inline DecK make_deck(const DecodeArgs& a) {
   k.units = a.plan.units;
   k.min_tiles = a.plan.min_tiles;
   k.early_metadata = a.early_metadata;
+  k.shares = a.plan.ncta;
   k.scale_log2 = a.sm_scale * 1.4426950408889634f;
   return k;
 }

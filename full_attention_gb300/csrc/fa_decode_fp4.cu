@@ -47,8 +47,9 @@ struct F4Cfg {
   static constexpr int SC_BYTES = NT * kTile * 4;      // one step's K (or V) row scales
   static constexpr int SLOT = NT * TILE_BYTES + 2 * SC_BYTES;   // rows; in K slots also both row scales
   static constexpr int NSLOT = D == 256 ? 6 : 3;
-  static constexpr int CTAS = 3;                       // per SM
-  static constexpr int NTHR = (NCW + 1) * 32;
+  static constexpr int GROUPS = 3;                     // shares a CTA works on side by side
+  static constexpr int GTHR = (NCW + 1) * 32;          // threads of a group
+  static constexpr int NTHR = GROUPS * GTHR;
   static constexpr int NJ = 8;                         // loads of NW words a lane makes per row
   static constexpr int MT = D / 4 / 16;                // m16 tiles of O^T per warp
   static constexpr int P_HEAD = 48;                    // bytes per head of a tile's weights (16 f16 + padding)
@@ -58,12 +59,12 @@ struct F4Cfg {
   static constexpr int OFF_MW = OFF_P + 2 * NT * P_TILE;   // [2][8 heads][NT] tile bases
   static constexpr int OFF_FLAG = OFF_MW + 2 * 8 * NT * 4; // [2][NT] the tile's base is its own
   static constexpr int OFF_ML = OFF_FLAG + 2 * NT * 4;     // [NCW][8] (m, l)
-  static constexpr int OFF_W = OFF_ML + NCW * 8 * 8;       // merge weights [4][8], then [8] (M, m, L, 0)
-  static constexpr int OFF_BAR = OFF_W + (4 * 8 + 4 * 8) * 4;
-  static constexpr int SMEM = OFF_BAR + (2 * NSLOT + 1) * 8;
+  static constexpr int OFF_BAR = OFF_ML + NCW * 8 * 8;
+  static constexpr int GSMEM = (OFF_BAR + (2 * NSLOT + 1) * 8 + 127) / 128 * 128;   // a group's
+  static constexpr int SMEM = GROUPS * GSMEM;
   static_assert(SLOT % 128 == 0, "slot alignment");
-  static_assert(NSLOT * SLOT >= 3 * 8 * D * 4, "the ring holds three partials");
-  static_assert(CTAS * (SMEM + 1024 + 256) <= 228 * 1024, "CTAs per SM");
+  static_assert(NSLOT * SLOT >= 3 * 8 * D * 4 + 8 * 16, "the ring holds three partials, or one and its (M, m, L)");
+  static_assert(SMEM + 256 <= 227 * 1024, "shared memory");
 };
 
 // "No score yet": finite, so that differences against it are never NaN.
@@ -150,150 +151,271 @@ __device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
   }
 }
 
-// Combine the partial rows of unit u that its nct CTAs cf .. leave, as a tree of
-// groups of four in CTA order: the last CTA of a group to arrive merges the
-// group's partials and goes on to the next level, the others are done.  (One
-// CTA merging all of a long sequence's partials alone, 57 of 16 KB with 8
-// sequences on 152 SMs, took 32 us after the last byte had been read; four
-// levels of at most four take 2 us each, most of them before that.)  The
-// order of the sums depends on the tree only, so results do not depend on who
-// arrives last.  Run by the 128 consumer threads once the CTA's own partial is
-// written; i is its index in the unit, wbuf 4 * 8 + 32 floats.
+// floor(c * T / n) for c <= n, in 32 bits: with T = q n + r it is c q + floor(c r / n).
+__device__ __forceinline__ uint32_t share_begin(uint32_t c, uint32_t n, uint32_t q, uint32_t r) {
+  return c * q + (r ? c * r / n : 0u);
+}
+
+// One group's share of the concatenated tile lists: tiles [s_beg, s_end) of the
+// T, starting in unit u0, whose first tile is p0.
+struct F4Share {
+  int s_beg, s_end, T, u0, p0;
+  int n, i, nb;        // shares in use, this one, CTAs in use
+  int sb, se;          // the CTA's shares
+  int cf, nct;         // the whole-unit cut: the unit's first share and its shares (nct 0: laid end to end)
+};
+
+// The cut, found by one warp from shuffles: one round of loads up to 32
+// sequences, and 32-bit divisions only (a 64-bit one costs some 0.3 us on the
+// way to the first copy).  Where it can, it gives every
+// share a part of one unit only: unit u is cut into ceil(n_u / Q) equal parts, Q
+// the smallest quota found for which the launch's shares suffice.  A share that
+// crosses from one unit to the next pays a second query load, epilogue and merge
+// in the middle of its stream, which costs more than the uneven parts as long as
+// Q stays below 3/2 of the even share; past that (many units, few shares for
+// each) all lists are laid end to end and cut evenly.  The shares go to the CTAs
+// evenly, in order.  False: nothing to do for this group; s.n is set all the same.
+//
+// A sequence's units (KV head x chunk) are all alike, so a lane looks at
+// sequences only.  Past 128 of them the loops stay rolled and read the lengths
+// again (from L1): the whole kernel has to come through the instruction cache
+// once per launch, and unrolled copies cost short launches more than the loads.
+__device__ __forceinline__ bool cut_share_warp(const DecK& p, int cta, int nblk, int group, F4Share& s) {
+  const int lane = threadIdx.x & 31;
+  const int per = (p.B + 31) / 32;       // sequences of a lane: [lane * per, ...)
+  const int hc = p.Hkv * p.chunks;       // units of a sequence
+  bool past = false;
+  auto tiles = [&](int i) {              // of each unit of the lane's sequence i
+    const int b = lane * per + i;
+    int len = b < p.B ? __ldg(p.seq_lens + b) : 0;
+    past |= len > p.max_seq_len;
+    len = min(len, p.max_seq_len);
+    if (len <= 0) return 0;
+    const uint32_t lo = p.kind == FA_SLIDING ? max(0, len - p.window) : 0;
+    return static_cast<int>(static_cast<uint32_t>(len - 1) / kTile + 1 - lo / kTile);
+  };
+  auto scan = [&](int v) {               // inclusive, over the lanes
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += t;
+    }
+    return v;
+  };
+  int n4[4];                             // the first four stay in registers
+#pragma unroll
+  for (int i = 0; i < 4; ++i) n4[i] = i < per ? tiles(i) : 0;
+  int sum = n4[0] + n4[1] + n4[2] + n4[3], some = (n4[0] > 0) + (n4[1] > 0) + (n4[2] > 0) + (n4[3] > 0);
+#pragma unroll 1
+  for (int i = 4; i < per; ++i) {
+    const int n = tiles(i);
+    sum += n;
+    some += n > 0;
+  }
+  if (past && cta == 0 && group == 0) atomicOr(p.err, FA_DEV_ERR_BOUND);
+  sum *= hc;
+  const int incl = scan(sum);
+  const int T = __shfl_sync(0xffffffffu, incl, 31);
+  s.T = T;
+  s.nct = s.cf = s.n = 0;
+  if (T == 0) return false;
+  const int grid = p.shares;
+  const uint32_t even = max((static_cast<uint32_t>(T) + grid - 1) / grid, static_cast<uint32_t>(p.min_tiles));
+  int ks = 0, total = __reduce_add_sync(0xffffffffu, some * hc);
+  const bool few = total <= grid;        // else no whole-unit cut: there are more units than shares
+  uint32_t Q = even;
+  float rq;
+  auto parts = [&](int n) {              // ceil(n / Q): the fp32 estimate is put right by one either way
+    const int m = n + static_cast<int>(Q) - 1;
+    int c = static_cast<int>(static_cast<float>(m) * rq);
+    c -= c * static_cast<int>(Q) > m;
+    c += (c + 1) * static_cast<int>(Q) <= m;
+    return c;
+  };
+  while (few) {
+    rq = __frcp_rn(static_cast<float>(Q));
+    ks = parts(n4[0]) + parts(n4[1]) + parts(n4[2]) + parts(n4[3]);
+#pragma unroll 1
+    for (int i = 4; i < per; ++i) ks += parts(tiles(i));
+    ks *= hc;
+    total = __reduce_add_sync(0xffffffffu, ks);
+    if (total <= grid || 2 * Q >= 3 * even) break;
+    // in proportion, as far as the fractions of a part allow
+    Q = max(Q + 1, static_cast<uint32_t>(static_cast<float>(Q) * total / grid));
+  }
+  const bool whole = total <= grid;
+  const int ncta = whole ? total : min(grid, static_cast<int>((static_cast<uint32_t>(T) + p.min_tiles - 1) / p.min_tiles));
+  s.n = ncta;
+  // as few CTAs as the fullest one allows: fewer units lie across two of them
+  const uint32_t most = (static_cast<uint32_t>(ncta) + nblk - 1) / nblk;
+  const uint32_t nb = s.nb = (ncta + most - 1) / most, bq = static_cast<uint32_t>(ncta) / nb, br = ncta - bq * nb;
+  if (cta >= s.nb) return false;
+  s.sb = share_begin(cta, nb, bq, br);
+  s.se = share_begin(cta + 1, nb, bq, br);
+  const int me = s.i = s.sb + group;
+  if (me >= s.se) return false;
+  const uint32_t q = static_cast<uint32_t>(T) / ncta, r = T - q * ncta;
+  const int s_beg = share_begin(me, ncta, q, r);
+  int b0 = -1, p0 = 0, un = 0, k0 = 0, c0 = 0, P = incl - sum, K = scan(ks) - ks;
+  auto look = [&](int i, int n) {
+    const int k = whole ? parts(n) : 0;
+    if (whole ? K <= me && me < K + k * hc : P <= s_beg && s_beg < P + n * hc) {
+      b0 = lane * per + i;
+      p0 = P;
+      un = n;
+      k0 = k;
+      c0 = K;
+    }
+    P += n * hc;
+    K += k * hc;
+  };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) look(i, n4[i]);
+#pragma unroll 1
+  for (int i = 4; i < per; ++i) look(i, tiles(i));
+  const int src = __ffs(__ballot_sync(0xffffffffu, b0 >= 0)) - 1;
+  b0 = __shfl_sync(0xffffffffu, b0, src);
+  p0 = __shfl_sync(0xffffffffu, p0, src);
+  un = __shfl_sync(0xffffffffu, un, src);
+  if (whole) {
+    c0 = __shfl_sync(0xffffffffu, c0, src);
+    k0 = __shfl_sync(0xffffffffu, k0, src);
+    const int j = static_cast<uint32_t>(me - c0) / static_cast<uint32_t>(k0);   // unit in the sequence
+    s.u0 = b0 * hc + j;
+    s.p0 = p0 + j * un;
+    s.cf = c0 + j * k0;
+    s.nct = k0;
+    const uint32_t i = me - s.cf, uq = static_cast<uint32_t>(un) / k0, ur = un - uq * k0;
+    s.s_beg = s.p0 + share_begin(i, k0, uq, ur);
+    s.s_end = s.p0 + share_begin(i + 1, k0, uq, ur);
+  } else {
+    const int j = static_cast<uint32_t>(s_beg - p0) / static_cast<uint32_t>(un);
+    s.u0 = b0 * hc + j;
+    s.p0 = p0 + j * un;
+    s.s_beg = s_beg;
+    s.s_end = share_begin(me + 1, ncta, q, r);
+  }
+  return true;
+}
+
+// The part that owns item g of T cut over n: cta_of without its 64-bit division.
+// The quotient is estimated in fp32 and put right against share_begin.
+static __device__ __noinline__ int part_of(uint32_t g, uint32_t n, uint32_t T) {
+  const uint32_t q = T / n, r = T - q * n;
+  int c = static_cast<int>(__fdividef(static_cast<float>(g) * static_cast<float>(n), static_cast<float>(T)));
+  c = max(0, min(c, static_cast<int>(n) - 1));
+  while (c > 0 && share_begin(c, n, q, r) > g) --c;
+  while (c + 1 < static_cast<int>(n) && share_begin(c + 1, n, q, r) <= g) ++c;
+  return c;
+}
+
+// Combine the partials that n CTAs (or shares) have of one unit, as a tree of
+// groups of four in order: the last of a group to arrive merges the group's
+// partials and goes on to the next level; false: someone else does.  (One CTA
+// merging all of a long sequence's partials alone, 57 of 16 KB with 8 sequences
+// on 152 SMs, took 32 us after the last byte had been read.)  A partial lies in
+// memory lane by lane as the registers do, so the last to arrive keeps its own
+// and adds the others to it: (own + neighbour) + (the other two), each sum of two
+// products rounded alike either way round, so results do not depend on who
+// arrives last.  Run by the 128 consumer threads of a group; slot0: the slot of
+// the unit's first partial, i: this one's place; o, and Mo, m, l (of head gid).
 template <int D>
-__device__ void merge_tree(const DecK& p, int u, const Unit& x, int nh, int head0, int cf, int nct, int i, float* wbuf,
-                           volatile int* sh_last, uint8_t* ring, uint64_t* bar, uint32_t& phase) {
-  constexpr int ITEMS = 8 * (D / 4) / 128;   // float4 pieces of a partial per thread
-  constexpr int HPI = 8 / ITEMS;             // heads a round of 128 pieces covers
-  const int tid = threadIdx.x;
-  int n = nct, st = 1;
-  for (int level = 0;; ++level, i >>= 2, st *= 4) {
-    const int first = i & ~3, cnt = min(4, n - first);
-    const size_t base = static_cast<size_t>(cf) + u + static_cast<size_t>(first) * st;   // slot of the group's first partial
+__device__ __forceinline__ bool merge_tree(const DecK& p, size_t slot0, int n, int i, float (&o)[F4Cfg<D>::MT][4], float& Mo,
+                                           float& m, float& l, volatile int* last, uint8_t* ring, uint64_t* bar,
+                                           uint32_t& phase, int tid, int bid) {
+  using C = F4Cfg<D>;
+  constexpr int PART = 8 * D * 4;
+  const int gid = (tid & 31) >> 2, tig = tid & 3;
+  int st = 1;
+#pragma unroll 1
+  for (int level = 0; n > 1; ++level, i >>= 2, st *= 4) {
+    const int first = i & ~3, mine = i & 3, cnt = min(4, n - first);
+    const size_t base = slot0 + static_cast<size_t>(first) * st;   // slot of the group's first partial
     n = (n + 3) >> 2;
-    if (cnt == 1) continue;   // alone in its group (others exist: n > 1): the partial stands for the group
+    if (cnt == 1) continue;   // alone in its group (others exist: n > 1)
+    {
+      const size_t slot = base + static_cast<size_t>(mine) * st;
+      float4* dst = reinterpret_cast<float4*>(p.o_part + slot * 8 * D) + tid;
+#pragma unroll
+      for (int j = 0; j < C::MT; ++j) dst[j * 128] = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
+      if (tid < 32 && tig == 0) reinterpret_cast<float4*>(p.ml_part)[slot * 8 + gid] = make_float4(Mo, m, l, 0.f);
+    }
     // arrive: the barrier orders the CTA's partial writes before thread 0's
     // release/acquire add, which publishes them and, for the last arrival,
     // makes the other CTAs' rows visible.  A group's counter lies in its own
     // slots: at level l its partials are 4^l slots apart, and the offset l
     // (past 3, l + 1) keeps the levels' counters apart.
-    named_bar_sync(1, 128);
+    named_bar_sync(bid, 128);
     if (tid == 0) {
       int* c = p.counters + base + level + (level > 3 ? 1 : 0);
       const int old = atom_add_acq_rel_gpu(c, 1);
       if (old == cnt - 1) atomicExch(c, 0);   // zero for the next call
       else if (old >= cnt) atomicOr(p.err, FA_DEV_ERR_WORKSPACE);
-      *sh_last = old == cnt - 1;
+      *last = old == cnt - 1;
+      if (old == cnt - 1 && ring) {
+        // the others (three at most) by bulk copies into the ring, idle by now
+        fence_proxy_async_global();   // the other CTAs' rows, seen through the acquire, for the bulk copies
+        fence_proxy_async_smem();     // the ring's generic reads and zeroed scales before them
+        mbar_arrive_expect_tx(bar, (cnt - 1) * PART);
+        for (int k = 0; k < cnt; ++k)
+          if (k != mine)
+            bulk_load(ring + (k - (k > mine)) * PART, p.o_part + (base + static_cast<size_t>(k) * st) * 8 * D, PART, bar);
+      }
     }
-    named_bar_sync(1, 128);
-    if (!*sh_last) return;
-    // the last partial by loads, the others (three at most) by bulk copies into
-    // the ring, idle by now, or one after the other by loads
-    constexpr int PART = 8 * D * 4;
-    if (ring && tid == 0) {
-      fence_proxy_async_global();   // the other CTAs' rows, seen through the acquire, for the bulk copies
-      fence_proxy_async_smem();     // the ring's generic reads and zeroed scales before them
-      mbar_arrive_expect_tx(bar, (cnt - 1) * nh * D * 4);
-      for (int k = 0; k < cnt - 1; ++k)
-        bulk_load(ring + k * PART, p.o_part + (base + static_cast<size_t>(k) * st) * 8 * D, nh * D * 4, bar);
-    }
-    // the group's last partial by loads, issued before its weight is known
-    float4 acc[ITEMS];
-    auto part = [&](int k) {
-      return reinterpret_cast<const float4*>(p.o_part + (base + static_cast<size_t>(k) * st) * 8 * D) + tid;
-    };
+    named_bar_sync(bid, 128);
+    if (!*last) return false;
+    float4 v[4];
 #pragma unroll
-    for (int j = 0; j < ITEMS; ++j)
-      acc[j] = j * HPI < nh ? __ldcg(part(cnt - 1) + j * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
-    if (tid < 32) {   // lane: partial k = tid / 8, head tid % 8
-      const int k = tid >> 3;
-      float4 v = make_float4(kNoScore, kNoScore, 0.f, 0.f);
-      if (k < cnt) v = __ldcg(reinterpret_cast<const float4*>(p.ml_part) + (base + static_cast<size_t>(k) * st) * 8 + (tid & 7));
-      float M = v.x, m = v.y;
-      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 8));
-      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-      float L = v.z * ex2(v.y - m);
-      L += __shfl_xor_sync(0xffffffffu, L, 8);
-      L += __shfl_xor_sync(0xffffffffu, L, 16);
-      wbuf[tid] = ex2(v.x - M);
-      if (k == 0) *reinterpret_cast<float4*>(wbuf + 32 + 4 * tid) = make_float4(M, m, L, 0.f);
-    }
-    named_bar_sync(1, 128);
-    auto weight = [&](int k, int j) { return wbuf[k * 8 + j * HPI + tid / (128 / HPI)]; };
+    for (int k = 0; k < 4; ++k)
+      v[k] = k < cnt ? __ldcg(reinterpret_cast<const float4*>(p.ml_part) + (base + static_cast<size_t>(k) * st) * 8 + gid)
+                     : make_float4(kNoScore, kNoScore, 0.f, 0.f);
+    Mo = fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x));
+    m = fmaxf(fmaxf(v[0].y, v[1].y), fmaxf(v[2].y, v[3].y));
+    l = 0.f;
+    float w[4];
 #pragma unroll
-    for (int j = 0; j < ITEMS; ++j) {
-      const float w = weight(cnt - 1, j);
-      acc[j].x *= w;
-      acc[j].y *= w;
-      acc[j].z *= w;
-      acc[j].w *= w;
+    for (int k = 0; k < 4; ++k) {
+      l += v[k].z * ex2(v[k].y - m);
+      w[k] = ex2(v[k].x - Mo);
     }
-    auto add = [&](int k, int j, float4 v) {
-      const float w = weight(k, j);
-      acc[j].x += w * v.x;
-      acc[j].y += w * v.y;
-      acc[j].z += w * v.z;
-      acc[j].w += w * v.w;
+    const int kq = mine ^ 1, kr = mine < 2 ? 2 : 0;   // the neighbour; the other two
+    const float ow = mine == 0 ? w[0] : mine == 1 ? w[1] : mine == 2 ? w[2] : w[3];
+    const float qw = mine == 0 ? w[1] : mine == 1 ? w[0] : mine == 2 ? w[3] : w[2];
+    const float rw = mine < 2 ? w[2] : w[0], sw = mine < 2 ? w[3] : w[1];
+    auto head2 = [&](float x, float (&y)[2]) {
+      y[0] = __shfl_sync(0xffffffffu, x, 8 * tig);
+      y[1] = __shfl_sync(0xffffffffu, x, 8 * tig + 4);
     };
+    float wo[2], wq[2], wr[2], ws[2];
+    head2(ow, wo);
+    head2(qw, wq);
+    head2(rw, wr);
+    head2(sw, ws);
     if (ring) {
-      if (!mbar_wait(bar, phase)) *sh_last = 2;
+      if (!mbar_wait(bar, phase)) *last = 2;
       phase ^= 1;
-      named_bar_sync(1, 128);
-      if (*sh_last == 2) {   // a copy that did not land in time: everyone leaves
+      named_bar_sync(bid, 128);
+      if (*last == 2) {   // a copy that did not land in time: everyone leaves
         if (tid == 0) atomicOr(p.err, FA_DEV_ERR_TIMEOUT);
-        return;
+        return false;
       }
-      for (int k = 0; k < cnt - 1; ++k) {
-        const float4* src = reinterpret_cast<const float4*>(ring + k * PART) + tid;
-#pragma unroll
-        for (int j = 0; j < ITEMS; ++j)
-          if (j * HPI < nh) add(k, j, src[j * 128]);
-      }
-    } else {
-      for (int k = 0; k < cnt - 1; ++k)
-#pragma unroll
-        for (int j = 0; j < ITEMS; ++j)
-          if (j * HPI < nh) add(k, j, __ldcg(part(k) + j * 128));
     }
-    if (n == 1) {
+    auto part = [&](int k, int j) {   // piece j of partial k
+      if (k >= cnt) return make_float4(0.f, 0.f, 0.f, 0.f);
+      if (ring) return reinterpret_cast<const float4*>(ring + (k - (k > mine)) * PART)[j * 128 + tid];
+      return __ldcg(reinterpret_cast<const float4*>(p.o_part + (base + static_cast<size_t>(k) * st) * 8 * D) + j * 128 + tid);
+    };
+    auto two = [](float a, float wa, float b, float wb) { return __fadd_rn(__fmul_rn(a, wa), __fmul_rn(b, wb)); };
 #pragma unroll
-      for (int j = 0; j < ITEMS; ++j) {
-        const int hh = j * HPI + tid / (128 / HPI), d = (tid % (128 / HPI)) * 4;
-        if (hh >= nh) continue;
-        const float4 fm = *reinterpret_cast<const float4*>(wbuf + 32 + 4 * hh);
-        const float f = ex2(fm.x - fm.y) / fm.z;
-        *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(x.b) * p.Hq + head0 + hh) * D + d) =
-            make_uint2(pack_bf16x2(acc[j].x * f, acc[j].y * f), pack_bf16x2(acc[j].z * f, acc[j].w * f));
-      }
-      if (p.lse && tid < nh) {
-        const float4 fm = *reinterpret_cast<const float4*>(wbuf + 32 + 4 * tid);
-        p.lse[static_cast<size_t>(x.b) * p.Hq + head0 + tid] = (fm.y + __log2f(fm.z)) * 0.69314718055994531f;
-      }
-      named_bar_sync(1, 128);   // the scratch is free again
-      return;
+    for (int j = 0; j < C::MT; ++j) {
+      const float4 q = part(kq, j), r = part(kr, j), s = part(kr + 1, j);
+      o[j][0] = __fadd_rn(two(o[j][0], wo[0], q.x, wq[0]), two(r.x, wr[0], s.x, ws[0]));
+      o[j][1] = __fadd_rn(two(o[j][1], wo[1], q.y, wq[1]), two(r.y, wr[1], s.y, ws[1]));
+      o[j][2] = __fadd_rn(two(o[j][2], wo[0], q.z, wq[0]), two(r.z, wr[0], s.z, ws[0]));
+      o[j][3] = __fadd_rn(two(o[j][3], wo[1], q.w, wq[1]), two(r.w, wr[1], s.w, ws[1]));
     }
-    float4* dst = reinterpret_cast<float4*>(p.o_part + base * 8 * D) + tid;
-#pragma unroll
-    for (int j = 0; j < ITEMS; ++j) dst[j * 128] = acc[j];
-    if (tid < 8) reinterpret_cast<float4*>(p.ml_part)[base * 8 + tid] = *reinterpret_cast<const float4*>(wbuf + 32 + 4 * tid);
   }
-}
-
-// The block-wide cut, for more sequences than a warp's.
-static __device__ __noinline__ bool cut_share_block(const DecK& p, int cta, int grid, Share* out) {   // out: shared memory
-  Share s;
-  const bool any = cut_share(p, cta, grid, s);
-  if (any) {
-    __syncthreads();
-    finish_share(cta, s);
-  }
-  if (threadIdx.x == 0) {
-    s.nct = 0;
-    *out = s;
-  }
-  __syncthreads();
-  return any;
+  return true;
 }
 
 // The current token's rows of (sequence b, KV head h) into their slot (one warp).
@@ -324,50 +446,56 @@ __device__ __noinline__ void empty_units(const DecK& p, int cta, int ncta, int t
 }
 
 template <int D>
-__device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, const int grid) {
+__device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, const int nblk) {
   using C = F4Cfg<D>;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem_all[];
+  __shared__ int abort_flags[C::GROUPS], lasts[C::GROUPS], local_cnt[C::GROUPS];
+  __shared__ F4Share shares[C::GROUPS];   // what the epilogue needs of the cut, out of the registers meanwhile
+
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int group = wid / (C::NCW + 1), warp = wid - group * (C::NCW + 1);   // a group: 4 consumer warps, a producer
+  const int tid = warp * 32 + lane;
+  const int gid = lane >> 2, tig = lane & 3;
+  uint8_t* smem = smem_all + group * C::GSMEM;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* empty = full + C::NSLOT;
   uint64_t* mbar_merge = empty + C::NSLOT;
-  __shared__ int abort_flag, sh_last;
-  __shared__ Share share;   // what the epilogue needs of the cut, out of the registers meanwhile
+  int& abort_flag = abort_flags[group];
+  F4Share& share = shares[group];
+  const int bid = 1 + group;   // the barrier of the group's consumers
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int gid = lane >> 2, tig = lane & 3;
-
-  if (threadIdx.x == 0) {
+  if (tid == 0) {
     for (int s = 0; s < C::NSLOT; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], C::NCW);
     }
     mbar_init(mbar_merge, 1);
     abort_flag = 0;
+    local_cnt[group] = 0;
     fence_mbar_init();
   }
+  __syncthreads();
   if (!p.early_metadata) griddep_wait();
   griddep_launch_dependents();
 
-  Share sh;
-  const bool small = p.B <= kWarpSeqs;
-  bool any;
-  if (small) {
-    any = cut_share_warp(p, cta, grid, sh);
-  } else {
-    any = cut_share_block(p, cta, grid, &share);
-    sh = share;
+  // one warp of a group finds its share: all fifteen warps of the CTA at it
+  // would share the issue slots, 1 us or more on the way to the first copy
+  if (warp == C::NCW) {
+    F4Share sh;
+    const bool any = cut_share_warp(p, cta, nblk, group, sh);
+    if (!any) sh.i = -1;
+    if (lane == 0) share = sh;
   }
-  if (!any) {
-    if (sh.ncta == 0 && cta == 0) {   // nothing visible anywhere: only empty outputs to write
+  named_bar_sync(1 + C::GROUPS + group, C::GTHR);
+  const F4Share& sh = share;
+  if (sh.i < 0) {
+    if (sh.n == 0 && cta == 0 && group == 0) {   // nothing visible anywhere: only empty outputs to write
       griddep_wait();
-      empty_units<D>(p, 0, 1, threadIdx.x, blockDim.x);
+      empty_units<D>(p, 0, 1, tid, C::GTHR);
     }
     return;
   }
-  if (small && threadIdx.x == 0) share = sh;
-  __syncthreads();
-  const int u0 = sh.u0, p0 = sh.p0;
-  const int s_beg = static_cast<int>(sh.s_beg), s_end = static_cast<int>(sh.s_end);   // T fits an int
+  const int u0 = sh.u0, p0 = sh.p0, s_beg = sh.s_beg, s_end = sh.s_end;
 
   if (warp == C::NCW) {
     // ------------------------------------------------------------ producer
@@ -465,7 +593,7 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
 
   // -------------------------------------------------------------- consumers
   griddep_wait();
-  empty_units<D>(p, cta, sh.ncta, threadIdx.x, C::NCW * 32);
+  empty_units<D>(p, sh.i, sh.n, tid, C::NCW * 32);
   constexpr float P_OFF = 4.0f;    // weights reach 2^P_OFF against a base of their own tile's,
   constexpr float SLACK = 8.0f;    // and 2^(P_OFF + SLACK) against O's base before it is raised
   int e = 0, step = 0;
@@ -501,7 +629,7 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
         *reinterpret_cast<uint4*>(smem + C::OFF_Q + (jw * 32 + lane) * 16) = make_uint4(f[0], f[1], f[2], f[3]);
       }
       if (__any_sync(0xffffffffu, qbig != 0) && lane == 0) atomicOr(p.err, FA_DEV_ERR_RANGE);
-      named_bar_sync(1, C::NCW * 32);
+      named_bar_sync(bid, C::NCW * 32);
     }
 
     float o[C::MT][4];
@@ -606,7 +734,7 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[kst]);
-      named_bar_sync(1, C::NCW * 32);   // every tile's weights and base are there
+      named_bar_sync(bid, C::NCW * 32);   // every tile's weights and base are there
       if (*reinterpret_cast<volatile int*>(&abort_flag)) return;
 
       // ---- tiles with a base of their own: raise O's base to the largest, and
@@ -707,7 +835,7 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
       }
       if (gid == 0) mls[warp * 8 + 2 * tig + h] = make_float2(ml[h], ll[h]);
     }
-    named_bar_sync(1, C::NCW * 32);
+    named_bar_sync(bid, C::NCW * 32);
     if (*reinterpret_cast<volatile int*>(&abort_flag)) return;
     float m = kNoScore, l = 0.f;   // of head gid
 #pragma unroll
@@ -717,14 +845,77 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
       const float2 v = mls[w * 8 + gid];
       l += v.y * ex2(v.x - m);
     }
-    const float Mo = M - P_OFF;
-    int c_first = share.cf, nct = share.nct;
-    if (nct == 0) {   // not the whole-unit cut
-      c_first = cta_of_fast(static_cast<uint32_t>(P), share.ncta, share.T);
-      nct = cta_of_fast(static_cast<uint32_t>(P + x.n - 1), share.ncta, share.T) - c_first + 1;
+    float Mo = M - P_OFF;
+    // The partials of the unit's shares in this CTA (the whole-unit cut) meet in
+    // shared memory: each group leaves its own in the idle ring, lane by lane as
+    // the registers lie; the last to arrive adds them up in order and goes on.
+    bool here = false;   // and they are all there are
+    if (share.nct > 0) {
+      const int sb = max(share.sb, share.cf), cnt = min(share.se, share.cf + share.nct) - sb, mine = share.i - sb;
+      here = cnt == share.nct;
+      if (cnt > 1) {
+        constexpr int PART = 8 * D * 4;
+        float4* dst = reinterpret_cast<float4*>(smem) + tid;
+#pragma unroll
+        for (int i = 0; i < C::MT; ++i) dst[i * 128] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+        if (warp == 0 && tig == 0) reinterpret_cast<float4*>(smem + PART)[gid] = make_float4(Mo, m, l, 0.f);
+        volatile int* last = &lasts[group];
+        named_bar_sync(bid, C::NCW * 32);
+        if (tid == 0) {
+          __threadfence_block();
+          *last = atomicAdd(&local_cnt[sb - share.sb], 1) == cnt - 1;
+          __threadfence_block();
+        }
+        named_bar_sync(bid, C::NCW * 32);
+        if (!*last) return;   // its only segment
+        const uint8_t* src = smem - mine * C::GSMEM;
+        float4 v[C::GROUPS];
+        Mo = m = kNoScore;
+#pragma unroll
+        for (int k = 0; k < C::GROUPS; ++k) {
+          v[k] = k < cnt ? reinterpret_cast<const float4*>(src + k * C::GSMEM + PART)[gid]
+                         : make_float4(kNoScore, kNoScore, 0.f, 0.f);
+          Mo = fmaxf(Mo, v[k].x);
+          m = fmaxf(m, v[k].y);
+        }
+        l = 0.f;
+        float acc[C::MT][4] = {};
+#pragma unroll
+        for (int k = 0; k < C::GROUPS; ++k) {
+          if (k >= cnt) continue;
+          l += v[k].z * ex2(v[k].y - m);
+          const float w = ex2(v[k].x - Mo);
+          const float wA = __shfl_sync(0xffffffffu, w, 8 * tig), wB = __shfl_sync(0xffffffffu, w, 8 * tig + 4);
+#pragma unroll
+          for (int i = 0; i < C::MT; ++i) {
+            const float4 t = reinterpret_cast<const float4*>(src + k * C::GSMEM)[i * 128 + tid];
+            acc[i][0] += wA * t.x;
+            acc[i][1] += wB * t.y;
+            acc[i][2] += wA * t.z;
+            acc[i][3] += wB * t.w;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < C::MT; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[i][c] = acc[i][c];
+      }
     }
-    const int d0 = (8 * warp + gid) * 8 * C::NW;   // this lane's columns: 8 NW from d0 on
-    if (nct == 1) {
+    // The unit's partials in memory: slot (less u) of the first, their number,
+    // this one's place
+    int cf = 0, nct = 1, me = 0;
+    if (!here) {
+      const bool whole = share.nct > 0;   // one partial a CTA, else one a share
+      const int a = whole ? share.cf : P, z = whole ? a + share.nct - 1 : P + x.n - 1;
+      const int parts = whole ? share.nb : share.n, of = whole ? share.n : share.T;
+      cf = part_of(a, parts, of);
+      nct = part_of(z, parts, of) - cf + 1;
+      me = (whole ? cta : share.i) - cf;
+    }
+    const bool mine = merge_tree<D>(p, static_cast<size_t>(cf) + u, nct, me, o, Mo, m, l, &lasts[group],
+                                    P + x.n >= s_end ? smem : nullptr, mbar_merge, merge_phase, tid, bid);
+    if (mine) {
+      const int d0 = (8 * warp + gid) * 8 * C::NW;   // this lane's columns: 8 NW from d0 on
       const float r = ex2(Mo - m) / l;
       const float r2[2] = {__shfl_sync(0xffffffffu, r, 8 * tig), __shfl_sync(0xffffffffu, r, 8 * tig + 4)};
 #pragma unroll
@@ -741,26 +932,13 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
       }
       if (p.lse && warp == 0 && tig == 0 && hv)
         p.lse[static_cast<size_t>(x.b) * p.Hq + head0 + gid] = (m + __log2f(l)) * 0.69314718055994531f;
-    } else {
-      const size_t slot = static_cast<size_t>(cta) + u;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float4* dst = reinterpret_cast<float4*>(p.o_part + (slot * 8 + 2 * tig + h) * D + d0);
-#pragma unroll
-        for (int i = 0; i < C::MT / 2; ++i)
-          dst[i] = make_float4(o[2 * i][h], o[2 * i][2 + h], o[2 * i + 1][h], o[2 * i + 1][2 + h]);
-      }
-      if (warp == 0 && tig == 0) reinterpret_cast<float4*>(p.ml_part)[slot * 8 + gid] = make_float4(Mo, m, l, 0.f);
-      merge_tree<D>(p, u, x, nh, head0, c_first, nct, cta - c_first,
-                    reinterpret_cast<float*>(smem + C::OFF_W), &sh_last, P + x.n >= s_end ? smem : nullptr, mbar_merge,
-                    merge_phase);
     }
     P += x.n;
   }
 }
 
 template <int D>
-__global__ void __launch_bounds__(F4Cfg<D>::NTHR, F4Cfg<D>::CTAS) decode_fp4_kernel(const __grid_constant__ DecK p) {
+__global__ void __launch_bounds__(F4Cfg<D>::NTHR, 1) decode_fp4_kernel(const __grid_constant__ DecK p) {
   decode_fp4_body<D>(p, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
 }
 
@@ -772,7 +950,7 @@ struct F4Layers {
 };
 
 template <int D>
-__global__ void __launch_bounds__(F4Cfg<D>::NTHR, F4Cfg<D>::CTAS) decode_fp4_layers_kernel(const __grid_constant__ F4Layers m) {
+__global__ void __launch_bounds__(F4Cfg<D>::NTHR, 1) decode_fp4_layers_kernel(const __grid_constant__ F4Layers m) {
   const int b = static_cast<int>(blockIdx.x);
   int li = 0;
   while (li + 1 < m.n && b >= m.cta0[li + 1]) ++li;
@@ -787,7 +965,7 @@ static cudaError_t launch_fp4(const DecodeArgs* a, int n, cudaStream_t s) {
     static unsigned int done = 0;
     e = set_smem_once(reinterpret_cast<const void*>(decode_fp4_kernel<D>), C::SMEM, &done);
     if (e != cudaSuccess) return e;
-    return launch_pdl(decode_fp4_kernel<D>, dim3(a->plan.ncta), dim3(C::NTHR), C::SMEM, s, make_deck(*a));
+    return launch_pdl(decode_fp4_kernel<D>, dim3(a->plan.blocks), dim3(C::NTHR), C::SMEM, s, make_deck(*a));
   }
   static unsigned int done = 0;
   e = set_smem_once(reinterpret_cast<const void*>(decode_fp4_layers_kernel<D>), C::SMEM, &done);
@@ -796,7 +974,7 @@ static cudaError_t launch_fp4(const DecodeArgs* a, int n, cudaStream_t s) {
   m.n = n;
   for (int i = 0; i < n; ++i) {
     m.k[i] = make_deck(a[i]);
-    m.cta0[i + 1] = m.cta0[i] + a[i].plan.ncta;
+    m.cta0[i + 1] = m.cta0[i] + a[i].plan.blocks;
   }
   return launch_pdl(decode_fp4_layers_kernel<D>, dim3(m.cta0[n]), dim3(C::NTHR), C::SMEM, s, m);
 }

@@ -91,7 +91,8 @@ struct DecodePlan {
   int units = 0;            // B * Hkv * head_chunks
   int max_tiles = 0;        // 16-row tiles a unit can touch under the length bound
   int min_tiles = 0;        // fewest tiles a CTA is given
-  int ncta = 0;             // CTAs launched
+  int ncta = 0;             // shares the work may be cut into: CTAs launched (fp4: three a CTA)
+  int blocks = 0;           // fp4: CTAs launched
   size_t off_ml = 0, off_o = 0;   // workspace layout (bytes); counters [units] at 0
   size_t ws_bytes = 0;
 };
