@@ -63,7 +63,8 @@ struct F4Cfg {
   static constexpr int GSMEM = (OFF_BAR + (2 * NSLOT + 1) * 8 + 127) / 128 * 128;   // a group's
   static constexpr int SMEM = GROUPS * GSMEM;
   static_assert(SLOT % 128 == 0, "slot alignment");
-  static_assert(NSLOT * SLOT >= 3 * 8 * D * 4 + 8 * 16, "the ring holds three partials, or one and its (M, m, L)");
+  static constexpr int R = D == 256 ? 6 : 5;           // partials merged at a time
+  static_assert(OFF_MW >= (R - 1) * 8 * D * 4, "the ring, Q and weights hold the others");
   static_assert(SMEM + 256 <= 227 * 1024, "shared memory");
 };
 
@@ -310,28 +311,28 @@ static __device__ __noinline__ int part_of(uint32_t g, uint32_t n, uint32_t T) {
 }
 
 // Combine the partials that n CTAs (or shares) have of one unit, as a tree of
-// groups of four in order: the last of a group to arrive merges the group's
+// groups of R in order: the last of a group to arrive merges the group's
 // partials and goes on to the next level; false: someone else does.  (One CTA
 // merging all of a long sequence's partials alone, 57 of 16 KB with 8 sequences
 // on 152 SMs, took 32 us after the last byte had been read.)  A partial lies in
 // memory lane by lane as the registers do, so the last to arrive keeps its own
-// and adds the others to it: (own + neighbour) + (the other two), each sum of two
-// products rounded alike either way round, so results do not depend on who
-// arrives last.  Run by the 128 consumer threads of a group; slot0: the slot of
+// and adds the others to it: ((0 + 1) + (2 + 3)) + (4 + 5), each sum rounded
+// alike either way round, so results do not depend on who arrives last.  R (six
+// at head_dim 256, five at 512) is what one round of copies can bring in.  Run by the 128 consumer threads of a group; slot0: the slot of
 // the unit's first partial, i: this one's place; o, and Mo, m, l (of head gid).
 template <int D>
 __device__ __forceinline__ bool merge_tree(const DecK& p, size_t slot0, int n, int i, float (&o)[F4Cfg<D>::MT][4], float& Mo,
                                            float& m, float& l, volatile int* last, uint8_t* ring, uint64_t* bar,
                                            uint32_t& phase, int tid, int bid) {
   using C = F4Cfg<D>;
-  constexpr int PART = 8 * D * 4;
+  constexpr int PART = 8 * D * 4, R = C::R;
   const int gid = (tid & 31) >> 2, tig = tid & 3;
   int st = 1;
 #pragma unroll 1
-  for (int level = 0; n > 1; ++level, i >>= 2, st *= 4) {
-    const int first = i & ~3, mine = i & 3, cnt = min(4, n - first);
+  for (int level = 0; n > 1; ++level, i /= R, st *= R) {
+    const int mine = i % R, first = i - mine, cnt = min(R, n - first);
     const size_t base = slot0 + static_cast<size_t>(first) * st;   // slot of the group's first partial
-    n = (n + 3) >> 2;
+    n = (n + R - 1) / R;
     if (cnt == 1) continue;   // alone in its group (others exist: n > 1)
     {
       const size_t slot = base + static_cast<size_t>(mine) * st;
@@ -343,54 +344,60 @@ __device__ __forceinline__ bool merge_tree(const DecK& p, size_t slot0, int n, i
     // arrive: the barrier orders the CTA's partial writes before thread 0's
     // release/acquire add, which publishes them and, for the last arrival,
     // makes the other CTAs' rows visible.  A group's counter lies in its own
-    // slots: at level l its partials are 4^l slots apart, and the offset l
-    // (past 3, l + 1) keeps the levels' counters apart.
+    // slots: at level l < R its partials are R^l slots apart, and the offset l
+    // keeps the levels' counters apart.
     named_bar_sync(bid, 128);
+    // the pairs: this one's neighbour q, the first other pair a, a + 1, the
+    // second b, b + 1 (of five, the last has no neighbour: b + 1 takes its place in the ring)
+    const int mp = mine >> 1, kq = mine ^ 1, ka = mp == 0 ? 2 : 0, kb = mp == 2 ? 2 : 4;
     if (tid == 0) {
-      int* c = p.counters + base + level + (level > 3 ? 1 : 0);
+      int* c = p.counters + base + level;
       const int old = atom_add_acq_rel_gpu(c, 1);
       if (old == cnt - 1) atomicExch(c, 0);   // zero for the next call
       else if (old >= cnt) atomicOr(p.err, FA_DEV_ERR_WORKSPACE);
       *last = old == cnt - 1;
       if (old == cnt - 1 && ring) {
-        // the others (three at most) by bulk copies into the ring, idle by now
+        // the others by bulk copies into the ring, Q and weights, idle by now
         fence_proxy_async_global();   // the other CTAs' rows, seen through the acquire, for the bulk copies
         fence_proxy_async_smem();     // the ring's generic reads and zeroed scales before them
         mbar_arrive_expect_tx(bar, (cnt - 1) * PART);
-        for (int k = 0; k < cnt; ++k)
-          if (k != mine)
-            bulk_load(ring + (k - (k > mine)) * PART, p.o_part + (base + static_cast<size_t>(k) * st) * 8 * D, PART, bar);
+#pragma unroll 1
+        for (int k = 0; k < R - 1; ++k) {
+          const int of = k == 0 ? (kq < R ? kq : kb + 1) : k < 3 ? ka + k - 1 : kb + k - 3;
+          if (of < cnt) bulk_load(ring + k * PART, p.o_part + (base + static_cast<size_t>(of) * st) * 8 * D, PART, bar);
+        }
       }
     }
     named_bar_sync(bid, 128);
     if (!*last) return false;
-    float4 v[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      v[k] = k < cnt ? __ldcg(reinterpret_cast<const float4*>(p.ml_part) + (base + static_cast<size_t>(k) * st) * 8 + gid)
-                     : make_float4(kNoScore, kNoScore, 0.f, 0.f);
-    Mo = fmaxf(fmaxf(v[0].x, v[1].x), fmaxf(v[2].x, v[3].x));
-    m = fmaxf(fmaxf(v[0].y, v[1].y), fmaxf(v[2].y, v[3].y));
-    l = 0.f;
-    float w[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      l += v[k].z * ex2(v[k].y - m);
-      w[k] = ex2(v[k].x - Mo);
-    }
-    const int kq = mine ^ 1, kr = mine < 2 ? 2 : 0;   // the neighbour; the other two
-    const float ow = mine == 0 ? w[0] : mine == 1 ? w[1] : mine == 2 ? w[2] : w[3];
-    const float qw = mine == 0 ? w[1] : mine == 1 ? w[0] : mine == 2 ? w[3] : w[2];
-    const float rw = mine < 2 ? w[2] : w[0], sw = mine < 2 ? w[3] : w[1];
-    auto head2 = [&](float x, float (&y)[2]) {
-      y[0] = __shfl_sync(0xffffffffu, x, 8 * tig);
-      y[1] = __shfl_sync(0xffffffffu, x, 8 * tig + 4);
+    auto from = [&](int k, int j) {   // piece j of partial k in memory
+      if (k >= cnt) return make_float4(0.f, 0.f, 0.f, 0.f);
+      return __ldcg(reinterpret_cast<const float4*>(p.o_part + (base + static_cast<size_t>(k) * st) * 8 * D) + j * 128 + tid);
     };
-    float wo[2], wq[2], wr[2], ws[2];
-    head2(ow, wo);
-    head2(qw, wq);
-    head2(rw, wr);
-    head2(sw, ws);
+    auto two = [](float a, float wa, float b, float wb) { return __fadd_rn(__fmul_rn(a, wa), __fmul_rn(b, wb)); };
+    auto six = [&](float own, float a, float b) { return __fadd_rn(__fadd_rn(a, mp == 2 ? b : own), mp == 2 ? own : b); };
+    // bases, denominator and weights, by part played: own, q, a, a + 1, b, b + 1
+    float w[6][2];
+    {
+      float4 v[6];
+      Mo = m = kNoScore;
+#pragma unroll
+      for (int r = 0; r < 6; ++r) {
+        const int k = r == 0 ? mine : r == 1 ? kq : r < 4 ? ka + r - 2 : kb + r - 4;
+        v[r] = k < cnt ? __ldcg(reinterpret_cast<const float4*>(p.ml_part) + (base + static_cast<size_t>(k) * st) * 8 + gid)
+                       : make_float4(kNoScore, kNoScore, 0.f, 0.f);
+        Mo = fmaxf(Mo, v[r].x);
+        m = fmaxf(m, v[r].y);
+      }
+#pragma unroll
+      for (int r = 0; r < 6; ++r) {
+        const float x = ex2(v[r].x - Mo);
+        w[r][0] = __shfl_sync(0xffffffffu, x, 8 * tig);
+        w[r][1] = __shfl_sync(0xffffffffu, x, 8 * tig + 4);
+        v[r].z = __fmul_rn(v[r].z, ex2(v[r].y - m));
+      }
+      l = six(__fadd_rn(v[0].z, v[1].z), __fadd_rn(v[2].z, v[3].z), __fadd_rn(v[4].z, v[5].z));
+    }
     if (ring) {
       if (!mbar_wait(bar, phase)) *last = 2;
       phase ^= 1;
@@ -400,19 +407,21 @@ __device__ __forceinline__ bool merge_tree(const DecK& p, size_t slot0, int n, i
         return false;
       }
     }
-    auto part = [&](int k, int j) {   // piece j of partial k
+    auto part = [&](int slot, int k, int j) {
       if (k >= cnt) return make_float4(0.f, 0.f, 0.f, 0.f);
-      if (ring) return reinterpret_cast<const float4*>(ring + (k - (k > mine)) * PART)[j * 128 + tid];
-      return __ldcg(reinterpret_cast<const float4*>(p.o_part + (base + static_cast<size_t>(k) * st) * 8 * D) + j * 128 + tid);
+      return ring ? reinterpret_cast<const float4*>(ring + slot * PART)[j * 128 + tid] : from(k, j);
     };
-    auto two = [](float a, float wa, float b, float wb) { return __fadd_rn(__fmul_rn(a, wa), __fmul_rn(b, wb)); };
 #pragma unroll
     for (int j = 0; j < C::MT; ++j) {
-      const float4 q = part(kq, j), r = part(kr, j), s = part(kr + 1, j);
-      o[j][0] = __fadd_rn(two(o[j][0], wo[0], q.x, wq[0]), two(r.x, wr[0], s.x, ws[0]));
-      o[j][1] = __fadd_rn(two(o[j][1], wo[1], q.y, wq[1]), two(r.y, wr[1], s.y, ws[1]));
-      o[j][2] = __fadd_rn(two(o[j][2], wo[0], q.z, wq[0]), two(r.z, wr[0], s.z, ws[0]));
-      o[j][3] = __fadd_rn(two(o[j][3], wo[1], q.w, wq[1]), two(r.w, wr[1], s.w, ws[1]));
+      const float4 q = part(0, kq, j), a = part(1, ka, j), a1 = part(2, ka + 1, j), b = part(3, kb, j), b1 = part(R == 6 ? 4 : 0, kb + 1, j);
+      const float qq[4] = {q.x, q.y, q.z, q.w}, aa[4] = {a.x, a.y, a.z, a.w}, aa1[4] = {a1.x, a1.y, a1.z, a1.w};
+      const float bb[4] = {b.x, b.y, b.z, b.w}, bb1[4] = {b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int h = c & 1;
+        o[j][c] = six(two(o[j][c], w[0][h], qq[c], w[1][h]), two(aa[c], w[2][h], aa1[c], w[3][h]),
+                      two(bb[c], w[4][h], bb1[c], w[5][h]));
+      }
     }
   }
   return true;
@@ -487,23 +496,21 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
     if (lane == 0) share = sh;
   }
   named_bar_sync(1 + C::GROUPS + group, C::GTHR);
-  const F4Share& sh = share;
-  if (sh.i < 0) {
-    if (sh.n == 0 && cta == 0 && group == 0) {   // nothing visible anywhere: only empty outputs to write
+  if (share.i < 0) {
+    if (share.n == 0 && cta == 0 && group == 0) {   // nothing visible anywhere: only empty outputs to write
       griddep_wait();
       empty_units<D>(p, 0, 1, tid, C::GTHR);
     }
     return;
   }
-  const int u0 = sh.u0, p0 = sh.p0, s_beg = sh.s_beg, s_end = sh.s_end;
-
   if (warp == C::NCW) {
     // ------------------------------------------------------------ producer
     int e = 0;   // slots filled
     bool ok = true, first = true;
     const bool one = p.tiles_per_page == 1;   // the usual page of 16: no division
-    int P = p0;
-    for (int u = u0; ok && P < s_end; ++u) {
+    const int s_beg = share.s_beg, s_end = share.s_end;
+    int P = share.p0;
+    for (int u = share.u0; ok && P < s_end; ++u) {
       const Unit x = unit_at(p, u);
       if (x.n > 0) {
         const int ta = x.t_first + max(s_beg, P) - P;
@@ -593,17 +600,17 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
 
   // -------------------------------------------------------------- consumers
   griddep_wait();
-  empty_units<D>(p, sh.i, sh.n, tid, C::NCW * 32);
+  empty_units<D>(p, share.i, share.n, tid, C::NCW * 32);
   constexpr float P_OFF = 4.0f;    // weights reach 2^P_OFF against a base of their own tile's,
   constexpr float SLACK = 8.0f;    // and 2^(P_OFF + SLACK) against O's base before it is raised
   int e = 0, step = 0;
   uint32_t merge_phase = 0;
-  int P = p0;
-  for (int u = u0; P < s_end; ++u) {
+  int P = share.p0;
+  for (int u = share.u0; P < share.s_end; ++u) {
     const Unit x = unit_at(p, u);
     if (x.n == 0) continue;   // an empty unit advances nothing
-    const int ta = x.t_first + max(s_beg, P) - P;
-    const int tz = x.t_first + min(s_end, P + x.n) - P;
+    const int ta = x.t_first + max(share.s_beg, P) - P;
+    const int tz = x.t_first + min(share.s_end, P + x.n) - P;
     const int nh = min(8, p.g - x.c * 8), head0 = x.h * p.g + x.c * 8;
     const int qpos = x.L - 1, lo = x.lo;
     const bool hv = gid < nh;
@@ -913,7 +920,7 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
       me = (whole ? cta : share.i) - cf;
     }
     const bool mine = merge_tree<D>(p, static_cast<size_t>(cf) + u, nct, me, o, Mo, m, l, &lasts[group],
-                                    P + x.n >= s_end ? smem : nullptr, mbar_merge, merge_phase, tid, bid);
+                                    P + x.n >= share.s_end ? smem : nullptr, mbar_merge, merge_phase, tid, bid);
     if (mine) {
       const int d0 = (8 * warp + gid) * 8 * C::NW;   // this lane's columns: 8 NW from d0 on
       const float r = ex2(Mo - m) / l;
@@ -957,6 +964,9 @@ __global__ void __launch_bounds__(F4Cfg<D>::NTHR, 1) decode_fp4_layers_kernel(co
   decode_fp4_body<D>(m.k[li], b - m.cta0[li], m.cta0[li + 1] - m.cta0[li]);
 }
 
+// Groups of a CTA: no more than the plan's shares need.
+static int groups_of(const DecodePlan& p) { return (p.ncta + p.blocks - 1) / p.blocks; }
+
 template <int D>
 static cudaError_t launch_fp4(const DecodeArgs* a, int n, cudaStream_t s) {
   using C = F4Cfg<D>;
@@ -965,18 +975,21 @@ static cudaError_t launch_fp4(const DecodeArgs* a, int n, cudaStream_t s) {
     static unsigned int done = 0;
     e = set_smem_once(reinterpret_cast<const void*>(decode_fp4_kernel<D>), C::SMEM, &done);
     if (e != cudaSuccess) return e;
-    return launch_pdl(decode_fp4_kernel<D>, dim3(a->plan.blocks), dim3(C::NTHR), C::SMEM, s, make_deck(*a));
+    return launch_pdl(decode_fp4_kernel<D>, dim3(a->plan.blocks), dim3(groups_of(a->plan) * C::GTHR),
+                      groups_of(a->plan) * C::GSMEM, s, make_deck(*a));
   }
   static unsigned int done = 0;
   e = set_smem_once(reinterpret_cast<const void*>(decode_fp4_layers_kernel<D>), C::SMEM, &done);
   if (e != cudaSuccess) return e;
   F4Layers m{};
   m.n = n;
+  int groups = 1;
   for (int i = 0; i < n; ++i) {
     m.k[i] = make_deck(a[i]);
     m.cta0[i + 1] = m.cta0[i] + a[i].plan.blocks;
+    groups = max(groups, groups_of(a[i].plan));
   }
-  return launch_pdl(decode_fp4_layers_kernel<D>, dim3(m.cta0[n]), dim3(C::NTHR), C::SMEM, s, m);
+  return launch_pdl(decode_fp4_layers_kernel<D>, dim3(m.cta0[n]), dim3(groups * C::GTHR), groups * C::GSMEM, s, m);
 }
 
 cudaError_t launch_decode_fp4(const DecodeArgs* a, int n, cudaStream_t s) {
