@@ -22,7 +22,7 @@ struct DecK {
   const int32_t* slots;
   __nv_bfloat16* out;
   float* lse;
-  int* counters;    // [U] arrival count per unit (fp4: [ncta + U], per group of partials; null: no
+  int* counters;    // [U] arrival count per unit (fp4: [ncta + U], per node of partials; null: no
                     // workspace, one CTA); zero between calls
   float* ml_part;   // [(ncta + U) * 8][2] (fp4: [4])
   float* o_part;    // [(ncta + U) * 8][D]

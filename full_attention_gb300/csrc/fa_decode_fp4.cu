@@ -10,29 +10,38 @@
 // their weights out of f16's range, nor an all-zero V row (e = -116) under a
 // sink token's weight; L keeps a base of its own.
 //
-// What bounds it: HBM (a row is 148 bytes at head_dim 256, 292 at 512), then
-// the conversion: every code passes through one e2m1 -> f16 conversion and one
-// f16 product with its block's scale before a matrix instruction can take it,
-// about 2.1 instructions a code pair with the loads.
+// What bounds it: a row is 148 bytes at head_dim 256 and 292 at 512, but every
+// pair of codes passes through one e2m1 -> f16 conversion and one f16 product
+// with its block's scale before a matrix instruction can take it: 2 cycles of a
+// scheduler each for a warp's 64 codes, side by side on two pipes, and the matrix
+// instructions (8.5 cycles) do not run beside them.  Measured with the loads left
+// out, long sequences took 98% of their time: 8 sequences of 32k to 131k keys at
+// 512 take 89 us, 4.8 TB/s of 6.8; 64 of 512 to 4096 keys 29 us, 128 windows of
+// 1024 at 256 19 us, where the start (3 us to the first copy, 2 more until it
+// lands) and the joining of the parts (3 to 6 us) weigh as much.
 //
-// Work decomposition: the shares of fa_decode.cuh.  A step is 64 keys at
-// head_dim 512 and 128 at 256 (18 KB of K, as much of V): wide enough that one
-// barrier between the consumer warps per step is cheap.
-//   warp 4      producer: per step one bulk copy per 16-row tile of K and of V
-//               (a tile's rows are contiguous) and of their row scales, into a
-//               ring of five slots, K and V alternating;
-//   warps 0-3   S^T = K Q^T, each warp whole tiles over the full head_dim
-//               (keys on the MMA's M side, the 8 heads on N), the softmax
-//               weights of its own tiles against the tile's own base M_w,
-//               rounded up to an integer, into shared memory as f16; barrier;
-//               then O^T += V^T P^T, each warp a quarter of the columns, the
-//               weights of tile w times 2^(M_w - M), a power of two.
+// Work decomposition: one CTA per SM of three groups, each with a share of the
+// tile lists and shared memory, barriers and five warps of its own.  (Three CTAs
+// of one group on an SM read as fast, but joined their partials through memory:
+// 95.5, 31.4 and 22.6 us for the above.)  A step is 64 keys, four tiles:
+//   warp 4      producer: finds the share; per step one bulk copy per 16-row tile
+//               of K and of V (a tile's rows are contiguous) and of their row
+//               scales, into a ring of six slots at 256 and three at 512, K and V
+//               alternating;
+//   warps 0-3   S^T = K Q^T, each warp one tile over the full head_dim (keys on
+//               the MMA's M side, the 8 heads on N), the softmax weights of its
+//               tile against O's base, or the tile's own base where it exceeds
+//               that by more than the slack, into shared memory as f16; barrier;
+//               then O^T += V^T P^T, each warp a quarter of the columns.
+// The weights' rounding to f16 is the only one below 32 bits: 2^-11 relative
+// each, while the sum of the weights, in fp32, takes them unrounded.
+//
 // Rows are 144 or 288 bytes apart in shared memory, so the fragment loads (one
 // 4-byte word of 8 codes a lane at 256, 8 bytes at 512) hit 32 different banks
 // without any swizzle; at 512 the MMA's key index r stands for tile row
 // key_row(r) to that end.  The MMA contraction over head_dim may run in any
 // order, so a lane's codes are taken in the order they are stored, and Q
-// likewise.
+// likewise (as f16, whose 11 bits hold bf16's 8; past f16's range it is reported).
 #include "fa_decode.cuh"
 
 namespace fa {

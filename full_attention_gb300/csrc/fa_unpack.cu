@@ -2,12 +2,13 @@
 //
 // An extend over a 4-bit slab multiplies every prefix key with every 128-row
 // block of queries.  Converting codes inside the kernel repeats the conversion
-// for each block and paces it (286 and 213 TFLOP/s on the two shapes below);
-// a value of the format has 6 significant bits, so a bf16 row holds it exactly,
+// for each block and paces it: 8 sequences of 4096 keys at head_dim 512, 2 KV
+// heads, 256 queries each, take 1218 us converting and 556 us unpacked.  A value of the format has 6 significant bits, so a bf16 row holds it exactly,
 // and the bf16 kernel over unpacked rows does the same arithmetic without it.
 // This kernel writes them: a memory pass over the rows some query can see, 0.58
 // bytes in and 2 out per value, most of which the extend kernel then finds in
-// L2.
+// L2: 12 us for 4 sequences, a window of 1024 before chunks of 512, at 256 with 8
+// KV heads.
 //
 // The rows of sequence b and KV head h form a ring of `ring` rows (a multiple
 // of 16): position pos lies in row (b * Hkv + h) * ring + pos % ring.  To the
