@@ -383,6 +383,8 @@ class Cache:
                      lse=None, stream=None) -> None:
         """fa_paged_decode_multi_attn: several new tokens per sequence, their rows
         already stored; every key from the slab."""
+        if self.kv_dtype == KV_FP4:
+            self._extend_args(layer, q, qo_indptr, seq_lens, block_table, out, lse)
         _check(_lib.fa_paged_decode_multi_attn(self._h, layer, _p(q), _p(qo_indptr), _p(seq_lens), _p(block_table),
                                                int(block_table.shape[1]), int(seq_lens.numel()), int(q.shape[0]),
                                                int(max_q_len), int(max_seq_len), _p(out), _p(lse), _s(stream)))

@@ -85,7 +85,7 @@ DecodePlan plan_decode(const fa_cache* c, int layer, int B, int max_seq_len, lon
   const int g = d.num_q_heads / d.num_kv_heads;
   p.head_chunks = (g + 7) / 8;
   if (B <= 0 || max_seq_len <= 0) return p;
-  int tiles = (max_seq_len + kTile - 1) / kTile;
+  int tiles = (max_seq_len - 1) / kTile + 1;
   if (d.kind == FA_SLIDING) {
     const int win_tiles = (d.window + kTile - 2) / kTile + 1;   // tiles a W-row window can span
     if (win_tiles < tiles) tiles = win_tiles;
@@ -593,6 +593,13 @@ size_t fa_decode_layers_workspace_bytes(const fa_cache* c, int32_t n, const int3
 }
 
 namespace fa {
+// fp4 decode counts a launch's tiles in 32 bits.
+static fa_status check_tiles(const fa_cache* c, const DecodePlan& p) {
+  if (c->kv_dtype == FA_KV_FP4 && static_cast<long long>(p.units) * p.max_tiles > INT32_MAX)
+    return fail(FA_ERR_UNSUPPORTED, "fp4 decode: %d units of up to %d tiles are more than 2^31 - 1 tiles", p.units, p.max_tiles);
+  return FA_OK;
+}
+
 // The launch arguments of one layer's decode (validated by the caller).
 static void fill_decode_args(DecodeArgs& a, const fa_cache* c, int32_t layer, const Slab* s, const DecodePlan& p,
                              const void* q, const void* k_new, const void* v_new, const int32_t* slots,
@@ -651,10 +658,11 @@ static fa_status decode_call(fa_cache* c, int32_t layer, const void* q, const vo
     return fail(FA_ERR_INVALID_ARG, "q, block_table, seq_lens, out must be non-NULL");
   if (!aligned16(q) || !aligned16(out)) return fail(FA_ERR_INVALID_ARG, "q, out must be 16-byte aligned");
   if (max_seq_len < 1) return fail(FA_ERR_INVALID_ARG, "max_seq_len must be >= 1");
-  if (max_pages_per_seq < (max_seq_len + c->page_size - 1) / c->page_size)
+  if (max_pages_per_seq < (max_seq_len - 1) / c->page_size + 1)
     return fail(FA_ERR_INVALID_ARG, "max_pages_per_seq %d cannot hold max_seq_len %d", max_pages_per_seq,
                 max_seq_len);
   DecodePlan p = plan_decode(c, layer, B, max_seq_len);
+  if ((st = check_tiles(c, p))) return st;
   if (workspace_bytes < p.ws_bytes || (p.ws_bytes && !workspace))
     return fail(FA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, p.ws_bytes);
   if (p.ws_bytes && (reinterpret_cast<uintptr_t>(workspace) & 255u))
@@ -710,7 +718,7 @@ fa_status fa_paged_decode_attn_layers(fa_cache* c, int32_t n, const int32_t* lay
   if (B < 0) return fail(FA_ERR_INVALID_ARG, "B must be >= 0");
   if (!seq_lens) return fail(FA_ERR_INVALID_ARG, "seq_lens must be non-NULL");
   if (max_seq_len < 1) return fail(FA_ERR_INVALID_ARG, "max_seq_len must be >= 1");
-  if (max_pages_per_seq < (max_seq_len + c->page_size - 1) / c->page_size)
+  if (max_pages_per_seq < (max_seq_len - 1) / c->page_size + 1)
     return fail(FA_ERR_INVALID_ARG, "max_pages_per_seq %d cannot hold max_seq_len %d", max_pages_per_seq, max_seq_len);
   fa_status st;
   int D = 0;
@@ -741,6 +749,7 @@ fa_status fa_paged_decode_attn_layers(fa_cache* c, int32_t n, const int32_t* lay
     const Slab* s = nullptr;
     if ((st = check_bound(c, layers[i], &s))) return st;
     const DecodePlan& p = plans[i];
+    if ((st = check_tiles(c, p))) return st;
     a[i] = DecodeArgs{};
     fill_decode_args(a[i], c, layers[i], s, p, q[i], nullptr, nullptr, nullptr, block_table[i], max_pages_per_seq,
                      seq_lens, B, max_seq_len, out[i], lse ? lse[i] : nullptr,
@@ -951,7 +960,7 @@ fa_status fa_paged_decode_multi_attn(fa_cache* c, int32_t layer, const void* q, 
   if (!q || !qo_indptr || !seq_lens || !block_table || !out) return fail(FA_ERR_INVALID_ARG, "a required pointer is NULL");
   if (!aligned16(q) || !aligned16(out)) return fail(FA_ERR_INVALID_ARG, "q, out must be 16-byte aligned");
   if (max_seq_len < 1) return fail(FA_ERR_INVALID_ARG, "max_seq_len must be >= 1");
-  if (max_pages_per_seq < (max_seq_len + c->page_size - 1) / c->page_size)
+  if (max_pages_per_seq < (max_seq_len - 1) / c->page_size + 1)
     return fail(FA_ERR_INVALID_ARG, "max_pages_per_seq %d cannot hold max_seq_len %d", max_pages_per_seq, max_seq_len);
   cudaError_t ce;
   unsigned int* err = device_error_word(c, &ce);

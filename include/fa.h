@@ -276,7 +276,8 @@ FA_API size_t fa_kv_bytes_per_token(const fa_cache* cache, int32_t kind);
  * k, v: bf16 [T][Hkv][D] post-RoPE rows of T new tokens (device).
  * slot_mapping: int32 [T] (device); token t goes to slot slot_mapping[t];
  * a negative slot is padding and is skipped; a slot >= num_pages * page_size
- * is skipped and sets FA_DEV_ERR_SLOT.
+ * is skipped and sets FA_DEV_ERR_SLOT.  The other slots of one call must be
+ * distinct: of two tokens for one slot, parts of both may stay.
  * bf16 format: a bit-exact copy.  int8 format: per (token, head), separately
  * for K and V, a = max|x| in fp32, s = a / 127 (IEEE division), codes
  * c = clamp(rint(x / s), -127, 127) with rint rounding half to even; a = 0
@@ -334,7 +335,9 @@ FA_API size_t fa_decode_workspace_bytes(const fa_cache* cache, int32_t layer, in
  * them zero again, so the same buffer serves later calls on the same stream
  * without clearing.  Calls that run concurrently must not share a workspace.
  * After a call that reported FA_DEV_ERR_TIMEOUT, zero it again (a counter
- * found non-zero sets FA_DEV_ERR_WORKSPACE).  Reference: "unsloth commit
+ * found non-zero sets FA_DEV_ERR_WORKSPACE).  fp4 format: a call whose sequences
+ * could hold 2^31 16-row tiles or more (B * num_kv_heads * ceil(g / 8) times
+ * those of max_seq_len or the window) is FA_ERR_UNSUPPORTED.  Reference: "unsloth commit
  * dee9371" (shared layers read the source's paged cache on decode) and the
  * regimes above. */
 FA_API fa_status fa_paged_decode_attn(fa_cache* cache, int32_t layer, const void* q,

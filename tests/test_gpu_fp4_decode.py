@@ -32,6 +32,15 @@ CASES = [
     (W.SLIDING, 256, 8, 1, 1024, [1024, 5000, 3000, 1023, 2048, 1500], 16),   # equal units: cut into equal parts
     (W.FULL, 512, 8, 1, 0, list(range(0, 400, 2)), 16),      # more units than threads
     (W.FULL, 256, 2, 2, 0, [0, 0], 16),                      # nothing visible
+    # partials joined: 4 to 7 and 26 CTAs of one share, then CTAs of two and of three shares
+    *[(W.FULL, D, 8, 1, 0, [n], 16) for D in (256, 512) for n in (512, 640, 768, 896, 3328, 20_011)],
+    (W.FULL, 512, 8, 1, 0, [60_001], 64),
+    (W.FULL, 256, 8, 2, 0, [30_000, 17, 0, 9_000], 16),
+    (W.FULL, 512, 2, 1, 0, [4000, 900, 5000, 100, 2500, 3000, 1, 700, 6000, 2222], 16),
+    # sequences past a warp's registers, in a whole-unit cut and with more units than shares
+    (W.FULL, 256, 4, 1, 0, [(37 * i) % 90 if i % 50 else 1700 for i in range(200)], 16),
+    (W.FULL, 256, 4, 2, 0, [(53 * i) % 97 for i in range(333)], 16),
+    (W.SLIDING, 512, 8, 1, 40, [(29 * i) % 75 for i in range(1025)], 32),
 ]
 
 
@@ -187,6 +196,13 @@ def test_bad_pages_lengths_queries_and_workspaces_are_reported():
     with pytest.raises(fa.FAError) as e:
         c.decode(0, case.q[0], case.bt[0], case.lens_dev, case.max_len, out, lse, ws[:-1])
     assert e.value.status == fa.ERR_WORKSPACE
+    # 33 sequences of up to 2^26 tiles: more than the kernel counts (all empty, were it to run)
+    q33, none = torch.zeros((33, 8, 512), dtype=torch.bfloat16, device="cuda"), torch.zeros(33, dtype=torch.int32, device="cuda")
+    big_ws, o33 = fa.workspace(c.decode_workspace_bytes(0, 33, 1 << 30)), torch.empty_like(q33)
+    for n, st in ((1 << 30, fa.ERR_UNSUPPORTED), (1 << 29, fa.OK)):
+        assert fa.lib().fa_paged_decode_attn(c._h, 0, q33.data_ptr(), none.data_ptr(), 1 << 26, none.data_ptr(), 33, n,
+                                             o33.data_ptr(), None, big_ws.data_ptr(), big_ws.numel(), None) == st
+    assert (o33 == 0).all()
     for q, o in ((case.q[0].float(), out), (case.q[0].transpose(1, 2), out), (case.q[0], out[:, ::2])):
         with pytest.raises(fa.FAError) as e:
             c.decode(0, q, case.bt[0], case.lens_dev, case.max_len, o, lse, ws)

@@ -186,6 +186,13 @@ def test_refusals_and_reports():
         with pytest.raises(fa.FAError) as e:
             cache.extend(0, **args(**bad))
         assert e.value.status == fa.ERR_INVALID_ARG
+    multi = lambda **m: cache.decode_multi(**{**dict(layer=0, q=c.q[0], qo_indptr=c.indptr_dev, seq_lens=c.prefix_dev,
+                                                     block_table=c.bt, max_q_len=30, max_seq_len=40, out=out, lse=lse), **m})
+    for bad in (dict(q=c.q[0].float()), dict(q=c.q[0].transpose(0, 1)), dict(seq_lens=c.prefix_dev.long()),
+                dict(qo_indptr=c.indptr_dev[:2]), dict(block_table=c.bt[:1]), dict(out=out[:5]), dict(lse=lse.half())):
+        with pytest.raises(fa.FAError) as e:
+            multi(**bad)
+        assert e.value.status == fa.ERR_INVALID_ARG
     bt = c.bt.clone()
     bt[0, 1] = cache.num_pages
     cache.extend(0, **args(block_table=bt))
