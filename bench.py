@@ -377,7 +377,7 @@ def gpu_arm(args, rank, world):
     # the event-bracketed graph above gives each layer's time run alone.
     launch_bytes = step.step_bytes / nl
     achieved = step.step_bytes / t_step / 1e9
-    digest = source_digest("fa_decode.cu", "fa_ptx.cuh")
+    digest = source_digest("fa_decode.cu", "fa_decode.cuh", "fa_ptx.cuh")
     traffic = profiled_traffic(f"decode_{args.workload}", digest)
     clocks = clk.summary()
     res = {
@@ -499,8 +499,8 @@ def decode_subrecord(name, args, dev, flush):
                     "roofline": {"kernel": "decode_kernel", "bound": "hbm", "achieved": round(gbs, 1),
                                  "peak": hbm, "unit": "GB/s", "frac": round(gbs / hbm, 3),
                                  "algorithmic_bytes_per_launch": round(step.step_bytes / len(step.layers)),
-                                 "traffic": profiled_traffic(f"decode_{name}", source_digest("fa_decode.cu",
-                                                                                            "fa_ptx.cuh"))},
+                                 "traffic": profiled_traffic(f"decode_{name}", source_digest(
+                        "fa_decode.cu", "fa_decode.cuh", "fa_ptx.cuh"))},
                     "multi_layer_step": {"ms_per_step": round(tm * 1e3, 4),
                                          "unique_gb_per_s": round(step.unique_bytes / tm / 1e9, 1),
                                          "frac_unique_of_peak": round(step.unique_bytes / tm / 1e9 / hbm, 3)}})

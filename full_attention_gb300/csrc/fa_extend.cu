@@ -59,7 +59,10 @@
 // fp4 slabs run the same path: a prefix slot's codes and block scales land as
 // boxes of 16 rows x 32 bytes (64 codes, or a row's block scales) in the slot's
 // upper half, each row group inside the rows that its own converting warp will
-// overwrite, and become the exact f16 products code * block scale.
+// overwrite, and become the exact f16 products code * block scale.  The
+// conversion paces it (1218 us for 8 sequences of 4096 keys at head_dim 512, 2 KV
+// heads, 256 queries each, against 556 over rows unpacked to bf16 first); it
+// serves short calls and caches without a workspace for the unpacked rows.
 // Every wait is bounded; tensor memory is always freed.
 #include <algorithm>
 #include <cfloat>
