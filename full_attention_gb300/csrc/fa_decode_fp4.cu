@@ -319,6 +319,21 @@ static __device__ __noinline__ int part_of(uint32_t g, uint32_t n, uint32_t T) {
   return c;
 }
 
+// ((0 + 1) + (2 + 3)) + (4 + 5) by index of R terms given by the part played in
+// merge_tree (mp: this one's pair); the sums of two are the same either way round.
+__device__ __forceinline__ float add_rn(float a, float b) { return __fadd_rn(a, b); }
+__device__ __forceinline__ uint64_t add_rn(uint64_t a, uint64_t b) { return add_f32x2(a, b); }
+template <int R, typename T>
+__device__ __forceinline__ T sum_parts(const T* x, int mp) {
+  const T a = add_rn(x[2], x[3]);
+  if constexpr (R == 6) {
+    const T own = add_rn(x[0], x[1]), b = add_rn(x[4], x[5]);
+    return add_rn(add_rn(a, mp == 2 ? b : own), mp == 2 ? own : b);
+  } else {
+    return add_rn(add_rn(a, add_rn(mp == 2 ? x[4] : x[0], x[1])), mp == 2 ? x[0] : x[4]);
+  }
+}
+
 // Combine the partials that n CTAs (or shares) have of one unit, as a tree of
 // groups of R in order: the last of a group to arrive merges the group's
 // partials and goes on to the next level; false: someone else does.  (One CTA
@@ -356,9 +371,15 @@ __device__ __forceinline__ bool merge_tree(const DecK& p, size_t slot0, int n, i
     // slots: at level l < R its partials are R^l slots apart, and the offset l
     // keeps the levels' counters apart.
     named_bar_sync(bid, 128);
-    // the pairs: this one's neighbour q, the first other pair a, a + 1, the
-    // second b, b + 1 (of five, the last has no neighbour: b + 1 takes its place in the ring)
-    const int mp = mine >> 1, kq = mine ^ 1, ka = mp == 0 ? 2 : 0, kb = mp == 2 ? 2 : 4;
+    // the parts played: 0 this one, 1 its neighbour, 2 and 3 the first other
+    // pair, 4 and 5 the second.  (Of five, only the last has two other pairs and
+    // no neighbour: 1 is then the second pair's second.)
+    const int mp = mine >> 1, ka = mp == 0 ? 2 : 0, kb = mp == 2 ? 2 : 4;
+    auto index = [&](int part) {
+      if (part == 0) return mine;
+      if (part == 1) return R == 5 && mp == 2 ? kb + 1 : mine ^ 1;
+      return part < 4 ? ka + part - 2 : kb + part - 4;
+    };
     if (tid == 0) {
       int* c = p.counters + base + level;
       const int old = atom_add_acq_rel_gpu(c, 1);
@@ -372,40 +393,34 @@ __device__ __forceinline__ bool merge_tree(const DecK& p, size_t slot0, int n, i
         mbar_arrive_expect_tx(bar, (cnt - 1) * PART);
 #pragma unroll 1
         for (int k = 0; k < R - 1; ++k) {
-          const int of = k == 0 ? (kq < R ? kq : kb + 1) : k < 3 ? ka + k - 1 : kb + k - 3;
+          const int of = index(k + 1);
           if (of < cnt) bulk_load(ring + k * PART, p.o_part + (base + static_cast<size_t>(of) * st) * 8 * D, PART, bar);
         }
       }
     }
     named_bar_sync(bid, 128);
     if (!*last) return false;
-    auto from = [&](int k, int j) {   // piece j of partial k in memory
-      if (k >= cnt) return make_float4(0.f, 0.f, 0.f, 0.f);
-      return __ldcg(reinterpret_cast<const float4*>(p.o_part + (base + static_cast<size_t>(k) * st) * 8 * D) + j * 128 + tid);
-    };
-    auto two = [](float a, float wa, float b, float wb) { return __fadd_rn(__fmul_rn(a, wa), __fmul_rn(b, wb)); };
-    auto six = [&](float own, float a, float b) { return __fadd_rn(__fadd_rn(a, mp == 2 ? b : own), mp == 2 ? own : b); };
-    // bases, denominator and weights, by part played: own, q, a, a + 1, b, b + 1
-    float w[6][2];
+    // bases, denominator and weights
+    uint64_t w[R];   // of this lane's two heads
     {
-      float4 v[6];
+      float4 v[R];
       Mo = m = kNoScore;
 #pragma unroll
-      for (int r = 0; r < 6; ++r) {
-        const int k = r == 0 ? mine : r == 1 ? kq : r < 4 ? ka + r - 2 : kb + r - 4;
+      for (int r = 0; r < R; ++r) {
+        const int k = index(r);
         v[r] = k < cnt ? __ldcg(reinterpret_cast<const float4*>(p.ml_part) + (base + static_cast<size_t>(k) * st) * 8 + gid)
                        : make_float4(kNoScore, kNoScore, 0.f, 0.f);
         Mo = fmaxf(Mo, v[r].x);
         m = fmaxf(m, v[r].y);
       }
+      float lp[R];
 #pragma unroll
-      for (int r = 0; r < 6; ++r) {
+      for (int r = 0; r < R; ++r) {
         const float x = ex2(v[r].x - Mo);
-        w[r][0] = __shfl_sync(0xffffffffu, x, 8 * tig);
-        w[r][1] = __shfl_sync(0xffffffffu, x, 8 * tig + 4);
-        v[r].z = __fmul_rn(v[r].z, ex2(v[r].y - m));
+        w[r] = pack_f32x2(__shfl_sync(0xffffffffu, x, 8 * tig), __shfl_sync(0xffffffffu, x, 8 * tig + 4));
+        lp[r] = __fmul_rn(v[r].z, ex2(v[r].y - m));
       }
-      l = six(__fadd_rn(v[0].z, v[1].z), __fadd_rn(v[2].z, v[3].z), __fadd_rn(v[4].z, v[5].z));
+      l = sum_parts<R>(lp, mp);
     }
     if (ring) {
       if (!mbar_wait(bar, phase)) *last = 2;
@@ -416,22 +431,38 @@ __device__ __forceinline__ bool merge_tree(const DecK& p, size_t slot0, int n, i
         return false;
       }
     }
-    auto part = [&](int slot, int k, int j) {
-      if (k >= cnt) return make_float4(0.f, 0.f, 0.f, 0.f);
-      return ring ? reinterpret_cast<const float4*>(ring + slot * PART)[j * 128 + tid] : from(k, j);
-    };
+    // a partial that is not there has weight 0 and stands for one that is
+    const int some = index(1) < cnt ? 1 : 2;
+    auto add_up = [&](auto at, auto load) {
+      decltype(at(1)) src[R];
 #pragma unroll
-    for (int j = 0; j < C::MT; ++j) {
-      const float4 q = part(0, kq, j), a = part(1, ka, j), a1 = part(2, ka + 1, j), b = part(3, kb, j), b1 = part(R == 6 ? 4 : 0, kb + 1, j);
-      const float qq[4] = {q.x, q.y, q.z, q.w}, aa[4] = {a.x, a.y, a.z, a.w}, aa1[4] = {a1.x, a1.y, a1.z, a1.w};
-      const float bb[4] = {b.x, b.y, b.z, b.w}, bb1[4] = {b1.x, b1.y, b1.z, b1.w};
+      for (int r = 1; r < R; ++r) src[r] = at(index(r) < cnt ? r : some);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int h = c & 1;
-        o[j][c] = six(two(o[j][c], w[0][h], qq[c], w[1][h]), two(aa[c], w[2][h], aa1[c], w[3][h]),
-                      two(bb[c], w[4][h], bb1[c], w[5][h]));
+      for (int j = 0; j < C::MT; ++j) {
+        float4 v[R];
+        v[0] = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
+#pragma unroll
+        for (int r = 1; r < R; ++r) v[r] = load(src[r], j);
+#pragma unroll
+        for (int h = 0; h < 4; h += 2) {
+          uint64_t x[R];
+#pragma unroll
+          for (int r = 0; r < R; ++r) x[r] = mul_f32x2(h ? pack_f32x2(v[r].z, v[r].w) : pack_f32x2(v[r].x, v[r].y), w[r]);
+          unpack_f32x2(sum_parts<R>(x, mp), o[j][h], o[j][h + 1]);
+        }
       }
-    }
+    };
+    if (ring)
+      add_up([&](int r) { return smem_u32(ring) + (r - 1) * PART + tid * 16; },
+             [](uint32_t at, int j) {
+               float4 v;
+               asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at + j * 2048) : "memory");
+               return v;
+             });
+    else
+      add_up([&](int r) { return reinterpret_cast<const float4*>(p.o_part + (base + static_cast<size_t>(index(r)) * st) * 8 * D) + tid; },
+             [](const float4* at, int j) { return __ldcg(at + j * 128); });
   }
   return true;
 }
