@@ -52,10 +52,11 @@ struct F4Cfg {
   static constexpr int ROWB = kRowBytes<D, FA_KV_FP4>; // 144, 288
   static constexpr int TILE_BYTES = kTile * ROWB;
   static constexpr int NCW = 4;                        // consumer warps
-  static constexpr int NT = NCW;                       // tiles per step
+  static constexpr int TPW = D == 256 ? 2 : 1;         // tiles of a step whose scores a warp works out
+  static constexpr int NT = TPW * NCW;                 // tiles per step
   static constexpr int SC_BYTES = NT * kTile * 4;      // one step's K (or V) row scales
   static constexpr int SLOT = NT * TILE_BYTES + 2 * SC_BYTES;   // rows; in K slots also both row scales
-  static constexpr int NSLOT = D == 256 ? 6 : 3;
+  static constexpr int NSLOT = 3;
   static constexpr int GROUPS = 3;                     // shares a CTA works on side by side
   static constexpr int GTHR = (NCW + 1) * 32;          // threads of a group
   static constexpr int NTHR = GROUPS * GTHR;
@@ -65,9 +66,9 @@ struct F4Cfg {
   static constexpr int P_TILE = 8 * P_HEAD;
   static constexpr int OFF_Q = NSLOT * SLOT;           // Q^T fragments [NJ][NW][32 lanes] of 16 bytes
   static constexpr int OFF_P = OFF_Q + 8 * D * 2;      // [2][NT] tiles of weights
-  static constexpr int OFF_MW = OFF_P + 2 * NT * P_TILE;   // [2][8 heads][NT] tile bases
-  static constexpr int OFF_FLAG = OFF_MW + 2 * 8 * NT * 4; // [2][NT] the tile's base is its own
-  static constexpr int OFF_ML = OFF_FLAG + 2 * NT * 4;     // [NCW][8] (m, l)
+  static constexpr int OFF_MW = OFF_P + 2 * NT * P_TILE;   // [2][8 heads][NCW] bases of a warp's tiles
+  static constexpr int OFF_FLAG = OFF_MW + 2 * 8 * NCW * 4; // [2][NCW] they are the warp's own
+  static constexpr int OFF_ML = OFF_FLAG + 2 * NCW * 4;    // [NCW][8] (m, l)
   static constexpr int OFF_BAR = OFF_ML + NCW * 8 * 8;
   static constexpr int GSMEM = (OFF_BAR + (2 * NSLOT + 1) * 8 + 127) / 128 * 128;   // a group's
   static constexpr int SMEM = GROUPS * GSMEM;
@@ -690,8 +691,8 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
       const int ntl = min(C::NT, tz - tile0);
       const int buf = step & 1;
       uint8_t* pbuf = smem + C::OFF_P + buf * C::NT * C::P_TILE;
-      float* mw = reinterpret_cast<float*>(smem + C::OFF_MW) + buf * 8 * C::NT;
-      int* flag = reinterpret_cast<int*>(smem + C::OFF_FLAG) + buf * C::NT;
+      float* mw = reinterpret_cast<float*>(smem + C::OFF_MW) + buf * 8 * C::NCW;
+      int* flag = reinterpret_cast<int*>(smem + C::OFF_FLAG) + buf * C::NCW;
       const bool edge = tile0 * kTile < lo || (tile0 + ntl) * kTile - 1 > qpos;   // some keys are masked
       const int kst = e % C::NSLOT;
       if (!__all_sync(0xffffffffu, mbar_wait(&full[kst], (e / C::NSLOT) & 1)) && lane == 0) {
@@ -702,79 +703,100 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
       const uint8_t* kslot = smem + kst * C::SLOT;
       const float* scl = reinterpret_cast<const float*>(kslot + C::NT * C::TILE_BYTES);
       if (warp < ntl) {
-        // ---- S^T of this warp's tile: keys gid, gid + 8 (as MMA rows), heads 2 tig, 2 tig + 1
-        const uint8_t* ra = kslot + warp * C::TILE_BYTES + key_row<D>(gid) * C::ROWB;
-        const uint8_t* rb = ra + 8 * C::ROWB;   // key_row(gid + 8) = key_row(gid) + 8
-        float acc[2][4] = {};
+        // ---- S^T of this warp's tiles, warp and (TPW = 2) warp + 4: keys gid, gid
+        // + 8 (as MMA rows), heads 2 tig, 2 tig + 1.  A tile past the step's last
+        // runs over whatever the slot holds; its keys count as masked.
+        const uint8_t* ra = kslot + warp * C::TILE_BYTES + key_row<D>(gid) * C::ROWB;   // key_row(gid + 8) = key_row(gid) + 8
+        float acc[C::TPW][2][4] = {};
 #pragma unroll
         for (int i = 0; i < C::NJ / 2; ++i) {
-          const __half2 sca = block_scales<D>(ra + D / 2, i, tig), scb = block_scales<D>(rb + D / 2, i, tig);
+          __half2 sca[C::TPW], scb[C::TPW];
+#pragma unroll
+          for (int t = 0; t < C::TPW; ++t) {
+            sca[t] = block_scales<D>(ra + t * C::NCW * C::TILE_BYTES + D / 2, i, tig);
+            scb[t] = block_scales<D>(ra + t * C::NCW * C::TILE_BYTES + 8 * C::ROWB + D / 2, i, tig);
+          }
 #pragma unroll
           for (int jj = 0; jj < 2; ++jj) {
             const int j = 2 * i + jj;
-            const __half2 fa_ = jj ? __high2half2(sca) : __low2half2(sca), fb_ = jj ? __high2half2(scb) : __low2half2(scb);
-            uint32_t wa[C::NW], wb[C::NW];
-            lds_words(ra + (4 * j + tig) * 4 * C::NW, wa);
-            lds_words(rb + (4 * j + tig) * 4 * C::NW, wb);
+            uint32_t wa[C::TPW][C::NW], wb[C::TPW][C::NW];
+#pragma unroll
+            for (int t = 0; t < C::TPW; ++t) {
+              lds_words(ra + t * C::NCW * C::TILE_BYTES + (4 * j + tig) * 4 * C::NW, wa[t]);
+              lds_words(ra + t * C::NCW * C::TILE_BYTES + 8 * C::ROWB + (4 * j + tig) * 4 * C::NW, wb[t]);
+            }
 #pragma unroll
             for (int w = 0; w < C::NW; ++w) {
               const uint4 qf = *reinterpret_cast<const uint4*>(smem + C::OFF_Q + ((j * C::NW + w) * 32 + lane) * 16);
-              uint32_t ha[4], hb[4];
-              e2m1x8_to_f16(wa[w], ha);
-              e2m1x8_to_f16(wb[w], hb);
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                ha[c] = hmul2(ha[c], fa_);
-                hb[c] = hmul2(hb[c], fb_);
+              for (int t = 0; t < C::TPW; ++t) {
+                const __half2 fa_ = jj ? __high2half2(sca[t]) : __low2half2(sca[t]);
+                const __half2 fb_ = jj ? __high2half2(scb[t]) : __low2half2(scb[t]);
+                uint32_t ha[4], hb[4];
+                e2m1x8_to_f16(wa[t][w], ha);
+                e2m1x8_to_f16(wb[t][w], hb);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  ha[c] = hmul2(ha[c], fa_);
+                  hb[c] = hmul2(hb[c], fb_);
+                }
+                mma_f16(acc[t][0], ha[0], hb[0], ha[1], hb[1], qf.x, qf.y);
+                mma_f16(acc[t][1], ha[2], hb[2], ha[3], hb[3], qf.z, qf.w);
               }
-              mma_f16(acc[0], ha[0], hb[0], ha[1], hb[1], qf.x, qf.y);
-              mma_f16(acc[1], ha[2], hb[2], ha[3], hb[3], qf.z, qf.w);
             }
           }
         }
         // ---- scores and weights
-        const int key = warp * kTile + key_row<D>(gid);
-        float s[2][2], se[2][2];
+        const bool part = C::TPW > 1 && warp + (C::TPW - 1) * C::NCW >= ntl;   // the last tile is not there
+        float s[C::TPW][2][2], se[C::TPW][2][2];
         bool grow = false;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int pos = tile0 * kTile + key + 8 * r;
-          const bool vis = !edge || (pos >= lo && pos <= qpos);
-          const float ks = scl[key + 8 * r] * p.scale_log2;
-          const float ve =
-              static_cast<float>(static_cast<int>(__float_as_uint(scl[C::NT * kTile + key + 8 * r]) >> 23) - 127);
+        for (int t = 0; t < C::TPW; ++t)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            s[r][h] = vis ? (acc[0][2 * r + h] + acc[1][2 * r + h]) * ks : -INFINITY;
-            se[r][h] = s[r][h] + ve;
-            grow |= se[r][h] > Mh[h] + SLACK || s[r][h] > ml[h] + 30.0f;
+          for (int r = 0; r < 2; ++r) {
+            const int key = (warp + t * C::NCW) * kTile + key_row<D>(gid) + 8 * r;
+            const int pos = tile0 * kTile + key;
+            const bool vis = !(part && t == C::TPW - 1) && (!edge || (pos >= lo && pos <= qpos));
+            const float ks = scl[key] * p.scale_log2;
+            const float ve = static_cast<float>(static_cast<int>(__float_as_uint(scl[C::NT * kTile + key]) >> 23) - 127);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              s[t][r][h] = vis ? (acc[t][0][2 * r + h] + acc[t][1][2 * r + h]) * ks : -INFINITY;
+              se[t][r][h] = s[t][r][h] + ve;
+              grow |= se[t][r][h] > Mh[h] + SLACK || s[t][r][h] > ml[h] + 30.0f;
+            }
           }
-        }
         float base[2] = {Mh[0], Mh[1]};
         grow = __any_sync(0xffffffffu, grow);
         if (grow) {
-          // rare once O's base has settled: this tile's own base where it
+          // rare once O's base has settled: these tiles' own base where it
           // exceeds O's by more than the slack, and the denominators' bases
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float mn = fmaxf(ml[h], fmaxf(s[0][h], s[1][h]));
+            float mn = ml[h], v = -INFINITY;
+#pragma unroll
+            for (int t = 0; t < C::TPW; ++t) {
+              mn = fmaxf(mn, fmaxf(s[t][0][h], s[t][1][h]));
+              v = fmaxf(v, fmaxf(se[t][0][h], se[t][1][h]));
+            }
             ll[h] *= ex2(ml[h] - mn);
             ml[h] = mn;
-            float v = fmaxf(se[0][h], se[1][h]);
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
             if (v > Mh[h] + SLACK) base[h] = ceilf(v);
-            if (gid == 0) mw[(2 * tig + h) * C::NT + warp] = base[h];
+            if (gid == 0) mw[(2 * tig + h) * C::NCW + warp] = base[h];
           }
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          ll[h] += ex2(s[0][h] - ml[h]) + ex2(s[1][h] - ml[h]);
-          uint8_t* ph = pbuf + warp * C::P_TILE + (2 * tig + h) * C::P_HEAD + gid * 2;
-          *reinterpret_cast<__half*>(ph) = __float2half_rn(ex2(se[0][h] - base[h] + P_OFF));
-          *reinterpret_cast<__half*>(ph + 16) = __float2half_rn(ex2(se[1][h] - base[h] + P_OFF));
-        }
+        for (int t = 0; t < C::TPW; ++t)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            ll[h] += ex2(s[t][0][h] - ml[h]) + ex2(s[t][1][h] - ml[h]);
+            uint8_t* ph = pbuf + (warp + t * C::NCW) * C::P_TILE + (2 * tig + h) * C::P_HEAD + gid * 2;
+            *reinterpret_cast<__half*>(ph) = __float2half_rn(ex2(se[t][0][h] - base[h] + P_OFF));
+            *reinterpret_cast<__half*>(ph + 16) = __float2half_rn(ex2(se[t][1][h] - base[h] + P_OFF));
+          }
         if (lane == 0) flag[warp] = grow;
       } else if (lane == 0) {
         flag[warp] = 0;
@@ -786,10 +808,10 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
 
       // ---- tiles with a base of their own: raise O's base to the largest, and
       // bring every tile's weights to it (exact powers of two)
-      float f[C::NT] = {1.f, 1.f, 1.f, 1.f};
+      float f[C::NCW] = {1.f, 1.f, 1.f, 1.f};
       const int4 fl = *reinterpret_cast<const int4*>(flag);
       if (fl.x | fl.y | fl.z | fl.w) {
-        const float4 v = *reinterpret_cast<const float4*>(mw + gid * C::NT);
+        const float4 v = *reinterpret_cast<const float4*>(mw + gid * C::NCW);
         f[0] = fl.x ? v.x : M;
         f[1] = fl.y ? v.y : M;
         f[2] = fl.z ? v.z : M;
@@ -798,7 +820,7 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
         const float r = ex2(M - Mn);   // 0 where O is still empty
         M = Mn;
 #pragma unroll
-        for (int i = 0; i < C::NT; ++i) f[i] = ex2(f[i] - M);
+        for (int i = 0; i < C::NCW; ++i) f[i] = ex2(f[i] - M);
         const float rA = __shfl_sync(0xffffffffu, r, 8 * tig), rB = __shfl_sync(0xffffffffu, r, 8 * tig + 4);
         Mh[0] = __shfl_sync(0xffffffffu, M, 8 * tig);
         Mh[1] = __shfl_sync(0xffffffffu, M, 8 * tig + 4);
@@ -863,7 +885,7 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
         }
       };
 #pragma unroll 2
-      for (int t = 0; t < ntl; ++t) pv_tile(t, t == 0 ? f[0] : t == 1 ? f[1] : t == 2 ? f[2] : f[3]);
+      for (int t = 0; t < ntl; ++t) pv_tile(t, (t & 3) == 0 ? f[0] : (t & 3) == 1 ? f[1] : (t & 3) == 2 ? f[2] : f[3]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[vst]);
     }
@@ -926,26 +948,25 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
           m = fmaxf(m, v[k].y);
         }
         l = 0.f;
-        float acc[C::MT][4] = {};
+        uint64_t acc[C::MT][2] = {};
 #pragma unroll
         for (int k = 0; k < C::GROUPS; ++k) {
           if (k >= cnt) continue;
           l += v[k].z * ex2(v[k].y - m);
           const float w = ex2(v[k].x - Mo);
-          const float wA = __shfl_sync(0xffffffffu, w, 8 * tig), wB = __shfl_sync(0xffffffffu, w, 8 * tig + 4);
+          const uint64_t w2 = pack_f32x2(__shfl_sync(0xffffffffu, w, 8 * tig), __shfl_sync(0xffffffffu, w, 8 * tig + 4));
 #pragma unroll
           for (int i = 0; i < C::MT; ++i) {
             const float4 t = reinterpret_cast<const float4*>(src + k * C::GSMEM)[i * 128 + tid];
-            acc[i][0] += wA * t.x;
-            acc[i][1] += wB * t.y;
-            acc[i][2] += wA * t.z;
-            acc[i][3] += wB * t.w;
+            acc[i][0] = fma_f32x2(pack_f32x2(t.x, t.y), w2, acc[i][0]);
+            acc[i][1] = fma_f32x2(pack_f32x2(t.z, t.w), w2, acc[i][1]);
           }
         }
 #pragma unroll
-        for (int i = 0; i < C::MT; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) o[i][c] = acc[i][c];
+        for (int i = 0; i < C::MT; ++i) {
+          unpack_f32x2(acc[i][0], o[i][0], o[i][1]);
+          unpack_f32x2(acc[i][1], o[i][2], o[i][3]);
+        }
       }
     }
     // The unit's partials in memory: slot (less u) of the first, their number,
