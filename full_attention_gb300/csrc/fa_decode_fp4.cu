@@ -644,7 +644,14 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
   empty_units<D>(p, share.i, share.n, tid, C::NCW * 32);
   constexpr float P_OFF = 4.0f;    // weights reach 2^P_OFF against a base of their own tile's,
   constexpr float SLACK = 8.0f;    // and 2^(P_OFF + SLACK) against O's base before it is raised
-  int e = 0, step = 0;
+  int slot = 0, step = 0;      // the ring's next slot, and its round's parity
+  uint32_t round = 0;
+  auto advance = [&]() {
+    if (++slot == C::NSLOT) {
+      slot = 0;
+      round ^= 1;
+    }
+  };
   uint32_t merge_phase = 0;
   int P = share.p0;
   for (int u = share.u0; P < share.s_end; ++u) {
@@ -694,12 +701,12 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
       float* mw = reinterpret_cast<float*>(smem + C::OFF_MW) + buf * 8 * C::NCW;
       int* flag = reinterpret_cast<int*>(smem + C::OFF_FLAG) + buf * C::NCW;
       const bool edge = tile0 * kTile < lo || (tile0 + ntl) * kTile - 1 > qpos;   // some keys are masked
-      const int kst = e % C::NSLOT;
-      if (!__all_sync(0xffffffffu, mbar_wait(&full[kst], (e / C::NSLOT) & 1)) && lane == 0) {
+      const int kst = slot;
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[kst], round)) && lane == 0) {
         abort_flag = 1;   // everyone leaves at the barrier below
         atomicOr(p.err, FA_DEV_ERR_TIMEOUT);
       }
-      ++e;
+      advance();
       const uint8_t* kslot = smem + kst * C::SLOT;
       const float* scl = reinterpret_cast<const float*>(kslot + C::NT * C::TILE_BYTES);
       if (warp < ntl) {
@@ -758,7 +765,8 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
             const int pos = tile0 * kTile + key;
             const bool vis = !(part && t == C::TPW - 1) && (!edge || (pos >= lo && pos <= qpos));
             const float ks = scl[key] * p.scale_log2;
-            const float ve = static_cast<float>(static_cast<int>(__float_as_uint(scl[C::NT * kTile + key]) >> 23) - 127);
+            // the exponent of the row's V scale, as a float: behind 2^23, without its bias
+            const float ve = __uint_as_float(0x4b000000u | (__float_as_uint(scl[C::NT * kTile + key]) >> 23)) - 8388735.0f;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               s[t][r][h] = vis ? (acc[t][0][2 * r + h] + acc[t][1][2 * r + h]) * ks : -INFINITY;
@@ -833,12 +841,12 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
         }
       }
 
-      const int vst = e % C::NSLOT;
-      if (!__all_sync(0xffffffffu, mbar_wait(&full[vst], (e / C::NSLOT) & 1)) && lane == 0) {
+      const int vst = slot;
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[vst], round)) && lane == 0) {
         abort_flag = 1;   // everyone leaves at the next barrier
         atomicOr(p.err, FA_DEV_ERR_TIMEOUT);
       }
-      ++e;
+      advance();
       uint8_t* vslot = smem + vst * C::SLOT;
       constexpr int SB = D / 64;   // this warp's block scales per row (bytes)
       if (edge) {
