@@ -818,7 +818,8 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
       // bring every tile's weights to it (exact powers of two)
       float f[C::NCW] = {1.f, 1.f, 1.f, 1.f};
       const int4 fl = *reinterpret_cast<const int4*>(flag);
-      if (fl.x | fl.y | fl.z | fl.w) {
+      const bool scaled = (fl.x | fl.y | fl.z | fl.w) != 0;
+      if (scaled) {
         const float4 v = *reinterpret_cast<const float4*>(mw + gid * C::NCW);
         f[0] = fl.x ? v.x : M;
         f[1] = fl.y ? v.y : M;
@@ -864,12 +865,15 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
         __syncwarp();
       }
       // ---- O^T += V^T P^T over this warp's columns
-      auto pv_tile = [&](int t, float ft) {
+      auto pv_tile = [&](int t) {
         const uint8_t* vt = vslot + t * C::TILE_BYTES;
         const uint32_t* pw = reinterpret_cast<const uint32_t*>(pbuf + t * C::P_TILE + gid * C::P_HEAD);
-        const __half2 fh = __float2half2_rn(ft);
-        const uint32_t fu = *reinterpret_cast<const uint32_t*>(&fh);
-        const uint32_t b0 = hmul2(pw[tig], fu), b1 = hmul2(pw[tig + 4], fu);
+        uint32_t b0 = pw[tig], b1 = pw[tig + 4];
+        if (scaled) {
+          const __half2 fh = __float2half2_rn((t & 3) == 0 ? f[0] : (t & 3) == 1 ? f[1] : (t & 3) == 2 ? f[2] : f[3]);
+          b0 = hmul2(b0, fh);
+          b1 = hmul2(b1, fh);
+        }
         uint32_t w[4][C::NW], sc[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {   // keys 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9
@@ -893,7 +897,7 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
         }
       };
 #pragma unroll 2
-      for (int t = 0; t < ntl; ++t) pv_tile(t, (t & 3) == 0 ? f[0] : (t & 3) == 1 ? f[1] : (t & 3) == 2 ? f[2] : f[3]);
+      for (int t = 0; t < ntl; ++t) pv_tile(t);
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[vst]);
     }
