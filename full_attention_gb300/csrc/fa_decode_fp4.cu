@@ -853,6 +853,7 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
       if (edge) {
         // masked keys have weight 0, but their rows may hold anything (block
         // scales of NaN included): zero this warp's block scales of those rows
+#pragma unroll 1
         for (int r = lane; r < ntl * kTile; r += 32) {
           const int pos = tile0 * kTile + r;
           if (pos < lo || pos > qpos) {
@@ -896,7 +897,7 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
             mma_f16(o[4 * q + i], hmul2(e01[i], s01), hmul2(d01[i], s01), hmul2(e23[i], s23), hmul2(d23[i], s23), b0, b1);
         }
       };
-#pragma unroll 2
+#pragma unroll 4
       for (int t = 0; t < ntl; ++t) pv_tile(t);
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[vst]);
