@@ -243,6 +243,7 @@ struct UnpackArgs {
   int B, Hkv, D, window, page_size, num_pages, max_pages_per_seq, max_len, max_q_len, early_metadata;
   int ring, table_pages;
   unsigned int* err;
+  FastDiv by_page, by_ring;   // page_size, ring (set by the launch)
 };
 cudaError_t launch_unpack(const UnpackArgs& a, cudaStream_t s);
 

@@ -42,22 +42,19 @@ __global__ void __launch_bounds__(256) unpack_kernel(UnpackArgs a) {
     griddep_wait();   // the grid ends only after the kernel before it
     return;
   }
-  int row[R / 2];
-#pragma unroll
-  for (int i = 0; i < R / 2; ++i) {
-    row[i] = -1;
-    if (pos0 + i >= P) continue;
-    const int pg = (pos0 + i) / a.page_size;
-    const int pid = __ldg(a.block_table + static_cast<size_t>(b) * a.max_pages_per_seq + pg);
-    if (pid >= 0 && pid < a.num_pages) row[i] = (pid * a.Hkv + h) * a.page_size + (pos0 + i - pg * a.page_size);
-    else if (lane == 0) atomicOr(a.err, FA_DEV_ERR_PAGE);   // reads as zeros
-  }
+  // R / 2 divides 16, so a warp's positions share a page and lie together in the ring
+  const int pg = a.by_page.div(pos0);
+  const int pid = __ldg(a.block_table + static_cast<size_t>(b) * a.max_pages_per_seq + pg);
+  const bool there = pid >= 0 && pid < a.num_pages;
+  if (!there && lane == 0) atomicOr(a.err, FA_DEV_ERR_PAGE);   // reads as zeros
+  const size_t src = there ? (static_cast<size_t>(pid) * a.Hkv + h) * a.page_size + (pos0 - pg * a.page_size) : 0;
+  const size_t dst = (static_cast<size_t>(b) * a.Hkv + h) * a.ring + (pos0 - static_cast<int>(a.by_ring.div(pos0)) * a.ring);
   griddep_wait();
   RawRow<D, FA_KV_FP4> raw[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    if (row[i / 2] >= 0) {
-      const size_t r = row[i / 2];
+    if (there && pos0 + i / 2 < P) {
+      const size_t r = src + i / 2;
       raw_load<D, FA_KV_FP4>(raw[i], static_cast<const uint8_t*>((i & 1) ? a.v_slab : a.k_slab) + r * kRowBytes<D, FA_KV_FP4>,
                              ((i & 1) ? a.v_scale : a.k_scale) + r, lane);
     } else {
@@ -66,14 +63,15 @@ __global__ void __launch_bounds__(256) unpack_kernel(UnpackArgs a) {
   }
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const int pos = pos0 + i / 2;
-    if (pos >= P) continue;
-    const size_t dst = (static_cast<size_t>(b) * a.Hkv + h) * a.ring + pos % a.ring;
-    raw_to_bf16<D, FA_KV_FP4>(raw[i], static_cast<__nv_bfloat16*>((i & 1) ? a.v : a.k) + dst * D, lane);
+    if (pos0 + i / 2 >= P) continue;
+    raw_to_bf16<D, FA_KV_FP4>(raw[i], static_cast<__nv_bfloat16*>((i & 1) ? a.v : a.k) + (dst + i / 2) * D, lane);
   }
 }
 
-cudaError_t launch_unpack(const UnpackArgs& a, cudaStream_t s) {
+cudaError_t launch_unpack(const UnpackArgs& args, cudaStream_t s) {
+  UnpackArgs a = args;
+  a.by_page = FastDiv(a.page_size);
+  a.by_ring = FastDiv(a.ring);
   const int per_block = 8 * (a.D == 256 ? 4 : 2);   // positions
   const int span = a.ring < a.max_len ? a.ring : a.max_len;
   const long long gy = static_cast<long long>(a.B) * a.Hkv;
