@@ -95,12 +95,15 @@ DecodePlan plan_decode(const fa_cache* c, int layer, int B, int max_seq_len, lon
   // a pipeline step moves 32 KB of K and V; a CTA gets at least 4 steps
   const int tile_bytes = 2 * kTile * d.head_dim * static_cast<int>(elem_bytes(c->kv_dtype));
   p.min_tiles = 4 * (32768 / tile_bytes);
-  // fp4: a CTA gets at least two steps of 64 keys
+  // fp4: a part of a unit holds at least 128 keys, and every unit may have a
+  // share of its own: one after the other they cost some 3.5 us each (10
+  // sequences of 2 to 4 keys, 8 KV heads, 8 units a share: 28.5 us)
   const bool fp4 = c->kv_dtype == FA_KV_FP4;
   if (fp4) p.min_tiles = 8;
   const long long t_bound = static_cast<long long>(p.units) * tiles;
   const long long slots = max_cta > 0 ? max_cta : decode_slots(c);
   long long n = (t_bound + p.min_tiles - 1) / p.min_tiles;
+  if (fp4 && n < p.units) n = p.units;
   if (n > slots) n = slots;
   if (n < 1) n = 1;
   p.ncta = static_cast<int>(n);

@@ -255,7 +255,7 @@ __device__ __forceinline__ bool cut_share_warp(const DecK& p, int cta, int nblk,
     Q = max(Q + 1, static_cast<uint32_t>(static_cast<float>(Q) * total / grid));
   }
   const bool whole = total <= grid;
-  const int ncta = whole ? total : min(grid, static_cast<int>((static_cast<uint32_t>(T) + p.min_tiles - 1) / p.min_tiles));
+  const int ncta = whole ? total : min(grid, T);
   s.n = ncta;
   // as few CTAs as the fullest one allows: fewer units lie across two of them
   const uint32_t most = (static_cast<uint32_t>(ncta) + nblk - 1) / nblk;

@@ -37,6 +37,9 @@ CASES = [
     (W.FULL, 512, 8, 1, 0, [60_001], 64),
     (W.FULL, 256, 8, 2, 0, [30_000, 17, 0, 9_000], 16),
     (W.FULL, 512, 2, 1, 0, [4000, 900, 5000, 100, 2500, 3000, 1, 700, 6000, 2222], 16),
+    # more short units than parts of full length: a share each
+    (W.SLIDING, 256, 24, 8, 1450, [2, 3, 4, 0, 3, 4, 2, 1, 17, 4], 32),
+    (W.FULL, 512, 13, 1, 0, [81, 83], 128),
     # sequences past a warp's registers, in a whole-unit cut and with more units than shares
     (W.FULL, 256, 4, 1, 0, [(37 * i) % 90 if i % 50 else 1700 for i in range(200)], 16),
     (W.FULL, 256, 4, 2, 0, [(53 * i) % 97 for i in range(333)], 16),
