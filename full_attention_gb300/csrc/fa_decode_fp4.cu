@@ -60,6 +60,7 @@ struct F4Cfg {
   static constexpr int GROUPS = 3;                     // shares a CTA works on side by side
   static constexpr int GTHR = (NCW + 1) * 32;          // threads of a group
   static constexpr int NTHR = GROUPS * GTHR;
+  static constexpr int JOIN = D == 256 ? 48 : 24;      // tiles a share reads in the time that joining parts takes it
   static constexpr int NJ = 8;                         // loads of NW words a lane makes per row
   static constexpr int MT = D / 4 / 16;                // m16 tiles of O^T per warp
   static constexpr int P_HEAD = 48;                    // bytes per head of a tile's weights (16 f16 + padding)
@@ -174,6 +175,8 @@ struct F4Share {
   int n, i, nb;        // shares in use, this one, CTAs in use
   int sb, se;          // the CTA's shares
   int cf, nct;         // the whole-unit cut: the unit's first share and its shares (nct 0: laid end to end)
+  int u_end;           // where units are not split: the end of the share's units; else of all
+  bool unsplit;
 };
 
 // The cut, found by one warp from shuffles: one round of loads up to 32
@@ -184,13 +187,20 @@ struct F4Share {
 // crosses from one unit to the next pays a second query load, epilogue and merge
 // in the middle of its stream, which costs more than the uneven parts as long as
 // Q stays below 3/2 of the even share; past that (many units, few shares for
-// each) all lists are laid end to end and cut evenly.  The shares go to the CTAs
-// evenly, in order.  False: nothing to do for this group; s.n is set all the same.
+// each) all lists are laid end to end and cut evenly; but where there are more
+// units than shares and a share's units together are not much longer than the even
+// share, units are dealt out unsplit: parts of units that lie across two shares
+// cost both about what JOIN tiles do.  (Cut evenly against unsplit, us: 255
+// sequences of 4 to 34 keys, 10 heads at 512 19.4 : 11.7; 8 KV heads, 128 sequences
+// of 200 to 256 keys at 512 49.0 : 41.7; at 256 of 1 to 64 keys 27.8 : 15.5, 256
+// sequences of 128 to 256 keys 59.4 : 45.8.)  The shares go to the CTAs evenly, in
+// order.  False: nothing to do for this group; s.n is set all the same.
 //
 // A sequence's units (KV head x chunk) are all alike, so a lane looks at
 // sequences only.  Past 128 of them the loops stay rolled and read the lengths
 // again (from L1): the whole kernel has to come through the instruction cache
 // once per launch, and unrolled copies cost short launches more than the loads.
+template <int JOIN>
 __device__ __forceinline__ bool cut_share_warp(const DecK& p, int cta, int nblk, int group, F4Share& s) {
   const int lane = threadIdx.x & 31;
   const int per = (p.B + 31) / 32;       // sequences of a lane: [lane * per, ...)
@@ -216,11 +226,12 @@ __device__ __forceinline__ bool cut_share_warp(const DecK& p, int cta, int nblk,
   int n4[4];                             // the first four stay in registers
 #pragma unroll
   for (int i = 0; i < 4; ++i) n4[i] = i < per ? tiles(i) : 0;
-  int sum = n4[0] + n4[1] + n4[2] + n4[3], some = (n4[0] > 0) + (n4[1] > 0) + (n4[2] > 0) + (n4[3] > 0);
+  int sum = n4[0] + n4[1] + n4[2] + n4[3], most_n = max(max(n4[0], n4[1]), max(n4[2], n4[3])), some = (n4[0] > 0) + (n4[1] > 0) + (n4[2] > 0) + (n4[3] > 0);
 #pragma unroll 1
   for (int i = 4; i < per; ++i) {
     const int n = tiles(i);
     sum += n;
+    most_n = max(most_n, n);
     some += n > 0;
   }
   if (past && cta == 0 && group == 0) atomicOr(p.err, FA_DEV_ERR_BOUND);
@@ -229,11 +240,14 @@ __device__ __forceinline__ bool cut_share_warp(const DecK& p, int cta, int nblk,
   const int T = __shfl_sync(0xffffffffu, incl, 31);
   s.T = T;
   s.nct = s.cf = s.n = 0;
+  s.u_end = p.units;
   if (T == 0) return false;
   const int grid = p.shares;
   const uint32_t even = max((static_cast<uint32_t>(T) + grid - 1) / grid, static_cast<uint32_t>(p.min_tiles));
   int ks = 0, total = __reduce_add_sync(0xffffffffu, some * hc);
   const bool few = total <= grid;        // else no whole-unit cut: there are more units than shares
+  most_n = __reduce_max_sync(0xffffffffu, most_n);
+  s.unsplit = !few && (p.units + grid - 1) / grid * most_n <= T / grid + JOIN;
   uint32_t Q = even;
   float rq;
   auto parts = [&](int n) {              // ceil(n / Q): the fp32 estimate is put right by one either way
@@ -265,6 +279,14 @@ __device__ __forceinline__ bool cut_share_warp(const DecK& p, int cta, int nblk,
   s.se = share_begin(cta + 1, nb, bq, br);
   const int me = s.i = s.sb + group;
   if (me >= s.se) return false;
+  if (s.unsplit) {
+    const uint32_t q = static_cast<uint32_t>(p.units) / ncta, r = p.units - q * ncta;
+    s.u0 = share_begin(me, ncta, q, r);
+    s.u_end = share_begin(me + 1, ncta, q, r);
+    s.p0 = s.s_beg = 0;
+    s.s_end = INT_MAX;
+    return true;
+  }
   const uint32_t q = static_cast<uint32_t>(T) / ncta, r = T - q * ncta;
   const int s_beg = share_begin(me, ncta, q, r);
   int b0 = -1, p0 = 0, un = 0, k0 = 0, c0 = 0, P = incl - sum, K = scan(ks) - ks;
@@ -532,7 +554,7 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
   // would share the issue slots, 1 us or more on the way to the first copy
   if (warp == C::NCW) {
     F4Share sh;
-    const bool any = cut_share_warp(p, cta, nblk, group, sh);
+    const bool any = cut_share_warp<C::JOIN>(p, cta, nblk, group, sh);
     if (!any) sh.i = -1;
     if (lane == 0) share = sh;
   }
@@ -551,7 +573,7 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
     const bool one = p.tiles_per_page == 1;   // the usual page of 16: no division
     const int s_beg = share.s_beg, s_end = share.s_end;
     int P = share.p0;
-    for (int u = share.u0; ok && P < s_end; ++u) {
+    for (int u = share.u0; ok && P < s_end && u < share.u_end; ++u) {
       const Unit x = unit_at(p, u);
       if (x.n > 0) {
         const int ta = x.t_first + max(s_beg, P) - P;
@@ -654,7 +676,7 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
   };
   uint32_t merge_phase = 0;
   int P = share.p0;
-  for (int u = share.u0; P < share.s_end; ++u) {
+  for (int u = share.u0; P < share.s_end && u < share.u_end; ++u) {
     const Unit x = unit_at(p, u);
     if (x.n == 0) continue;   // an empty unit advances nothing
     const int ta = x.t_first + max(share.s_beg, P) - P;
@@ -931,7 +953,7 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
     // The partials of the unit's shares in this CTA (the whole-unit cut) meet in
     // shared memory: each group leaves its own in the idle ring, lane by lane as
     // the registers lie; the last to arrive adds them up in order and goes on.
-    bool here = false;   // and they are all there are
+    bool here = share.unsplit;   // and they are all there are
     if (share.nct > 0) {
       const int sb = max(share.sb, share.cf), cnt = min(share.se, share.cf + share.nct) - sb, mine = share.i - sb;
       here = cnt == share.nct;

@@ -44,6 +44,8 @@ CASES = [
     (W.FULL, 256, 4, 1, 0, [(37 * i) % 90 if i % 50 else 1700 for i in range(200)], 16),
     (W.FULL, 256, 4, 2, 0, [(53 * i) % 97 for i in range(333)], 16),
     (W.SLIDING, 512, 8, 1, 40, [(29 * i) % 75 for i in range(1025)], 32),
+    (W.FULL, 512, 10, 1, 0, [(31 * i) % 260 for i in range(255)], 16),    # units of up to 17 tiles
+    (W.FULL, 512, 10, 1, 0, [(31 * i) % 257 for i in range(255)], 16),    # and of up to 16
 ]
 
 
