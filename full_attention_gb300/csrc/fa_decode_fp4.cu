@@ -16,23 +16,23 @@
 // scheduler each for a warp's 64 codes, side by side on two pipes, and the matrix
 // instructions (8.5 cycles) do not run beside them.  Measured with the loads left
 // out, long sequences took 98% of their time: 8 sequences of 32k to 131k keys at
-// 512 take 89 us, 4.8 TB/s of 6.8; 64 of 512 to 4096 keys 29 us, 128 windows of
-// 1024 at 256 19 us, where the start (3 us to the first copy, 2 more until it
-// lands) and the joining of the parts (3 to 6 us) weigh as much.
+// 512 take 85 us, 5.0 TB/s of 6.8; 64 of 512 to 4096 keys 28 us, 128 windows of
+// 1024 at 256 18 us, where the start (3 us to the first copy, 2 more until it
+// lands) and the joining of the parts (1 to 5 us) weigh as much.
 //
 // Work decomposition: one CTA per SM of three groups, each with a share of the
 // tile lists and shared memory, barriers and five warps of its own.  (Three CTAs
 // of one group on an SM read as fast, but joined their partials through memory:
-// 95.5, 31.4 and 22.6 us for the above.)  A step is 64 keys, four tiles:
+// 95.5, 31.4 and 22.6 us for the above.)  A step is 128 keys at 256, 64 at 512
+// (64 at 256 as well: 18.6 us for the windows):
 //   warp 4      producer: finds the share; per step one bulk copy per 16-row tile
 //               of K and of V (a tile's rows are contiguous) and of their row
-//               scales, into a ring of six slots at 256 and three at 512, K and V
-//               alternating;
-//   warps 0-3   S^T = K Q^T, each warp one tile over the full head_dim (keys on
-//               the MMA's M side, the 8 heads on N), the softmax weights of its
-//               tile against O's base, or the tile's own base where it exceeds
-//               that by more than the slack, into shared memory as f16; barrier;
-//               then O^T += V^T P^T, each warp a quarter of the columns.
+//               scales, into a ring of three slots, K and V alternating;
+//   warps 0-3   S^T = K Q^T, each warp two tiles or one over the full head_dim
+//               (keys on the MMA's M side, the 8 heads on N), the softmax weights
+//               of its tiles against O's base, or a base of their own where they
+//               exceed that by more than the slack, into shared memory as f16;
+//               barrier; then O^T += V^T P^T, each warp a quarter of the columns.
 // The weights' rounding to f16 is the only one below 32 bits: 2^-11 relative
 // each, while the sum of the weights, in fp32, takes them unrounded.
 //
