@@ -109,7 +109,12 @@ DecodePlan plan_decode(const fa_cache* c, int layer, int B, int max_seq_len, lon
   p.ncta = static_cast<int>(n);
   if (fp4) p.blocks = static_cast<int>(std::min(n, std::max(1LL, slots / 3)));
   if (p.ncta > 1) {
-    const size_t rows = static_cast<size_t>(p.ncta + p.units) * 8;   // partial slots x heads
+    // partial slots x heads.  fp4: one partial a CTA, not a share, where the cut
+    // gives every share one unit's part, as it does with up to a third as many
+    // units as shares (at 3/2 of the even share, ceil(n_u / Q) over the units sum
+    // to at most 2/3 of the shares + the units)
+    const int parts = fp4 && 3LL * p.units <= p.ncta ? p.blocks : p.ncta;
+    const size_t rows = static_cast<size_t>(parts + p.units) * 8;
     // arrival counters: one per unit; fp4: one per partial slot
     p.off_ml = (static_cast<size_t>(p.units + (fp4 ? p.ncta : 0)) * 4 + 255) / 256 * 256;
     p.off_o = p.off_ml + (rows * (fp4 ? 4 : 2) * sizeof(float) + 255) / 256 * 256;

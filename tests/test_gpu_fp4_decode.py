@@ -99,6 +99,35 @@ def test_layer_stack_fused_layers_and_noalloc_agree(window_pool):
     assert a.cache.device_error() == 0 and b.cache.device_error() == 0
 
 
+@pytest.mark.parametrize("D,hkv,lens", [(512, 1, [(97 * i) % 700 for i in range(128)]), (256, 2, [(53 * i) % 97 for i in range(333)]),
+                                        (256, 1, [9000, 0, 40]), (512, 2, [(41 * i) % 350 for i in range(130)]),
+                                        (512, 1, [700 + i for i in range(152)])],
+                         ids=["batch 128", "unsplit", "split", "end to end", "equal"])
+def test_fused_store_and_noalloc_in_every_cut(D, hkv, lens):
+    """The fused store and the allocation-free call, the same bits as store, then decode."""
+    layer = [lay(W.FULL, D, 4 * hkv, hkv)]
+    a, b = (DecodeCase4(layer, lens, 16, seed=13) for _ in range(2))
+    a.store_current()
+    ref = a.decode(0)
+    assert a.cache.device_error() == 0
+    a.check(0, *ref, range(0, len(lens), 41))
+    got = b.decode(0, fused=True)
+    for x, y in zip(a.slabs[0], b.slabs[0]):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    out, lse = a.outs(0)
+    noalloc = lambda: a.cache.decode_noalloc(0, a.q[0], a.bt[0], a.lens_dev, a.max_len, out, lse)
+    if a.cache.decode_workspace_bytes(0, a.B, a.max_len) > 8 << 20:   # more than the library's fixed scratch
+        with pytest.raises(a.fa.FAError) as e:
+            noalloc()
+        assert e.value.status == a.fa.ERR_WORKSPACE and lens != [(97 * i) % 700 for i in range(128)]
+        out, lse = got
+    else:
+        noalloc()
+    for o, l in (got, (out, lse)):
+        assert torch.equal(o.view(torch.int16), ref[0].view(torch.int16)) and torch.equal(l, ref[1])
+    assert a.cache.device_error() == 0 and b.cache.device_error() == 0
+
+
 def test_value_scales_far_apart():
     """Zero V rows under large weights, and V rows 2^110 apart in magnitude: the
     weights follow score + value scale, the denominator the scores alone."""
