@@ -85,6 +85,7 @@ def _load() -> ctypes.CDLL:
 
 _lib = _load()
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # absent in a CPU-only torch
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _live = weakref.WeakSet()   # every Cache not yet destroyed (for device_error())
 
 
@@ -104,7 +105,7 @@ def _p(t):
 def _s(stream):
     # the raw handle: building a torch Stream object costs more than the rest of a call's marshalling
     if stream is None:
-        return _raw_stream(torch._C._cuda_getDevice()) if _raw_stream else torch.cuda.current_stream().cuda_stream
+        return _raw_stream(_get_device()) if _raw_stream else torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream
 
 
@@ -115,7 +116,10 @@ def _ptrs(ts):
 
 def _device() -> int:
     """The current device; -2, which no tensor is on, where no GPU can be reached."""
-    return torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -2
+    try:
+        return _get_device()
+    except Exception:
+        return -2
 
 
 def _need(what, t, dtype, numel, dev):
