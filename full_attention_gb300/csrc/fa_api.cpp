@@ -106,15 +106,18 @@ DecodePlan plan_decode(const fa_cache* c, int layer, int B, int max_seq_len, lon
   if (fp4 && n < p.units) n = p.units;
   if (n > slots) n = slots;
   if (n < 1) n = 1;
+  // With 3 U <= n shares for U units the cut gives every share one unit's part
+  // (at 3/2 of the even share, ceil(n_u / Q) over the units sum to at most 2/3 of
+  // the shares + U), so that a CTA leaves one partial, not one a share.  Fewer
+  // shares than that are no more than the CTAs: the workspace never shrinks as
+  // max_seq_len grows.
+  const long long most = std::max(1LL, slots / 3);
+  if (fp4 && p.units <= most && n < 3LL * p.units && n > most) n = most;
   p.ncta = static_cast<int>(n);
-  if (fp4) p.blocks = static_cast<int>(std::min(n, std::max(1LL, slots / 3)));
+  if (fp4) p.blocks = static_cast<int>(std::min(n, most));
   if (p.ncta > 1) {
-    // partial slots x heads.  fp4: one partial a CTA, not a share, where the cut
-    // gives every share one unit's part, as it does with up to a third as many
-    // units as shares (at 3/2 of the even share, ceil(n_u / Q) over the units sum
-    // to at most 2/3 of the shares + the units)
-    const int parts = fp4 && 3LL * p.units <= p.ncta ? p.blocks : p.ncta;
-    const size_t rows = static_cast<size_t>(parts + p.units) * 8;
+    const int parts = fp4 && p.units <= most ? p.blocks : p.ncta;
+    const size_t rows = static_cast<size_t>(parts + p.units) * 8;   // partial slots x heads
     // arrival counters: one per unit; fp4: one per partial slot
     p.off_ml = (static_cast<size_t>(p.units + (fp4 ? p.ncta : 0)) * 4 + 255) / 256 * 256;
     p.off_o = p.off_ml + (rows * (fp4 ? 4 : 2) * sizeof(float) + 255) / 256 * 256;

@@ -147,6 +147,19 @@ def test_sizes(fa):
     assert e.value.status == fa.ERR_UNSUPPORTED
 
 
+def test_decode_workspace_grows_with_the_call(fa):
+    """A workspace sized for the largest call serves every smaller one."""
+    for D, hq, hkv in ((512, 8, 1), (256, 8, 2), (512, 13, 1), (256, 32, 8)):
+        c = fa.Cache([lay(FULL, D, hq, hkv), lay(SLIDING, D, hq, hkv, 300)], 8, 16, fa.KV_FP4)
+        for layer in (0, 1):
+            lens = [1, 16, 100, 129, 200, 300, 333, 400, 600, 1000, 2000, 5000, 100_000]
+            n = [[c.decode_workspace_bytes(layer, B, L) for L in lens] for B in (1, 2, 3, 7, 19, 50, 51, 75, 100, 150, 152, 153, 200, 456, 500)]
+            for row in n:
+                assert row == sorted(row), (D, hq, layer, row)
+            for col in zip(*n):
+                assert list(col) == sorted(col), (D, hq, layer, col)
+
+
 def test_load_refusals(fa):
     """fa_kv_load checks its arguments on the host, before any launch."""
     lib = fa.lib()
