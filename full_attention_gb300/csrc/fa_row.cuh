@@ -181,6 +181,12 @@ __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
   return r;
 }
 
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // The fp4 format (fa.h, fa_kv_dtype): the row scale 2^e, per block of 16 values
 // the e4m3 scale b nearest to amax_b / (6 * 2^e), per value the e2m1 code
 // nearest to x / (2^e b).  Every rounding is decided exactly without a division
@@ -190,8 +196,8 @@ __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
 //    is off by 2^-25 relative, less than half a step of any midpoint, which has
 //    5 significant bits), and otherwise stays on its side (the quotient of an
 //    8-bit number by 6 is 2^-9 or more away from every midpoint, relatively);
-//  * x * (2^-e / b), with the reciprocal rounded once, is within 2^-21 of the
-//    quotient where that is below 8, and rounding it to a multiple of 2^-12 (a
+//  * x * (2^-e / b), with the hardware's reciprocal (2^-23 relative), is within
+//    2^-20 of the quotient where that is below 8, and rounding it to a multiple of 2^-12 (a
 //    fused product and sum with 2560, whose last place is 2^-12, and the sum
 //    undone) puts an exact tie between two e2m1 values, a multiple of 1/4, back
 //    on the midpoint and moves nothing across one: a quotient of 8 significant
@@ -250,7 +256,7 @@ __device__ __forceinline__ void row_store_fp4(const RowRegs<D>& r, uint8_t* dst,
     const float ab = __uint_as_float(blk[i] << 16) * inv_s;
     const uint32_t sb = __nv_cvt_float_to_fp8(__fmul_rn(ab, 1.0f / 6.0f), __NV_SATFINITE, __NV_E4M3);
     const float b = __half2float(__ushort_as_half(static_cast<unsigned short>(e4m3x2_to_f16x2(sb) & 0xffffu)));
-    const float t = sb ? inv_s * __frcp_rn(b) : 0.0f;
+    const float t = sb ? inv_s * rcp_approx(b) : 0.0f;
     const uint64_t t2 = pack_f32x2(t, t), c2 = pack_f32x2(2560.0f, 2560.0f), n2 = pack_f32x2(-2560.0f, -2560.0f);
     float q[8];
 #pragma unroll

@@ -111,8 +111,10 @@ __device__ __forceinline__ void store_rows(const StoreArgs& a, int warp, int lan
 // fp4: the same with the warp's R rows those of R consecutive tokens for one
 // (KV head, K or V).  Tokens stored together mostly lie in consecutive slots, so
 // the warp's 144- or 288-byte rows and their scales are neighbours in the slab
-// and share their sectors.  A memory pass whose arithmetic just fits beside it:
-// 30011 tokens of 2 KV heads at head_dim 512, 158 MB, take 30 us, 5.2 TB/s of 6.8.
+// and share their sectors.  A memory pass whose arithmetic just fits beside it at
+// head_dim 512: 30011 tokens of 2 KV heads, 158 MB, take 27 us, 5.8 TB/s of 6.8;
+// at 256 it does not quite: 8192 tokens of 8 KV heads, 86 MB, 18 us (with a
+// reciprocal rounded to the last place 30 and 21 us).
 template <int D>
 __device__ __forceinline__ void store_rows_fp4(const StoreArgs& a, int warp, int lane) {
   constexpr int R = StoreShape<D>::R;
@@ -227,7 +229,7 @@ cudaError_t launch_store(const StoreArgs& args, cudaStream_t s) {
 
 // The reverse, any format: a warp's R rows are those of R consecutive tokens for
 // one (KV head, K or V).  Slots, then every row's raw bytes, then the rows out:
-// loads in flight are what it needs.  fp4, the shape above: 27 us, 5.9 TB/s.
+// loads in flight are what it needs.  fp4, the shapes above: 26 and 15 us.
 template <int D, int KV>
 __global__ void __launch_bounds__(256) load_kernel(LoadArgs a) {
   constexpr int R = StoreShape<D>::R;
