@@ -55,6 +55,38 @@ def test_store_bit_for_bit(D, H, ps, T):
         assert np.array_equal(got.cpu().numpy(), w)
 
 
+@pytest.mark.parametrize("D", [256, 512])
+def test_every_quotient_of_a_value_by_a_block_scale(D):
+    """Each block scale with every bf16 magnitude from its largest code's value down to
+    1/128 of that: the store decides each quotient, ties included, as the oracle."""
+    import full_attention_gb300 as fa
+    blocks = []
+    for b in oracle.e4m3_value(np.arange(1, 0x7F, dtype=np.uint8)):
+        top = 6.0 * b                                     # the block's largest magnitude: scale b exactly
+        x = np.ldexp(np.arange(128, 256)[None], np.floor(np.log2(top)).astype(int) - np.arange(7)[:, None] - 7).ravel()
+        x = x[x <= top] * np.where(np.arange((x <= top).sum()) % 3 == 1, -1.0, 1.0)
+        x = np.concatenate([x, np.zeros(-len(x) % 15)]).reshape(-1, 15)
+        blocks.append(np.concatenate([np.full((len(x), 1), top), x], axis=1))
+    blocks = np.concatenate(blocks)
+    per = D // 16 - 1                                     # and a block of 2688, so that the row scale is 1
+    blocks = np.concatenate([blocks, np.zeros((-len(blocks) % per, 16))]).reshape(-1, per, 16)
+    x = np.concatenate([np.full((len(blocks), 1, 16), 2688.0), blocks], axis=1).reshape(len(blocks), 1, D)
+    k = torch.from_numpy(x).to(torch.bfloat16)
+    assert np.array_equal(k.double().numpy(), x)
+    pool = -(-len(x) // 16)
+    cache, slab = _cache(fa, D, 1, 16, pool, fa.KV_FP4)
+    want = [np.zeros(t.shape, t.cpu().numpy().dtype) for t in slab]
+    for t in slab:
+        t.zero_()
+    slots = np.arange(len(x), dtype=np.int32)
+    oracle.store_fp4(*want, bits(k), bits(-k), slots, 16)
+    cache.store(0, k.cuda(), (-k).cuda(), torch.from_numpy(slots).cuda())
+    assert cache.device_error() == 0
+    for got, w in zip(slab, want):
+        assert np.array_equal(got.cpu().numpy(), w)
+    assert set(np.unique(want[0][..., D // 2:])) >= set(range(1, 0x7F)) and (want[2].ravel()[: len(x)] == 1).all()
+
+
 def test_store_layers_and_slot_past_the_pool():
     import full_attention_gb300 as fa
     layers = [W.layer(W.SLIDING, 256, 8, 2, 64), W.layer(W.FULL, 512, 8, 1), W.layer(W.FULL, 512, 8, 1, 0, W.KV_AUTO)]
