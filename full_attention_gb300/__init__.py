@@ -25,7 +25,8 @@ MAX_CACHES = 4096
 FLAG_EARLY_METADATA = 1
 FLAG_EXTEND_SPLIT_ALL = 2
 
-NOALLOC_SCRATCH_BYTES = 8 << 20
+DECODE_COUNTER_BYTES = 32 << 10
+NOALLOC_SCRATCH_BYTES = (8 << 20) + DECODE_COUNTER_BYTES
 MAX_LAYERS_PER_LAUNCH = 16
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_NOT_BOUND, ERR_WORKSPACE, ERR_CUDA = 0, 1, 2, 3, 4, 5

@@ -77,7 +77,9 @@ static size_t slab_row_bytes(int kv_dtype, int D) {
 // ----------------------------------------------------------------- planning
 // Shares of a decode launch the device works on at once: two per SM (a CTA
 // each), three in fp4 (one CTA).
-static long long decode_slots(const fa_cache* c) { return (c->kv_dtype == FA_KV_FP4 ? 3LL : 2LL) * sm_count(); }
+static long long decode_slots(const fa_cache* c) {
+  return std::min((c->kv_dtype == FA_KV_FP4 ? 3LL : 2LL) * sm_count(), static_cast<long long>(kLayerCounters));
+}
 
 DecodePlan plan_decode(const fa_cache* c, int layer, int B, int max_seq_len, long long max_cta) {
   DecodePlan p;
@@ -118,10 +120,8 @@ DecodePlan plan_decode(const fa_cache* c, int layer, int B, int max_seq_len, lon
   if (p.ncta > 1) {
     const int parts = fp4 && p.units <= most ? p.blocks : p.ncta;
     const size_t rows = static_cast<size_t>(parts + p.units) * 8;   // partial slots x heads
-    // arrival counters: one per unit; fp4: one per partial slot
-    p.off_ml = (static_cast<size_t>(p.units + (fp4 ? p.ncta : 0)) * 4 + 255) / 256 * 256;
-    p.off_o = p.off_ml + (rows * (fp4 ? 4 : 2) * sizeof(float) + 255) / 256 * 256;
-    p.ws_bytes = p.off_o + rows * d.head_dim * sizeof(float);
+    p.off_o = (rows * (fp4 ? 4 : 2) * sizeof(float) + 255) / 256 * 256;
+    p.part_bytes = p.off_o + rows * d.head_dim * sizeof(float);
   }
   return p;
 }
@@ -533,7 +533,7 @@ fa_status fa_kv_load(fa_cache* c, int32_t layer, const int32_t* slot_mapping, in
 
 size_t fa_decode_workspace_bytes(const fa_cache* c, int32_t layer, int32_t B, int32_t max_seq_len) {
   if (check_layer(c, layer) != FA_OK || B <= 0 || max_seq_len <= 0) return 0;
-  return plan_decode(c, layer, B, max_seq_len).ws_bytes;
+  return plan_decode(c, layer, B, max_seq_len).ws_bytes();
 }
 
 fa_status fa_kv_store_layers(fa_cache* c, int32_t n, const int32_t* layers, const void* const* k,
@@ -599,8 +599,8 @@ size_t fa_decode_layers_workspace_bytes(const fa_cache* c, int32_t n, const int3
   DecodePlan p[FA_MAX_LAYERS_PER_LAUNCH];
   plan_decode_layers(c, n, layers, B, max_seq_len, p);
   size_t total = 0;
-  for (int i = 0; i < n; ++i) total += (p[i].ws_bytes + 255) / 256 * 256;
-  return total;
+  for (int i = 0; i < n; ++i) total += (p[i].part_bytes + 255) / 256 * 256;
+  return total ? kCounterBytes + total : 0;
 }
 
 namespace fa {
@@ -611,12 +611,13 @@ static fa_status check_tiles(const fa_cache* c, const DecodePlan& p) {
   return FA_OK;
 }
 
-// The launch arguments of one layer's decode (validated by the caller).
+// The launch arguments of one layer's decode (validated by the caller): the
+// place-th of its launch, its partials `off` bytes behind the counters.
 static void fill_decode_args(DecodeArgs& a, const fa_cache* c, int32_t layer, const Slab* s, const DecodePlan& p,
                              const void* q, const void* k_new, const void* v_new, const int32_t* slots,
                              const int32_t* block_table, int32_t max_pages_per_seq, const int32_t* seq_lens,
                              int32_t B, int32_t max_seq_len, void* out, float* lse, void* workspace,
-                             unsigned int* err) {
+                             int place, size_t off, unsigned int* err) {
   const Layer& L = c->layers[layer];
   a.q = q;
   a.block_table = block_table;
@@ -630,7 +631,10 @@ static void fill_decode_args(DecodeArgs& a, const fa_cache* c, int32_t layer, co
   a.v_scale = s->v_scale;
   a.out = out;
   a.lse = lse;
-  a.workspace = p.ws_bytes ? workspace : nullptr;
+  if (p.part_bytes) {
+    a.counters = static_cast<int32_t*>(workspace) + place * kLayerCounters;
+    a.partials = static_cast<char*>(workspace) + kCounterBytes + off;
+  }
   a.tm_k = &s->tm_kt;
   a.tm_v = &s->tm_vt;
   a.tm_ks = &s->tm_ks;
@@ -674,9 +678,10 @@ static fa_status decode_call(fa_cache* c, int32_t layer, const void* q, const vo
                 max_seq_len);
   DecodePlan p = plan_decode(c, layer, B, max_seq_len);
   if ((st = check_tiles(c, p))) return st;
-  if (workspace_bytes < p.ws_bytes || (p.ws_bytes && !workspace))
-    return fail(FA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, p.ws_bytes);
-  if (p.ws_bytes && (reinterpret_cast<uintptr_t>(workspace) & 255u))
+  const size_t need = p.ws_bytes();
+  if (workspace_bytes < need || (need && !workspace))
+    return fail(FA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+  if (need && (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return fail(FA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   cudaError_t ce;
   unsigned int* err = device_error_word(c, &ce);
@@ -684,7 +689,7 @@ static fa_status decode_call(fa_cache* c, int32_t layer, const void* q, const vo
   (void)L;
   DecodeArgs a{};
   fill_decode_args(a, c, layer, s, p, q, k_new, v_new, slots, block_table, max_pages_per_seq, seq_lens, B,
-                   max_seq_len, out, lse, workspace, err);
+                   max_seq_len, out, lse, workspace, 0, 0, err);
   ce = launch_decode(a, static_cast<cudaStream_t>(stream));
   if (ce != cudaSuccess) return fail(FA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(ce));
   return ok();
@@ -764,8 +769,8 @@ fa_status fa_paged_decode_attn_layers(fa_cache* c, int32_t n, const int32_t* lay
     a[i] = DecodeArgs{};
     fill_decode_args(a[i], c, layers[i], s, p, q[i], nullptr, nullptr, nullptr, block_table[i], max_pages_per_seq,
                      seq_lens, B, max_seq_len, out[i], lse ? lse[i] : nullptr,
-                     p.ws_bytes ? static_cast<char*>(workspace) + off : nullptr, err);
-    off += (p.ws_bytes + 255) / 256 * 256;
+                     workspace, i, off, err);
+    off += (p.part_bytes + 255) / 256 * 256;
   }
   ce = launch_decode_layers(a, n, static_cast<cudaStream_t>(stream));
   if (ce != cudaSuccess) return fail(FA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(ce));

@@ -720,11 +720,12 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
         named_bar_sync(1, C::NCW * 32);
         if (threadIdx.x == 0) {
           const int nct = c_last - c_first + 1;
-          const int old = atom_add_acq_rel_gpu(p.counters + u, 1);
+          int* counter = p.counters + c_first + 1;
+          const int old = atom_add_acq_rel_gpu(counter, 1);
           int last = 0;
           if (old == nct - 1) {
             last = 1;
-            atomicExch(p.counters + u, 0);   // leave the counter zero for the next call
+            atomicExch(counter, 0);   // leave the counter zero for the next call
           } else if (old >= nct) {
             atomicOr(p.err, FA_DEV_ERR_WORKSPACE);
           }
@@ -879,20 +880,20 @@ extern "C" fa_status fa_paged_decode_attn_noalloc(fa_cache* cache, int32_t layer
     return fa_paged_decode_attn(cache, layer, q, block_table, max_pages_per_seq, seq_lens, B, max_seq_len, out,
                                 lse, nullptr, 0, stream);
   const fa::DecodePlan plan = fa::plan_decode(cache, layer, B, max_seq_len);
-  if (plan.ws_bytes > FA_NOALLOC_SCRATCH_BYTES)
+  if (plan.ws_bytes() > FA_NOALLOC_SCRATCH_BYTES)
     return fa::fail(FA_ERR_WORKSPACE,
                     "allocation-free decode needs %zu bytes of scratch for B=%d, max_seq_len=%d; its fixed "
                     "scratch holds %zu bytes (use fa_paged_decode_attn with a caller workspace)",
-                    plan.ws_bytes, B, max_seq_len, static_cast<size_t>(FA_NOALLOC_SCRATCH_BYTES));
+                    plan.ws_bytes(), B, max_seq_len, static_cast<size_t>(FA_NOALLOC_SCRATCH_BYTES));
   void* ws = nullptr;
-  if (plan.ws_bytes) {
+  if (plan.ws_bytes()) {
     cudaError_t ce;
     ws = fa::noalloc_scratch(&ce);
     if (!ws) return fa::fail(FA_ERR_CUDA, "scratch address lookup: %s", cudaGetErrorString(ce));
     // the arrival counters must start at zero whatever an earlier call left
-    ce = cudaMemsetAsync(ws, 0, plan.off_ml, static_cast<cudaStream_t>(stream));
+    ce = cudaMemsetAsync(ws, 0, fa::kLayerCounters * sizeof(int32_t), static_cast<cudaStream_t>(stream));
     if (ce != cudaSuccess) return fa::fail(FA_ERR_CUDA, "clearing scratch counters: %s", cudaGetErrorString(ce));
   }
   return fa_paged_decode_attn(cache, layer, q, block_table, max_pages_per_seq, seq_lens, B, max_seq_len, out, lse,
-                              ws, plan.ws_bytes, stream);
+                              ws, plan.ws_bytes(), stream);
 }

@@ -22,8 +22,8 @@ struct DecK {
   const int32_t* slots;
   __nv_bfloat16* out;
   float* lse;
-  int* counters;    // [U] arrival count per unit (fp4: [ncta + U], per node of partials; null: no
-                    // workspace, one CTA); zero between calls
+  int* counters;    // arrivals, indexed by share: a unit's by the second of its shares, the first that
+                    // begins inside it (fp4: see merge_tree); zero between calls; null: one CTA
   float* ml_part;   // [(ncta + U) * 8][2] (fp4: [4])
   float* o_part;    // [(ncta + U) * 8][D]
   unsigned int* err;
@@ -268,11 +268,10 @@ inline DecK make_deck(const DecodeArgs& a) {
   k.slots = a.slots;
   k.out = static_cast<__nv_bfloat16*>(a.out);
   k.lse = a.lse;
-  if (a.workspace) {
-    char* ws = static_cast<char*>(a.workspace);
-    k.counters = reinterpret_cast<int*>(ws);
-    k.ml_part = reinterpret_cast<float*>(ws + a.plan.off_ml);
-    k.o_part = reinterpret_cast<float*>(ws + a.plan.off_o);
+  if (a.partials) {
+    k.counters = a.counters;
+    k.ml_part = static_cast<float*>(a.partials);
+    k.o_part = reinterpret_cast<float*>(static_cast<char*>(a.partials) + a.plan.off_o);
   }
   k.err = a.err;
   k.B = a.B;

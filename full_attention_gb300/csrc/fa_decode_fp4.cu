@@ -365,10 +365,11 @@ __device__ __forceinline__ T sum_parts(const T* x, int mp) {
 // memory lane by lane as the registers do, so the last to arrive keeps its own
 // and adds the others to it: ((0 + 1) + (2 + 3)) + (4 + 5), each sum rounded
 // alike either way round, so results do not depend on who arrives last.  R (six
-// at head_dim 256, five at 512) is what one round of copies can bring in.  Run by the 128 consumer threads of a group; slot0: the slot of
-// the unit's first partial, i: this one's place; o, and Mo, m, l (of head gid).
+// at head_dim 256, five at 512) is what one round of copies can bring in.  Run by the 128 consumer threads of a group; cf: the CTA (or share)
+// of the unit's first partial, slot0: its slot, i: this one's place; o, and Mo,
+// m, l (of head gid).
 template <int D>
-__device__ __forceinline__ bool merge_tree(const DecK& p, size_t slot0, int n, int i, float (&o)[F4Cfg<D>::MT][4], float& Mo,
+__device__ __forceinline__ bool merge_tree(const DecK& p, int cf, size_t slot0, int n, int i, float (&o)[F4Cfg<D>::MT][4], float& Mo,
                                            float& m, float& l, volatile int* last, uint8_t* ring, uint64_t* bar,
                                            uint32_t& phase, int tid, int bid) {
   using C = F4Cfg<D>;
@@ -390,9 +391,9 @@ __device__ __forceinline__ bool merge_tree(const DecK& p, size_t slot0, int n, i
     }
     // arrive: the barrier orders the CTA's partial writes before thread 0's
     // release/acquire add, which publishes them and, for the last arrival,
-    // makes the other CTAs' rows visible.  A group's counter lies in its own
-    // slots: at level l < R its partials are R^l slots apart, and the offset l
-    // keeps the levels' counters apart.
+    // makes the other CTAs' rows visible.  A group's counter is that of one of
+    // its CTAs past the first, all of which begin inside this unit: at level l <
+    // R its partials are R^l apart, and the offset l + 1 keeps the levels' apart.
     named_bar_sync(bid, 128);
     // the parts played: 0 this one, 1 its neighbour, 2 and 3 the first other
     // pair, 4 and 5 the second.  (Of five, only the last has two other pairs and
@@ -404,7 +405,7 @@ __device__ __forceinline__ bool merge_tree(const DecK& p, size_t slot0, int n, i
       return part < 4 ? ka + part - 2 : kb + part - 4;
     };
     if (tid == 0) {
-      int* c = p.counters + base + level;
+      int* c = p.counters + cf + first * st + 1 + level;
       const int old = atom_add_acq_rel_gpu(c, 1);
       if (old == cnt - 1) atomicExch(c, 0);   // zero for the next call
       else if (old >= cnt) atomicOr(p.err, FA_DEV_ERR_WORKSPACE);
@@ -1015,7 +1016,7 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
       nct = part_of(z, parts, of) - cf + 1;
       me = (whole ? cta : share.i) - cf;
     }
-    const bool mine = merge_tree<D>(p, static_cast<size_t>(cf) + u, nct, me, o, Mo, m, l, &lasts[group],
+    const bool mine = merge_tree<D>(p, cf, static_cast<size_t>(cf) + u, nct, me, o, Mo, m, l, &lasts[group],
                                     P + x.n >= share.s_end ? smem : nullptr, mbar_merge, merge_phase, tid, bid);
     if (mine) {
       const int d0 = (8 * warp + gid) * 8 * C::NW;   // this lane's columns: 8 NW from d0 on

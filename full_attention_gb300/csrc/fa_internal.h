@@ -85,7 +85,19 @@ cudaError_t set_smem_once(const void* fn, int bytes, unsigned int* done_mask);
 // The decode kernel splits the concatenated tile lists of all (sequence, KV
 // head, head chunk) units evenly over at most `ncta` CTAs; a unit whose tiles
 // land on one CTA is finished there, the others are merged by the last CTA of
-// the unit to finish (an arrival counter per unit lives in the workspace).
+// the unit to finish, through arrival counters at the head of the workspace.
+//
+// Counters have to be zero when a call starts, partial rows may be anything, and
+// one workspace serves calls of every size: so the counters' place is the same
+// for every call whatever its layers, batch, bound, format or device.  It can be,
+// because a counter belongs to a share of the cut, not to a unit: parts of a unit
+// are joined only where shares begin inside it, a share begins inside one unit
+// at most, and a launch has at most kLayerCounters shares a layer.  (Counters by
+// unit, in front of partials that began where they ended, took an earlier call's
+// partials for counters as soon as a call's batch or bound was larger.)
+constexpr int kLayerCounters = 512;   // three shares on each of up to 170 SMs
+constexpr size_t kCounterBytes = kMaxLayersPerLaunch * kLayerCounters * sizeof(int32_t);   // layer i's at i * kLayerCounters
+static_assert(kCounterBytes == FA_DECODE_COUNTER_BYTES, "fa.h");
 struct DecodePlan {
   int head_chunks = 1;      // ceil(g / 8): query heads are packed 8 per MMA column block
   int units = 0;            // B * Hkv * head_chunks
@@ -93,8 +105,10 @@ struct DecodePlan {
   int min_tiles = 0;        // fewest tiles a CTA is given
   int ncta = 0;             // shares the work may be cut into: CTAs launched (fp4: three a CTA)
   int blocks = 0;           // fp4: CTAs launched
-  size_t off_ml = 0, off_o = 0;   // workspace layout (bytes); counters [units] at 0
-  size_t ws_bytes = 0;
+  size_t off_o = 0;         // partials: (m, l) rows, then from off_o on the rows of O (bytes)
+  size_t part_bytes = 0;    // 0: nothing to join, no workspace needed
+  // the workspace of a call of this layer alone: counters, partials
+  size_t ws_bytes() const { return part_bytes ? kCounterBytes + part_bytes : 0; }
 };
 // max_cta > 0 caps the launch's CTAs for this layer (default: two per SM).
 DecodePlan plan_decode(const fa_cache* c, int layer, int B, int max_seq_len, long long max_cta = 0);
@@ -176,7 +190,8 @@ struct DecodeArgs {
   const float* v_scale;
   void* out;
   float* lse;
-  void* workspace;
+  int32_t* counters;        // [kLayerCounters] (null: nothing to join)
+  void* partials;
   const CUtensorMap* tm_k;
   const CUtensorMap* tm_v;
   const CUtensorMap* tm_ks;

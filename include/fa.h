@@ -306,10 +306,13 @@ FA_API fa_status fa_kv_store(fa_cache* cache, int32_t layer, const void* k, cons
 FA_API fa_status fa_kv_load(fa_cache* cache, int32_t layer, const int32_t* slot_mapping, int32_t T, void* k,
                      void* v, void* stream);
 
+/* Bytes at the head of a decode workspace that hold arrival counters. */
+#define FA_DECODE_COUNTER_BYTES (32u << 10)
+
 /* Workspace bytes fa_paged_decode_attn needs for this layer, batch and bound
- * on the sequence lengths: one arrival counter per (sequence, KV head, group
- * of up to 8 query heads) followed by the split-K partial rows.  0 when a
- * single CTA serves the whole call.  Host only. */
+ * on the sequence lengths: FA_DECODE_COUNTER_BYTES of arrival counters, then
+ * the split-K partial rows.  0 when a single CTA serves the whole call.  Host
+ * only. */
 FA_API size_t fa_decode_workspace_bytes(const fa_cache* cache, int32_t layer, int32_t B,
                                  int32_t max_seq_len);
 
@@ -332,8 +335,10 @@ FA_API size_t fa_decode_workspace_bytes(const fa_cache* cache, int32_t layer, in
  * fa_decode_workspace_bytes(cache, layer, B, max_seq_len) bytes (may be NULL
  * when that is 0), 256-byte aligned.  Zero it once before its first use: its
  * leading counters must start at zero, and every call that completes leaves
- * them zero again, so the same buffer serves later calls on the same stream
- * without clearing.  Calls that run concurrently must not share a workspace.
+ * them zero again.  The counters are the first FA_DECODE_COUNTER_BYTES in every
+ * call, so a buffer large enough for each of them serves later calls on the
+ * same stream without clearing, whatever their layers, batch, bound and format,
+ * multi-layer calls among them.  Calls that run concurrently must not share a workspace.
  * After a call that reported FA_DEV_ERR_TIMEOUT, zero it again (a counter
  * found non-zero sets FA_DEV_ERR_WORKSPACE).  fp4 format: a call whose sequences
  * could hold 2^31 16-row tiles or more (B * num_kv_heads * ceil(g / 8) times
@@ -383,9 +388,9 @@ FA_API fa_status fa_kv_store_layers(fa_cache* cache, int32_t n, const int32_t* l
                                     const void* const* v, const int32_t* const* slot_mapping, int32_t T,
                                     void* stream);
 
-/* Workspace bytes fa_paged_decode_attn_layers needs: the per-layer
- * workspaces of the n layers laid end to end (each 256-byte aligned).  0 on
- * invalid arguments.  Host only. */
+/* Workspace bytes fa_paged_decode_attn_layers needs: the counters, then the
+ * partial rows of the n layers laid end to end (each 256-byte aligned).  0 on
+ * invalid arguments or where no layer has any.  Host only. */
 FA_API size_t fa_decode_layers_workspace_bytes(const fa_cache* cache, int32_t n, const int32_t* layers,
                                                int32_t B, int32_t max_seq_len);
 
@@ -402,8 +407,8 @@ FA_API size_t fa_decode_layers_workspace_bytes(const fa_cache* cache, int32_t n,
  * fa_paged_decode_attn (lse[i] may be NULL; lse itself may be NULL for no
  * lse at all).  seq_lens, B, max_seq_len and max_pages_per_seq are common to
  * all layers.  workspace: at least fa_decode_layers_workspace_bytes bytes,
- * 256-byte aligned, zeroed once, left zero by every completed call (as for
- * fa_paged_decode_attn).  1 <= n <= FA_MAX_LAYERS_PER_LAUNCH. */
+ * 256-byte aligned, zeroed once, its counters left zero by every completed call
+ * (as for fa_paged_decode_attn, whose calls it may serve too).  1 <= n <= FA_MAX_LAYERS_PER_LAUNCH. */
 FA_API fa_status fa_paged_decode_attn_layers(fa_cache* cache, int32_t n, const int32_t* layers,
                                              const void* const* q, const int32_t* const* block_table,
                                              int32_t max_pages_per_seq, const int32_t* seq_lens, int32_t B,
@@ -411,7 +416,7 @@ FA_API fa_status fa_paged_decode_attn_layers(fa_cache* cache, int32_t n, const i
                                              void* workspace, size_t workspace_bytes, void* stream);
 
 /* Largest scratch the allocation-free decode below can use (bytes). */
-#define FA_NOALLOC_SCRATCH_BYTES (8u << 20)
+#define FA_NOALLOC_SCRATCH_BYTES ((8u << 20) + FA_DECODE_COUNTER_BYTES)
 
 /* Allocation-free paged decode attention.  The paper has no counterpart: this
  * entry point exists for callers that cannot allocate device memory, such as
@@ -424,7 +429,8 @@ FA_API fa_status fa_paged_decode_attn_layers(fa_cache* cache, int32_t n, const i
  * loads the library keeps until the process exits.
  * - Limit: a call whose fa_decode_workspace_bytes(cache, layer, B,
  *   max_seq_len) exceeds FA_NOALLOC_SCRATCH_BYTES returns FA_ERR_WORKSPACE and
- *   launches nothing (8 MiB covers, e.g., a batch of 128 at head_dim 512).
+ *   launches nothing (8 MiB of partial rows cover, e.g., a batch of 128 at
+ *   head_dim 512).
  * - Set-up: the first call on each device looks up the array's device address
  *   (with that device current); make that first call before any CUDA-graph
  *   stream capture.
