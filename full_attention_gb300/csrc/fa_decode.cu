@@ -726,7 +726,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
           if (old == nct - 1) {
             last = 1;
             atomicExch(counter, 0);   // leave the counter zero for the next call
-          } else if (old >= nct) {
+          } else if (old < 0 || old >= nct) {
             atomicOr(p.err, FA_DEV_ERR_WORKSPACE);
           }
           sh_last = last;

@@ -408,7 +408,7 @@ __device__ __forceinline__ bool merge_tree(const DecK& p, int cf, size_t slot0, 
       int* c = p.counters + cf + first * st + 1 + level;
       const int old = atom_add_acq_rel_gpu(c, 1);
       if (old == cnt - 1) atomicExch(c, 0);   // zero for the next call
-      else if (old >= cnt) atomicOr(p.err, FA_DEV_ERR_WORKSPACE);
+      else if (old < 0 || old >= cnt) atomicOr(p.err, FA_DEV_ERR_WORKSPACE);
       *last = old == cnt - 1;
       if (old == cnt - 1 && ring) {
         // the others by bulk copies into the ring, Q and weights, idle by now

@@ -88,3 +88,21 @@ def test_one_workspace_serves_caches_of_every_format():
             assert c.cache.device_error() == 0, s
             for g, w in zip(got, want):
                 assert torch.equal(g, w), s
+
+
+@pytest.mark.parametrize("word", [3, -7], ids=["positive", "negative"])
+@pytest.mark.parametrize("kv_dtype", FORMATS, ids=IDS)
+def test_a_workspace_that_was_not_zeroed_is_reported(kv_dtype, word):
+    """Counters that did not start at zero: reported whatever they hold, and a
+    workspace zeroed again serves the next call."""
+    c = Calls(kv_dtype)
+    n, call = c.run(0, 1, 20_000)
+    want = call(c.fa.workspace(n))
+    ws = c.fa.workspace(n)
+    ws[: 1024].view(torch.int32).fill_(word * 1000)
+    call(ws)
+    assert c.cache.device_error() == c.fa.DEV_ERR_WORKSPACE
+    ws.zero_()
+    for g, w in zip(call(ws), want):
+        assert torch.equal(g, w)
+    assert c.cache.device_error() == 0
