@@ -454,6 +454,10 @@ __device__ __forceinline__ bool merge_tree(const DecK& p, int cf, size_t slot0, 
         if (tid == 0) atomicOr(p.err, FA_DEV_ERR_TIMEOUT);
         return false;
       }
+    } else {
+      // warp 0 writes the next level's bases over this one's first: not before
+      // every warp has read them (with the ring the barrier above sees to it)
+      named_bar_sync(bid, 128);
     }
     // a partial that is not there has weight 0 and stands for one that is
     const int some = index(1) < cnt ? 1 : 2;

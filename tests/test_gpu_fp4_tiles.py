@@ -105,3 +105,23 @@ def test_every_tile_counts_once_in_a_launch_of_several_layers():
             for i, (o, l) in zip(ids, outs):
                 check(*cases[i], o, l)
     assert cache.device_error() == 0
+
+
+@pytest.mark.parametrize("D", [256, 512])
+def test_joins_of_shares_that_go_on_to_the_next_unit(D):
+    """Long units between short ones, laid end to end: the share that ends a long
+    unit joins several levels of its parts with its next unit's rows already
+    landing in the ring.  Random values, the same bits on every one of many runs."""
+    rng = np.random.default_rng(3)
+    lens = [int(n) for n in rng.integers(1, 40, 460)]
+    for b, n in ((40, 5003), (41, 9001), (222, 12_345), (300, 3000), (459, 7007)):
+        lens[b] = n
+    case = DecodeCase4([W.layer(W.FULL, D, 8, 1)], lens, 16, seed=21)
+    case.store_current()
+    ws = case.workspace(0)
+    out, lse = case.decode(0, ws)
+    case.check(0, out, lse, [0, 39, 40, 41, 42, 222, 223, 300, 301, 459])
+    for _ in range(200):
+        o, l = case.decode(0, ws)
+        assert torch.equal(o.view(torch.int16), out.view(torch.int16)) and torch.equal(l, lse)
+    assert case.cache.device_error() == 0
