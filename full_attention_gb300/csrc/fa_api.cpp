@@ -835,11 +835,11 @@ static fa_status unpack_for_extend(const fa_cache* c, int32_t layer, ExtendArgs&
   const UnpackLayout ul = unpack_layout(c, layer, a.B, a.max_q_len, a.max_prefix_len);
   if (ul.ring == 0 || ul.bytes > c->unpack_bytes || !unpack_pays(a, ul.ring)) return FA_OK;
   char* ws = static_cast<char*>(c->unpack_ws);
-  const UnpackArgs u{a.keys_in_pages ? a.seq_lens : a.prefix_lens, a.keys_in_pages ? a.qo_indptr : nullptr, a.block_table,
+  const UnpackArgs u{a.keys_in_pages ? a.seq_lens : a.prefix_lens, a.qo_indptr, a.block_table,
                      a.k_slab, a.v_slab, a.k_scale, a.v_scale, ws, ws + ul.off_v,
                      reinterpret_cast<int32_t*>(ws + ul.off_table), a.B, a.Hkv, a.D, a.kind == FA_SLIDING ? a.window : 0,
                      a.page_size, a.num_pages, a.max_pages_per_seq, a.max_prefix_len, a.max_q_len, a.early_metadata,
-                     ul.ring, ul.table_pages, a.err};
+                     a.keys_in_pages, ul.ring, ul.table_pages, a.err};
   const uint64_t rows = static_cast<uint64_t>(a.B) * L.d.num_kv_heads * ul.ring;
   fa_status st;
   if ((st = encode_slab_map(&tm[0], u.k, a.D, FA_KV_BF16, rows))) return st;

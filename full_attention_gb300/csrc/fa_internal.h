@@ -245,8 +245,8 @@ cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t s);
 
 // The fp4 rows of an extend or multi-token decode call as bf16 (fa_unpack.cu).
 struct UnpackArgs {
-  const int32_t* lens;        // prefix lengths, or with qo_indptr sequence lengths
-  const int32_t* qo_indptr;   // multi-token decode: the queries are the last tokens
+  const int32_t* lens;        // prefix lengths, or (stored) sequence lengths
+  const int32_t* qo_indptr;
   const int32_t* block_table;
   const void* k_slab;
   const void* v_slab;
@@ -256,6 +256,7 @@ struct UnpackArgs {
   void* v;
   int32_t* table;   // [B][table_pages]
   int B, Hkv, D, window, page_size, num_pages, max_pages_per_seq, max_len, max_q_len, early_metadata;
+  int stored;   // multi-token decode: the queries are the sequences' last tokens
   int ring, table_pages;
   unsigned int* err;
   FastDiv by_page, by_ring;   // page_size, ring (set by the launch)

@@ -28,17 +28,19 @@ __global__ void __launch_bounds__(256) unpack_kernel(UnpackArgs a) {
   const int b = blockIdx.y / a.Hkv, h = blockIdx.y % a.Hkv;
   const int lane = threadIdx.x & 31;
   // rows [first, P): extend, the prefix; multi-token decode, the whole sequence,
-  // whose last n tokens are the queries
-  const int P = min(__ldg(a.lens + b), a.max_len);
-  const int n = a.qo_indptr ? min(max(__ldg(a.qo_indptr + b + 1) - __ldg(a.qo_indptr + b), 0), a.max_q_len) : 0;
+  // whose last n tokens are the queries.  Nothing sees the rows of a sequence
+  // without new tokens: its pages may be anyone's.
+  const int fresh = min(max(__ldg(a.qo_indptr + b + 1) - __ldg(a.qo_indptr + b), 0), a.max_q_len);
+  const int P = fresh > 0 ? min(__ldg(a.lens + b), a.max_len) : 0;
+  const int n = a.stored ? fresh : 0;
   if (blockIdx.x == 0 && h == 0) {
     griddep_wait();   // the table may still be read by the previous call's kernel
     for (int i = threadIdx.x; i < a.table_pages; i += blockDim.x) a.table[static_cast<size_t>(b) * a.table_pages + i] = b;
   }
   // the first query sees from P - W + 1 on; the extend kernel's tiles start on 16 rows
-  const int lo = a.window > 0 ? max(0, P - n - a.window + 1) & ~15 : 0;
-  const int pos0 = lo + (blockIdx.x * 8 + (threadIdx.x >> 5)) * (R / 2);
-  if (pos0 >= P) {
+  const int first = a.window > 0 ? max(0, P - n - a.window + 1) : 0;
+  const int pos0 = (first & ~15) + (blockIdx.x * 8 + (threadIdx.x >> 5)) * (R / 2);
+  if (first >= P || pos0 >= P) {
     griddep_wait();   // the grid ends only after the kernel before it
     return;
   }
