@@ -249,10 +249,10 @@ class Cache:
         """(k, v, k_scale, v_scale) tensors the layer reads (its source's for a shared layer)."""
         return self._slabs[self.source(layer)]
 
-    def _rows(self, layer: int, k, v, slot_mapping) -> None:
-        """fp4 caches: refuse rows or slots the store would misread."""
+    def _rows(self, layer: int, k, v, slot_mapping, T=None) -> None:
+        """fp4 caches: refuse rows or slots the store of T tokens (None: of every slot) would misread."""
         d, dev = self._layer(layer), _device()
-        _need("slot_mapping", slot_mapping, torch.int32, None, dev)
+        _need("slot_mapping", slot_mapping, torch.int32, T, dev)
         n = slot_mapping.numel() * d["num_kv_heads"] * d["head_dim"]
         _need("k", k, torch.bfloat16, n, dev)
         _need("v", v, torch.bfloat16, n, dev)
@@ -352,7 +352,7 @@ class Cache:
         if self.kv_dtype == KV_FP4:
             self._decode_args(layer, q, block_table, seq_lens, out, lse)
             if self._owns(layer):
-                self._rows(layer, k_new, v_new, slot_mapping)
+                self._rows(layer, k_new, v_new, slot_mapping, q.shape[0])
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         _check(_lib.fa_paged_decode_store_attn(self._h, layer, _p(q), _p(k_new), _p(v_new), _p(slot_mapping),
                                                _p(block_table), int(block_table.shape[1]), _p(seq_lens),

@@ -1,0 +1,63 @@
+"""The binding's checks of a 4-bit cache's tensors, without a GPU: host tensors
+stand for device ones, and what passes the checks meets the library's own refusal
+of a slab that is not bound."""
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+STREAM = SimpleNamespace(cuda_stream=0)
+B, D, HQ, HKV, LEN = 3, 256, 8, 2, 32
+
+
+@pytest.fixture
+def fa(monkeypatch):
+    import __graft_entry__
+    __graft_entry__.build()
+    import full_attention_gb300 as fa
+    monkeypatch.setattr(fa, "_device", lambda: -1)   # where host tensors are
+    return fa
+
+
+def i32(*shape):
+    return torch.zeros(shape, dtype=torch.int32)
+
+
+def bf16(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+@pytest.fixture
+def cache(fa):
+    lay = dict(kind=fa.FULL, head_dim=D, num_q_heads=HQ, num_kv_heads=HKV, window=0, kv_source=fa.KV_OWN, sm_scale=0.0625)
+    return fa.Cache([lay, lay], 8, 16, fa.KV_FP4)
+
+
+def status(fa, call, *args, **kw):
+    with pytest.raises(fa.FAError) as e:
+        call(*args, stream=STREAM, **kw)
+    return e.value.status
+
+
+def decode_args(**m):
+    return {**dict(layer=0, q=bf16(B, HQ, D), block_table=i32(B, LEN // 16), seq_lens=i32(B), max_seq_len=LEN,
+                   out=bf16(B, HQ, D), lse=torch.zeros(B, HQ)), **m}
+
+
+def store_args(**m):
+    return decode_args(k_new=bf16(B, HKV, D), v_new=bf16(B, HKV, D), slot_mapping=i32(B), **m)
+
+
+def test_what_fits_is_taken(fa, cache):
+    assert status(fa, cache.decode, **decode_args()) == fa.ERR_NOT_BOUND
+    assert status(fa, cache.decode_store, **store_args()) == fa.ERR_NOT_BOUND
+    assert status(fa, cache.store, 0, bf16(B, HKV, D), bf16(B, HKV, D), i32(B)) == fa.ERR_NOT_BOUND
+
+
+@pytest.mark.parametrize("rows", [0, 1, B - 1])
+def test_a_fused_store_needs_a_slot_and_rows_for_each_sequence(fa, cache, rows):
+    """The kernel reads slot_mapping[b] of every sequence of the batch."""
+    bad = dict(slot_mapping=i32(rows), k_new=bf16(rows, HKV, D), v_new=bf16(rows, HKV, D))
+    assert status(fa, cache.decode_store, **{**store_args(), **bad}) == fa.ERR_INVALID_ARG
+    for name in bad:
+        assert status(fa, cache.decode_store, **{**store_args(), name: bad[name]}) == fa.ERR_INVALID_ARG
