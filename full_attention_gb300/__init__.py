@@ -133,6 +133,13 @@ def _need(what, t, dtype, numel, dev):
         raise FAError(ERR_INVALID_ARG, f"{what} holds {t.numel()} elements, not {numel}")
 
 
+def _per_layer(layers, **lists) -> None:
+    """Refuse lists the library would read past: one entry for each layer."""
+    for name, xs in lists.items():
+        if xs is not None and len(xs) < max(1, len(layers)):
+            raise FAError(ERR_INVALID_ARG, f"{name} has {len(xs)} entries for {len(layers)} layers")
+
+
 def _i32s(xs):
     return (ctypes.c_int32 * len(xs))(*[int(x) for x in xs])
 
@@ -280,6 +287,7 @@ class Cache:
     def store_layers(self, layers, ks, vs, slot_mappings, stream=None) -> None:
         """fa_kv_store_layers: the stores of several layers in one launch
         (shared layers are skipped)."""
+        _per_layer(layers, ks=ks, vs=vs, slot_mappings=slot_mappings)
         if self.kv_dtype == KV_FP4:
             for i, k, v, s in zip(layers, ks, vs, slot_mappings):
                 if self.source(i) == i:
@@ -307,8 +315,14 @@ class Cache:
                       workspace=None, stream=None) -> None:
         """fa_paged_decode_attn_layers: decode several layers of one head_dim
         in one launch (the current rows must already be stored)."""
+        _per_layer(layers, qs=qs, block_tables=block_tables, outs=outs, lses=lses)
         if self.kv_dtype == KV_FP4:
+            B, width = qs[0].shape[0], block_tables[0].shape[1]
             for n, i in enumerate(layers):
+                bt = block_tables[n]   # every layer's rows are read at the first one's width
+                if bt.shape[1] < width or (B > 1 and bt.shape[1] != width):
+                    raise FAError(ERR_INVALID_ARG, f"block_tables of one launch must have rows of one length, not {bt.shape[1]} "
+                                                   f"and {width}")
                 self._decode_args(i, qs[n], block_tables[n], seq_lens, outs[n], None if lses is None else lses[n])
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         _check(_lib.fa_paged_decode_attn_layers(self._h, len(layers), _i32s(layers), _ptrs(qs), _ptrs(block_tables),

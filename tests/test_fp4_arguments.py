@@ -61,3 +61,34 @@ def test_a_fused_store_needs_a_slot_and_rows_for_each_sequence(fa, cache, rows):
     assert status(fa, cache.decode_store, **{**store_args(), **bad}) == fa.ERR_INVALID_ARG
     for name in bad:
         assert status(fa, cache.decode_store, **{**store_args(), name: bad[name]}) == fa.ERR_INVALID_ARG
+
+
+def layers_args(**m):
+    return {**dict(layers=[0, 1], qs=[bf16(B, HQ, D)] * 2, block_tables=[i32(B, LEN // 16)] * 2, seq_lens=i32(B),
+                   max_seq_len=LEN, outs=[bf16(B, HQ, D)] * 2, lses=[torch.zeros(B, HQ)] * 2), **m}
+
+
+TAKEN = ("ERR_NOT_BOUND", "ERR_WORKSPACE")   # the library's, past the binding's checks
+
+
+def test_block_tables_of_one_launch_are_alike(fa, cache):
+    """All layers' tables are read with one row length, the first one's."""
+    assert status(fa, cache.decode_layers, **layers_args()) in [getattr(fa, s) for s in TAKEN]
+    for narrow in (i32(B, 1), i32(2 * B, 1), i32(B, LEN // 16 + 1)):
+        bad = layers_args(block_tables=[i32(B, LEN // 16), narrow])
+        assert status(fa, cache.decode_layers, **bad) == fa.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kv_dtype", ["KV_BF16", "KV_INT8", "KV_FP8", "KV_FP4"])
+def test_lists_of_a_launch_have_an_entry_for_each_layer(fa, kv_dtype):
+    """The library reads n pointers from each list."""
+    lay = dict(kind=fa.FULL, head_dim=D, num_q_heads=HQ, num_kv_heads=HKV, window=0, kv_source=fa.KV_OWN, sm_scale=0.0625)
+    cache = fa.Cache([lay, lay], 8, 16, getattr(fa, kv_dtype))
+    for name in ("qs", "block_tables", "outs", "lses"):
+        for n in (0, 1):
+            bad = layers_args(**{name: (layers_args()[name] * 2)[:n]})
+            assert status(fa, cache.decode_layers, **bad) == fa.ERR_INVALID_ARG, (name, n)
+    rows = lambda n: [bf16(B, HKV, D)] * n
+    for k, v, s in ((1, 2, 2), (2, 1, 2), (2, 2, 1), (0, 0, 0)):
+        assert status(fa, cache.store_layers, [0, 1], rows(k), rows(v), [i32(B)] * s) == fa.ERR_INVALID_ARG, (k, v, s)
+    assert status(fa, cache.store_layers, [0, 1], rows(2), rows(2), [i32(B)] * 2) != fa.ERR_INVALID_ARG
