@@ -123,14 +123,17 @@ def _device() -> int:
         return -2
 
 
-def _need(what, t, dtype, numel, dev):
+def _need(what, t, dtype, dev, rows=None, per=1):
     """Refuse a tensor the kernels would misread: not on device `dev`, another
-    type, not dense, or (numel not None) another size."""
+    type, not dense, or (rows not None) neither rows * per elements nor more
+    rows of per elements than `rows`."""
     if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != dev:
         raise FAError(ERR_INVALID_ARG, f"{what} must be a dense {dtype} tensor on the current CUDA device, not "
                                        f"{t.dtype}, strides {tuple(t.stride())}, on {t.device}")
-    if numel is not None and t.numel() != numel:
-        raise FAError(ERR_INVALID_ARG, f"{what} holds {t.numel()} elements, not {numel}")
+    if rows is None or t.numel() == rows * per:
+        return
+    if t.dim() == 0 or t.shape[0] < rows or t.numel() != t.shape[0] * per:
+        raise FAError(ERR_INVALID_ARG, f"{what}, of shape {tuple(t.shape)}, must hold {rows} rows of {per} elements")
 
 
 def _per_layer(layers, **lists) -> None:
@@ -222,10 +225,10 @@ class Cache:
     def bind(self, layer: int, k, v, k_scale=None, v_scale=None) -> None:
         if self.kv_dtype == KV_FP4 and None not in (k, v, k_scale, v_scale):
             kv, sc = self.slab_bytes(layer)
-            dev = _device()
+            dev, pages = _device(), self.layer_pages(layer) if kv else None   # a shared layer's refusal is the library's
             for name, t, dt, n in (("k", k, torch.uint8, kv), ("v", v, torch.uint8, kv),
                                    ("k_scale", k_scale, torch.float32, sc // 4), ("v_scale", v_scale, torch.float32, sc // 4)):
-                _need(name, t, dt, n if kv else None, dev)   # a shared layer's refusal is the library's
+                _need(name, t, dt, dev, pages, n // (pages or 1))
         _check(_lib.fa_cache_bind_slab(self._h, layer, _p(k), _p(v), _p(k_scale), _p(v_scale)))
         self._slabs[layer] = (k, v, k_scale, v_scale)
 
@@ -259,10 +262,10 @@ class Cache:
     def _rows(self, layer: int, k, v, slot_mapping, T=None) -> None:
         """fp4 caches: refuse rows or slots the store of T tokens (None: of every slot) would misread."""
         d, dev = self._layer(layer), _device()
-        _need("slot_mapping", slot_mapping, torch.int32, T, dev)
-        n = slot_mapping.numel() * d["num_kv_heads"] * d["head_dim"]
-        _need("k", k, torch.bfloat16, n, dev)
-        _need("v", v, torch.bfloat16, n, dev)
+        _need("slot_mapping", slot_mapping, torch.int32, dev, T)
+        T, row = slot_mapping.numel() if T is None else T, d["num_kv_heads"] * d["head_dim"]
+        _need("k", k, torch.bfloat16, dev, T, row)
+        _need("v", v, torch.bfloat16, dev, T, row)
 
     def store(self, layer: int, k, v, slot_mapping, stream=None) -> None:
         if self.kv_dtype == KV_FP4 and self._owns(layer):
@@ -275,13 +278,12 @@ class Cache:
         [T][Hkv][D]; either may be None), from a slab of any format; a negative
         slot leaves its rows as they were."""
         d, dev = self._layer(layer), _device()
-        _need("slot_mapping", slot_mapping, torch.int32, None, dev)
-        T = slot_mapping.numel()
-        n = T * d["num_kv_heads"] * d["head_dim"]
+        _need("slot_mapping", slot_mapping, torch.int32, dev)
+        T, row = slot_mapping.numel(), d["num_kv_heads"] * d["head_dim"]
         if k is not None:
-            _need("k", k, torch.bfloat16, n, dev)
+            _need("k", k, torch.bfloat16, dev, T, row)
         if v is not None:
-            _need("v", v, torch.bfloat16, n, dev)
+            _need("v", v, torch.bfloat16, dev, T, row)
         _check(_lib.fa_kv_load(self._h, layer, _p(slot_mapping), T, _p(k), _p(v), _s(stream)))
 
     def store_layers(self, layers, ks, vs, slot_mappings, stream=None) -> None:
@@ -291,8 +293,7 @@ class Cache:
         if self.kv_dtype == KV_FP4:
             for i, k, v, s in zip(layers, ks, vs, slot_mappings):
                 if self.source(i) == i:
-                    self._rows(i, k, v, s)
-                    _need("slot_mappings", s, torch.int32, slot_mappings[0].numel(), _device())
+                    self._rows(i, k, v, s, slot_mappings[0].numel())
         T = int(slot_mappings[0].numel())
         _check(_lib.fa_kv_store_layers(self._h, len(layers), _i32s(layers), _ptrs(ks), _ptrs(vs),
                                        _ptrs(slot_mappings), T, _s(stream)))
@@ -300,13 +301,13 @@ class Cache:
     def _decode_args(self, layer: int, q, block_table, seq_lens, out, lse) -> None:
         """fp4 caches: refuse tensors the decode kernel would misread."""
         d, B, dev = self._layer(layer), q.shape[0], _device()
-        n = B * d["num_q_heads"]
-        _need("q", q, torch.bfloat16, n * d["head_dim"], dev)
-        _need("out", out, torch.bfloat16, n * d["head_dim"], dev)
-        _need("seq_lens", seq_lens, torch.int32, B, dev)
-        _need("block_table", block_table, torch.int32, B * block_table.shape[1], dev)
+        row = d["num_q_heads"] * d["head_dim"]
+        _need("q", q, torch.bfloat16, dev, B, row)
+        _need("out", out, torch.bfloat16, dev, B, row)
+        _need("seq_lens", seq_lens, torch.int32, dev, B)
+        _need("block_table", block_table, torch.int32, dev, B, block_table.shape[1])
         if lse is not None:
-            _need("lse", lse, torch.float32, n, dev)
+            _need("lse", lse, torch.float32, dev, B, d["num_q_heads"])
 
     def decode_layers_workspace_bytes(self, layers, batch: int, max_seq_len: int) -> int:
         return int(_lib.fa_decode_layers_workspace_bytes(self._h, len(layers), _i32s(layers), batch, max_seq_len))
@@ -386,17 +387,18 @@ class Cache:
     def _extend_args(self, layer: int, q, indptr, lens, block_table, out, lse, k_ext=None, v_ext=None) -> None:
         """fp4 caches: refuse tensors the extend kernel would misread."""
         d, N, B, dev = self._layer(layer), q.shape[0], lens.numel(), _device()
-        _need("q", q, torch.bfloat16, N * d["num_q_heads"] * d["head_dim"], dev)
-        _need("out", out, torch.bfloat16, q.numel(), dev)
-        _need("qo_indptr", indptr, torch.int32, B + 1, dev)
-        _need("lengths", lens, torch.int32, None, dev)
+        row = d["num_q_heads"] * d["head_dim"]
+        _need("q", q, torch.bfloat16, dev, N, row)
+        _need("out", out, torch.bfloat16, dev, N, row)
+        _need("qo_indptr", indptr, torch.int32, dev, B + 1)
+        _need("lengths", lens, torch.int32, dev)
         for name, t in (("k_ext", k_ext), ("v_ext", v_ext)):
             if t is not None:
-                _need(name, t, torch.bfloat16, N * d["num_kv_heads"] * d["head_dim"], dev)
+                _need(name, t, torch.bfloat16, dev, N, d["num_kv_heads"] * d["head_dim"])
         if block_table is not None:
-            _need("block_table", block_table, torch.int32, B * block_table.shape[1], dev)
+            _need("block_table", block_table, torch.int32, dev, B, block_table.shape[1])
         if lse is not None:
-            _need("lse", lse, torch.float32, N * d["num_q_heads"], dev)
+            _need("lse", lse, torch.float32, dev, N, d["num_q_heads"])
 
     def decode_multi(self, layer: int, q, qo_indptr, seq_lens, block_table, max_q_len: int, max_seq_len: int, out,
                      lse=None, stream=None) -> None:

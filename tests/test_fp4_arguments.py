@@ -92,3 +92,34 @@ def test_lists_of_a_launch_have_an_entry_for_each_layer(fa, kv_dtype):
     for k, v, s in ((1, 2, 2), (2, 1, 2), (2, 2, 1), (0, 0, 0)):
         assert status(fa, cache.store_layers, [0, 1], rows(k), rows(v), [i32(B)] * s) == fa.ERR_INVALID_ARG, (k, v, s)
     assert status(fa, cache.store_layers, [0, 1], rows(2), rows(2), [i32(B)] * 2) != fa.ERR_INVALID_ARG
+
+
+def test_buffers_with_rows_to_spare_are_taken(fa, cache):
+    """Tables, lengths and outputs kept for a larger batch, as a captured graph's are."""
+    spare = dict(seq_lens=i32(B + 5), block_table=i32(B + 5, LEN // 16), out=bf16(B + 5, HQ, D), lse=torch.zeros(B + 5, HQ))
+    slots = dict(slot_mapping=i32(B + 5), k_new=bf16(B + 5, HKV, D), v_new=bf16(B + 5, HKV, D))
+    for name in spare:
+        assert status(fa, cache.decode, **decode_args(**{name: spare[name]})) == fa.ERR_NOT_BOUND, name
+    assert status(fa, cache.decode, **decode_args(**spare)) == fa.ERR_NOT_BOUND
+    assert status(fa, cache.decode_noalloc, **decode_args(**spare)) != fa.ERR_INVALID_ARG
+    assert status(fa, cache.decode_store, **{**store_args(**spare), **slots}) == fa.ERR_NOT_BOUND
+    assert status(fa, cache.store, 0, bf16(B + 5, HKV, D), bf16(B + 5, HKV, D), i32(B)) == fa.ERR_NOT_BOUND
+    wide = layers_args(seq_lens=i32(B + 5), block_tables=[i32(B + 1, 2), i32(B + 5, 2)], outs=[bf16(B + 5, HQ, D)] * 2)
+    assert status(fa, cache.decode_layers, **wide) in [getattr(fa, s) for s in TAKEN]
+    for kv in (fa.KV_BF16, fa.KV_FP4):
+        c = fa.Cache(cache.layers, 8, 16, kv)
+        assert status(fa, c.load, 0, i32(B), bf16(B + 5, HKV, D), bf16(B + 5, HKV, D)) == fa.ERR_NOT_BOUND
+    N = 7
+    ext = dict(layer=0, q=bf16(N, HQ, D), qo_indptr=i32(B + 9), block_table=i32(B + 5, 2), max_q_len=4, out=bf16(N + 5, HQ, D),
+               lse=torch.zeros(N + 5, HQ))
+    assert status(fa, cache.extend, **ext, k_ext=bf16(N + 5, HKV, D), v_ext=bf16(N + 5, HKV, D), prefix_lens=i32(B),
+                  max_prefix_len=LEN) == fa.ERR_NOT_BOUND
+    assert status(fa, cache.decode_multi, **ext, seq_lens=i32(B), max_seq_len=LEN) == fa.ERR_NOT_BOUND
+
+
+def test_buffers_too_small_or_not_dense_are_refused(fa, cache):
+    for bad in (dict(seq_lens=i32(B - 1)), dict(block_table=i32(B - 1, 2)), dict(out=bf16(B - 1, HQ, D)),
+                dict(lse=torch.zeros(B - 1, HQ)), dict(block_table=i32(B, 4)[:, :2]), dict(seq_lens=i32(2 * B)[::2]),
+                dict(q=bf16(B, HQ, 2 * D)[..., ::2]), dict(seq_lens=i32(B).long()), dict(q=bf16(B, HQ, D).half()),
+                dict(q=bf16(B, HQ, D - 16))):
+        assert status(fa, cache.decode, **decode_args(**bad)) == fa.ERR_INVALID_ARG, bad.keys()

@@ -29,3 +29,17 @@ def test_a_window_of_one_reads_no_prefix_pages():
         out, lse = c.run(0)
         assert c.cache.device_error() == 0, split
         c.check(0, out, lse)
+
+
+def test_padded_buffers_as_kept_for_a_captured_graph():
+    """Tables, lengths and outputs with rows to spare: the rows past the batch stay as they are."""
+    from fp4_case import DecodeCase4
+    case = DecodeCase4([W.layer(W.FULL, 512, 8, 1)], [300, 40, 0, 1000], 16, seed=63)
+    case.store_current()
+    want = case.decode(0)
+    pad = lambda t, fill: torch.cat([t, torch.full((3, *t.shape[1:]), fill, dtype=t.dtype, device="cuda")])
+    out, lse = (torch.full((7, *t.shape[1:]), 9.0, dtype=t.dtype, device="cuda") for t in want)
+    case.cache.decode(0, case.q[0], pad(case.bt[0], 1 << 30), pad(case.lens_dev, 1 << 30), case.max_len, out, lse, case.workspace(0))
+    assert case.cache.device_error() == 0
+    for got, w in zip((out, lse), want):
+        assert torch.equal(got[:4], w) and (got[4:] == 9.0).all()
