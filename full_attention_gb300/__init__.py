@@ -124,9 +124,11 @@ def _device() -> int:
 
 
 def _need(what, t, dtype, dev, rows=None, per=1):
-    """Refuse a tensor the kernels would misread: not on device `dev`, another
+    """Refuse a tensor the kernels would misread: none, not on device `dev`, another
     type, not dense, or (rows not None) neither rows * per elements nor more
     rows of per elements than `rows`."""
+    if t is None:
+        raise FAError(ERR_INVALID_ARG, f"{what} must be non-NULL")
     if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != dev:
         raise FAError(ERR_INVALID_ARG, f"{what} must be a dense {dtype} tensor on the current CUDA device, not "
                                        f"{t.dtype}, strides {tuple(t.stride())}, on {t.device}")

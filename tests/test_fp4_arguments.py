@@ -123,3 +123,15 @@ def test_buffers_too_small_or_not_dense_are_refused(fa, cache):
                 dict(q=bf16(B, HQ, 2 * D)[..., ::2]), dict(seq_lens=i32(B).long()), dict(q=bf16(B, HQ, D).half()),
                 dict(q=bf16(B, HQ, D - 16))):
         assert status(fa, cache.decode, **decode_args(**bad)) == fa.ERR_INVALID_ARG, bad.keys()
+
+
+@pytest.mark.parametrize("kv_dtype", ["KV_BF16", "KV_FP4"])
+def test_a_missing_tensor_is_refused_as_in_the_other_formats(fa, kv_dtype):
+    """(Past the layer and the slab, which the library looks at first.)"""
+    lay = dict(kind=fa.FULL, head_dim=D, num_q_heads=HQ, num_kv_heads=HKV, window=0, kv_source=fa.KV_OWN, sm_scale=0.0625)
+    cache = fa.Cache([lay, lay], 8, 16, getattr(fa, kv_dtype))
+    refused = (fa.ERR_INVALID_ARG, fa.ERR_NOT_BOUND)
+    assert status(fa, cache.store, 0, None, bf16(B, HKV, D), i32(B)) in refused
+    assert status(fa, cache.store, 0, bf16(B, HKV, D), None, i32(B)) in refused
+    for name in ("k_new", "v_new", "slot_mapping", "seq_lens", "out"):
+        assert status(fa, cache.decode_store, **{**store_args(), name: None}) in refused, name
