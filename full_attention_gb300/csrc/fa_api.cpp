@@ -89,7 +89,7 @@ DecodePlan plan_decode(const fa_cache* c, int layer, int B, int max_seq_len, lon
   if (B <= 0 || max_seq_len <= 0) return p;
   int tiles = (max_seq_len - 1) / kTile + 1;
   if (d.kind == FA_SLIDING) {
-    const int win_tiles = (d.window + kTile - 2) / kTile + 1;   // tiles a W-row window can span
+    const int win_tiles = static_cast<int>((static_cast<int64_t>(d.window) + kTile - 2) / kTile) + 1;   // tiles a W-row window can span
     if (win_tiles < tiles) tiles = win_tiles;
   }
   p.max_tiles = tiles;
@@ -909,7 +909,7 @@ fa_status fa_paged_extend_attn(fa_cache* c, int32_t layer, const void* q, const 
     return fail(FA_ERR_INVALID_ARG, "a required pointer is NULL");
   if (!aligned16(q) || !aligned16(k_ext) || !aligned16(v_ext) || !aligned16(out))
     return fail(FA_ERR_INVALID_ARG, "q, k_ext, v_ext, out must be 16-byte aligned");
-  if (max_prefix_len > 0 && max_pages_per_seq < (max_prefix_len + c->page_size - 1) / c->page_size)
+  if (max_prefix_len > 0 && max_pages_per_seq < (max_prefix_len - 1) / c->page_size + 1)
     return fail(FA_ERR_INVALID_ARG, "max_pages_per_seq %d cannot hold max_prefix_len %d", max_pages_per_seq,
                 max_prefix_len);
   cudaError_t ce;

@@ -135,3 +135,18 @@ def test_a_missing_tensor_is_refused_as_in_the_other_formats(fa, kv_dtype):
     assert status(fa, cache.store, 0, bf16(B, HKV, D), None, i32(B)) in refused
     for name in ("k_new", "v_new", "slot_mapping", "seq_lens", "out"):
         assert status(fa, cache.decode_store, **{**store_args(), name: None}) in refused, name
+
+
+@pytest.mark.parametrize("kv_dtype", ["KV_BF16", "KV_INT8", "KV_FP8", "KV_FP4"])
+def test_a_window_of_any_size_is_planned(fa, kv_dtype):
+    """A window past every length plans as a full layer does, up to the largest int."""
+    def need(window, n):
+        lay = dict(kind=fa.SLIDING if window else fa.FULL, head_dim=D, num_q_heads=HQ, num_kv_heads=HKV, window=window,
+                   kv_source=fa.KV_OWN, sm_scale=0.0625)
+        c = fa.Cache([lay, lay], 8, 16, getattr(fa, kv_dtype))
+        return c.decode_workspace_bytes(0, B, n), c.decode_layers_workspace_bytes([0, 1], B, n)
+    for n in (5000, 100_000, 2**31 - 1):
+        full = need(0, n)
+        assert full[0] > 0
+        for window in (2**31 - 17, 2**31 - 16, 2**31 - 15, 2**31 - 1):
+            assert need(window, n) == full

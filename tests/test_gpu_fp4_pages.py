@@ -43,3 +43,21 @@ def test_padded_buffers_as_kept_for_a_captured_graph():
     assert case.cache.device_error() == 0
     for got, w in zip((out, lse), want):
         assert torch.equal(got[:4], w) and (got[4:] == 9.0).all()
+
+
+@pytest.mark.parametrize("kv_dtype", [W.KV_BF16, W.KV_INT8, W.KV_FP8, W.KV_FP4], ids=["bf16", "int8", "fp8", "fp4"])
+def test_tables_too_narrow_for_the_largest_bounds_are_refused(kv_dtype):
+    """Refused on the host, before any launch."""
+    import full_attention_gb300 as fa
+    cache = fa.Cache([W.layer(W.FULL, 256, 8, 1)], 8, 16, kv_dtype)
+    cache.allocate("cuda")
+    q, kv = torch.zeros((2, 8, 256), dtype=torch.bfloat16, device="cuda"), torch.zeros((2, 1, 256), dtype=torch.bfloat16, device="cuda")
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    bt = torch.zeros((2, 4), dtype=torch.int32, device="cuda")
+    for bound in (65, 2**31 - 20, 2**31 - 1):
+        for call in (lambda: cache.extend(0, q, kv, kv, i32(0, 1, 2), i32(3, 3), bt, 1, bound, torch.empty_like(q)),
+                     lambda: cache.decode_multi(0, q, i32(0, 1, 2), i32(3, 3), bt, 1, bound, torch.empty_like(q)),
+                     lambda: cache.decode(0, q, bt, i32(3, 3), bound, torch.empty_like(q))):
+            with pytest.raises(fa.FAError) as e:
+                call()
+            assert e.value.status == fa.ERR_INVALID_ARG, bound
