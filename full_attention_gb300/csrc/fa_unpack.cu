@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(256) unpack_kernel(UnpackArgs a) {
   // without new tokens: its pages may be anyone's.
   const int fresh = min(max(__ldg(a.qo_indptr + b + 1) - __ldg(a.qo_indptr + b), 0), a.max_q_len);
   const int P = fresh > 0 ? min(__ldg(a.lens + b), a.max_len) : 0;
-  const int n = a.stored ? fresh : 0;
+  const int n = a.stored ? min(fresh, P) : 0;   // (a length below the new tokens is reported by the extend kernel)
   if (blockIdx.x == 0 && h == 0) {
     griddep_wait();   // the table may still be read by the previous call's kernel
     for (int i = threadIdx.x; i < a.table_pages; i += blockDim.x) a.table[static_cast<size_t>(b) * a.table_pages + i] = b;

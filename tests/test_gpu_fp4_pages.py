@@ -61,3 +61,17 @@ def test_tables_too_narrow_for_the_largest_bounds_are_refused(kv_dtype):
             with pytest.raises(fa.FAError) as e:
                 call()
             assert e.value.status == fa.ERR_INVALID_ARG, bound
+
+
+def test_a_length_below_its_new_tokens_under_the_widest_window():
+    """Reported; what the call still computes is the same with and without unpacked rows."""
+    layer = W.layer(W.SLIDING, 512, 8, 1, 2**31 - 1)
+    outs = []
+    for split in (None, "unpack"):
+        c = ExtendCase4([layer], [700, 300], [40, 6], 16, seed=64, stored=True, split=split)
+        c.check(0, *c.run(0))
+        c.lens_dev[1] = 1
+        out, lse = c.run(0)
+        assert c.cache.device_error() == c.fa.DEV_ERR_BOUND
+        outs.append(out)
+    assert torch.equal(outs[0][40], outs[1][40])   # one key: its value, exact on both paths
