@@ -105,7 +105,9 @@ typedef enum {
  * that rounds to zero is code 0.  e2m1 codes 0 .. 7 stand for 0, 0.5, 1, 1.5, 2, 3, 4, 6, codes 8 .. 15
  * for their negatives.  A block whose scale is 0 keeps zeros.  The value of a
  * code is code * b * s: 6 significant bits, so reading a row back into bf16
- * rounds nothing.  A NaN element is stored as 0, a magnitude above 2^127 (the
+ * rounds nothing.  Slabs written by other means than this library have to keep
+ * to it, the row scales powers of two in [2^-116, 2^116] above all: the decode
+ * kernel takes a V scale's exponent alone.  A NaN element is stored as 0, a magnitude above 2^127 (the
  * infinities included) as 2^127.  A token costs 2 * (D * 9 / 16 + 4) bytes per
  * KV head: 3.5 times less than bf16. */
 typedef enum { FA_KV_BF16 = 0, FA_KV_INT8 = 1, FA_KV_FP8 = 2, FA_KV_FP4 = 3 } fa_kv_dtype;
@@ -224,7 +226,12 @@ FA_API fa_status fa_cache_bind_extend_workspace(fa_cache* cache, void* workspace
  * bf16), and a block table.  Bind a workspace of fa_extend_workspace_bytes()
  * plus the largest of these of the layers and calls it serves: such calls then
  * unpack once and run the bf16 kernel where that is faster (about twice on
- * long chunks); q and the chunk have no f16 range there.  A call that needs
+ * long chunks).  That kernel takes q and the chunk as they are, without f16's
+ * range, and rounds the softmax weights p_j to bf16, where the converting one
+ * rounds them to f16: an output may be off by 2^-7 |out| + 1.5 * 2^-8 sum_j p_j
+ * |v_j| instead of 2^-8 of both (out's own rounding to bf16 included).  Whether
+ * a call unpacks goes by its sizes, the bounds and the room, not by the data.
+ * A call that needs
  * more room than the workspace has, or has none bound, converts the codes
  * inside the kernel.  0 in the other formats.  Host only. */
 FA_API size_t fa_extend_unpack_bytes(const fa_cache* cache, int32_t layer, int32_t B, int32_t max_q_len,
@@ -317,7 +324,8 @@ FA_API size_t fa_decode_workspace_bytes(const fa_cache* cache, int32_t layer, in
                                  int32_t max_seq_len);
 
 /* Paged decode attention, one new token per sequence (split-K online softmax,
- * GQA-packed so each KV page is read once for all Hq / Hkv query heads).
+ * GQA-packed: each KV page is read once for up to 8 query heads of its KV head,
+ * so ceil(Hq / Hkv / 8) times).
  * q: bf16 [B][Hq][D] (device).  block_table: int32 [B][max_pages_per_seq].
  * seq_lens: int32 [B], the context length INCLUDING the current token, whose
  * k, v must already be stored; the query sits at q_pos = seq_lens[b] - 1.
@@ -331,7 +339,8 @@ FA_API size_t fa_decode_workspace_bytes(const fa_cache* cache, int32_t layer, in
  * sum-exp of the scaled scores.  seq_lens[b] <= 0 gives out = 0 and
  * lse = -inf.  Over 8- and 4-bit slabs q is converted to f16 for the tensor cores:
  * an element of magnitude 65536 or more saturates to +-65504 and sets
- * FA_DEV_ERR_RANGE.  workspace: device scratch of at least
+ * FA_DEV_ERR_RANGE; one below f16's smallest normal (6.1e-5) is rounded to a
+ * multiple of 2^-24, to 0 up to 2^-25, and that is not reported.  workspace: device scratch of at least
  * fa_decode_workspace_bytes(cache, layer, B, max_seq_len) bytes (may be NULL
  * when that is 0), 256-byte aligned.  Zero it once before its first use: its
  * leading counters must start at zero, and every call that completes leaves
@@ -394,9 +403,12 @@ FA_API fa_status fa_kv_store_layers(fa_cache* cache, int32_t n, const int32_t* l
 FA_API size_t fa_decode_layers_workspace_bytes(const fa_cache* cache, int32_t n, const int32_t* layers,
                                                int32_t B, int32_t max_seq_len);
 
-/* Paged decode attention of n layers in one launch: the same result per
- * layer, bit for bit, as fa_paged_decode_attn on that layer, with one launch
- * ramp and one tail for all of them instead of one each.  For callers that have the queries of
+/* Paged decode attention of n layers in one launch: the result per layer of
+ * fa_paged_decode_attn on that layer, with one launch ramp and one tail for all
+ * of them instead of one each.  The layers share the device, so a sequence may
+ * be cut into fewer parts than by a call of its own, and the sums of the parts
+ * then round otherwise: the results agree within the format's rounding, and
+ * bit for bit with the same call made again.  For callers that have the queries of
  * several layers at once: a step that decodes several independent layer
  * stacks, or a benchmark of the attention of a whole step.  The layers must
  * share head_dim and the cache's KV format (a full and a sliding group take
@@ -460,8 +472,11 @@ FA_API fa_status fa_paged_decode_attn_noalloc(fa_cache* cache, int32_t layer, co
  * between 65280 and 65536, f16 nothing past 65504) saturates to +-65504 and
  * sets FA_DEV_ERR_RANGE; the output is then not the exact attention.  Stored
  * prefix rows have no such limit, and their small magnitudes keep full
- * relative accuracy; chunk values below f16's smallest normal (6.1e-5) are
- * kept as f16 subnormals in steps of 2^-24.  Every slab format: a scaled score |sm_scale * q.k|
+ * relative accuracy; q and chunk values below f16's smallest normal (6.1e-5)
+ * are kept as f16 subnormals in steps of 2^-24.  (A call over a 4-bit slab that
+ * unpacks its rows, fa_extend_unpack_bytes, computes as over a bf16 slab
+ * instead: bf16 operands without f16's range, and the softmax weights rounded to
+ * bf16, 8 significant bits for f16's 11.)  Every slab format: a scaled score |sm_scale * q.k|
  * of 32767 / log2(e) (about 22700) or more is out of range (FA_DEV_ERR_RANGE;
  * the two softmax halves of a row agree on an integer base, kept in 16 bits).
  * q: bf16 [N][Hq][D], k_ext, v_ext: bf16 [N][Hkv][D] with N = qo_indptr[B]
