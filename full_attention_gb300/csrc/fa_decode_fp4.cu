@@ -81,6 +81,9 @@ struct F4Cfg {
 
 // "No score yet": finite, so that differences against it are never NaN.
 constexpr float kNoScore = -3.402823466e38f;
+// O's base is an integer, so that sums with it and the values' exponents are
+// exact: up to this magnitude (a larger one is reported).
+constexpr float kMaxBase = 8388608.0f;   // 2^23
 
 // What runs once or rarely in a launch stays out of line: all of the code has to
 // come through the instruction cache, which short launches wait for.
@@ -782,7 +785,7 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
         }
         // ---- scores and weights
         const bool part = C::TPW > 1 && warp + (C::TPW - 1) * C::NCW >= ntl;   // the last tile is not there
-        float s[C::TPW][2][2], se[C::TPW][2][2];
+        float s[C::TPW][2][2], ve[C::TPW][2];
         bool grow = false;
 #pragma unroll
         for (int t = 0; t < C::TPW; ++t)
@@ -793,12 +796,11 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
             const bool vis = !(part && t == C::TPW - 1) && (!edge || (pos >= lo && pos <= qpos));
             const float ks = scl[key] * p.scale_log2;
             // the exponent of the row's V scale, as a float: behind 2^23, without its bias
-            const float ve = __uint_as_float(0x4b000000u | (__float_as_uint(scl[C::NT * kTile + key]) >> 23)) - 8388735.0f;
+            ve[t][r] = __uint_as_float(0x4b000000u | (__float_as_uint(scl[C::NT * kTile + key]) >> 23)) - 8388735.0f;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               s[t][r][h] = vis ? (acc[t][0][2 * r + h] + acc[t][1][2 * r + h]) * ks : -INFINITY;
-              se[t][r][h] = s[t][r][h] + ve;
-              grow |= se[t][r][h] > Mh[h] + SLACK || s[t][r][h] > ml[h] + 30.0f;
+              grow |= s[t][r][h] + ve[t][r] > Mh[h] + SLACK || s[t][r][h] > ml[h] + 30.0f;
             }
           }
         float base[2] = {Mh[0], Mh[1]};
@@ -812,7 +814,7 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
 #pragma unroll
             for (int t = 0; t < C::TPW; ++t) {
               mn = fmaxf(mn, fmaxf(s[t][0][h], s[t][1][h]));
-              v = fmaxf(v, fmaxf(se[t][0][h], se[t][1][h]));
+              v = fmaxf(v, fmaxf(s[t][0][h] + ve[t][0], s[t][1][h] + ve[t][1]));
             }
             ll[h] *= ex2(ml[h] - mn);
             ml[h] = mn;
@@ -823,14 +825,17 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
             if (gid == 0) mw[(2 * tig + h) * C::NCW + warp] = base[h];
           }
         }
+        // s - (base - P_OFF - e): the bracket holds integers alone and is exact, and
+        // so is a difference of neighbours; s + e would round at s's own scale
 #pragma unroll
         for (int t = 0; t < C::TPW; ++t)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
+            const float bp = base[h] - P_OFF;
             ll[h] += ex2(s[t][0][h] - ml[h]) + ex2(s[t][1][h] - ml[h]);
             uint8_t* ph = pbuf + (warp + t * C::NCW) * C::P_TILE + (2 * tig + h) * C::P_HEAD + gid * 2;
-            *reinterpret_cast<__half*>(ph) = __float2half_rn(ex2(se[t][0][h] - base[h] + P_OFF));
-            *reinterpret_cast<__half*>(ph + 16) = __float2half_rn(ex2(se[t][1][h] - base[h] + P_OFF));
+            *reinterpret_cast<__half*>(ph) = __float2half_rn(ex2(s[t][0][h] - (bp - ve[t][0])));
+            *reinterpret_cast<__half*>(ph + 16) = __float2half_rn(ex2(s[t][1][h] - (bp - ve[t][1])));
           }
         if (lane == 0) flag[warp] = grow;
       } else if (lane == 0) {
@@ -954,6 +959,7 @@ __device__ __forceinline__ void decode_fp4_body(const DecK& p, const int cta, co
       const float2 v = mls[w * 8 + gid];
       l += v.y * ex2(v.x - m);
     }
+    if (fabsf(M) >= kMaxBase && M > kNoScore) atomicOr(p.err, FA_DEV_ERR_RANGE);
     float Mo = M - P_OFF;
     // The partials of the unit's shares in this CTA (the whole-unit cut) meet in
     // shared memory: each group leaves its own in the idle ring, lane by lane as

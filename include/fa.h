@@ -127,9 +127,10 @@ typedef enum { FA_FULL = 0, FA_SLIDING = 1 } fa_layer_kind;
 #define FA_DEV_ERR_RANGE 0x20u     /* a value out of the kernels' range: an f16
                                       operand saturated (8- and 4-bit formats: a q, or
                                       an extend k_ext / v_ext, magnitude of 65520
-                                      or more), or an extend score with
-                                      |sm_scale * q.k| * log2(e) of 32767 or
-                                      more                                          */
+                                      or more), or a score |sm_scale * q.k| *
+                                      log2(e) of 32767 or more in extend, of 2^23
+                                      or more in decode over 4-bit slabs (there
+                                      plus or less the value's exponent)            */
 
 /* Most fa_cache descriptors that may be live at once (each holds one device
  * error word). */
@@ -340,7 +341,9 @@ FA_API size_t fa_decode_workspace_bytes(const fa_cache* cache, int32_t layer, in
  * lse = -inf.  Over 8- and 4-bit slabs q is converted to f16 for the tensor cores:
  * an element of magnitude 65536 or more saturates to +-65504 and sets
  * FA_DEV_ERR_RANGE; one below f16's smallest normal (6.1e-5) is rounded to a
- * multiple of 2^-24, to 0 up to 2^-25, and that is not reported.  workspace: device scratch of at least
+ * multiple of 2^-24, to 0 up to 2^-25, and that is not reported.  Over 4-bit
+ * slabs a row whose largest scaled score is 2^23 / log2(e) (5.8 million) or more
+ * in magnitude is out of range (FA_DEV_ERR_RANGE).  workspace: device scratch of at least
  * fa_decode_workspace_bytes(cache, layer, B, max_seq_len) bytes (may be NULL
  * when that is 0), 256-byte aligned.  Zero it once before its first use: its
  * leading counters must start at zero, and every call that completes leaves

@@ -260,3 +260,29 @@ def test_two_streams_with_their_own_workspaces():
     torch.cuda.synchronize()
     for out, lse in res:
         assert torch.equal(out.view(torch.int16), ref[0].view(torch.int16)) and torch.equal(lse, ref[1])
+
+
+@pytest.mark.parametrize("D", [256, 512])
+@pytest.mark.parametrize("grow", [1.0, 30.0, 1000.0, 2.0 ** 30])
+def test_one_key_gives_its_value_whatever_its_score(D, grow):
+    """Scores of tens of thousands to past 2^23.  The value's exponent joins the
+    score in the weight's exponent, which must not round at the score's own scale.
+    Past 2^23 in log2 units, where that cannot be had, the call reports its range."""
+    def edit(i, k, v):
+        k.mul_(grow)
+    case = DecodeCase4([lay(W.SLIDING, D, 8, 2, 1)], [1, 5, 16, 33, 100], 16, seed=2, edit=edit)
+    case.q[0].mul_(10_000.0)
+    out, lse = case.decode(0, fused=True)
+    q = case.q[0].double().cpu().numpy()
+    score = np.array([[case.layers[0]["sm_scale"] * (case.vals[0][b][0][-1, j // 4] @ q[b, j]) for j in range(8)]
+                      for b in range(case.B)])
+    err = np.array([[np.abs(case.vals[0][b][0][-1, j // 4]) @ np.abs(q[b, j]) for j in range(8)] for b in range(case.B)])
+    err *= case.layers[0]["sm_scale"] * 600 * 2.0 ** -24      # fp32 sums of 512 products, a few roundings more
+    log2 = np.abs(score) * np.log2(np.e)
+    inside = log2 < 2.0 ** 23 * 0.99
+    assert case.cache.device_error() == (0 if inside.all() else case.fa.DEV_ERR_RANGE)
+    assert inside.all() == (grow <= 30.0) and (grow < 2.0 ** 30 or not inside.any())
+    assert (np.abs(lse.double().cpu().numpy() - score) <= err + 2.0 ** -22 * np.abs(score))[inside].all()
+    got = out.double().cpu().numpy()
+    for b, j in zip(*np.nonzero(inside)):
+        assert np.array_equal(got[b, j], case.vals[0][b][1][-1, j // 4]), (b, j, score[b, j])
