@@ -14,14 +14,18 @@
 // of 16): position pos lies in row (b * Hkv + h) * ring + pos % ring.  To the
 // extend kernel that is a slab of pages of `ring` rows whose block table says b
 // for every page of sequence b; the table is written here too.
+#include <algorithm>
+
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
 #include "fa_row.cuh"
 
 namespace fa {
 
+constexpr long long kMaxBlocks = 16384;
+
 template <int D>
-__global__ void __launch_bounds__(256) unpack_kernel(UnpackArgs a) {
+__global__ void __launch_bounds__(256, 6) unpack_kernel(UnpackArgs a) {
   constexpr int R = D == 256 ? 8 : 4;   // rows a warp moves at a time, K and V alternating
   if (!a.early_metadata) griddep_wait();
   griddep_launch_dependents();
@@ -39,35 +43,34 @@ __global__ void __launch_bounds__(256) unpack_kernel(UnpackArgs a) {
   }
   // the first query sees from P - W + 1 on; the extend kernel's tiles start on 16 rows
   const int first = a.window > 0 ? max(0, P - n - a.window + 1) : 0;
-  const int pos0 = (first & ~15) + (blockIdx.x * 8 + (threadIdx.x >> 5)) * (R / 2);
-  if (first >= P || pos0 >= P) {
-    griddep_wait();   // the grid ends only after the kernel before it
-    return;
-  }
-  // R / 2 divides 16, so a warp's positions share a page and lie together in the ring
-  const int pg = a.by_page.div(pos0);
-  const int pid = __ldg(a.block_table + static_cast<size_t>(b) * a.max_pages_per_seq + pg);
-  const bool there = pid >= 0 && pid < a.num_pages;
-  if (!there && lane == 0) atomicOr(a.err, FA_DEV_ERR_PAGE);   // reads as zeros
-  const size_t src = there ? (static_cast<size_t>(pid) * a.Hkv + h) * a.page_size + (pos0 - pg * a.page_size) : 0;
-  const size_t dst = (static_cast<size_t>(b) * a.Hkv + h) * a.ring + (pos0 - static_cast<int>(a.by_ring.div(pos0)) * a.ring);
-  griddep_wait();
-  RawRow<D, FA_KV_FP4> raw[R];
+  const uint32_t last = first < P ? P : 0, step = gridDim.x * 8 * (R / 2);
+  for (uint32_t pos0 = (first & ~15) + (blockIdx.x * 8 + (threadIdx.x >> 5)) * (R / 2); pos0 < last; pos0 += step) {
+    // R / 2 divides 16, so a warp's positions share a page and lie together in the ring
+    const uint32_t pg = a.by_page.div(pos0);
+    const int pid = __ldg(a.block_table + static_cast<size_t>(b) * a.max_pages_per_seq + pg);
+    const bool there = pid >= 0 && pid < a.num_pages;
+    if (!there && lane == 0) atomicOr(a.err, FA_DEV_ERR_PAGE);   // reads as zeros
+    const size_t src = there ? (static_cast<size_t>(pid) * a.Hkv + h) * a.page_size + (pos0 - pg * a.page_size) : 0;
+    const size_t dst = (static_cast<size_t>(b) * a.Hkv + h) * a.ring + (pos0 - a.by_ring.div(pos0) * a.ring);
+    griddep_wait();
+    RawRow<D, FA_KV_FP4> raw[R];
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    if (there && pos0 + i / 2 < P) {
-      const size_t r = src + i / 2;
-      raw_load<D, FA_KV_FP4>(raw[i], static_cast<const uint8_t*>((i & 1) ? a.v_slab : a.k_slab) + r * kRowBytes<D, FA_KV_FP4>,
-                             ((i & 1) ? a.v_scale : a.k_scale) + r, lane);
-    } else {
-      raw[i] = RawRow<D, FA_KV_FP4>{};
+    for (int i = 0; i < R; ++i) {
+      if (there && pos0 + i / 2 < last) {
+        const size_t r = src + i / 2;
+        raw_load<D, FA_KV_FP4>(raw[i], static_cast<const uint8_t*>((i & 1) ? a.v_slab : a.k_slab) + r * kRowBytes<D, FA_KV_FP4>,
+                               ((i & 1) ? a.v_scale : a.k_scale) + r, lane);
+      } else {
+        raw[i] = RawRow<D, FA_KV_FP4>{};
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (pos0 + i / 2 >= last) continue;
+      raw_to_bf16<D, FA_KV_FP4>(raw[i], static_cast<__nv_bfloat16*>((i & 1) ? a.v : a.k) + (dst + i / 2) * D, lane);
     }
   }
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    if (pos0 + i / 2 >= P) continue;
-    raw_to_bf16<D, FA_KV_FP4>(raw[i], static_cast<__nv_bfloat16*>((i & 1) ? a.v : a.k) + (dst + i / 2) * D, lane);
-  }
+  griddep_wait();   // the grid ends only after the kernel before it
 }
 
 cudaError_t launch_unpack(const UnpackArgs& args, cudaStream_t s) {
@@ -78,7 +81,12 @@ cudaError_t launch_unpack(const UnpackArgs& args, cudaStream_t s) {
   const int span = a.ring < a.max_len ? a.ring : a.max_len;
   const long long gy = static_cast<long long>(a.B) * a.Hkv;
   if (gy > 65535) return cudaErrorInvalidConfiguration;   // the caller takes the direct path
-  const dim3 g(static_cast<unsigned>((span + per_block - 1) / per_block), static_cast<unsigned>(gy)), b(256);
+  // the bound may be far above the lengths, and blocks that find nothing cost their
+  // launch: 8 prefixes of 1000 rows, 2 KV heads at 512, under a bound of 131072 took
+  // 176 us with a block for every 16 rows of it, 62 with these, 54 with 4096 (which
+  // cost 64 prefixes of 4096 rows 538 us for 529); converting in the kernel 93
+  const long long most = std::max(1LL, (kMaxBlocks + gy - 1) / gy);
+  const dim3 g(static_cast<unsigned>(std::min<long long>((span + per_block - 1) / per_block, most)), static_cast<unsigned>(gy)), b(256);
   return a.D == 256 ? launch_pdl(unpack_kernel<256>, g, b, 0, s, a) : launch_pdl(unpack_kernel<512>, g, b, 0, s, a);
 }
 

@@ -75,3 +75,44 @@ def test_a_length_below_its_new_tokens_under_the_widest_window():
         assert c.cache.device_error() == c.fa.DEV_ERR_BOUND
         outs.append(out)
     assert torch.equal(outs[0][40], outs[1][40])   # one key: its value, exact on both paths
+
+
+@pytest.mark.parametrize("stored", [False, True], ids=["extend", "multi-token decode"])
+def test_unpacking_more_rows_than_one_sweep_of_its_blocks(stored):
+    """256 sequences over one page list, prefixes up to 3000 rows, a bound past that:
+    each block of the unpacking kernel takes several stretches of rows."""
+    import full_attention_gb300 as fa
+    B, T, D, hq = 256, 3000, 512, 8
+    layer = W.layer(W.FULL, D, hq, 1)
+    cache = fa.Cache([layer], 200, 16, fa.KV_FP4)
+    cache.allocate("cuda")
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)
+    slots = torch.arange(T, dtype=torch.int32, device="cuda")
+    cache.store(0, rnd(T, 1, D), rnd(T, 1, D), slots)
+    K, V = rnd(T, 1, D), rnd(T, 1, D)
+    cache.load(0, slots, K, V)
+    K, V = K[:, 0].double(), V[:, 0].double()
+    lens = (torch.arange(B, device="cuda") * 97 % (T - 1) + 1).int()
+    q, kx, vx = rnd(B, hq, D), rnd(B, 1, D), rnd(B, 1, D)
+    bt = torch.arange(200, dtype=torch.int32, device="cuda").expand(B, -1).contiguous()
+    ptr = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    bound = 3200
+    ws = fa.workspace(cache.extend_workspace_bytes(0, B, 1, bound))
+    ws.fill_(255)
+    cache.bind_extend_workspace(ws)
+    out = torch.empty_like(q)
+    if stored:
+        cache.decode_multi(0, q, ptr, lens, bt, 1, bound, out)
+    else:
+        cache.extend(0, q, kx, vx, ptr, lens, bt, 1, bound, out)
+    assert cache.device_error() == 0
+    s = layer["sm_scale"] * q.double() @ K.T
+    s = torch.where(torch.arange(T, device="cuda") < lens[:, None, None], s, -torch.inf)
+    if not stored:
+        s = torch.cat([s, layer["sm_scale"] * (q.double() * kx.double()).sum(-1, keepdim=True)], -1)
+    p = torch.softmax(s, -1)
+    ref, mag = p[..., :T] @ V, p[..., :T] @ V.abs()
+    if not stored:
+        ref, mag = ref + p[..., T:] * vx.double(), mag + p[..., T:] * vx.double().abs()
+    assert ((out.double() - ref).abs() <= 2.0 ** -7 * ref.abs() + 1.5 * 2.0 ** -8 * mag).all()
