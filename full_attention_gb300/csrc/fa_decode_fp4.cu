@@ -34,7 +34,10 @@
 //               exceed that by more than the slack, into shared memory as f16;
 //               barrier; then O^T += V^T P^T, each warp a quarter of the columns.
 // The weights' rounding to f16 is the only one below 32 bits: 2^-11 relative
-// each, while the sum of the weights, in fp32, takes them unrounded.
+// each, and below 2^-14 steps of 2^-24, while the largest lies between 2^3 and
+// 2^12 (P_OFF, SLACK): a key whose weight times value scale is 2^-17 of the
+// largest or less loses bits, together at most 2^-28 of the largest a key.  The
+// sum of the weights, in fp32, takes them unrounded.
 //
 // Rows are 144 or 288 bytes apart in shared memory, so the fragment loads (one
 // 4-byte word of 8 codes a lane at 256, 8 bytes at 512) hit 32 different banks

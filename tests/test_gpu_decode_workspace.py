@@ -106,3 +106,32 @@ def test_a_workspace_that_was_not_zeroed_is_reported(kv_dtype, word):
     for g, w in zip(call(ws), want):
         assert torch.equal(g, w)
     assert c.cache.device_error() == 0
+
+
+@pytest.mark.parametrize("kv_dtype", FORMATS, ids=IDS)
+def test_captured_graphs_of_different_sizes_share_a_workspace(kv_dtype):
+    c = Calls(kv_dtype)
+    steps = [(0, 8, 4096), ([0, 2, 4], 8, 1000), (1, 70, 4096), (0, 1, 20_000)]
+    calls = [c.run(*s) for s in steps]
+    want = [call(c.fa.workspace(n)) for n, call in calls]
+    ws = c.fa.workspace(max(n for n, _ in calls))
+    graphs = []
+    for what, B, bound in steps:
+        ids = [what] if isinstance(what, int) else what
+        a = [c.args(i, B, bound) for i in ids]
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            if isinstance(what, int):
+                c.cache.decode(what, *a[0][:3], bound, *a[0][3:], ws)
+            else:
+                c.cache.decode_layers(ids, [x[0] for x in a], [x[1] for x in a], a[0][2], bound, [x[3] for x in a],
+                                      [x[4] for x in a], ws)
+        graphs.append((g, [t for x in a for t in x[3:]], a))
+    for i in (0, 1, 2, 3, 0, 3, 1, 2, 0):
+        g, outs, _ = graphs[i]
+        for t in outs:
+            t.fill_(float("nan"))
+        g.replay()
+        for got, w in zip(outs, want[i]):
+            assert torch.equal(got, w), (i, steps[i])
+    assert c.cache.device_error() == 0
