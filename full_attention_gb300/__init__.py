@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import weakref
+from fractions import Fraction
 
 import torch
 
@@ -20,6 +21,9 @@ FULL, SLIDING = 0, 1
 KV_BF16, KV_INT8, KV_FP8, KV_FP4 = 0, 1, 2, 3
 KV_OWN, KV_AUTO = -1, -2
 DEV_ERR_PAGE, DEV_ERR_SLOT, DEV_ERR_BOUND, DEV_ERR_TIMEOUT, DEV_ERR_WORKSPACE, DEV_ERR_RANGE = 1, 2, 4, 8, 16, 32
+DEV_ERR_POOL = 64
+NORM_Q, NORM_K, NORM_V = 1, 2, 4
+MAX_STEP_BATCH = 8192
 MAX_CACHES = 4096
 
 FLAG_EARLY_METADATA = 1
@@ -38,6 +42,12 @@ class LayerDesc(ctypes.Structure):
                 ("sm_scale", ctypes.c_float)]
 
 
+class NormRopeDesc(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("steps", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float), ("norm", ctypes.c_uint32),
+                ("rotary_dim", ctypes.c_int32)]
+
+
 class FAError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"{_lib.fa_status_string(status).decode()}: {msg}")
@@ -48,7 +58,7 @@ def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with full_attention_gb300.build.build()")
     lib = ctypes.CDLL(LIB_PATH)
-    vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+    vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     sig = {
         "fa_cache_create": (i32, [ctypes.POINTER(LayerDesc), i32, i32, i32, i32, ctypes.POINTER(vp)]),
         "fa_cache_destroy": (None, [vp]),
@@ -60,6 +70,9 @@ def _load() -> ctypes.CDLL:
         "fa_kv_bytes_per_token": (sz, [vp, i32]),
         "fa_kv_store": (i32, [vp, i32, vp, vp, vp, i32, vp]),
         "fa_kv_load": (i32, [vp, i32, vp, i32, vp, vp, vp]),
+        "fa_norm_rope_store": (i32, [vp, i32, ctypes.POINTER(NormRopeDesc), vp, i64, vp, i64, vp, i64, vp, vp, i32, vp, vp,
+                                     vp, vp]),
+        "fa_plan_step": (i32, [vp, i32, vp, i32, vp, vp, vp, vp, i32, vp, vp, vp, vp, i32, vp]),
         "fa_decode_workspace_bytes": (sz, [vp, i32, i32, i32]),
         "fa_extend_workspace_bytes": (sz, []),
         "fa_extend_unpack_bytes": (sz, [vp, i32, i32, i32, i32]),
@@ -152,6 +165,34 @@ def _i32s(xs):
 def _desc(d: dict) -> LayerDesc:
     return LayerDesc(int(d["kind"]), int(d["head_dim"]), int(d["num_q_heads"]), int(d["num_kv_heads"]),
                      int(d.get("window", 0)), int(d.get("kv_source", KV_OWN)), float(d["sm_scale"]))
+
+
+_TWO_PI = Fraction(6283185307179586476925286766559005768394338798750211641949889184615, 10 ** 66)
+
+
+def rope_steps(inv_freq) -> list:
+    """fa_norm_rope's steps: each frequency (radians a position) in turns times 2^64, modulo 2^64."""
+    return [round(Fraction(float(f)) * (1 << 64) / _TWO_PI) % (1 << 64) for f in inv_freq]
+
+
+class NormRope:
+    """How a layer's projected rows are normed and rotated (fa_norm_rope): the
+    weights of queries and keys (bf16 [head_dim] or None), the norms applied, and the
+    frequencies of the rotated pairs (i, i + R / 2) in radians a position, R / 2 of them
+    (None: no rotation)."""
+
+    def __init__(self, head_dim: int, inv_freq=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 weight_offset: float = 0.0, norm_q: bool = True, norm_k: bool = True, norm_v: bool = False,
+                 device="cuda"):
+        self.head_dim = int(head_dim)
+        steps = [] if inv_freq is None else rope_steps(inv_freq)
+        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is not None and (w.dtype is not torch.bfloat16 or not w.is_contiguous() or w.numel() != self.head_dim):
+                raise FAError(ERR_INVALID_ARG, f"{name} must be a dense torch.bfloat16 tensor of {self.head_dim} elements")
+        self.q_weight, self.k_weight = q_weight, k_weight
+        self.steps = torch.tensor([v - (1 << 64) if v >> 63 else v for v in steps], dtype=torch.int64, device=device) if steps else None
+        norm = NORM_Q * bool(norm_q) | NORM_K * bool(norm_k) | NORM_V * bool(norm_v)
+        self.desc = NormRopeDesc(_p(q_weight), _p(k_weight), _p(self.steps), float(eps), float(weight_offset), norm, 2 * len(steps))
 
 
 class Cache:
@@ -288,6 +329,51 @@ class Cache:
             _need("v", v, torch.bfloat16, dev, T, row)
         _check(_lib.fa_kv_load(self._h, layer, _p(slot_mapping), T, _p(k), _p(v), _s(stream)))
 
+    def norm_rope_store(self, layer: int, how: NormRope, q, k, v, positions, slot_mapping, q_out=None, k_out=None,
+                        v_out=None, stream=None) -> None:
+        """fa_norm_rope_store: norms and rotation of new rows q [T][Hq][D], k, v
+        [T][Hkv][D] (slices of one projection's rows are taken as they lie), and the
+        store of k and v at slot_mapping (None: not stored), in one launch."""
+        d, dev = self._layer(layer), _device()
+        D, owns = d["head_dim"], self._owns(layer)
+        if how.head_dim != D:
+            raise FAError(ERR_INVALID_ARG, f"how is for head_dim {how.head_dim}, layer {layer} has {D}")
+        for t in (how.q_weight, how.k_weight, how.steps):
+            if t is not None and t.get_device() != dev:
+                raise FAError(ERR_INVALID_ARG, f"how's tensors are on {t.device}, not on the current CUDA device")
+        if not owns:
+            k = v = slot_mapping = k_out = v_out = None
+        first = next((x for x in (q, k) if x is not None), None)
+        T = 0 if first is None else first.shape[0]
+        strides = []
+        for name, x, h in (("q", q, d["num_q_heads"]), ("k", k, d["num_kv_heads"]), ("v", v, d["num_kv_heads"])):
+            if x is None:
+                strides.append(0)
+                continue
+            shape, rows = tuple(x.shape), ((T, h, D), (T, h * D))
+            dense = x.stride(-1) == 1 and (x.dim() < 3 or x.stride(1) == D or h == 1)
+            if x.dtype is not torch.bfloat16 or x.get_device() != dev or shape not in rows or not dense:
+                raise FAError(ERR_INVALID_ARG, f"{name} must hold bf16 rows {rows[0]} on the current CUDA device, dense within a token, "
+                                               f"not {x.dtype}, {shape}, strides {tuple(x.stride())}, on {x.device}")
+            strides.append(x.stride(0) if T > 1 else h * D)
+        for name, x, h in (("q_out", q_out, d["num_q_heads"]), ("k_out", k_out, d["num_kv_heads"]), ("v_out", v_out, d["num_kv_heads"])):
+            if x is not None:
+                _need(name, x, torch.bfloat16, dev, T, h * D)
+        for name, x in (("positions", positions), ("slot_mapping", slot_mapping)):
+            if x is not None:
+                _need(name, x, torch.int32, dev, T)
+        _check(_lib.fa_norm_rope_store(self._h, layer, ctypes.byref(how.desc), _p(q), strides[0], _p(k), strides[1], _p(v),
+                                       strides[2], _p(positions), _p(slot_mapping), T, _p(q_out), _p(k_out), _p(v_out),
+                                       _s(stream)))
+
+    def page_table(self, kind: int, batch: int, max_pages_per_seq: int, device="cuda") -> PageTable:
+        """The tables of an empty batch (fa_plan_step): every page of the kind's pool free."""
+        pages = self.window_pages if kind == SLIDING and self.window_pages > 0 else self.num_pages
+        state = torch.zeros(4 + 2 * int(batch), dtype=torch.int32)
+        state[1] = pages
+        return PageTable(self, kind, torch.full((int(batch), int(max_pages_per_seq)), -1, dtype=torch.int32, device=device),
+                         torch.arange(pages, dtype=torch.int32, device=device), state.to(device))
+
     def store_layers(self, layers, ks, vs, slot_mappings, stream=None) -> None:
         """fa_kv_store_layers: the stores of several layers in one launch
         (shared layers are skipped)."""
@@ -421,6 +507,43 @@ class Cache:
                                          _p(prefix_lens), _p(block_table), maxp, int(prefix_lens.numel()),
                                          int(q.shape[0]), int(max_q_len), int(max_prefix_len), _p(out), _p(lse),
                                          _s(stream)))
+
+
+class PageTable:
+    """The pages of a batch of sequences, kept on the GPU (fa_plan_step): block_table
+    [B][max_pages_per_seq], the ring of free pages and the state, int32, which
+    every step changes.  Cache.page_table makes one."""
+
+    def __init__(self, cache: Cache, kind: int, block_table, free_pages, state):
+        if block_table.dim() != 2:
+            raise FAError(ERR_INVALID_ARG, f"block_table must have two dimensions, not {block_table.dim()}")
+        self.cache, self.kind = cache, int(kind)
+        self.block_table, self.free_pages, self.state = block_table, free_pages, state
+
+    @property
+    def batch(self) -> int:
+        return self.block_table.shape[0]
+
+    @property
+    def seq_lens(self):
+        """The sequences' lengths after the last step, as decode reads them (a view of the state)."""
+        return self.state[4: 4 + self.batch]
+
+    def step(self, new_lens, qo_indptr, prefix_lens, positions, slot_mapping, state_out=None, stream=None) -> None:
+        """One step: new_lens[b] tokens join sequence b (negative: it ends); the outputs
+        are filled for the calls of the step."""
+        B, dev, c = self.batch, _device(), self.cache
+        N = slot_mapping.numel()
+        pages = c.window_pages if self.kind == SLIDING and c.window_pages > 0 else c.num_pages
+        for name, t, n in (("new_lens", new_lens, B), ("qo_indptr", qo_indptr, B + 1), ("prefix_lens", prefix_lens, B),
+                           ("positions", positions, N), ("slot_mapping", slot_mapping, N), ("free_pages", self.free_pages, pages),
+                           ("state", self.state, 4 + 2 * B), ("block_table", self.block_table, self.block_table.numel())):
+            _need(name, t, torch.int32, dev, n)
+        if state_out is not None:
+            _need("state_out", state_out, torch.int32, dev, 4 + 2 * B)
+        _check(_lib.fa_plan_step(c._h, self.kind, _p(new_lens), B, _p(self.state), _p(self.state if state_out is None else state_out),
+                                 _p(self.free_pages), _p(self.block_table), self.block_table.shape[1], _p(qo_indptr),
+                                 _p(prefix_lens), _p(positions), _p(slot_mapping), N, _s(stream)))
 
 
 def device_error(stream=None) -> int:

@@ -531,6 +531,111 @@ fa_status fa_kv_load(fa_cache* c, int32_t layer, const int32_t* slot_mapping, in
   return ok();
 }
 
+fa_status fa_norm_rope_store(fa_cache* c, int32_t layer, const fa_norm_rope* how, const void* q, int64_t q_stride,
+                             const void* k, int64_t k_stride, const void* v, int64_t v_stride, const int32_t* positions,
+                             const int32_t* slot_mapping, int32_t T, void* q_out, void* k_out, void* v_out, void* stream) {
+  fa_status st = check_layer(c, layer);
+  if (st) return st;
+  if (!how) return fail(FA_ERR_INVALID_ARG, "how is NULL");
+  if (T < 0) return fail(FA_ERR_INVALID_ARG, "T must be >= 0");
+  const Layer& L = c->layers[layer];
+  const int D = L.d.head_dim, R = how->rotary_dim;
+  if (how->norm & ~static_cast<uint32_t>(FA_NORM_Q | FA_NORM_K | FA_NORM_V)) return fail(FA_ERR_INVALID_ARG, "unknown norm bits 0x%x", how->norm);
+  if (how->norm && !(how->eps >= 1e-30f && how->eps <= 1e30f)) return fail(FA_ERR_INVALID_ARG, "eps must lie in [1e-30, 1e30]");
+  if (!std::isfinite(how->weight_offset)) return fail(FA_ERR_INVALID_ARG, "weight_offset must be finite");
+  if (R < 0 || R % 16 != 0 || R > D) return fail(FA_ERR_UNSUPPORTED, "rotary_dim %d: must be a multiple of 16, at most head_dim %d", R, D);
+  if (!aligned16(how->q_weight) || !aligned16(how->k_weight) || !aligned16(how->steps))
+    return fail(FA_ERR_INVALID_ARG, "weights and steps must be 16-byte aligned");
+  if (L.owner != layer) k = v = nullptr;   // a shared layer has queries alone
+  if (T == 0) return ok();
+  if (!q && !k && !v) return fail(FA_ERR_INVALID_ARG, L.owner == layer ? "one of q and k, v must be non-NULL" : "q must be non-NULL");
+  if ((k == nullptr) != (v == nullptr)) return fail(FA_ERR_INVALID_ARG, "k and v must both be given or both be NULL");
+  if (q && !q_out) return fail(FA_ERR_INVALID_ARG, "q_out must be non-NULL");
+  if (!k) slot_mapping = nullptr, k_out = v_out = nullptr;
+  if (k && !slot_mapping && !k_out && !v_out) return fail(FA_ERR_INVALID_ARG, "k and v go nowhere: slot_mapping, k_out and v_out are NULL");
+  if (R > 0 && (!how->steps || !positions)) return fail(FA_ERR_INVALID_ARG, "a rotation needs steps and positions");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_out) || !aligned16(v_out))
+    return fail(FA_ERR_INVALID_ARG, "q, k, v and the rows out must be 16-byte aligned");
+  const int64_t row_q = static_cast<int64_t>(L.d.num_q_heads) * D, row_kv = static_cast<int64_t>(L.d.num_kv_heads) * D;
+  auto bad_stride = [&](const void* x, int64_t stride, int64_t row) { return x && (stride % 8 != 0 || stride < row); };
+  if (bad_stride(q, q_stride, row_q) || bad_stride(k, k_stride, row_kv) || bad_stride(v, v_stride, row_kv))
+    return fail(FA_ERR_INVALID_ARG, "a token stride must be a multiple of 8 elements and hold the token's rows");
+  const Slab* s = nullptr;
+  if (slot_mapping && (st = check_bound(c, layer, &s))) return st;
+  cudaError_t ce;
+  unsigned int* err = device_error_word(c, &ce);
+  if (!err) return fail(FA_ERR_CUDA, "device error word: %s", cudaGetErrorString(ce));
+  RowsArgs a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_weight = how->q_weight;
+  a.k_weight = how->k_weight;
+  a.steps = how->steps;
+  a.positions = positions;
+  a.slots = slot_mapping;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  if (s) {
+    a.k_slab = s->k;
+    a.v_slab = s->v;
+    a.k_scale = s->k_scale;
+    a.v_scale = s->v_scale;
+  }
+  a.T = T;
+  a.Hq = L.d.num_q_heads;
+  a.Hkv = L.d.num_kv_heads;
+  a.D = D;
+  a.rotary_dim = R;
+  a.norm = static_cast<int>(how->norm);
+  a.page_size = c->page_size;
+  a.num_pages = layer_pages(c, layer);
+  a.kv_dtype = c->kv_dtype;
+  a.eps = how->eps;
+  a.weight_offset = how->weight_offset;
+  a.err = err;
+  ce = launch_rows(a, static_cast<cudaStream_t>(stream));
+  if (ce != cudaSuccess) return fail(FA_ERR_CUDA, "norm and rotation launch: %s", cudaGetErrorString(ce));
+  return ok();
+}
+
+fa_status fa_plan_step(fa_cache* c, int32_t kind, const int32_t* new_lens, int32_t B, const int32_t* state,
+                       int32_t* state_out, int32_t* free_pages, int32_t* block_table, int32_t max_pages_per_seq,
+                       int32_t* qo_indptr, int32_t* prefix_lens, int32_t* positions, int32_t* slot_mapping,
+                       int32_t num_tokens, void* stream) {
+  if (!c) return fail(FA_ERR_INVALID_ARG, "cache is NULL");
+  if (kind != FA_FULL && kind != FA_SLIDING) return fail(FA_ERR_INVALID_ARG, "kind %d", kind);
+  if (B < 1 || B > FA_MAX_STEP_BATCH) return fail(FA_ERR_INVALID_ARG, "B must be in [1, %d]", FA_MAX_STEP_BATCH);
+  if (num_tokens < 0) return fail(FA_ERR_INVALID_ARG, "num_tokens must be >= 0");
+  if (max_pages_per_seq < 1 || static_cast<int64_t>(max_pages_per_seq) * c->page_size >= (1LL << 31) - 256)
+    return fail(FA_ERR_INVALID_ARG, "max_pages_per_seq * page_size must be positive and below 2^31 - 256");
+  if (!new_lens || !state || !state_out || !free_pages || !block_table || !qo_indptr || !prefix_lens ||
+      (num_tokens > 0 && (!positions || !slot_mapping)))
+    return fail(FA_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned16(positions) || !aligned16(slot_mapping)) return fail(FA_ERR_INVALID_ARG, "positions, slot_mapping must be 16-byte aligned");
+  int window = 0, pages = c->num_pages, layers = 0;
+  for (size_t i = 0; i < c->layers.size(); ++i) {
+    const fa_layer_desc& d = c->layers[i].d;
+    if (d.kind != kind) continue;
+    ++layers;
+    pages = layer_pages(c, static_cast<int32_t>(i));
+    if (kind == FA_SLIDING) window = std::max(window, d.window);
+  }
+  if (layers == 0) return fail(FA_ERR_INVALID_ARG, "the cache has no layer of kind %d", kind);
+  cudaError_t ce;
+  unsigned int* err = device_error_word(c, &ce);
+  if (!err) return fail(FA_ERR_CUDA, "device error word: %s", cudaGetErrorString(ce));
+  const PlanArgs a{new_lens, state, state_out, free_pages, block_table, qo_indptr, prefix_lens, positions, slot_mapping,
+                   B, num_tokens, c->page_size, pages, max_pages_per_seq, window, err};
+  ce = launch_plan(a, static_cast<cudaStream_t>(stream));
+  if (ce != cudaSuccess) return fail(FA_ERR_CUDA, "step plan launch: %s", cudaGetErrorString(ce));
+  return ok();
+}
+
 size_t fa_decode_workspace_bytes(const fa_cache* c, int32_t layer, int32_t B, int32_t max_seq_len) {
   if (check_layer(c, layer) != FA_OK || B <= 0 || max_seq_len <= 0) return 0;
   return plan_decode(c, layer, B, max_seq_len).ws_bytes();

@@ -177,6 +177,46 @@ struct LoadArgs {
 };
 cudaError_t launch_load(const LoadArgs& a, cudaStream_t s);
 
+// Norms, rotation and store of one layer's rows (fa_rows.cu).
+struct RowsArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  long long q_stride, k_stride, v_stride;   // elements from token to token
+  const void* q_weight;
+  const void* k_weight;
+  const uint64_t* steps;
+  const int32_t* positions;
+  const int32_t* slots;   // null: nothing is stored
+  void* q_out;
+  void* k_out;
+  void* v_out;
+  void* k_slab;
+  void* v_slab;
+  float* k_scale;
+  float* v_scale;
+  int T, Hq, Hkv, D, rotary_dim, norm, page_size, num_pages, kv_dtype;   // norm: bit 0 q, 1 k, 2 v
+  float eps, weight_offset;
+  unsigned int* err;
+};
+cudaError_t launch_rows(const RowsArgs& a, cudaStream_t s);
+
+// One step's tables and slots (fa_plan.cu).
+struct PlanArgs {
+  const int32_t* new_lens;
+  const int32_t* state_in;
+  int32_t* state_out;
+  int32_t* free_pages;
+  int32_t* block_table;
+  int32_t* qo_indptr;
+  int32_t* prefix_lens;
+  int32_t* positions;
+  int32_t* slots;
+  int B, num_tokens, page_size, num_pages, max_pages_per_seq, window;   // window 0: every page is kept
+  unsigned int* err;
+};
+cudaError_t launch_plan(const PlanArgs& a, cudaStream_t s);
+
 struct DecodeArgs {
   const void* q;
   const int32_t* block_table;

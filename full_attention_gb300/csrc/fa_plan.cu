@@ -1,0 +1,251 @@
+// One step's block tables and slot maps, from the numbers of new tokens
+// (fa_plan_step): what a serving loop otherwise builds on the host and copies
+// before every step ("FreeToken PR #898", description: tables and slots per
+// group of layers; "pegainfer issue #807", Description: the sliding group gives
+// pages up that the full group still reads).
+//
+// Sequence b holds len_b tokens in pages first_b .. ceil(len_b / ps) - 1 of its
+// table row; n_b tokens join it.  With
+//   have = ceil(len / ps), want = ceil((len + n) / ps), keep = max(first, (len - W + 1)+ / ps)
+// its row takes want - have pages off the head of the ring of free pages and its
+// pages [first, keep) go behind the ring's end, in order of sequence and page:
+// prefix sums over b give every sequence its place in the tokens, the ring's
+// head and the ring's end.
+//
+// One launch.  Every CTA sums over all sequences (12 bytes each, from L2) and
+// keeps the sums in shared memory; its share of the tokens then finds its
+// sequence by bisection.  The ring's pops and pushes never meet (they lie count
+// apart in a ring that holds every page), so only the state is written late, by
+// the CTA that arrives last: the state read and the one written may be the same.
+#include <algorithm>
+
+#include "fa_internal.h"
+#include "fa_ptx.cuh"
+
+namespace fa {
+
+constexpr int kPlanThreads = 256;
+
+struct PlanK {
+  const int32_t* new_lens;
+  const int32_t* state_in;
+  int32_t* state_out;   // may be state_in
+  int32_t* ring;
+  int32_t* table;
+  int32_t* qo_indptr;
+  int32_t* prefix_lens;
+  int32_t* positions;
+  int32_t* slots;
+  unsigned int* err;
+  int B, N, page_size, num_pages, max_pages, window;   // window 0: every page is kept
+  FastDiv by_page;
+};
+
+struct Sums {   // of sequences before one: new tokens, pages taken, pages given up
+  long long tok, need, gone;
+};
+__device__ __forceinline__ Sums operator+(const Sums& a, const Sums& b) { return {a.tok + b.tok, a.need + b.need, a.gone + b.gone}; }
+
+struct PlanSeq {
+  int len, first, n, have, want, keep;
+  bool ended;
+  unsigned bad;   // FA_DEV_ERR_* bits
+};
+
+__device__ __forceinline__ PlanSeq plan_seq(const PlanK& p, int b) {
+  PlanSeq s;
+  s.len = p.state_in[4 + b];
+  s.first = p.state_in[4 + p.B + b];
+  const int n = __ldg(p.new_lens + b);
+  s.ended = n < 0;
+  s.n = max(n, 0);
+  s.bad = 0;
+  const long long room = static_cast<long long>(p.max_pages) * p.page_size;   // below 2^31
+  if (s.len < 0 || s.len > room || s.first < 0) s.bad |= FA_DEV_ERR_WORKSPACE;
+  if (static_cast<long long>(s.len) + s.n > room || s.n > p.N) s.bad |= FA_DEV_ERR_BOUND;
+  if (s.bad) {
+    s.n = s.have = s.want = s.keep = 0;
+    return s;
+  }
+  s.have = static_cast<int>(p.by_page.div(s.len + p.page_size - 1));
+  if (s.first > s.have) s.bad |= FA_DEV_ERR_WORKSPACE;
+  s.want = s.ended ? s.have : static_cast<int>(p.by_page.div(s.len + s.n + p.page_size - 1));
+  s.keep = s.first;
+  if (s.ended) s.keep = s.have;
+  else if (p.window > 0 && s.len >= p.window) s.keep = max(s.first, static_cast<int>(p.by_page.div(s.len - p.window + 1)));
+  return s;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanK p) {
+  extern __shared__ int32_t sh[];   // [B + 1] tokens before, [B] pages taken before, [B] given up before, [B] lengths
+  int32_t* tok = sh;
+  int32_t* need = tok + p.B + 1;
+  int32_t* gone = need + p.B;
+  int32_t* len = gone + p.B;
+  __shared__ Sums warp_sums[kPlanThreads / 32];
+  __shared__ unsigned warp_bad[kPlanThreads / 32];
+  __shared__ int last;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int head = p.state_in[0], count = p.state_in[1];
+
+  Sums run{0, 0, 0};
+  unsigned bad = 0;
+  for (int base = 0; base < p.B; base += kPlanThreads) {
+    const int b = base + tid;
+    Sums mine{0, 0, 0};
+    unsigned mybad = 0;
+    if (b < p.B) {
+      const PlanSeq s = plan_seq(p, b);
+      mine = {s.n, s.want - s.have, s.keep - s.first};
+      mybad = s.bad;
+      len[b] = s.len;
+    }
+    Sums incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const Sums up{__shfl_up_sync(0xffffffffu, incl.tok, o), __shfl_up_sync(0xffffffffu, incl.need, o),
+                    __shfl_up_sync(0xffffffffu, incl.gone, o)};
+      if (lane >= o) incl = incl + up;
+    }
+    mybad = __reduce_or_sync(0xffffffffu, mybad);
+    if (lane == 31) warp_sums[warp] = incl;
+    if (lane == 0) warp_bad[warp] = mybad;
+    __syncthreads();
+    Sums before = run;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+      if (w < warp) before = before + warp_sums[w];
+      run = run + warp_sums[w];
+      bad |= warp_bad[w];
+    }
+    if (b < p.B) {   // a sum past 32 bits is refused below and its low bits are not used
+      tok[b] = static_cast<int32_t>(before.tok + incl.tok - mine.tok);
+      need[b] = static_cast<int32_t>(before.need + incl.need - mine.need);
+      gone[b] = static_cast<int32_t>(before.gone + incl.gone - mine.gone);
+    }
+    __syncthreads();
+  }
+  if (head < 0 || head >= p.num_pages || count < 0 || count > p.num_pages || count + run.gone > p.num_pages)
+    bad |= FA_DEV_ERR_WORKSPACE;
+  if (run.tok > p.N) bad |= FA_DEV_ERR_BOUND;
+  if (run.need > count) bad |= FA_DEV_ERR_POOL;
+  if (tid == 0) {
+    tok[p.B] = static_cast<int32_t>(run.tok);
+    if (bad && blockIdx.x == 0) atomicOr(p.err, bad);
+  }
+  __syncthreads();
+  const int total = bad ? 0 : static_cast<int>(run.tok);   // a refused step has no tokens and changes nothing
+  auto in_ring = [&](int i) { return i - (i >= 2 * p.num_pages ? 2 * p.num_pages : i >= p.num_pages ? p.num_pages : 0); };
+
+  if (blockIdx.x == 0)
+    for (int b = tid; b <= p.B; b += kPlanThreads) {
+      p.qo_indptr[b] = bad ? 0 : tok[b];
+      if (b < p.B) p.prefix_lens[b] = !bad && __ldg(p.new_lens + b) < 0 ? 0 : len[b];
+    }
+
+  // ---- pages given up, behind the ring's end: a warp a sequence
+  if (!bad && run.gone > 0) {
+    const int warps = gridDim.x * (kPlanThreads / 32);
+    for (int b = blockIdx.x * (kPlanThreads / 32) + warp; b < p.B; b += warps) {
+      const int n = (b + 1 < p.B ? gone[b + 1] : static_cast<int>(run.gone)) - gone[b];
+      if (n == 0) continue;
+      const int32_t* row = p.table + static_cast<size_t>(b) * p.max_pages + p.state_in[4 + p.B + b];
+      for (int i = lane; i < n; i += 32) p.ring[in_ring(head + count + gone[b] + i)] = row[i];
+    }
+  }
+
+  // ---- the tokens, four a thread: position, slot, and at a page's first token its table entry
+  const int quads = (p.N + 3) / 4;
+  for (int q = blockIdx.x * kPlanThreads + tid; q < quads; q += gridDim.x * kPlanThreads) {
+    int pos[4], slot[4];
+    int b = -1, end = 0, page = -1;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int t = 4 * q + e;
+      pos[e] = 0;
+      slot[e] = -1;
+      if (t >= total) continue;
+      if (t >= end) {   // the last sequence that begins at t or before (those with no new token end where they begin)
+        int lo = 0, hi = p.B;
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (tok[mid] <= t) lo = mid;
+          else hi = mid;
+        }
+        b = lo;
+        end = tok[b + 1];
+        page = -1;
+      }
+      pos[e] = len[b] + t - tok[b];
+      const int pi = static_cast<int>(p.by_page.div(pos[e])), off = pos[e] - pi * p.page_size;
+      if (page < 0 || off == 0) {
+        int32_t* entry = p.table + static_cast<size_t>(b) * p.max_pages + pi;
+        const int have = static_cast<int>(p.by_page.div(len[b] + p.page_size - 1));
+        if (pi < have) {
+          page = *entry;
+        } else {
+          page = p.ring[in_ring(head + need[b] + pi - have)];
+          if (off == 0) *entry = page;
+        }
+        if (page < 0 || page >= p.num_pages) {
+          atomicOr(p.err, FA_DEV_ERR_PAGE);
+          page = -1;
+        }
+      }
+      if (page >= 0) slot[e] = page * p.page_size + off;   // below 2^31 (fa_cache_create)
+    }
+    if (4 * q + 4 <= p.N) {
+      reinterpret_cast<int4*>(p.positions)[q] = make_int4(pos[0], pos[1], pos[2], pos[3]);
+      reinterpret_cast<int4*>(p.slots)[q] = make_int4(slot[0], slot[1], slot[2], slot[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (4 * q + e < p.N) {
+          p.positions[4 * q + e] = pos[e];
+          p.slots[4 * q + e] = slot[e];
+        }
+    }
+  }
+
+  // ---- the state, once every CTA has read it
+  __syncthreads();
+  if (gridDim.x > 1) {
+    if (tid == 0) {
+      const int old = atom_add_acq_rel_gpu(p.state_out + 2, 1);
+      last = old == static_cast<int>(gridDim.x) - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+  }
+  for (int b = tid; b < p.B; b += kPlanThreads) {
+    const int first = p.state_in[4 + p.B + b];
+    int l = len[b], f = first;
+    if (!bad) {
+      const int n = __ldg(p.new_lens + b);
+      l = n < 0 ? 0 : l + n;
+      f = n < 0 ? 0 : first + (b + 1 < p.B ? gone[b + 1] : static_cast<int>(run.gone)) - gone[b];
+    }
+    p.state_out[4 + b] = l;
+    p.state_out[4 + p.B + b] = f;
+  }
+  if (tid == 0) {
+    p.state_out[0] = bad ? head : in_ring(head + static_cast<int>(run.need));
+    p.state_out[1] = bad ? count : count - static_cast<int>(run.need) + static_cast<int>(run.gone);
+    p.state_out[2] = 0;   // arrivals
+  }
+}
+
+cudaError_t launch_plan(const PlanArgs& a, cudaStream_t s) {
+  PlanK k{a.new_lens, a.state_in, a.state_out, a.free_pages, a.block_table, a.qo_indptr, a.prefix_lens, a.positions, a.slots,
+          a.err, a.B, a.num_tokens, a.page_size, a.num_pages, a.max_pages_per_seq, a.window, FastDiv(a.page_size)};
+  const int smem = (4 * a.B + 1) * static_cast<int>(sizeof(int32_t));
+  static unsigned int done = 0;
+  const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(plan_kernel), (4 * FA_MAX_STEP_BATCH + 1) * 4, &done);
+  if (e != cudaSuccess) return e;
+  // a CTA to 2048 tokens (two rounds of four a thread), at most two CTAs an SM
+  const long long ctas = std::min((static_cast<long long>(a.num_tokens) + 2047) / 2048, 2LL * sm_count());
+  return launch_pdl(plan_kernel, dim3(static_cast<unsigned>(std::max(ctas, 1LL))), dim3(kPlanThreads), static_cast<size_t>(smem), s, k);
+}
+
+}  // namespace fa

@@ -132,6 +132,8 @@ typedef enum { FA_FULL = 0, FA_SLIDING = 1 } fa_layer_kind;
                                       or more in decode over 4-bit slabs (there
                                       plus or less the value's exponent)            */
 
+#define FA_DEV_ERR_POOL 0x40u      /* a step needed more pages than its pool had free */
+
 /* Most fa_cache descriptors that may be live at once (each holds one device
  * error word). */
 #define FA_MAX_CACHES 4096
@@ -313,6 +315,110 @@ FA_API fa_status fa_kv_store(fa_cache* cache, int32_t layer, const void* k, cons
  * a cache of another format or page size, or to inspect it). */
 FA_API fa_status fa_kv_load(fa_cache* cache, int32_t layer, const int32_t* slot_mapping, int32_t T, void* k,
                      void* v, void* stream);
+
+/* How a layer's projected rows become the rows that are stored and attended
+ * (fa_norm_rope_store).  norm: FA_NORM_* of the rows that are normed, each over
+ * its own head_dim values x: y = x / sqrt(mean(x^2) + eps) * (weight_offset + w),
+ * w the head_dim bf16 weights of queries or keys (NULL: no weights; values have
+ * none).  eps: in [1e-30, 1e30].  rotary_dim R: 0 for no rotation, else a multiple of 16,
+ * at most head_dim: of queries and keys each pair (y[i], y[i + R / 2]), i < R / 2,
+ * is turned by position * f_i.  steps: uint64 [R / 2] (device), f_i in turns times
+ * 2^64, modulo 2^64, rounded to the nearest: angles are exact at every position (a step of 0
+ * leaves its pair as it is, so a rotation that skips pairs has zeros there). */
+#define FA_NORM_Q 0x1u
+#define FA_NORM_K 0x2u
+#define FA_NORM_V 0x4u
+typedef struct {
+  const void* q_weight;
+  const void* k_weight;
+  const uint64_t* steps;
+  float eps;
+  float weight_offset;
+  uint32_t norm;
+  int32_t rotary_dim;
+} fa_norm_rope;
+
+/* Norms and rotation of a layer's new rows, and the K and V rows' store, in one
+ * launch: the step between a layer's projection and its attention, whose q, k, v
+ * are "post-RoPE" ("unsloth commit dee9371": the store layer writes its
+ * post-rotary k, v into its paged cache).
+ * q: bf16 rows of T tokens, Hq rows of D values each, token t's at q + t * q_stride
+ * (elements; a multiple of 8, at least Hq * D), so that one projection's [T][(Hq +
+ * 2 Hkv) * D] is read where it lies; k, v: the same with Hkv rows.  q may be NULL
+ * (keys and values alone), k and v both NULL (queries alone).
+ * positions: int32 [T], each token's position (any int32; may be NULL where
+ * rotary_dim is 0).  All arithmetic is fp32, each
+ * row rounded to bf16 once; a row neither normed nor turned goes on bit for bit.
+ * q_out: bf16 [T][Hq][D].  k_out, v_out: bf16 [T][Hkv][D], either may be NULL
+ * (extend takes the chunk's rows from them).  An output may be its own input where
+ * that is dense; otherwise outputs overlap no input.  slot_mapping: as in fa_kv_store,
+ * which the stored bytes equal bit for bit, given the bf16 rows k_out, v_out (padding tokens'
+ * rows are still written there); NULL: nothing is stored.
+ * A KV-shared layer takes its queries alone: k, v, k_out, v_out and slot_mapping
+ * are ignored.  Infinities and NaN go the formula's way: a normed row with an infinity has NaN there
+ * (and in its turned partner) and 0 elsewhere, one with a NaN is NaN.
+ * positions and slot_mapping are read after the kernel before has finished, under
+ * FA_FLAG_EARLY_METADATA too.  T == 0: FA_OK, no launch. */
+FA_API fa_status fa_norm_rope_store(fa_cache* cache, int32_t layer, const fa_norm_rope* how, const void* q,
+                                    int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                    int64_t v_stride, const int32_t* positions, const int32_t* slot_mapping,
+                                    int32_t T, void* q_out, void* k_out, void* v_out, void* stream);
+
+/* Most sequences of one fa_plan_step call. */
+#define FA_MAX_STEP_BATCH 8192
+
+/* int32 words of the state of a batch of B sequences (fa_plan_step). */
+#define FA_PLAN_STATE_WORDS(B) (4 + 2 * (B))
+
+/* One step's block tables and slot maps, built on the GPU from the numbers of new
+ * tokens: the index arrays that every store, decode and extend call reads, with
+ * nothing copied from the host ("FreeToken PR #898", description: a group of
+ * layers shares its tables and slots; "pegainfer issue #807", Description: the
+ * sliding group gives up pages that the full group still reads).
+ * kind: FA_FULL or FA_SLIDING, a group of the cache's layers and its pool
+ * (num_pages, or window_pages where the sliding layers have a pool of their own).
+ * FA_SLIDING keeps of each sequence the pages that a window W, the largest of the
+ * cache's sliding layers, can still see; FA_FULL keeps every page (also for
+ * sliding layers that share the full layers' table).
+ * State, all of it the caller's device memory, changed by each call:
+ *   state        int32 [FA_PLAN_STATE_WORDS(B)]: the place of the first free page
+ *                in free_pages, the number of free pages, two words of 0, the B
+ *                sequences' lengths, the first page that each still holds;
+ *   free_pages   int32 [pages of the pool]: a ring of the free pages;
+ *   block_table  int32 [B][max_pages_per_seq].
+ * At the start: state 0 but for the number of free pages, free_pages 0, 1, 2, ..., no page in use.
+ * new_lens: int32 [B].  n >= 0: n tokens join sequence b behind its len tokens.
+ * n < 0: it ends; its pages become free, its length 0, and it has no tokens in
+ * this step (its row may start another sequence in the next).
+ * A step takes the pages that the new tokens need off the ring's head, in order
+ * of sequence and page, and writes them to the table.  Pages whose last position
+ * lies before len - W + 1, which the step's first query does not see, and pages of
+ * sequences that ended go behind the ring's end in the same order; their table
+ * entries stay as they were, and calls of later steps take them.  Entries past a
+ * sequence's pages stay as they were too.
+ * Out: qo_indptr int32 [B + 1], the new tokens' offsets; prefix_lens int32 [B],
+ * the lengths before the step (0 where one ended); the lengths after it are the state's; positions,
+ * slot_mapping int32 [num_tokens]: of new token i of sequence b at row
+ * qo_indptr[b] + i; rows behind the last sequence's get position 0 and slot -1,
+ * so padded buffers store nothing there.  All of these are as decode, extend,
+ * fa_kv_store and fa_norm_rope_store read them.
+ * state_out may be state (the usual case) or another buffer, whose third word has
+ * to be 0; then state stays as it was and the same step can be made again.
+ * A step that cannot be made leaves state, ring and table as they were and has no
+ * tokens (offsets 0, slots -1, prefix_lens the lengths): FA_DEV_ERR_POOL where free
+ * pages are too few (those that this step gives up do not count), FA_DEV_ERR_BOUND
+ * where a sequence outgrows max_pages_per_seq or the new tokens num_tokens,
+ * FA_DEV_ERR_WORKSPACE for a state that no step leaves.  A ring or table entry
+ * outside the pool sets FA_DEV_ERR_PAGE and its tokens' slots to -1.
+ * 1 <= B <= FA_MAX_STEP_BATCH; max_pages_per_seq * page_size below 2^31 - 256.
+ * Calls on one state run in stream order.  A cache with FA_FLAG_EARLY_METADATA: the call
+ * launched right behind this one must not be one that reads its arrays before it
+ * has finished; fa_norm_rope_store and fa_plan_step do not. */
+FA_API fa_status fa_plan_step(fa_cache* cache, int32_t kind, const int32_t* new_lens, int32_t B,
+                              const int32_t* state, int32_t* state_out, int32_t* free_pages,
+                              int32_t* block_table, int32_t max_pages_per_seq, int32_t* qo_indptr,
+                              int32_t* prefix_lens, int32_t* positions, int32_t* slot_mapping,
+                              int32_t num_tokens, void* stream);
 
 /* Bytes at the head of a decode workspace that hold arrival counters. */
 #define FA_DECODE_COUNTER_BYTES (32u << 10)
