@@ -80,6 +80,9 @@ def _load() -> ctypes.CDLL:
         "fa_paged_decode_attn": (i32, [vp, i32, vp, vp, i32, vp, i32, i32, vp, vp, vp, sz, vp]),
         "fa_paged_decode_store_attn": (i32, [vp, i32, vp, vp, vp, vp, vp, i32, vp, i32, i32, vp, vp, vp, sz, vp]),
         "fa_paged_decode_attn_noalloc": (i32, [vp, i32, vp, vp, i32, vp, i32, i32, vp, vp, vp]),
+        "fa_decode_diff_workspace_bytes": (sz, [vp, i32, i32, i32]),
+        "fa_paged_decode_diff_attn": (i32, [vp, i32, vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, vp, vp, vp, sz, vp]),
+        "fa_paged_extend_diff_attn": (i32, [vp, i32, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp]),
         "fa_kv_store_layers": (i32, [vp, i32, vp, vp, vp, vp, i32, vp]),
         "fa_paged_decode_multi_attn": (i32, [vp, i32, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp]),
         "fa_decode_layers_workspace_bytes": (sz, [vp, i32, vp, i32, i32]),
@@ -303,7 +306,7 @@ class Cache:
         return self._slabs[self.source(layer)]
 
     def _rows(self, layer: int, k, v, slot_mapping, T=None) -> None:
-        """fp4 caches: refuse rows or slots the store of T tokens (None: of every slot) would misread."""
+        """fp4 caches and differential attention: refuse rows or slots the store of T tokens (None: of every slot) would misread."""
         d, dev = self._layer(layer), _device()
         _need("slot_mapping", slot_mapping, torch.int32, dev, T)
         T, row = slot_mapping.numel() if T is None else T, d["num_kv_heads"] * d["head_dim"]
@@ -387,7 +390,7 @@ class Cache:
                                        _ptrs(slot_mappings), T, _s(stream)))
 
     def _decode_args(self, layer: int, q, block_table, seq_lens, out, lse) -> None:
-        """fp4 caches: refuse tensors the decode kernel would misread."""
+        """fp4 caches and differential attention: refuse tensors the decode kernel would misread."""
         d, B, dev = self._layer(layer), q.shape[0], _device()
         row = d["num_q_heads"] * d["head_dim"]
         _need("q", q, torch.bfloat16, dev, B, row)
@@ -472,8 +475,30 @@ class Cache:
                                                  _p(seq_lens), int(q.shape[0]), int(max_seq_len), _p(out), _p(lse),
                                                  _s(stream)))
 
+    def decode_diff_workspace_bytes(self, layer: int, batch: int, max_seq_len: int) -> int:
+        return int(_lib.fa_decode_diff_workspace_bytes(self._h, layer, batch, max_seq_len))
+
+    def decode_diff(self, layer: int, q, lam, block_table, seq_lens, max_seq_len: int, out, lse=None, workspace=None,
+                    k_new=None, v_new=None, slot_mapping=None, stream=None) -> None:
+        """fa_paged_decode_diff_attn: differential attention of one new token per
+        sequence, lam (fp32) a number for each query head; with k_new, v_new and
+        slot_mapping the current rows are stored first, as by decode_store."""
+        d, B = self._layer(layer), q.shape[0]
+        self._decode_args(layer, q, block_table, seq_lens, out, None)
+        _need("lam", lam, torch.float32, _device(), d["num_q_heads"])
+        if lse is not None:
+            _need("lse", lse, torch.float32, _device(), B, 2 * d["num_q_heads"])
+        if not self._owns(layer):
+            k_new = v_new = slot_mapping = None
+        if k_new is not None or v_new is not None or slot_mapping is not None:
+            self._rows(layer, k_new, v_new, slot_mapping, B)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _check(_lib.fa_paged_decode_diff_attn(self._h, layer, _p(q), _p(lam), _p(k_new), _p(v_new), _p(slot_mapping),
+                                              _p(block_table), int(block_table.shape[1]), _p(seq_lens), int(B),
+                                              int(max_seq_len), _p(out), _p(lse), _p(workspace), ws_bytes, _s(stream)))
+
     def _extend_args(self, layer: int, q, indptr, lens, block_table, out, lse, k_ext=None, v_ext=None) -> None:
-        """fp4 caches: refuse tensors the extend kernel would misread."""
+        """fp4 caches and differential attention: refuse tensors the extend kernel would misread."""
         d, N, B, dev = self._layer(layer), q.shape[0], lens.numel(), _device()
         row = d["num_q_heads"] * d["head_dim"]
         _need("q", q, torch.bfloat16, dev, N, row)
@@ -507,6 +532,23 @@ class Cache:
                                          _p(prefix_lens), _p(block_table), maxp, int(prefix_lens.numel()),
                                          int(q.shape[0]), int(max_q_len), int(max_prefix_len), _p(out), _p(lse),
                                          _s(stream)))
+
+    def extend_diff(self, layer: int, q, lam, k_ext, v_ext, qo_indptr, prefix_lens, block_table, max_q_len: int,
+                    max_prefix_len: int, out, lse=None, stream=None) -> None:
+        """fa_paged_extend_diff_attn: differential attention of a chunk over its prefix."""
+        d = self._layer(layer)
+        for name, t in (("k_ext", k_ext), ("v_ext", v_ext)):
+            if t is None:
+                raise FAError(ERR_INVALID_ARG, f"{name} must be non-NULL")
+        self._extend_args(layer, q, qo_indptr, prefix_lens, block_table, out, None, k_ext, v_ext)
+        _need("lam", lam, torch.float32, _device(), d["num_q_heads"])
+        if lse is not None:
+            _need("lse", lse, torch.float32, _device(), q.shape[0], 2 * d["num_q_heads"])
+        maxp = int(block_table.shape[1]) if block_table is not None else 0
+        _check(_lib.fa_paged_extend_diff_attn(self._h, layer, _p(q), _p(lam), _p(k_ext), _p(v_ext), _p(qo_indptr),
+                                              _p(prefix_lens), _p(block_table), maxp, int(prefix_lens.numel()),
+                                              int(q.shape[0]), int(max_q_len), int(max_prefix_len), _p(out), _p(lse),
+                                              _s(stream)))
 
 
 class PageTable:

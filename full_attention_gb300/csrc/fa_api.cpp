@@ -81,7 +81,7 @@ static long long decode_slots(const fa_cache* c) {
   return std::min((c->kv_dtype == FA_KV_FP4 ? 3LL : 2LL) * sm_count(), static_cast<long long>(kLayerCounters));
 }
 
-DecodePlan plan_decode(const fa_cache* c, int layer, int B, int max_seq_len, long long max_cta) {
+DecodePlan plan_decode(const fa_cache* c, int layer, int B, int max_seq_len, long long max_cta, int maps) {
   DecodePlan p;
   const fa_layer_desc& d = c->layers[layer].d;
   const int g = d.num_q_heads / d.num_kv_heads;
@@ -119,8 +119,8 @@ DecodePlan plan_decode(const fa_cache* c, int layer, int B, int max_seq_len, lon
   if (fp4) p.blocks = static_cast<int>(std::min(n, most));
   if (p.ncta > 1) {
     const int parts = fp4 && p.units <= most ? p.blocks : p.ncta;
-    const size_t rows = static_cast<size_t>(parts + p.units) * 8;   // partial slots x heads
-    p.off_o = (rows * (fp4 ? 4 : 2) * sizeof(float) + 255) / 256 * 256;
+    const size_t rows = static_cast<size_t>(parts + p.units) * 8 * maps;   // partial slots x heads x maps
+    p.off_o = (rows * (fp4 || maps == 2 ? 4 : 2) * sizeof(float) + 255) / 256 * 256;
     p.part_bytes = p.off_o + rows * d.head_dim * sizeof(float);
   }
   return p;
@@ -213,6 +213,7 @@ static fa_status encode_fp4_map(CUtensorMap* tm, void* base, int D, uint64_t row
 
 // Queries q [N][Hq][D] as 4-D (64-column block elements, head, token, block
 // index): a box (64, g, 128/g, 1) lands as 128 rows ordered (token, head) x 128 B.
+// Differential attention passes 2 Hq heads of D / 2 values and 2 g: rows (token, head, half).
 static fa_status encode_q_map(CUtensorMap* tm, const void* q, int N, int Hq, int D, int g) {
   auto enc = get_encoder();
   if (!enc) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
@@ -762,11 +763,11 @@ static void fill_decode_args(DecodeArgs& a, const fa_cache* c, int32_t layer, co
 }
 
 // Decode with an optional store of the current token (k_new, v_new, slots
-// non-null for an owning layer).
+// non-null for an owning layer); lambda non-null: differential attention.
 static fa_status decode_call(fa_cache* c, int32_t layer, const void* q, const void* k_new, const void* v_new,
                              const int32_t* slots, const int32_t* block_table, int32_t max_pages_per_seq,
                              const int32_t* seq_lens, int32_t B, int32_t max_seq_len, void* out, float* lse,
-                             void* workspace, size_t workspace_bytes, void* stream) {
+                             void* workspace, size_t workspace_bytes, void* stream, const float* lambda = nullptr) {
   fa_status st = check_layer(c, layer);
   if (st) return st;
   if (B < 0) return fail(FA_ERR_INVALID_ARG, "B must be >= 0");
@@ -781,7 +782,7 @@ static fa_status decode_call(fa_cache* c, int32_t layer, const void* q, const vo
   if (max_pages_per_seq < (max_seq_len - 1) / c->page_size + 1)
     return fail(FA_ERR_INVALID_ARG, "max_pages_per_seq %d cannot hold max_seq_len %d", max_pages_per_seq,
                 max_seq_len);
-  DecodePlan p = plan_decode(c, layer, B, max_seq_len);
+  DecodePlan p = plan_decode(c, layer, B, max_seq_len, 0, lambda ? 2 : 1);
   if ((st = check_tiles(c, p))) return st;
   const size_t need = p.ws_bytes();
   if (workspace_bytes < need || (need && !workspace))
@@ -795,7 +796,8 @@ static fa_status decode_call(fa_cache* c, int32_t layer, const void* q, const vo
   DecodeArgs a{};
   fill_decode_args(a, c, layer, s, p, q, k_new, v_new, slots, block_table, max_pages_per_seq, seq_lens, B,
                    max_seq_len, out, lse, workspace, 0, 0, err);
-  ce = launch_decode(a, static_cast<cudaStream_t>(stream));
+  a.lambda = lambda;
+  ce = lambda ? launch_decode_diff(a, static_cast<cudaStream_t>(stream)) : launch_decode(a, static_cast<cudaStream_t>(stream));
   if (ce != cudaSuccess) return fail(FA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(ce));
   return ok();
 }
@@ -827,6 +829,28 @@ fa_status fa_paged_decode_store_attn(fa_cache* c, int32_t layer, const void* q, 
   }
   return decode_call(c, layer, q, k_new, v_new, slot_mapping, block_table, max_pages_per_seq, seq_lens, B,
                      max_seq_len, out, lse, workspace, workspace_bytes, stream);
+}
+
+size_t fa_decode_diff_workspace_bytes(const fa_cache* c, int32_t layer, int32_t B, int32_t max_seq_len) {
+  if (check_layer(c, layer) != FA_OK || B <= 0 || max_seq_len <= 0 || c->kv_dtype == FA_KV_FP4) return 0;
+  return plan_decode(c, layer, B, max_seq_len, 0, 2).ws_bytes();
+}
+
+fa_status fa_paged_decode_diff_attn(fa_cache* c, int32_t layer, const void* q, const float* lambda, const void* k_new,
+                                    const void* v_new, const int32_t* slot_mapping, const int32_t* block_table,
+                                    int32_t max_pages_per_seq, const int32_t* seq_lens, int32_t B, int32_t max_seq_len,
+                                    void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  fa_status st = check_layer(c, layer);
+  if (st) return st;
+  if (c->kv_dtype == FA_KV_FP4) return fail(FA_ERR_UNSUPPORTED, "differential decode over a 4-bit slab");
+  if (B > 0 && !lambda) return fail(FA_ERR_INVALID_ARG, "lambda must be non-NULL");
+  if (c->layers[layer].owner != layer) k_new = v_new = nullptr, slot_mapping = nullptr;   // its source stored the rows
+  if (B > 0 && (k_new || v_new || slot_mapping)) {
+    if (!k_new || !v_new || !slot_mapping) return fail(FA_ERR_INVALID_ARG, "k_new, v_new, slot_mapping must all be given or all be NULL");
+    if (!aligned16(k_new) || !aligned16(v_new)) return fail(FA_ERR_INVALID_ARG, "k_new, v_new must be 16-byte aligned");
+  }
+  return decode_call(c, layer, q, k_new, v_new, slot_mapping, block_table, max_pages_per_seq, seq_lens, B, max_seq_len, out,
+                     lse, workspace, workspace_bytes, stream, lambda);
 }
 
 fa_status fa_paged_decode_attn_layers(fa_cache* c, int32_t n, const int32_t* layers, const void* const* q,
@@ -924,7 +948,7 @@ static UnpackLayout unpack_layout(const fa_cache* c, int32_t layer, int32_t B, i
 // heads, 8 sequences, 16 queries 36 : 44, 256 queries 111 : 84.
 static bool unpack_pays(const ExtendArgs& a, int ring) {
   const double span = a.kind == FA_SLIDING ? std::min(ring, a.max_prefix_len) : a.max_prefix_len;
-  const int T = 128 / (a.Hq / a.Hkv);
+  const int T = 128 / ((a.lambda ? 2 : 1) * a.Hq / a.Hkv);
   const double jobs = static_cast<double>((a.max_q_len + T - 1) / T) * a.Hkv * (a.D / 256) * a.B;
   const double waves = std::max(1.0, std::ceil(jobs / sm_count()));
   const double saved_us = waves * span / 64 * (a.D == 512 ? 2.5 : 0.6);
@@ -996,7 +1020,8 @@ fa_status fa_cache_bind_extend_workspace(fa_cache* c, void* workspace, size_t by
   return ok();
 }
 
-fa_status fa_paged_extend_attn(fa_cache* c, int32_t layer, const void* q, const void* k_ext, const void* v_ext,
+// Extend; lambda non-null: differential attention.
+static fa_status extend_call(fa_cache* c, int32_t layer, const void* q, const float* lambda, const void* k_ext, const void* v_ext,
                                const int32_t* qo_indptr, const int32_t* prefix_lens, const int32_t* block_table,
                                int32_t max_pages_per_seq, int32_t B, int32_t num_tokens, int32_t max_q_len,
                                int32_t max_prefix_len, void* out, float* lse, void* stream) {
@@ -1006,6 +1031,9 @@ fa_status fa_paged_extend_attn(fa_cache* c, int32_t layer, const void* q, const 
   if (B == 0 || max_q_len == 0 || num_tokens == 0) return ok();
   const Layer& L = c->layers[layer];
   const int g = L.d.num_q_heads / L.d.num_kv_heads;
+  const int maps = lambda ? 2 : 1;
+  if (lambda && 128 % (2 * g) != 0)
+    return fail(FA_ERR_UNSUPPORTED, "differential extend packs 2 Hq/Hkv = %d query halves into 128-row tiles; it must divide 128", 2 * g);
   if (128 % g != 0)
     return fail(FA_ERR_UNSUPPORTED, "extend packs Hq/Hkv = %d query heads into 128-row tiles; it must divide 128", g);
   const Slab* s = nullptr;
@@ -1053,8 +1081,9 @@ fa_status fa_paged_extend_attn(fa_cache* c, int32_t layer, const void* q, const 
   a.early_metadata = (c->flags & FA_FLAG_EARLY_METADATA) ? 1 : 0;
   a.sm_scale = L.d.sm_scale;
   a.err = err;
+  a.lambda = lambda;
   set_split(c, a);
-  if ((st = encode_q_map(&a.tm_q, q, num_tokens, L.d.num_q_heads, L.d.head_dim, g))) return st;
+  if ((st = encode_q_map(&a.tm_q, q, num_tokens, maps * L.d.num_q_heads, L.d.head_dim / maps, maps * g))) return st;
   if ((st = encode_ext_map(&a.tm_kx, k_ext, num_tokens, L.d.num_kv_heads, L.d.head_dim))) return st;
   if ((st = encode_ext_map(&a.tm_vx, v_ext, num_tokens, L.d.num_kv_heads, L.d.head_dim))) return st;
   CUtensorMap tm_unpacked[2];
@@ -1062,6 +1091,24 @@ fa_status fa_paged_extend_attn(fa_cache* c, int32_t layer, const void* q, const 
   ce = launch_extend(a, static_cast<cudaStream_t>(stream));
   if (ce != cudaSuccess) return fail(FA_ERR_CUDA, "extend launch: %s", cudaGetErrorString(ce));
   return ok();
+}
+
+fa_status fa_paged_extend_attn(fa_cache* c, int32_t layer, const void* q, const void* k_ext, const void* v_ext,
+                               const int32_t* qo_indptr, const int32_t* prefix_lens, const int32_t* block_table,
+                               int32_t max_pages_per_seq, int32_t B, int32_t num_tokens, int32_t max_q_len,
+                               int32_t max_prefix_len, void* out, float* lse, void* stream) {
+  return extend_call(c, layer, q, nullptr, k_ext, v_ext, qo_indptr, prefix_lens, block_table, max_pages_per_seq, B, num_tokens,
+                     max_q_len, max_prefix_len, out, lse, stream);
+}
+
+fa_status fa_paged_extend_diff_attn(fa_cache* c, int32_t layer, const void* q, const float* lambda, const void* k_ext,
+                                    const void* v_ext, const int32_t* qo_indptr, const int32_t* prefix_lens,
+                                    const int32_t* block_table, int32_t max_pages_per_seq, int32_t B, int32_t num_tokens,
+                                    int32_t max_q_len, int32_t max_prefix_len, void* out, float* lse, void* stream) {
+  if (!c) return fail(FA_ERR_INVALID_ARG, "cache is NULL");
+  if (!lambda) return fail(FA_ERR_INVALID_ARG, "lambda must be non-NULL");
+  return extend_call(c, layer, q, lambda, k_ext, v_ext, qo_indptr, prefix_lens, block_table, max_pages_per_seq, B, num_tokens,
+                     max_q_len, max_prefix_len, out, lse, stream);
 }
 
 fa_status fa_paged_decode_multi_attn(fa_cache* c, int32_t layer, const void* q, const int32_t* qo_indptr,

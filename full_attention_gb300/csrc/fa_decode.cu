@@ -252,9 +252,97 @@ __device__ void merge_unit(const DecK& p, int u, const Unit& x, int nh, int head
   named_bar_sync(1, 128);   // the scratch (the score-exchange buffer) is free again
 }
 
+// The same of a unit's two maps (differential attention): the 16 rows are (map m,
+// head h) at 8 m + h, their partials at ml_part [slot][16][4] (base, rounded sum,
+// unrounded sum, 0) and o_part [slot][16][D], and
+//   out_h = O_0h / l_0h - lambda_h O_1h / l_1h.
+// A thread holds the same columns of a head's two rows.  8 threads a row join the
+// (m, l) pairs; wbuf holds 16 x 64 weights, then 16 x (max, 1 / rounded sum, lse).
+template <int D>
+__device__ void merge_unit_diff(const DecK& p, int u, const Unit& x, int nh, int head0, int cf, int cl, float* wbuf) {
+  constexpr int CH = 64;                    // source CTAs per weight chunk
+  constexpr int ITEMS = 16 * (D / 4) / 128; // float4 sums per thread
+  const int tid = threadIdx.x;
+  const int nct = cl - cf + 1;
+  const float4* mlg = reinterpret_cast<const float4*>(p.ml_part);
+  float* Mr = wbuf + 16 * CH;
+  float* Ir = Mr + 16;
+  const int row = tid >> 3, k = tid & 7;
+  float M = -INFINITY, L = 0.f, A = 0.f;
+  for (int c = k; c < nct; c += 8) {
+    const float4 v = __ldcg(mlg + (static_cast<size_t>(cf + c) + u) * 16 + row);
+    if (v.x == -INFINITY) continue;
+    const float Mn = fmaxf(M, v.x), f = ex2(M - Mn), w = ex2(v.x - Mn);
+    L = L * f + v.y * w;
+    A = A * f + v.z * w;
+    M = Mn;
+  }
+#pragma unroll
+  for (int o = 4; o; o >>= 1) {
+    const float Mo = __shfl_xor_sync(0xffffffffu, M, o), Lo = __shfl_xor_sync(0xffffffffu, L, o), Ao = __shfl_xor_sync(0xffffffffu, A, o);
+    const float Mn = fmaxf(M, Mo);
+    const float f = Mn == -INFINITY ? 0.f : ex2(M - Mn), w = Mn == -INFINITY ? 0.f : ex2(Mo - Mn);
+    L = L * f + Lo * w;
+    A = A * f + Ao * w;
+    M = Mn;
+  }
+  if (k == 0) {
+    Mr[row] = M;
+    Ir[row] = L > 0.f ? 1.0f / L : 0.f;
+    if (p.lse && (row & 7) < nh)
+      p.lse[(static_cast<size_t>(x.b) * p.Hq + head0 + (row & 7)) * 2 + (row >> 3)] = (M + __log2f(A)) * 0.69314718055994531f;
+  }
+  float4 acc[ITEMS];
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c0 = 0; c0 < nct; c0 += CH) {
+    const int n = min(CH, nct - c0);
+    named_bar_sync(1, 128);
+    for (int e = tid; e < n * 16; e += 128) {
+      const int c = e >> 4, r = e & 15;
+      wbuf[e] = ((r & 7) < nh) ? ex2(__ldcg(p.ml_part + ((static_cast<size_t>(cf + c0 + c) + u) * 16 + r) * 4) - Mr[r]) : 0.f;
+    }
+    named_bar_sync(1, 128);
+#pragma unroll 2
+    for (int c = 0; c < n; ++c) {
+      const float* src = p.o_part + (static_cast<size_t>(cf + c0 + c) + u) * 16 * D;
+      float4 o[ITEMS];
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i) {
+        const int idx = tid + i * 128, r = idx / (D / 4), d = (idx % (D / 4)) * 4;
+        o[i] = ((r & 7) < nh) ? __ldcg(reinterpret_cast<const float4*>(src + r * D + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i) {
+        const float w = wbuf[c * 16 + (tid + i * 128) / (D / 4)];
+        acc[i].x += w * o[i].x;
+        acc[i].y += w * o[i].y;
+        acc[i].z += w * o[i].z;
+        acc[i].w += w * o[i].w;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < ITEMS / 2; ++i) {
+    const int idx = tid + i * 128, h = idx / (D / 4), d = (idx % (D / 4)) * 4;
+    if (h >= nh) continue;
+    const float w0 = Ir[h], w1 = -__ldg(p.lambda + head0 + h) * Ir[8 + h];
+    const float4 a = acc[i], b = acc[i + ITEMS / 2];
+    uint2 packed;
+    packed.x = pack_bf16x2(a.x * w0 + b.x * w1, a.y * w0 + b.y * w1);
+    packed.y = pack_bf16x2(a.z * w0 + b.z * w1, a.w * w0 + b.w * w1);
+    *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(x.b) * p.Hq + head0 + h) * D + d) = packed;
+  }
+  named_bar_sync(1, 128);   // the scratch (the score-exchange buffer) is free again
+}
+
 // One CTA of a layer's decode: CTA `cta` of the `grid` CTAs launched for the
 // layer (a launch may hold several layers; see decode_layers_kernel).
-template <int D, int KV>
+// MAPS = 2: differential attention.  A consumer warp's QK^T columns lie in one half
+// of the row, so its partial scores belong to one map: the exchange adds up each
+// map's warps apart, at no cost in MMAs; each lane then holds its head's weights of
+// both maps, and each V fragment feeds two MMAs.
+template <int D, int KV, int MAPS = 1>
 __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUtensorMap* tm_v,
                                             const CUtensorMap* tm_ks, const CUtensorMap* tm_vs, const DecK& p,
                                             const int cta, const int grid) {
@@ -284,7 +372,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
   if (!cut_share(p, cta, grid, sh)) {
     if (sh.ncta == 0 && cta == 0) {   // nothing visible anywhere: only empty outputs to write
       griddep_wait();
-      zero_empty_units<D, KV>(p, 0, 1, threadIdx.x, blockDim.x);
+      zero_empty_units<D, KV, MAPS>(p, 0, 1, threadIdx.x, blockDim.x);
     }
     return;
   }
@@ -423,7 +511,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
 
   // -------------------------------------------------------------- consumers
   griddep_wait();
-  zero_empty_units<D, KV>(p, cta, ncta, threadIdx.x, C::NCW * 32);
+  zero_empty_units<D, KV, MAPS>(p, cta, ncta, threadIdx.x, C::NCW * 32);
   const int qk_tile = warp % C::NT;
   const int qk_d0 = (warp / C::NT) * C::QK_COLS;
   const int pv_d0 = warp * C::PV_COLS;
@@ -480,10 +568,16 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
     __syncwarp();
     if (lane == 0) mbar_arrive(qempty);
 
-    float o[C::PV_MT][4];
+    // l_run: the sum of the weights as the PV MMA takes them; l_all (MAPS 2): unrounded, for lse
+    float o[MAPS][C::PV_MT][4];
+    float m_run[MAPS], l_run[MAPS], l_all[MAPS], sigma = 1.0f;
 #pragma unroll
-    for (int i = 0; i < C::PV_MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-    float m_run = -INFINITY, l_run = 0.0f, sigma = 1.0f;
+    for (int m = 0; m < MAPS; ++m) {
+      m_run[m] = -INFINITY;
+      l_run[m] = l_all[m] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < C::PV_MT; ++i) o[m][i][0] = o[m][i][1] = o[m][i][2] = o[m][i][3] = 0.0f;
+    }
 
     for (int tile0 = ta; tile0 < tz; tile0 += C::NT) {
       const int st = gi % C::NSTAGE;
@@ -532,31 +626,14 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
 
       {
         // ---- scores for this lane's head (gid), keys {2tig, 2tig+1, 2tig+8, 2tig+9} of each tile
-        float s[C::NT][4];
         bool valid[C::NT][4];
-        float mloc = -INFINITY;
 #pragma unroll
-        for (int t = 0; t < C::NT; ++t) {
+        for (int t = 0; t < C::NT; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int key = 2 * tig + (e & 1) + (e >> 1) * 8;
-            float v = 0.0f;
-#pragma unroll
-            for (int w = t; w < C::NCW; w += C::NT) v += sx[((buf * C::NCW + w) * kTile + key) * C::SX_STRIDE + gid];
-            const int pos = (tile0 + t) * kTile + key;
+            const int pos = (tile0 + t) * kTile + 2 * tig + (e & 1) + (e >> 1) * 8;
             valid[t][e] = (t < ntl) && pos >= lo && pos <= qpos;
-            float sc = p.scale_log2;
-            if constexpr (KV) sc *= scl[t * 32 + key];
-            s[t][e] = valid[t][e] ? v * sc : -INFINITY;
-            mloc = fmaxf(mloc, s[t][e]);
           }
-        }
-        mloc = fmaxf(mloc, __shfl_xor_sync(0xffffffffu, mloc, 1));
-        mloc = fmaxf(mloc, __shfl_xor_sync(0xffffffffu, mloc, 2));
-        const float m_new = fmaxf(m_run, mloc);
-        const float alpha = (m_run == -INFINITY) ? 0.0f : ex2(m_run - m_new);
-        float psum = 0.0f;
-        uint32_t pf[C::NT][2];
         float vmax = 1.0f, ivm = 1.0f;
         float vsc[C::NT][4];   // 8-bit: this lane's keys' V scales (0 where not visible)
         if constexpr (KV) {
@@ -573,46 +650,72 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
           vmax = vm > 0.0f ? vm : 1.0f;
           ivm = __frcp_rn(vmax);   // one reciprocal per step instead of a division per weight
         }
+        uint32_t pf[MAPS][C::NT][2];
 #pragma unroll
-        for (int t = 0; t < C::NT; ++t) {
-          float pe[4];
+        for (int m = 0; m < MAPS; ++m) {
+          float s[C::NT][4];
+          float mloc = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            pe[e] = ex2(s[t][e] - m_new);
-            if constexpr (KV) {
-              psum += pe[e];
-              pe[e] *= vsc[t][e] * ivm;
+          for (int t = 0; t < C::NT; ++t) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = 2 * tig + (e & 1) + (e >> 1) * 8;
+              float v = 0.0f;
+#pragma unroll
+              for (int w = t + m * (C::NCW / MAPS); w < (m + 1) * (C::NCW / MAPS); w += C::NT)
+                v += sx[((buf * C::NCW + w) * kTile + key) * C::SX_STRIDE + gid];
+              float sc = p.scale_log2;
+              if constexpr (KV) sc *= scl[t * 32 + key];
+              s[t][e] = valid[t][e] ? v * sc : -INFINITY;
+              mloc = fmaxf(mloc, s[t][e]);
             }
           }
-          if constexpr (!KV) {
-            // the denominator sums the bf16-rounded weights the PV MMA uses, so
-            // the weights of each output row sum to exactly one
-            pf[t][0] = pack_bf16x2(pe[0], pe[1]);
-            pf[t][1] = pack_bf16x2(pe[2], pe[3]);
-            psum += __uint_as_float(pf[t][0] << 16) + __uint_as_float(pf[t][0] & 0xffff0000u) +
-                    __uint_as_float(pf[t][1] << 16) + __uint_as_float(pf[t][1] & 0xffff0000u);
-          } else {
-            pf[t][0] = pack_f16x2(pe[0], pe[1]);
-            pf[t][1] = pack_f16x2(pe[2], pe[3]);
+          mloc = fmaxf(mloc, __shfl_xor_sync(0xffffffffu, mloc, 1));
+          mloc = fmaxf(mloc, __shfl_xor_sync(0xffffffffu, mloc, 2));
+          const float m_new = fmaxf(m_run[m], mloc);
+          const float alpha = (m_run[m] == -INFINITY) ? 0.0f : ex2(m_run[m] - m_new);
+          float psum = 0.0f, pall = 0.0f;
+#pragma unroll
+          for (int t = 0; t < C::NT; ++t) {
+            float pe[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              pe[e] = ex2(s[t][e] - m_new);
+              if constexpr (MAPS == 2 && !KV) pall += pe[e];
+              if constexpr (KV) {
+                psum += pe[e];
+                pe[e] *= vsc[t][e] * ivm;
+              }
+            }
+            if constexpr (!KV) {
+              // the denominator sums the bf16-rounded weights the PV MMA uses, so
+              // the weights of each output row sum to exactly one
+              pf[m][t][0] = pack_bf16x2(pe[0], pe[1]);
+              pf[m][t][1] = pack_bf16x2(pe[2], pe[3]);
+              psum += __uint_as_float(pf[m][t][0] << 16) + __uint_as_float(pf[m][t][0] & 0xffff0000u) +
+                      __uint_as_float(pf[m][t][1] << 16) + __uint_as_float(pf[m][t][1] & 0xffff0000u);
+            } else {
+              pf[m][t][0] = pack_f16x2(pe[0], pe[1]);
+              pf[m][t][1] = pack_f16x2(pe[2], pe[3]);
+            }
+          }
+          l_run[m] = l_run[m] * alpha + psum;
+          if constexpr (MAPS == 2 && !KV) l_all[m] = l_all[m] * alpha + pall;
+          m_run[m] = m_new;
+          float ofac = alpha;
+          if constexpr (KV) ofac = alpha * sigma * ivm;
+          // rescale O: this lane's O columns are heads 2tig and 2tig+1
+          const float fa_ = __shfl_sync(0xffffffffu, ofac, 8 * tig);
+          const float fb_ = __shfl_sync(0xffffffffu, ofac, 8 * tig + 4);
+#pragma unroll
+          for (int mt = 0; mt < C::PV_MT; ++mt) {
+            o[m][mt][0] *= fa_;
+            o[m][mt][1] *= fb_;
+            o[m][mt][2] *= fa_;
+            o[m][mt][3] *= fb_;
           }
         }
-        l_run = l_run * alpha + psum;
-        m_run = m_new;
-        float ofac = alpha;
-        if constexpr (KV) {
-          ofac = alpha * sigma * ivm;
-          sigma = vmax;
-        }
-        // rescale O: this lane's O columns are heads 2tig and 2tig+1
-        const float fa_ = __shfl_sync(0xffffffffu, ofac, 8 * tig);
-        const float fb_ = __shfl_sync(0xffffffffu, ofac, 8 * tig + 4);
-#pragma unroll
-        for (int mt = 0; mt < C::PV_MT; ++mt) {
-          o[mt][0] *= fa_;
-          o[mt][1] *= fb_;
-          o[mt][2] *= fa_;
-          o[mt][3] *= fb_;
-        }
+        if constexpr (KV) sigma = vmax;
 
         if constexpr (KV != FA_KV_INT8) {
           // masked keys have p = 0, but their V rows may hold anything (NaN
@@ -651,7 +754,8 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
               const int dc = pv_d0 + mt * 16 + ((lane >> 3) & 1) * 8;
               uint32_t a0, a1, a2, a3;
               ldsm_x4_t(smem_u32(vt + (dc >> 6) * 2048 + sw128(r, (dc & 63) >> 3)), a0, a1, a2, a3);
-              mma_bf16(o[mt], a0, a1, a2, a3, pf[t][0], pf[t][1]);
+              #pragma unroll
+              for (int m = 0; m < MAPS; ++m) mma_bf16(o[m][mt], a0, a1, a2, a3, pf[m][t][0], pf[m][t][1]);
             }
           } else {
 #pragma unroll
@@ -659,10 +763,13 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
               const int dc = pv_d0 + gi2 * 32 + ((lane >> 3) & 1) * 16;
               uint32_t r0, r1, r2, r3;
               ldsm_x4_t(smem_u32(vt + (dc >> 7) * 2048 + sw128(r, (dc & 127) >> 4)), r0, r1, r2, r3);
-              mma_f16(o[2 * gi2], codes_to_f16x2<KV, 0, 2>(r0), codes_to_f16x2<KV, 0, 2>(r1),
-                      codes_to_f16x2<KV, 0, 2>(r2), codes_to_f16x2<KV, 0, 2>(r3), pf[t][0], pf[t][1]);
-              mma_f16(o[2 * gi2 + 1], codes_to_f16x2<KV, 1, 3>(r0), codes_to_f16x2<KV, 1, 3>(r1),
-                      codes_to_f16x2<KV, 1, 3>(r2), codes_to_f16x2<KV, 1, 3>(r3), pf[t][0], pf[t][1]);
+#pragma unroll
+              for (int m = 0; m < MAPS; ++m) {
+                mma_f16(o[m][2 * gi2], codes_to_f16x2<KV, 0, 2>(r0), codes_to_f16x2<KV, 0, 2>(r1),
+                        codes_to_f16x2<KV, 0, 2>(r2), codes_to_f16x2<KV, 0, 2>(r3), pf[m][t][0], pf[m][t][1]);
+                mma_f16(o[m][2 * gi2 + 1], codes_to_f16x2<KV, 1, 3>(r0), codes_to_f16x2<KV, 1, 3>(r1),
+                        codes_to_f16x2<KV, 1, 3>(r2), codes_to_f16x2<KV, 1, 3>(r3), pf[m][t][0], pf[m][t][1]);
+              }
             }
           }
         }
@@ -674,11 +781,21 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
 
     {
       // ------------------------------------------------------ segment epilogue
-      l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
-      l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
       const int hA = 2 * tig, hB = 2 * tig + 1;
-      const float lA = __shfl_sync(0xffffffffu, l_run, 8 * tig);
-      const float lB = __shfl_sync(0xffffffffu, l_run, 8 * tig + 4);
+      float lA[MAPS], lB[MAPS];
+#pragma unroll
+      for (int m = 0; m < MAPS; ++m) {
+        l_run[m] += __shfl_xor_sync(0xffffffffu, l_run[m], 1);
+        l_run[m] += __shfl_xor_sync(0xffffffffu, l_run[m], 2);
+        if constexpr (MAPS == 2 && !KV) {
+          l_all[m] += __shfl_xor_sync(0xffffffffu, l_all[m], 1);
+          l_all[m] += __shfl_xor_sync(0xffffffffu, l_all[m], 2);
+        } else {
+          l_all[m] = l_run[m];
+        }
+        lA[m] = __shfl_sync(0xffffffffu, l_run[m], 8 * tig);
+        lB[m] = __shfl_sync(0xffffffffu, l_run[m], 8 * tig + 4);
+      }
       // output column d of C-fragment row (gid + 8 * half) of O^T tile mt
       auto out_d = [&](int mt, int half) -> int {
         if constexpr (!KV) return pv_d0 + mt * 16 + gid + 8 * half;
@@ -687,32 +804,54 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
       const int c_first = kper ? u * kper : cta_of(P, ncta, T);
       const int c_last = kper ? c_first + kper - 1 : cta_of(P + x.n - 1, ncta, T);
       if (c_first == c_last) {
-        const float iA = (lA > 0.f) ? sigma / lA : 0.f, iB = (lB > 0.f) ? sigma / lB : 0.f;
+        float iA[MAPS], iB[MAPS];
+#pragma unroll
+        for (int m = 0; m < MAPS; ++m) {
+          iA[m] = (lA[m] > 0.f) ? sigma / lA[m] : 0.f;
+          iB[m] = (lB[m] > 0.f) ? sigma / lB[m] : 0.f;
+        }
+        if constexpr (MAPS == 2) {   // the second map's weight: - lambda
+          iA[MAPS - 1] *= hA < nh ? -__ldg(p.lambda + head0 + hA) : 0.f;
+          iB[MAPS - 1] *= hB < nh ? -__ldg(p.lambda + head0 + hB) : 0.f;
+        }
 #pragma unroll
         for (int mt = 0; mt < C::PV_MT; ++mt)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             const int d = out_d(mt, half);
-            if (hA < nh)
-              p.out[(static_cast<size_t>(x.b) * p.Hq + head0 + hA) * D + d] = __float2bfloat16_rn(o[mt][2 * half] * iA);
-            if (hB < nh)
-              p.out[(static_cast<size_t>(x.b) * p.Hq + head0 + hB) * D + d] =
-                  __float2bfloat16_rn(o[mt][2 * half + 1] * iB);
+            float yA = o[0][mt][2 * half] * iA[0], yB = o[0][mt][2 * half + 1] * iB[0];
+            if constexpr (MAPS == 2) {
+              yA += o[MAPS - 1][mt][2 * half] * iA[MAPS - 1];
+              yB += o[MAPS - 1][mt][2 * half + 1] * iB[MAPS - 1];
+            }
+            if (hA < nh) p.out[(static_cast<size_t>(x.b) * p.Hq + head0 + hA) * D + d] = __float2bfloat16_rn(yA);
+            if (hB < nh) p.out[(static_cast<size_t>(x.b) * p.Hq + head0 + hB) * D + d] = __float2bfloat16_rn(yB);
           }
         if (p.lse && warp == 0 && tig == 0 && hv)
-          p.lse[static_cast<size_t>(x.b) * p.Hq + head0 + gid] = (m_run + __log2f(l_run)) * 0.69314718055994531f;
+#pragma unroll
+          for (int m = 0; m < MAPS; ++m)
+            p.lse[(static_cast<size_t>(x.b) * p.Hq + head0 + gid) * MAPS + m] = (m_run[m] + __log2f(l_all[m])) * 0.69314718055994531f;
       } else {
         const size_t slot = static_cast<size_t>(cta) + u;
 #pragma unroll
-        for (int mt = 0; mt < C::PV_MT; ++mt)
+        for (int m = 0; m < MAPS; ++m)
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int d = out_d(mt, half);
-            p.o_part[(slot * 8 + hA) * D + d] = o[mt][2 * half] * sigma;
-            p.o_part[(slot * 8 + hB) * D + d] = o[mt][2 * half + 1] * sigma;
+          for (int mt = 0; mt < C::PV_MT; ++mt)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const int d = out_d(mt, half);
+              p.o_part[((slot * MAPS + m) * 8 + hA) * D + d] = o[m][mt][2 * half] * sigma;
+              p.o_part[((slot * MAPS + m) * 8 + hB) * D + d] = o[m][mt][2 * half + 1] * sigma;
+            }
+        if (warp == 0 && tig == 0) {
+          if constexpr (MAPS == 1) {
+            reinterpret_cast<float2*>(p.ml_part)[slot * 8 + gid] = make_float2(m_run[0], l_run[0]);
+          } else {
+#pragma unroll
+            for (int m = 0; m < MAPS; ++m)
+              reinterpret_cast<float4*>(p.ml_part)[(slot * MAPS + m) * 8 + gid] = make_float4(m_run[m], l_run[m], l_all[m], 0.f);
           }
-        if (warp == 0 && tig == 0)
-          reinterpret_cast<float2*>(p.ml_part)[slot * 8 + gid] = make_float2(m_run, l_run);
+        }
         // arrive; the last of the unit's CTAs merges every partial row.  The
         // barrier orders the CTA's partial writes before thread 0's
         // release/acquire add, which publishes them and, for the last
@@ -735,8 +874,11 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
         if (sh_last) {
           // the ring is idle once this CTA's last segment is consumed: stage the merge there
           const bool idle = P + x.n >= s_end;
-          merge_unit<D, C::STAGE_ALL>(p, u, x, nh, head0, c_first, c_last, sx, idle ? smem : nullptr, mbar_merge,
-                                       &abort_flag);
+          if constexpr (MAPS == 1)
+            merge_unit<D, C::STAGE_ALL>(p, u, x, nh, head0, c_first, c_last, sx, idle ? smem : nullptr, mbar_merge,
+                                         &abort_flag);
+          else
+            merge_unit_diff<D>(p, u, x, nh, head0, c_first, c_last, sx);
         }
       }
     }
@@ -752,6 +894,14 @@ __global__ void __launch_bounds__(DecCfg<D, KV>::NTHR, 2)
                   const __grid_constant__ CUtensorMap tm_ks, const __grid_constant__ CUtensorMap tm_vs,
                   const DecK p) {
   decode_body<D, KV>(&tm_k, &tm_v, &tm_ks, &tm_vs, p, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
+}
+
+template <int D, int KV>
+__global__ void __launch_bounds__(DecCfg<D, KV>::NTHR, 2)
+    decode_diff_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                       const __grid_constant__ CUtensorMap tm_ks, const __grid_constant__ CUtensorMap tm_vs,
+                       const DecK p) {
+  decode_body<D, KV, 2>(&tm_k, &tm_v, &tm_ks, &tm_vs, p, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
 }
 
 // Several layers of one head_dim and KV format in one launch: the CTAs of
@@ -806,6 +956,27 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s) {
   }
   if (a.D == 256) return launch_decode_t<256, FA_KV_BF16>(a, k, s);
   return launch_decode_t<512, FA_KV_BF16>(a, k, s);
+}
+
+template <int D, int KV>
+static cudaError_t launch_decode_diff_t(const DecodeArgs& a, const DecK& k, cudaStream_t s) {
+  using C = DecCfg<D, KV>;
+  // a warp's QK^T columns within one half of the row; the merge's scratch
+  static_assert((C::NCW / C::NT) % 2 == 0 && C::QK_COLS * (C::NCW / C::NT) == D, "halves by warps");
+  static_assert(C::NCW == 4 && (16 * 64 + 32) * 4 <= C::SX_BYTES, "merge scratch");
+  static unsigned int done = 0;
+  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(decode_diff_kernel<D, KV>), C::SMEM_ALLOC, &done);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(decode_diff_kernel<D, KV>, dim3(a.plan.ncta), dim3(C::NTHR), C::SMEM_ALLOC, s, *a.tm_k, *a.tm_v,
+                    *a.tm_ks, *a.tm_vs, k);
+}
+
+cudaError_t launch_decode_diff(const DecodeArgs& a, cudaStream_t s) {
+  const DecK k = make_deck(a);
+  if (a.kv_dtype == FA_KV_INT8) return a.D == 256 ? launch_decode_diff_t<256, FA_KV_INT8>(a, k, s) : launch_decode_diff_t<512, FA_KV_INT8>(a, k, s);
+  if (a.kv_dtype == FA_KV_FP8) return a.D == 256 ? launch_decode_diff_t<256, FA_KV_FP8>(a, k, s) : launch_decode_diff_t<512, FA_KV_FP8>(a, k, s);
+  if (a.kv_dtype != FA_KV_BF16) return cudaErrorInvalidValue;
+  return a.D == 256 ? launch_decode_diff_t<256, FA_KV_BF16>(a, k, s) : launch_decode_diff_t<512, FA_KV_BF16>(a, k, s);
 }
 
 cudaError_t launch_decode_layers(const DecodeArgs* a, int n, cudaStream_t s) {

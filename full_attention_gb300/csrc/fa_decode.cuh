@@ -30,6 +30,7 @@ struct DecK {
   int B, Hq, Hkv, g, chunks, kind, window, page_size, tiles_per_page, num_pages, max_pages_per_seq;
   int max_seq_len, units, min_tiles, early_metadata;
   int shares;         // fp4: shares the work may be cut into
+  const float* lambda;   // differential attention: [Hq]
   float scale_log2;   // sm_scale * log2(e)
 };
 
@@ -233,8 +234,9 @@ __device__ __forceinline__ void store_current(const DecK& p, const RowRegs<D>& r
 }
 
 // Sequences of length <= 0 get out = 0 and lse = -inf; CTA `cta` of `ncta`
-// writes the units u with u % ncta == cta.
-template <int D, int KV>
+// writes the units u with u % ncta == cta.  MAPS: softmax maps a head (2 in
+// differential attention).
+template <int D, int KV, int MAPS = 1>
 __device__ void zero_empty_units(const DecK& p, int cta, int ncta, int tid, int nthr) {
   for (int u = cta; u < p.units; u += ncta) {
     const Unit x = unit_of(p, u);
@@ -249,7 +251,7 @@ __device__ void zero_empty_units(const DecK& p, int cta, int ncta, int tid, int 
     const int nh = min(8, p.g - x.c * 8), head0 = x.h * p.g + x.c * 8;
     for (int i = tid; i < nh * D; i += nthr)
       p.out[(static_cast<size_t>(x.b) * p.Hq + head0 + i / D) * D + i % D] = __float2bfloat16(0.0f);
-    if (p.lse && tid < nh) p.lse[static_cast<size_t>(x.b) * p.Hq + head0 + tid] = -INFINITY;
+    if (p.lse && tid < nh * MAPS) p.lse[(static_cast<size_t>(x.b) * p.Hq + head0) * MAPS + tid] = -INFINITY;
   }
 }
 
@@ -290,6 +292,7 @@ inline DecK make_deck(const DecodeArgs& a) {
   k.min_tiles = a.plan.min_tiles;
   k.early_metadata = a.early_metadata;
   k.shares = a.plan.ncta;
+  k.lambda = a.lambda;
   k.scale_log2 = a.sm_scale * 1.4426950408889634f;
   return k;
 }

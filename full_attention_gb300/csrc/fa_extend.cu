@@ -63,9 +63,20 @@
 // conversion paces it (1218 us for 8 sequences of 4096 keys at head_dim 512, 2 KV
 // heads, 256 queries each, against 556 over rows unpacked to bf16 first); it
 // serves short calls and caches without a workspace for the unpacked rows.
+// Differential attention (DIFF): a head's two query halves are two rows of the tile,
+// 2 i and 2 i + 1 (q read as 2 Hq heads of D / 2 values, so one 4-D box still
+// brings 128 rows, now of half the columns; g and T count halves).  Row m's
+// operand is its half in the columns of half m and zero in the other: moving Q to
+// tensor memory the softmax warps write those zeros, and where Q stays in shared
+// memory (the second half at head_dim 512) its even rows are zeroed.  Everything
+// after that is plain attention on 128 rows; the epilogue adds a head's two rows,
+// neighbouring lanes, with weights 1 / l_0 and - lambda / l_1.  The zeros double
+// the S products (4 MMAs of 128 x 64 x 64 columns for 3 that count); two S tiles
+// without them would need two O accumulators, twice the tensor memory there is.
 // Every wait is bounded; tensor memory is always freed.
 #include <algorithm>
 #include <cfloat>
+#include <type_traits>
 
 #include <cuda_fp8.h>
 
@@ -170,6 +181,7 @@ struct ExtK {
   unsigned int* err;
   int B, Hq, Hkv, g, T, kind, window, page_size, tiles_per_page, num_pages, max_pages_per_seq;
   int max_q_len, max_prefix_len, dslices, early_metadata, num_tokens, keys_in_pages;
+  const float* lambda;   // DIFF: [Hq / 2], Hq, g and T counting query halves
   float scale_log2;
   // Jobs (128-row block, KV head and column slice, sequence) are numbered
   // row block fastest (last block first), gx row blocks and gy (head,
@@ -351,7 +363,7 @@ __device__ __forceinline__ void bulk_store_drain() {
   asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
-template <int D, int KV>
+template <int D, int KV, bool DIFF>
 __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
     extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kx,
@@ -459,12 +471,14 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
       // slots, the rest into its shared-memory blocks (8-bit slabs: the
       // softmax warps then rewrite those in place as f16)
       prefetch_tmap(&tm_q);
-      mbar_arrive_expect_tx(qst_full, C::NQT * (C::M * 128));
-      for (int kb = 0; kb < C::NQT; ++kb)
+      // (DIFF: the map holds KB / 2 blocks; those beyond are the same ones again)
+      constexpr int QB = DIFF ? C::KB / 2 : C::KB, QTL = C::NQT < QB ? C::NQT : QB;
+      mbar_arrive_expect_tx(qst_full, QTL * (C::M * 128));
+      for (int kb = 0; kb < QTL; ++kb)
         tma_load_4d(ring + C::QST_OFF + kb * (C::M * 128), &tm_q, qst_full, 0, x.h * p.g, x.qo0 + x.t0, kb, pol);
       mbar_arrive_expect_tx(q_full, C::Q_BYTES);
       for (int kb = C::NQT; kb < C::KB; ++kb)
-        tma_load_4d(qs + (kb - C::NQT) * (C::M * 128), &tm_q, q_full, 0, x.h * p.g, x.qo0 + x.t0, kb, pol);
+        tma_load_4d(qs + (kb - C::NQT) * (C::M * 128), &tm_q, q_full, 0, x.h * p.g, x.qo0 + x.t0, kb % QB, pol);
     }
     if (lane == 0) {
       prefetch_tmap(&tm_k);
@@ -964,13 +978,17 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
       // so those values go as f16, and Q's shared-memory blocks are rewritten
       // in place as f16 too.  Then the staging slots are released.
       bool qok = mbar_wait(qst_full, 0);
-      if constexpr (C::Q8) qok = mbar_wait(q_full, 0) && qok;
+      constexpr bool QS = C::Q8 || DIFF;   // Q's shared-memory blocks are rewritten too
+      if constexpr (QS) qok = mbar_wait(q_full, 0) && qok;
       if (!__all_sync(0xffffffffu, qok) && lane == 0) atomicOr(p.err, FA_DEV_ERR_TIMEOUT);
-      constexpr int QBLK = C::Q8 ? C::KB : C::NQT;
+      constexpr int QBLK = QS ? C::KB : C::NQT;
       uint32_t qbig = 0;
 #pragma unroll 1
       for (int kb = half; kb < QBLK; kb += 2) {
-        uint8_t* blk = kb < C::NQT ? ring + C::QST_OFF + kb * (C::M * 128) : qs + (kb - C::NQT) * (C::M * 128);
+        constexpr int QB = DIFF ? C::KB / 2 : C::KB;
+        uint8_t* blk = kb < C::NQT ? ring + C::QST_OFF + (kb % QB) * (C::M * 128) : qs + (kb - C::NQT) * (C::M * 128);
+        const bool other = DIFF && (r & 1) != kb / QB;   // a block of the other half: zeros
+        if (!C::Q8 && kb >= C::NQT && !other) continue;  // (DIFF) in place as it is
         uint32_t w[32];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
@@ -987,16 +1005,20 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
             w[i] = pack_f16x2_sat(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
           }
         }
+        if constexpr (DIFF) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) w[i] = other ? 0u : w[i];
+        }
         if (kb < C::NQT) {
           tmem_st32(trow + C::Q_COL0 + kb * 32, w);
-        } else {   // 8-bit slabs only
+        } else {   // 8-bit slabs, DIFF
 #pragma unroll
           for (int u = 0; u < 8; ++u)
             *reinterpret_cast<uint4*>(blk + sw128(r, u)) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
         }
       }
+      if constexpr (QS) fence_proxy_async_smem();   // the Q rows written here, for the S MMA
       if constexpr (C::Q8) {
-        fence_proxy_async_smem();   // the Q rows written here, for the S MMA
         if (__any_sync(0xffffffffu, qbig != 0) && lane == 0) atomicOr(p.err, FA_DEV_ERR_RANGE);
       }
       tmem_st_wait();
@@ -1174,12 +1196,20 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
       for (int e = 0; e < 4; ++e)
         *reinterpret_cast<uint4*>(stg + ((c >> 5) * 4 + e) * 16) = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
     };
+    // DIFF: a head's output row leaves from its first half's lane (Hq / 2 rows a token)
+    const size_t head = static_cast<size_t>(x.qo0 + t) * p.Hq + x.h * p.g + hj;   // (DIFF) of halves: also lse's index
     auto write_rows = [&]() {
       const uint8_t* stg = ring + 4096 + (quarter * 2 + half) * (32 * 272) + lane * 272;
       fence_proxy_async_smem();   // the rows just written, for the bulk copy's reads
-      if (row_ok) bulk_store(p.out + (static_cast<size_t>(x.qo0 + t) * p.Hq + x.h * p.g + hj) * D + x.ds * C::DS + half * OH,
-                             stg, OH * 2);
+      if (row_ok && !(DIFF && (lane & 1)))
+        bulk_store(p.out + (DIFF ? head >> 1 : head) * D + x.ds * C::DS + half * OH, stg, OH * 2);
       bulk_store_drain();
+    };
+    // DIFF: the weight of a row's map in its head's output, and the head's two rows added
+    const float map_weight = DIFF && (lane & 1) ? -(row_ok ? __ldg(p.lambda + ((x.h * p.g + hj) >> 1)) : 0.f) : 1.0f;
+    auto joined = [&](float y) {
+      if constexpr (DIFF) return y + __shfl_xor_sync(0xffffffffu, y, 1);
+      else return y;
     };
     if (x.ks == 2) {
       // A split job: leave this CTA's partial (unnormalised O over its tiles,
@@ -1239,7 +1269,7 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
         const float lt = (first ? l_tot : om.y) * f0 + (first ? om.y : l_tot) * f1;
         const float la = (first ? l_all : om.z) * f0 + (first ? om.z : l_all) * f1;
         const float inv = (lt > 0.f) ? 1.0f / lt : 0.f;
-        const float w0 = f0 * inv, w1 = f1 * inv;
+        const float w0 = f0 * inv * map_weight, w1 = f1 * inv * map_weight;
         const float4* oo = p.ws_o + (pj + (x.s ^ 1)) * (C::M * C::DS / 4) + grp * 32 + lane;
         tc_fence_after();
 #pragma unroll 1
@@ -1256,7 +1286,7 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const float own = __uint_as_float(o[4 * e + k]);
-              y[k] = (first ? own : oth[k]) * w0 + (first ? oth[k] : own) * w1;
+              y[k] = joined((first ? own : oth[k]) * w0 + (first ? oth[k] : own) * w1);
             }
             w[2 * e] = pack_bf16x2(y[0], y[1]);
             w[2 * e + 1] = pack_bf16x2(y[2], y[3]);
@@ -1265,12 +1295,12 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
         }
         write_rows();
         if (row_ok && half == 0 && x.ds == 0 && p.lse)
-          p.lse[static_cast<size_t>(x.qo0 + t) * p.Hq + x.h * p.g + hj] =
+          p.lse[head] =
               (bm > -INFINITY && la > 0.f) ? (bm + __log2f(la)) * 0.69314718055994531f : -INFINITY;
       }
     } else if (fin) {
       tc_fence_after();
-      const float inv = (l_tot > 0.f) ? 1.0f / l_tot : 0.f;
+      const float inv = ((l_tot > 0.f) ? 1.0f / l_tot : 0.f) * map_weight;
 #pragma unroll 1
       for (int c = 0; c < OH; c += 32) {
         uint32_t o[32];
@@ -1279,12 +1309,12 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
         uint32_t w[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          w[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+          w[e] = pack_bf16x2(joined(__uint_as_float(o[2 * e]) * inv), joined(__uint_as_float(o[2 * e + 1]) * inv));
         stage(c, w);
       }
       write_rows();
       if (row_ok && half == 0 && x.ds == 0 && p.lse)
-        p.lse[static_cast<size_t>(x.qo0 + t) * p.Hq + x.h * p.g + hj] =
+        p.lse[head] =
             (m_run > -INFINITY && l_all > 0.f) ? (m_run - MB_OFF + __log2f(l_all)) * 0.69314718055994531f : -INFINITY;
     }
   }
@@ -1298,16 +1328,16 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
   }
 }
 
-template <int D, int KV>
+template <int D, int KV, bool DIFF>
 static cudaError_t launch_extend_t(const ExtendArgs& a, const ExtK& k, cudaStream_t s) {
   using C = ExtCfg<D, KV>;
   static unsigned int done = 0;
-  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(extend_kernel<D, KV>), C::SMEM_ALLOC, &done);
+  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(extend_kernel<D, KV, DIFF>), C::SMEM_ALLOC, &done);
   if (e != cudaSuccess) return e;
   const long long jobs = static_cast<long long>(k.gx) * k.gy * a.B;
   const long long ctas = k.split_from + 2 * (jobs - k.split_from);
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  return launch_pdl(extend_kernel<D, KV>, dim3(static_cast<unsigned>(ctas)), dim3(C::NTHR), C::SMEM_ALLOC, s, a.tm_q,
+  return launch_pdl(extend_kernel<D, KV, DIFF>, dim3(static_cast<unsigned>(ctas)), dim3(C::NTHR), C::SMEM_ALLOC, s, a.tm_q,
                     *a.tm_k, *a.tm_v, a.tm_kx, a.tm_vx, k);
 }
 
@@ -1347,9 +1377,11 @@ cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t s) {
   k.lse = a.lse;
   k.err = a.err;
   k.B = a.B;
-  k.Hq = a.Hq;
+  const int maps = a.lambda ? 2 : 1;   // differential attention: every head's two halves are rows
+  k.lambda = a.lambda;
+  k.Hq = maps * a.Hq;
   k.Hkv = a.Hkv;
-  k.g = a.Hq / a.Hkv;
+  k.g = maps * a.Hq / a.Hkv;
   k.T = 128 / k.g;
   k.kind = a.kind;
   k.window = a.window;
@@ -1375,13 +1407,17 @@ cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t s) {
     k.ws_ml = reinterpret_cast<float4*>(ws + l.off_ml);
     k.ws_o = reinterpret_cast<float4*>(ws + l.off_o);
   }
-  if (a.kv_dtype == FA_KV_INT8)
-    return a.D == 256 ? launch_extend_t<256, FA_KV_INT8>(a, k, s) : launch_extend_t<512, FA_KV_INT8>(a, k, s);
-  if (a.kv_dtype == FA_KV_FP8)
-    return a.D == 256 ? launch_extend_t<256, FA_KV_FP8>(a, k, s) : launch_extend_t<512, FA_KV_FP8>(a, k, s);
-  if (a.kv_dtype == FA_KV_FP4)
-    return a.D == 256 ? launch_extend_t<256, FA_KV_FP4>(a, k, s) : launch_extend_t<512, FA_KV_FP4>(a, k, s);
-  return a.D == 256 ? launch_extend_t<256, FA_KV_BF16>(a, k, s) : launch_extend_t<512, FA_KV_BF16>(a, k, s);
+  auto run = [&](auto diff) {
+    constexpr bool X = decltype(diff)::value;
+    if (a.kv_dtype == FA_KV_INT8)
+      return a.D == 256 ? launch_extend_t<256, FA_KV_INT8, X>(a, k, s) : launch_extend_t<512, FA_KV_INT8, X>(a, k, s);
+    if (a.kv_dtype == FA_KV_FP8)
+      return a.D == 256 ? launch_extend_t<256, FA_KV_FP8, X>(a, k, s) : launch_extend_t<512, FA_KV_FP8, X>(a, k, s);
+    if (a.kv_dtype == FA_KV_FP4)
+      return a.D == 256 ? launch_extend_t<256, FA_KV_FP4, X>(a, k, s) : launch_extend_t<512, FA_KV_FP4, X>(a, k, s);
+    return a.D == 256 ? launch_extend_t<256, FA_KV_BF16, X>(a, k, s) : launch_extend_t<512, FA_KV_BF16, X>(a, k, s);
+  };
+  return a.lambda ? run(std::true_type{}) : run(std::false_type{});
 }
 
 }  // namespace fa

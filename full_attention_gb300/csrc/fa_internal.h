@@ -111,7 +111,8 @@ struct DecodePlan {
   size_t ws_bytes() const { return part_bytes ? kCounterBytes + part_bytes : 0; }
 };
 // max_cta > 0 caps the launch's CTAs for this layer (default: two per SM).
-DecodePlan plan_decode(const fa_cache* c, int layer, int B, int max_seq_len, long long max_cta = 0);
+// maps: softmax maps a query head (2 in differential attention), each with partial rows.
+DecodePlan plan_decode(const fa_cache* c, int layer, int B, int max_seq_len, long long max_cta = 0, int maps = 1);
 
 // Launch with programmatic stream serialisation (overlaps launch latency with
 // the previous kernel's tail); every kernel waits on griddepcontrol first.
@@ -239,10 +240,13 @@ struct DecodeArgs {
   int B, Hq, Hkv, D, kind, window, page_size, num_pages, max_pages_per_seq, max_seq_len, kv_dtype;
   int early_metadata;
   float sm_scale;
+  const float* lambda;      // differential attention (null: plain): [Hq]
   DecodePlan plan;
   unsigned int* err;
 };
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s);
+// Differential attention (bf16 and 8-bit slabs).
+cudaError_t launch_decode_diff(const DecodeArgs& a, cudaStream_t s);
 // Several layers of one head_dim and KV format in one launch (n <= kMaxLayersPerLaunch).
 cudaError_t launch_decode_layers(const DecodeArgs* a, int n, cudaStream_t s);
 
@@ -272,6 +276,7 @@ struct ExtendArgs {
   int keys_in_pages;   // 1: every key from the slab (new tokens already stored), no k_ext / v_ext
   float sm_scale;
   unsigned int* err;
+  const float* lambda;   // differential attention (null: plain): [Hq]
   // per-call maps: q as (64-column block, head, token, block index) boxes of
   // (64, g, 128/g, 1); k_ext / v_ext as (64, block, KV head, token) boxes of (64, 1, 1, 64)
   CUtensorMap tm_q, tm_kx, tm_vx;

@@ -492,6 +492,31 @@ FA_API fa_status fa_paged_decode_store_attn(fa_cache* cache, int32_t layer, cons
                                      int32_t max_seq_len, void* out, float* lse, void* workspace,
                                      size_t workspace_bytes, void* stream);
 
+/* Workspace bytes fa_paged_decode_diff_attn needs (as fa_decode_workspace_bytes;
+ * twice the partial rows).  0 where a single CTA serves the call, and on an fp4 cache.  Host only. */
+FA_API size_t fa_decode_diff_workspace_bytes(const fa_cache* cache, int32_t layer, int32_t B,
+                                             int32_t max_seq_len);
+
+/* Differential attention over the paged cache, one new token per sequence: queries
+ * and keys of D values are two of D / 2, and head j of KV head h gives
+ *   out_j = (softmax(s q_j1 K_1^T) - lambda_j softmax(s q_j2 K_2^T)) V,
+ * q_j1, K_1 the first D / 2 columns, q_j2, K_2 the others, V all D, s = sm_scale
+ * (usually 1 / sqrt(D / 2)) and lambda_j a learned number: float [Hq] (device), as the
+ * model computes it from its vectors.  The norm that a model puts behind out is its own.
+ * Layers, slabs, masks, lengths, tables, bounds, ranges and errors as in fa_paged_decode_attn;
+ * each K and V row is read once for both maps.  k_new, v_new, slot_mapping: all NULL, or
+ * the current token's rows and slots, stored as by fa_paged_decode_store_attn (ignored for a
+ * KV-shared layer).  out: bf16 [B][Hq][D]; its error is one of the two terms, not
+ * of their difference.  lse: optional float [B][Hq][2], of both maps.  seq_lens[b]
+ * <= 0 gives out = 0, lse = -inf.  workspace: as in fa_paged_decode_attn, of
+ * fa_decode_diff_workspace_bytes; one buffer may serve both calls.  bf16 and 8-bit
+ * slabs; fp4 is FA_ERR_UNSUPPORTED (its decode kernel keeps one base a row; extend serves it). */
+FA_API fa_status fa_paged_decode_diff_attn(fa_cache* cache, int32_t layer, const void* q, const float* lambda,
+                                           const void* k_new, const void* v_new, const int32_t* slot_mapping,
+                                           const int32_t* block_table, int32_t max_pages_per_seq,
+                                           const int32_t* seq_lens, int32_t B, int32_t max_seq_len, void* out,
+                                           float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Most layers one multi-layer store or decode call takes. */
 #define FA_MAX_LAYERS_PER_LAUNCH 16
 
@@ -605,6 +630,17 @@ FA_API fa_status fa_paged_extend_attn(fa_cache* cache, int32_t layer, const void
                                int32_t max_pages_per_seq, int32_t B, int32_t num_tokens,
                                int32_t max_q_len, int32_t max_prefix_len, void* out, float* lse,
                                void* stream);
+
+/* Differential attention (fa_paged_decode_diff_attn) of a chunk of new tokens over a
+ * paged prefix: arguments, layers, masks, ranges and errors as in
+ * fa_paged_extend_attn, lambda and lse (float [N][Hq][2]) as above.  Every slab
+ * format; 2 * Hq / Hkv must divide 128. */
+FA_API fa_status fa_paged_extend_diff_attn(fa_cache* cache, int32_t layer, const void* q, const float* lambda,
+                                           const void* k_ext, const void* v_ext, const int32_t* qo_indptr,
+                                           const int32_t* prefix_lens, const int32_t* block_table,
+                                           int32_t max_pages_per_seq, int32_t B, int32_t num_tokens,
+                                           int32_t max_q_len, int32_t max_prefix_len, void* out, float* lse,
+                                           void* stream);
 
 /* Decode of n_b >= 1 new tokens per sequence whose k, v rows are already
  * stored: the verification step of speculative decoding, whose drafted

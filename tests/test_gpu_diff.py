@@ -1,0 +1,182 @@
+"""Differential attention over the paged cache, decode and extend, against 64 bits
+(bounds in diff_case.py)."""
+import pytest
+import torch
+
+import workloads as W
+from diff_case import DiffCase
+
+pytestmark = pytest.mark.gpu
+
+FORMATS = [W.KV_BF16, W.KV_INT8, W.KV_FP8]
+
+DECODE = [  # D, hq, hkv, page, window, lens
+    (256, 1, 1, 16, 0, [1]), (512, 8, 1, 16, 0, [1, 2, 15, 16, 17, 0, 33]), (256, 4, 1, 16, 64, [200]),
+    (512, 8, 1, 16, 0, [4096, 513, 70]), (256, 16, 8, 16, 100, [900, 99, 100, 101, 1, 0, 3000]),
+    (512, 12, 2, 48, 0, [1000, 5, 0, 2500, 31]), (256, 9, 1, 32, 1, [50, 1, 16, 17]), (512, 24, 1, 64, 33, [700, 20]),
+    (256, 34, 2, 256, 0, [2222, 300, 1, 0]), (512, 16, 2, 16, 1024, [5000, 1023, 1024, 1025]),
+    (256, 8, 1, 16, 0, [0, 0]), (512, 8, 8, 16, 0, [20000]), (256, 8, 1, 16, 0, list(range(1, 200))), (512, 4, 4, 16, 300, [299 + i for i in range(90)]),
+]
+
+
+@pytest.mark.parametrize("kv", FORMATS)
+@pytest.mark.parametrize("D,hq,hkv,ps,window,lens", DECODE)
+def test_decode(D, hq, hkv, ps, window, lens, kv):
+    c = DiffCase(D, hq, hkv, ps, lens, kv, window, seed=D + hq + len(lens))
+    c.check(*c.decode())
+
+
+@pytest.mark.parametrize("kv", FORMATS)
+@pytest.mark.parametrize("D,early", [(256, True), (512, False)])
+def test_decode_stores_the_current_rows(D, early, kv):
+    """One launch equals the store and the decode; the slab's bytes are the store's."""
+    lens = [1, 40, 0, 700, 16, 17, 3000]
+    c = DiffCase(D, 8, 2, 16, lens, kv, seed=D, early=early)
+    new = [torch.zeros((c.B, 2, D), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    slots = torch.full((c.B,), -1, dtype=torch.int32, device="cuda")
+    for b, n in enumerate(lens):
+        if n > 0:
+            slots[b] = int(c.bt[b, (n - 1) // 16]) * 16 + (n - 1) % 16
+            for i in range(2):
+                new[i][b] = c.raw[b][1][i][-1]
+    c.cache.store(0, *new, slots)
+    want = [t.clone() for t in c.decode()]
+    slab = [None if t is None else t.clone() for t in c.slabs]
+    for slot in slots[slots >= 0].tolist():
+        for i in range(2):
+            c.slabs[i][slot // 16, :, slot % 16] = 0x55 if kv else 3.0
+            if kv:
+                c.slabs[2 + i][slot // 16, :, slot % 16] = float("nan")
+    got = c.decode(k_new=new[0], v_new=new[1], slot_mapping=slots)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all(a is None or torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(slab, c.slabs))
+    c.check(*got)
+
+
+@pytest.mark.parametrize("lam", [0.0, 1.0, -2.5, 1e3])
+def test_lambda(lam):
+    c = DiffCase(512, 8, 1, 16, [300, 7], seed=3, lam=lam, offset=4.0)
+    c.check(*c.decode())
+    e = DiffCase(256, 4, 2, 16, [300, 0], new=[9, 130], seed=3, lam=lam, offset=4.0)
+    e.check(*e.extend())
+
+
+def test_equal_maps_leave_one_minus_lambda():
+    """The same halves give the same weights: (1 - lambda) softmax(..) v, and 0 at lambda 1 exactly."""
+    for kv in FORMATS:
+        c = DiffCase(256, 8, 1, 16, [1200, 50], kv, seed=4, lam=1.0)
+        h = c.D // 2
+        c.q[..., h:] = c.q[..., :h]
+        c.slabs[0][..., h:] = c.slabs[0][..., :h]
+        out, lse = c.decode()
+        assert torch.equal(lse[..., 0], lse[..., 1])
+        assert float(out.float().abs().max()) <= 2.0 ** -20
+
+
+def test_shared_layers_read_their_source():
+    c = DiffCase(512, 8, 2, 16, [400, 33], seed=5, shared=True)
+    c.check(*c.decode(k_new=None, v_new=None, slot_mapping=None))
+    e = DiffCase(256, 8, 2, 32, [400, 33], W.KV_INT8, new=[5, 60], seed=5, shared=True)
+    e.check(*e.extend())
+
+
+EXTEND = [  # D, hq, hkv, page, window, prefix, new
+    (256, 1, 1, 16, 0, [0], [1]), (512, 4, 2, 16, 0, [0, 5], [3, 1]), (256, 16, 8, 16, 100, [900, 99, 0], [64, 63, 130]),
+    (512, 16, 2, 32, 0, [1000, 0, 70, 16], [1, 300, 64, 0]), (256, 64, 1, 16, 0, [130], [40]), (512, 32, 1, 64, 40, [500, 39], [77, 2]),
+    (256, 8, 8, 48, 1, [100, 0], [33, 65]), (512, 2, 1, 16, 700, [3000, 699], [200, 5]), (256, 2, 1, 256, 0, [2047], [513]),
+]
+
+
+@pytest.mark.parametrize("kv", FORMATS + [W.KV_FP4])
+@pytest.mark.parametrize("D,hq,hkv,ps,window,prefix,new", EXTEND)
+@pytest.mark.parametrize("split", [None, "all"])
+def test_extend(D, hq, hkv, ps, window, prefix, new, split, kv):
+    if kv == W.KV_FP4:   # rows that the 4-bit cache keeps exactly: its own, read back
+        c = _fp4(D, hq, hkv, ps, window, prefix, new)
+    else:
+        c = DiffCase(D, hq, hkv, ps, prefix, kv, window, new, seed=D + hq + len(new))
+    if split:
+        fa = c.fa
+        ws = fa.workspace(c.cache.extend_workspace_bytes(c.layer, c.B, max(new), max(prefix)))
+        c.cache.bind_extend_workspace(ws)
+        c.cache.set_flags(fa.FLAG_EXTEND_SPLIT_ALL)
+    c.check(*c.extend())
+
+
+def _fp4(D, hq, hkv, ps, window, prefix, new):
+    import full_attention_gb300 as fa
+    c = DiffCase(D, hq, hkv, ps, prefix, W.KV_BF16, window, new, seed=D + hq + len(new))
+    lay = dict(c.cache.layers[0])
+    cache = fa.Cache([lay], c.cache.num_pages, ps, fa.KV_FP4)
+    c.slabs = cache.allocate("cuda")[0]
+    for t in c.slabs:
+        t.fill_(float("nan") if t.is_floating_point() else 0x7F)
+    rows = []
+    for b, n in enumerate(prefix):
+        lo, (k, v) = c.raw[b]
+        pos = torch.arange(lo, n, device="cuda")
+        if len(pos):
+            slots = (c.bt[b][pos // ps].long() * ps + pos % ps).int()
+            cache.store(0, k, v, slots)
+            kb, vb = torch.empty_like(k), torch.empty_like(v)
+            cache.load(0, slots, kb, vb)
+            k, v = kb, vb
+        rows.append((lo, k.double(), v.double()))
+    c.cache, c.rows, c.kv = cache, rows, W.KV_FP4
+    return c
+
+
+def test_one_workspace_serves_plain_and_differential_calls():
+    c = DiffCase(512, 8, 1, 16, [3000, 2000, 77], seed=6)
+    d = DiffCase(512, 8, 1, 16, [9000, 40], seed=7)
+    ws = c.fa.workspace(max(x.cache.decode_diff_workspace_bytes(0, x.B, x.max_len()) for x in (c, d)))
+    first = None
+    for _ in range(2):
+        c.check(*c.decode(ws))
+        plain = torch.empty_like(d.out)
+        d.cache.decode(0, d.q, d.bt, d.lens_dev, d.max_len(), plain, None, ws)
+        d.check(*d.decode(ws))
+        first = plain.clone() if first is None else first
+        assert torch.equal(first, plain)
+    assert int(ws[: c.fa.DECODE_COUNTER_BYTES].any()) == 0
+
+
+def test_captured_calls_and_another_stream():
+    c = DiffCase(256, 8, 2, 16, [3000, 1, 250], W.KV_FP8, seed=8)
+    e = DiffCase(512, 8, 2, 16, [300, 0], new=[40, 130], seed=8)
+    ws = c.fa.workspace(c.cache.decode_diff_workspace_bytes(0, c.B, c.max_len()))
+    want = [t.clone() for t in c.decode(ws) + e.extend()]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.decode(ws)
+        e.extend()
+    for t in (c.out, c.lse, e.out, e.lse):
+        t.fill_(7.0)
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((c.out, c.lse, e.out, e.lse), want))
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        c.decode(ws)
+        e.extend()
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((c.out, c.lse, e.out, e.lse), want))
+
+
+def test_faults_are_reported_not_followed():
+    fa = DiffCase(256, 2, 1, 16, [40], seed=1).fa
+    c = DiffCase(256, 2, 1, 16, [40, 40], seed=1)
+    c.bt[0, 1] = c.cache.num_pages
+    out, _ = c.decode()
+    assert c.cache.device_error() == fa.DEV_ERR_PAGE
+    ref, _, room = c.reference()
+    assert bool(((out[1].double() - ref[1]).abs() <= room[1]).all())
+    c = DiffCase(256, 2, 1, 16, [40, 40], seed=1)
+    ws = fa.workspace(c.cache.decode_diff_workspace_bytes(0, 2, 39))
+    c.cache.decode_diff(0, c.q, c.lam, c.bt, c.lens_dev, 39, c.out, c.lse, ws)
+    assert c.cache.device_error() == fa.DEV_ERR_BOUND
+    c = DiffCase(512, 2, 1, 16, [40], W.KV_INT8, seed=1)
+    c.q[0, 1, 300] = 1e5
+    c.decode()
+    assert c.cache.device_error() == fa.DEV_ERR_RANGE
