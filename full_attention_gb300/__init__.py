@@ -145,13 +145,26 @@ def _need(what, t, dtype, dev, rows=None, per=1):
     rows of per elements than `rows`."""
     if t is None:
         raise FAError(ERR_INVALID_ARG, f"{what} must be non-NULL")
-    if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != dev:
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
         raise FAError(ERR_INVALID_ARG, f"{what} must be a dense {dtype} tensor on the current CUDA device, not "
                                        f"{t.dtype}, strides {tuple(t.stride())}, on {t.device}")
     if rows is None or t.numel() == rows * per:
         return
     if t.dim() == 0 or t.shape[0] < rows or t.numel() != t.shape[0] * per:
         raise FAError(ERR_INVALID_ARG, f"{what}, of shape {tuple(t.shape)}, must hold {rows} rows of {per} elements")
+
+
+def _token_stride(what, t, T, heads, D, dev) -> int:
+    """Elements from token to token of bf16 rows [T][heads][D] (or [T][heads * D]), which
+    may be a slice of wider rows; refused where they are not dense within a token."""
+    if t is None:
+        return 0
+    if t.dtype is torch.bfloat16 and t.get_device() == dev:
+        st, shape = t.stride(), t.shape
+        if shape == (T, heads, D) and st[2] == 1 and (st[1] == D or heads == 1) or shape == (T, heads * D) and st[1] == 1:
+            return st[0] if T > 1 else heads * D
+    raise FAError(ERR_INVALID_ARG, f"{what} must hold bf16 rows {(T, heads, D)} on the current CUDA device, dense within a token, "
+                                   f"not {t.dtype}, {tuple(t.shape)}, strides {tuple(t.stride())}, on {t.device}")
 
 
 def _per_layer(layers, **lists) -> None:
@@ -195,7 +208,12 @@ class NormRope:
         self.q_weight, self.k_weight = q_weight, k_weight
         self.steps = torch.tensor([v - (1 << 64) if v >> 63 else v for v in steps], dtype=torch.int64, device=device) if steps else None
         norm = NORM_Q * bool(norm_q) | NORM_K * bool(norm_k) | NORM_V * bool(norm_v)
+        on = {t.get_device() for t in (q_weight, k_weight, self.steps) if t is not None}
+        if len(on) > 1:
+            raise FAError(ERR_INVALID_ARG, f"the weights and steps are on different devices: {sorted(on)}")
+        self.device = on.pop() if on else None   # None: nothing on a device
         self.desc = NormRopeDesc(_p(q_weight), _p(k_weight), _p(self.steps), float(eps), float(weight_offset), norm, 2 * len(steps))
+        self.ref = ctypes.byref(self.desc)
 
 
 class Cache:
@@ -338,36 +356,29 @@ class Cache:
         [T][Hkv][D] (slices of one projection's rows are taken as they lie), and the
         store of k and v at slot_mapping (None: not stored), in one launch."""
         d, dev = self._layer(layer), _device()
-        D, owns = d["head_dim"], self._owns(layer)
+        D, hq, hkv = d["head_dim"], d["num_q_heads"], d["num_kv_heads"]
         if how.head_dim != D:
             raise FAError(ERR_INVALID_ARG, f"how is for head_dim {how.head_dim}, layer {layer} has {D}")
-        for t in (how.q_weight, how.k_weight, how.steps):
-            if t is not None and t.get_device() != dev:
-                raise FAError(ERR_INVALID_ARG, f"how's tensors are on {t.device}, not on the current CUDA device")
-        if not owns:
+        if how.device is not None and how.device != dev:
+            raise FAError(ERR_INVALID_ARG, f"how's tensors are on CUDA device {how.device}, not on the current one")
+        if d.get("kv_source", KV_OWN) != KV_OWN:
             k = v = slot_mapping = k_out = v_out = None
-        first = next((x for x in (q, k) if x is not None), None)
+        first = k if q is None else q
         T = 0 if first is None else first.shape[0]
-        strides = []
-        for name, x, h in (("q", q, d["num_q_heads"]), ("k", k, d["num_kv_heads"]), ("v", v, d["num_kv_heads"])):
-            if x is None:
-                strides.append(0)
-                continue
-            shape, rows = tuple(x.shape), ((T, h, D), (T, h * D))
-            dense = x.stride(-1) == 1 and (x.dim() < 3 or x.stride(1) == D or h == 1)
-            if x.dtype is not torch.bfloat16 or x.get_device() != dev or shape not in rows or not dense:
-                raise FAError(ERR_INVALID_ARG, f"{name} must hold bf16 rows {rows[0]} on the current CUDA device, dense within a token, "
-                                               f"not {x.dtype}, {shape}, strides {tuple(x.stride())}, on {x.device}")
-            strides.append(x.stride(0) if T > 1 else h * D)
-        for name, x, h in (("q_out", q_out, d["num_q_heads"]), ("k_out", k_out, d["num_kv_heads"]), ("v_out", v_out, d["num_kv_heads"])):
-            if x is not None:
-                _need(name, x, torch.bfloat16, dev, T, h * D)
-        for name, x in (("positions", positions), ("slot_mapping", slot_mapping)):
-            if x is not None:
-                _need(name, x, torch.int32, dev, T)
-        _check(_lib.fa_norm_rope_store(self._h, layer, ctypes.byref(how.desc), _p(q), strides[0], _p(k), strides[1], _p(v),
-                                       strides[2], _p(positions), _p(slot_mapping), T, _p(q_out), _p(k_out), _p(v_out),
-                                       _s(stream)))
+        qs, ks, vs = (_token_stride("q", q, T, hq, D, dev), _token_stride("k", k, T, hkv, D, dev),
+                      _token_stride("v", v, T, hkv, D, dev))
+        if q_out is not None:
+            _need("q_out", q_out, torch.bfloat16, dev, T, hq * D)
+        if k_out is not None:
+            _need("k_out", k_out, torch.bfloat16, dev, T, hkv * D)
+        if v_out is not None:
+            _need("v_out", v_out, torch.bfloat16, dev, T, hkv * D)
+        if positions is not None:
+            _need("positions", positions, torch.int32, dev, T)
+        if slot_mapping is not None:
+            _need("slot_mapping", slot_mapping, torch.int32, dev, T)
+        _check(_lib.fa_norm_rope_store(self._h, layer, how.ref, _p(q), qs, _p(k), ks, _p(v), vs, _p(positions),
+                                       _p(slot_mapping), T, _p(q_out), _p(k_out), _p(v_out), _s(stream)))
 
     def page_table(self, kind: int, batch: int, max_pages_per_seq: int, device="cuda") -> PageTable:
         """The tables of an empty batch (fa_plan_step): every page of the kind's pool free."""
@@ -574,18 +585,22 @@ class PageTable:
     def step(self, new_lens, qo_indptr, prefix_lens, positions, slot_mapping, state_out=None, stream=None) -> None:
         """One step: new_lens[b] tokens join sequence b (negative: it ends); the outputs
         are filled for the calls of the step."""
-        B, dev, c = self.batch, _device(), self.cache
+        bt, c, dev, i32 = self.block_table, self.cache, _device(), torch.int32
+        B, cols = bt.shape
         N = slot_mapping.numel()
-        pages = c.window_pages if self.kind == SLIDING and c.window_pages > 0 else c.num_pages
-        for name, t, n in (("new_lens", new_lens, B), ("qo_indptr", qo_indptr, B + 1), ("prefix_lens", prefix_lens, B),
-                           ("positions", positions, N), ("slot_mapping", slot_mapping, N), ("free_pages", self.free_pages, pages),
-                           ("state", self.state, 4 + 2 * B), ("block_table", self.block_table, self.block_table.numel())):
-            _need(name, t, torch.int32, dev, n)
+        _need("new_lens", new_lens, i32, dev, B)
+        _need("qo_indptr", qo_indptr, i32, dev, B + 1)
+        _need("prefix_lens", prefix_lens, i32, dev, B)
+        _need("positions", positions, i32, dev, N)
+        _need("slot_mapping", slot_mapping, i32, dev, N)
+        _need("free_pages", self.free_pages, i32, dev, c.window_pages if self.kind == SLIDING and c.window_pages > 0 else c.num_pages)
+        _need("state", self.state, i32, dev, 4 + 2 * B)
+        _need("block_table", bt, i32, dev)
         if state_out is not None:
-            _need("state_out", state_out, torch.int32, dev, 4 + 2 * B)
+            _need("state_out", state_out, i32, dev, 4 + 2 * B)
         _check(_lib.fa_plan_step(c._h, self.kind, _p(new_lens), B, _p(self.state), _p(self.state if state_out is None else state_out),
-                                 _p(self.free_pages), _p(self.block_table), self.block_table.shape[1], _p(qo_indptr),
-                                 _p(prefix_lens), _p(positions), _p(slot_mapping), N, _s(stream)))
+                                 _p(self.free_pages), _p(bt), cols, _p(qo_indptr), _p(prefix_lens), _p(positions),
+                                 _p(slot_mapping), N, _s(stream)))
 
 
 def device_error(stream=None) -> int:

@@ -13,10 +13,10 @@
 // head and the ring's end.
 //
 // One launch.  Every CTA sums over all sequences (12 bytes each, from L2) and
-// keeps the sums in shared memory; its share of the tokens then finds its
-// sequence by bisection.  The ring's pops and pushes never meet (they lie count
-// apart in a ring that holds every page), so only the state is written late, by
-// the CTA that arrives last: the state read and the one written may be the same.
+// keeps the sums in shared memory; a warp's run of tokens then finds its
+// sequence by bisection, once where it lies in one.  The ring's pops and pushes never meet (they lie count
+// apart in a ring that holds every page), so only the state waits until every CTA has
+// read it: the last to arrive writes it, and the state read and the one written may be the same.
 #include <algorithm>
 
 #include "fa_internal.h"
@@ -38,13 +38,20 @@ struct PlanK {
   int32_t* slots;
   unsigned int* err;
   int B, N, page_size, num_pages, max_pages, window;   // window 0: every page is kept
+  int chunk;   // tokens a warp takes, a multiple of 128
+  int top;     // the largest power of two below B (0: one sequence)
   FastDiv by_page;
 };
 
-struct Sums {   // of sequences before one: new tokens, pages taken, pages given up
-  long long tok, need, gone;
+// Of sequences before one: new tokens, pages taken, pages given up.  Sums stop at 2^31 - 1,
+// more than any step has of each (a step with a sum there is refused).
+struct Sums {
+  uint32_t tok, need, gone;
 };
-__device__ __forceinline__ Sums operator+(const Sums& a, const Sums& b) { return {a.tok + b.tok, a.need + b.need, a.gone + b.gone}; }
+__device__ __forceinline__ uint32_t add_most(uint32_t a, uint32_t b) { return min(a + b, 0x7fffffffu); }
+__device__ __forceinline__ Sums operator+(const Sums& a, const Sums& b) {
+  return {add_most(a.tok, b.tok), add_most(a.need, b.need), add_most(a.gone, b.gone)};
+}
 
 struct PlanSeq {
   int len, first, n, have, want, keep;
@@ -98,7 +105,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     unsigned mybad = 0;
     if (b < p.B) {
       const PlanSeq s = plan_seq(p, b);
-      mine = {s.n, s.want - s.have, s.keep - s.first};
+      mine = {static_cast<uint32_t>(s.n), static_cast<uint32_t>(s.want - s.have), static_cast<uint32_t>(max(s.keep - s.first, 0))};
       mybad = s.bad;
       len[b] = s.len;
     }
@@ -119,17 +126,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       run = run + warp_sums[w];
       bad |= warp_bad[w];
     }
-    if (b < p.B) {   // a sum past 32 bits is refused below and its low bits are not used
+    if (b < p.B) {   // (a sum that reached 2^31 - 1 is refused below, and these are not used)
       tok[b] = static_cast<int32_t>(before.tok + incl.tok - mine.tok);
       need[b] = static_cast<int32_t>(before.need + incl.need - mine.need);
       gone[b] = static_cast<int32_t>(before.gone + incl.gone - mine.gone);
     }
     __syncthreads();
   }
-  if (head < 0 || head >= p.num_pages || count < 0 || count > p.num_pages || count + run.gone > p.num_pages)
+  if (head < 0 || head >= p.num_pages || count < 0 || count > p.num_pages ||
+      static_cast<long long>(count) + run.gone > p.num_pages)
     bad |= FA_DEV_ERR_WORKSPACE;
-  if (run.tok > p.N) bad |= FA_DEV_ERR_BOUND;
-  if (run.need > count) bad |= FA_DEV_ERR_POOL;
+  if (run.tok > static_cast<uint32_t>(p.N)) bad |= FA_DEV_ERR_BOUND;
+  if (count >= 0 && run.need > static_cast<uint32_t>(count)) bad |= FA_DEV_ERR_POOL;
   if (tid == 0) {
     tok[p.B] = static_cast<int32_t>(run.tok);
     if (bad && blockIdx.x == 0) atomicOr(p.err, bad);
@@ -155,69 +163,67 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     }
   }
 
-  // ---- the tokens, four a thread: position, slot, and at a page's first token its table entry
-  const int quads = (p.N + 3) / 4;
-  for (int q = blockIdx.x * kPlanThreads + tid; q < quads; q += gridDim.x * kPlanThreads) {
-    int pos[4], slot[4];
-    int b = -1, end = 0, page = -1;
+  // ---- this CTA has read the state; the last one to say so writes it, below
+  __syncthreads();
+  if (tid == 0) last = gridDim.x == 1 || atom_add_acq_rel_gpu(p.state_out + 2, 1) == static_cast<int>(gridDim.x) - 1;
+
+  // ---- the tokens: position, slot, and at a new page's first token its table entry.  Where
+  // a warp's next 128 tokens lie in one sequence they share its numbers; otherwise
+  // each finds its own, a lane's four side by side.
+  constexpr int R = 4;   // tokens a lane looks up at once
+  const int run_beg = static_cast<int>(min(static_cast<long long>(p.N), (static_cast<long long>(blockIdx.x) * (kPlanThreads / 32) + warp) * p.chunk));
+  const int run_end = static_cast<int>(min(static_cast<long long>(p.N), static_cast<long long>(run_beg) + p.chunk));
+  int seq = 0;   // a sequence that holds run tokens up to its end
+#pragma unroll 1
+  for (int t0 = run_beg; t0 < run_end; t0 += 32 * R) {
+    const int used = min(run_end, total) - t0;   // of the tokens from t0 on, some sequence's (the others: padding)
+    int b[R];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int t = 4 * q + e;
-      pos[e] = 0;
-      slot[e] = -1;
-      if (t >= total) continue;
-      if (t >= end) {   // the last sequence that begins at t or before (those with no new token end where they begin)
-        int lo = 0, hi = p.B;
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (tok[mid] <= t) lo = mid;
-          else hi = mid;
+    for (int r = 0; r < R; ++r) b[r] = seq;
+    if (used > 0 && min(t0 + 32 * R, t0 + used) > tok[seq + 1]) {
+      // the last sequence that begins at the token or before (those with no new token end where they begin)
+#pragma unroll
+      for (int r = 0; r < R; ++r) b[r] = 0;
+#pragma unroll 1
+      for (int step = p.top; step > 0; step >>= 1)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int next = b[r] + step;
+          if (next < p.B && tok[next] <= t0 + lane + 32 * r) b[r] = next;
         }
-        b = lo;
-        end = tok[b + 1];
-        page = -1;
-      }
-      pos[e] = len[b] + t - tok[b];
-      const int pi = static_cast<int>(p.by_page.div(pos[e])), off = pos[e] - pi * p.page_size;
-      if (page < 0 || off == 0) {
-        int32_t* entry = p.table + static_cast<size_t>(b) * p.max_pages + pi;
-        const int have = static_cast<int>(p.by_page.div(len[b] + p.page_size - 1));
-        if (pi < have) {
-          page = *entry;
-        } else {
-          page = p.ring[in_ring(head + need[b] + pi - have)];
-          if (off == 0) *entry = page;
-        }
-        if (page < 0 || page >= p.num_pages) {
-          atomicOr(p.err, FA_DEV_ERR_PAGE);
-          page = -1;
-        }
-      }
-      if (page >= 0) slot[e] = page * p.page_size + off;   // below 2^31 (fa_cache_create)
+      seq = __shfl_sync(0xffffffffu, b[R - 1], 31);
     }
-    if (4 * q + 4 <= p.N) {
-      reinterpret_cast<int4*>(p.positions)[q] = make_int4(pos[0], pos[1], pos[2], pos[3]);
-      reinterpret_cast<int4*>(p.slots)[q] = make_int4(slot[0], slot[1], slot[2], slot[3]);
-    } else {
+    int page[R], pos[R], off[R];
+    int32_t* entry[R];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (4 * q + e < p.N) {
-          p.positions[4 * q + e] = pos[e];
-          p.slots[4 * q + e] = slot[e];
-        }
+    for (int r = 0; r < R; ++r) {
+      entry[r] = nullptr;
+      page[r] = -1;
+      pos[r] = off[r] = 0;
+      if (lane + 32 * r >= used) continue;
+      const int l = len[b[r]];
+      pos[r] = l + t0 + lane + 32 * r - tok[b[r]];
+      const int pi = static_cast<int>(p.by_page.div(pos[r])), have = static_cast<int>(p.by_page.div(l + p.page_size - 1));
+      off[r] = pos[r] - pi * p.page_size;
+      int32_t* at = p.table + static_cast<size_t>(b[r]) * p.max_pages + pi;
+      if (off[r] == 0 && pi >= have) entry[r] = at;
+      page[r] = __ldcg(pi < have ? at : p.ring + in_ring(head + need[b[r]] + pi - have));
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int t = t0 + lane + 32 * r;
+      if (t >= run_end) break;
+      const bool good = page[r] >= 0 && page[r] < p.num_pages;
+      if (entry[r]) *entry[r] = page[r];
+      p.positions[t] = pos[r];
+      p.slots[t] = good ? page[r] * p.page_size + off[r] : -1;   // below 2^31 (fa_cache_create)
+      if (!good && lane + 32 * r < used) atomicOr(p.err, FA_DEV_ERR_PAGE);
     }
   }
 
-  // ---- the state, once every CTA has read it
+  // ---- the state
   __syncthreads();
-  if (gridDim.x > 1) {
-    if (tid == 0) {
-      const int old = atom_add_acq_rel_gpu(p.state_out + 2, 1);
-      last = old == static_cast<int>(gridDim.x) - 1;
-    }
-    __syncthreads();
-    if (!last) return;
-  }
+  if (!last) return;
   for (int b = tid; b < p.B; b += kPlanThreads) {
     const int first = p.state_in[4 + p.B + b];
     int l = len[b], f = first;
@@ -237,15 +243,19 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
 }
 
 cudaError_t launch_plan(const PlanArgs& a, cudaStream_t s) {
+  // two CTAs an SM at most, and no less than 128 tokens a warp
+  const long long warps = 2LL * sm_count() * (kPlanThreads / 32);
+  const long long chunk = std::max(1LL, (a.num_tokens + 128 * warps - 1) / (128 * warps)) * 128;
+  const long long per = chunk * (kPlanThreads / 32);
   PlanK k{a.new_lens, a.state_in, a.state_out, a.free_pages, a.block_table, a.qo_indptr, a.prefix_lens, a.positions, a.slots,
-          a.err, a.B, a.num_tokens, a.page_size, a.num_pages, a.max_pages_per_seq, a.window, FastDiv(a.page_size)};
+          a.err, a.B, a.num_tokens, a.page_size, a.num_pages, a.max_pages_per_seq, a.window, static_cast<int>(chunk), 0, FastDiv(a.page_size)};
+  for (int step = 1; step < a.B; step *= 2) k.top = step;
   const int smem = (4 * a.B + 1) * static_cast<int>(sizeof(int32_t));
   static unsigned int done = 0;
   const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(plan_kernel), (4 * FA_MAX_STEP_BATCH + 1) * 4, &done);
   if (e != cudaSuccess) return e;
-  // a CTA to 2048 tokens (two rounds of four a thread), at most two CTAs an SM
-  const long long ctas = std::min((static_cast<long long>(a.num_tokens) + 2047) / 2048, 2LL * sm_count());
-  return launch_pdl(plan_kernel, dim3(static_cast<unsigned>(std::max(ctas, 1LL))), dim3(kPlanThreads), static_cast<size_t>(smem), s, k);
+  return launch_pdl(plan_kernel, dim3(static_cast<unsigned>(std::max(1LL, (a.num_tokens + per - 1) / per))), dim3(kPlanThreads),
+                    static_cast<size_t>(smem), s, k);
 }
 
 }  // namespace fa

@@ -15,9 +15,20 @@
 // upper 32 bits leave an angle in [-pi, pi), where the hardware's sine and cosine
 // are off by 2^-21 at most: an 8192nd of a bf16 rounding of the pair's length.
 //
-// A memory pass: each row read once, written once (rows out, slab).  A warp takes
-// RH rows of one token, so that a token's sines serve several heads and RH * D / 256
-// 16-byte loads are in flight per lane.
+// With A_i = w_i cos, B_i = -w_{i+h} sin (i < h; A_{i+h} = w_{i+h} cos, B_{i+h} = w_i sin), made once
+// a token and weight, a value costs z = f (x A + x' B), x' its partner, f the row's 1 / root.
+//
+// With A_i = w_i cos, B_i = -w_{i+h} sin (i < h; A_{i+h} = w_{i+h} cos, B_{i+h} = w_i sin), made once
+// a warp, a value costs z = f (x A + x' B), x' its partner, f the row's 1 / root.
+//
+// A memory pass: each row read once, written once (rows out, slab).  Warps are
+// persistent and independent: each walks items (up to 8 heads of one kind of one
+// token: its sines serve them all), with the next rows' loads in flight
+// while it works on the ones before.  30011 tokens of 16 + 2 + 2 heads at head_dim 512, bf16:
+// 197 us, 6.25 TB/s of 6.8 (copied without arithmetic 186); 2048 tokens of 16 + 8 + 8 at 256
+// with the rows out: 17.8 us, 4.7 TB/s.  Blocks of their own for each token's heads took 224 and 20 us (their
+// loads waited for their sines, and blocks start at one a nanosecond), rows through
+// a ring of shared memory with a copying warp 263 and 18.6.
 #include <algorithm>
 
 #include "fa_internal.h"
@@ -25,6 +36,13 @@
 #include "fa_row.cuh"
 
 namespace fa {
+
+// A block's warps are independent: 64 threads so that it starts and ends easily.  16 warps an
+// SM at 128 registers: a warp's rows and the ones on their way (4 KB at
+// head_dim 512, 2 x 2 rows; 256, 2 x 4) without spills.  20 and 24 warps, which spill, took 1.2 to 1.8 times as long.
+constexpr int kRowsThreads = 64, kRowsWarps = 16;
+// Heads of an item, at most: 16 against 8, 30011 tokens of 16 + 2 + 2 heads at 512 197 us against 201.
+constexpr int kRowsHeads = 16;
 
 struct RowsK {
   const __nv_bfloat16* src[3];   // q, k, v
@@ -41,40 +59,31 @@ struct RowsK {
   int half8;                     // R / 16: 8-element vectors in half of the rotated columns
   int norm, page_size, num_pages;
   float eps, offset;
-  FastDiv by_groups, by_page;
+  int per_q, per_kv, groups_q, groups_kv;   // heads a warp, groups of a token (groups_kv of keys and of values each)
+  uint32_t items;                // groups x tokens, group by group
+  FastDiv by_T, by_page;
 };
 
-// Cosines and sines of pairs 8 c .. 8 c + 7 at position pos.
-__device__ __forceinline__ void turns8(const uint64_t* steps, int c, int pos, float (&cs)[8], float (&sn)[8]) {
-  const ulonglong2* s = reinterpret_cast<const ulonglong2*>(steps) + 4 * c;
-  const uint64_t p = static_cast<uint64_t>(static_cast<int64_t>(pos));
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const ulonglong2 w = __ldg(s + e);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int32_t phase = static_cast<int32_t>(static_cast<uint32_t>((p * (k ? w.y : w.x)) >> 32));
-      const float a = static_cast<float>(phase) * 1.4629180792671596e-9f;   // pi / 2^31
-      cs[2 * e + k] = __cosf(a);
-      sn[2 * e + k] = __sinf(a);
-    }
-  }
+// Cosine and sine of a phase, in turns of 2^64.
+__device__ __forceinline__ void turn1(uint64_t phase, float& c, float& s) {
+  const float a = static_cast<float>(static_cast<int32_t>(static_cast<uint32_t>(phase >> 32))) * 1.4629180792671596e-9f;   // pi / 2^31
+  c = __cosf(a);
+  s = __sinf(a);
 }
 
-template <int D>
-__device__ __forceinline__ float row_square_sum(const RowRegs<D>& r, float pre) {
-  float s0 = 0.f, s1 = 0.f;
+template <int NV>
+__device__ __forceinline__ float square_sum(const float (&x)[NV][8]) {
+  uint64_t acc = pack_f32x2(0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < RowRegs<D>::NV; ++i) {
-    float x[8];
-    bf16x8_to_f32(r.v[i], x);
+  for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
-      s0 = fmaf(x[e] * pre, x[e] * pre, s0);
-      s1 = fmaf(x[e + 1] * pre, x[e + 1] * pre, s1);
+      const uint64_t p = pack_f32x2(x[j][e], x[j][e + 1]);
+      acc = fma_f32x2(p, p, acc);
     }
-  }
-  return s0 + s1;
+  float lo, hi;
+  unpack_f32x2(acc, lo, hi);
+  return lo + hi;
 }
 
 __device__ __forceinline__ float warp_sum(float x) {
@@ -83,165 +92,233 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-// FULL: the whole head is rotated (R = D), and pairs sit in one lane (D = 512:
-// vectors l and l + 32) or 16 lanes apart (D = 256).  Otherwise partners meet
-// through a row of shared memory.
-template <int D, int KV, int RH, bool FULL>
-__global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ RowsK a) {
+// 1 / sqrt(mean(x^2) + eps) of a row.  Where the squares leave fp32 (magnitudes near 2^64,
+// infinities, NaN) the row is divided by 2^70 first.
+template <int D, int NV>
+__device__ __forceinline__ float row_factor(float (&x)[NV][8], float eps) {
+  const float ss = warp_sum(square_sum(x));
+  if (ss <= 1e38f) return rsqrtf(fmaf(ss, 1.0f / D, eps));
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[j][e] *= 8.470329472543003e-22f;
+  return rsqrtf(warp_sum(square_sum(x)) * (1.0f / D));
+}
+
+// Where a rotated vector's partner is: in its own lane (D = 512, R = D), in a lane's
+// first vector (2 R / 16 <= 32 vectors rotated), or in any.
+enum { kOwnLane, kFirst, kAnywhere };
+
+// Cosines and sines of pairs 8 c .. 8 c + 7 at position pos.
+__device__ __forceinline__ void turns8(const uint64_t* steps, int c, int pos, float (&cs)[8], float (&sn)[8]) {
+  const ulonglong2* s = reinterpret_cast<const ulonglong2*>(steps) + 4 * c;
+  const uint64_t p = static_cast<uint64_t>(static_cast<int64_t>(pos));
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const ulonglong2 w = __ldg(s + e);
+    turn1(p * w.x, cs[2 * e], sn[2 * e]);
+    turn1(p * w.y, cs[2 * e + 1], sn[2 * e + 1]);
+  }
+}
+
+// Some heads of one kind of one token, from head h on.
+struct RowItem {
+  uint32_t i;   // >= items: none
+  int kind, t, h, h1, pos, slot;
+  const uint4* src;
+};
+
+template <int D, int KV, int RH, int ROT>
+__global__ void __launch_bounds__(kRowsThreads, kRowsWarps * 32 / kRowsThreads)
+    rows_kernel(const __grid_constant__ RowsK a) {
   constexpr int NV = RowRegs<D>::NV;
-  constexpr int NC = FULL ? 1 : NV;   // sets of 8 cosines a lane needs
-  __shared__ float4 meet[FULL ? 1 : 8 * D / 4];
+  static_assert(ROT == kFirst || NV == 2, "head_dim 256 has one vector a lane");
+  constexpr int NR = ROT == kFirst ? 1 : NV;   // vectors that rotation reaches
   // Index arrays are read after the wait even under FA_FLAG_EARLY_METADATA: they
   // usually come from the kernel before (fa_plan_step).
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const uint32_t warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const uint32_t t = a.by_groups.div(warp);
-  if (t >= static_cast<uint32_t>(a.T)) return;
-  const int r0 = static_cast<int>(warp - t * a.by_groups.d) * RH;
-  auto kind_of = [&](int row) { return row < a.nq ? 0 : row < a.nq + a.Hkv ? 1 : 2; };
-  auto head_of = [&](int row, int kind) { return row - (kind == 0 ? 0 : kind == 1 ? a.nq : a.nq + a.Hkv); };
-
-  RowRegs<D> r[RH];
-#pragma unroll
-  for (int i = 0; i < RH; ++i) {
-    const int row = r0 + i;
-    if (row < a.rows) {
-      const int kind = kind_of(row);
-      const uint4* s = reinterpret_cast<const uint4*>(a.src[kind] + static_cast<size_t>(t) * a.stride[kind] +
-                                                      static_cast<size_t>(head_of(row, kind)) * D);
-#pragma unroll
-      for (int j = 0; j < NV; ++j) r[i].v[j] = s[j * 32 + lane];
-    } else {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) r[i].v[j] = make_uint4(0u, 0u, 0u, 0u);
+  const uint32_t nwarps = gridDim.x * (kRowsThreads / 32);
+  auto item = [&](uint32_t i) {
+    RowItem x;
+    x.i = i;
+    if (i >= a.items) {
+      x.kind = x.t = x.h = x.h1 = x.pos = 0;
+      x.slot = -1;
+      x.src = nullptr;
+      return x;
     }
-  }
-  const bool turned = a.half8 > 0 && kind_of(r0) < 2;
-  float cs[NC][8], sn[NC][8];
-  int part[NV];   // 0: first of its pair, 1: second, 2: not rotated
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int v = j * 32 + lane;
-    part[j] = v < a.half8 ? 0 : v < 2 * a.half8 ? 1 : 2;
-  }
-  if (turned) {
-    const int pos = __ldg(a.positions + t);
-#pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      const int v = j * 32 + lane;
-      const int c = FULL ? (D == 256 ? lane & 15 : lane) : part[j] == 0 ? v : part[j] == 1 ? v - a.half8 : 0;
-      turns8(a.steps, c, pos, cs[j], sn[j]);
+    int g = static_cast<int>(a.by_T.div(i));
+    x.t = static_cast<int>(i - g * a.by_T.d);
+    x.kind = 0;
+    if (g >= a.groups_q) {
+      g -= a.groups_q;
+      x.kind = g >= a.groups_kv ? 2 : 1;
+      g -= x.kind == 2 ? a.groups_kv : 0;
     }
-  }
-  float ss[RH];
+    const int per = x.kind == 0 ? a.per_q : a.per_kv;
+    x.h = g * per;
+    x.h1 = min(x.h + per, x.kind == 0 ? a.nq : a.Hkv);
+    const __nv_bfloat16* base = x.kind == 0 ? a.src[0] : x.kind == 1 ? a.src[1] : a.src[2];
+    const long long stride = x.kind == 0 ? a.stride[0] : x.kind == 1 ? a.stride[1] : a.stride[2];
+    x.src = reinterpret_cast<const uint4*>(base + static_cast<size_t>(x.t) * stride) + lane;
+    x.pos = a.half8 > 0 && x.kind < 2 ? __ldg(a.positions + x.t) : 0;
+    x.slot = x.kind > 0 && a.slots ? __ldg(a.slots + x.t) : -1;
+    return x;
+  };
+  auto load = [&](const RowItem& x, RowRegs<D> (&r)[RH]) {   // (plain loads: a row may be its own output)
 #pragma unroll
-  for (int i = 0; i < RH; ++i) ss[i] = row_square_sum<D>(r[i], 1.0f);
+    for (int i = 0; i < RH; ++i)
+      if (x.h + i < x.h1)
 #pragma unroll
-  for (int i = 0; i < RH; ++i) ss[i] = warp_sum(ss[i]);
-  const int slot = a.slots && r0 + RH > a.nq ? __ldg(a.slots + t) : -1;
+        for (int j = 0; j < NV; ++j) r[i].v[j] = x.src[(x.h + i) * (D / 8) + j * 32];
+  };
 
+  RowItem x = item((blockIdx.x * kRowsThreads + threadIdx.x) >> 5);
+  if (x.i >= a.items) return;
+  RowRegs<D> r[RH], next[RH];
+  load(x, r);
+  bool fresh = true, norm = false, turn = false;
+  long long to = -1;   // slab row of head 0
+  __nv_bfloat16* dst = nullptr;
+  uint8_t* slab = nullptr;
+  float* scale = nullptr;
+  // the coefficients of own values and partners, and where the partners are
+  float ca[NV][8], cb[NR][8];
+  int from[NR];
+  auto make = [&]() {
+    norm = (a.norm >> x.kind) & 1;
+    turn = a.half8 > 0 && x.kind < 2;
+    to = -1;
+    if (x.slot >= 0) {   // a negative slot is a padding token
+      const uint32_t page = a.by_page.div(x.slot), off = x.slot - page * a.page_size;
+      if (page < static_cast<uint32_t>(a.num_pages)) to = static_cast<long long>(page) * a.Hkv * a.page_size + off;
+      else if (lane == 0 && x.h == 0) atomicOr(a.err, FA_DEV_ERR_SLOT);
+    }
+    dst = x.kind == 0 ? a.dst[0] : x.kind == 1 ? a.dst[1] : a.dst[2];
+    if (dst) dst += static_cast<size_t>(x.t) * (x.kind == 0 ? a.Hq : a.Hkv) * D;
+    slab = x.kind == 2 ? a.slab[1] : a.slab[0];
+    scale = x.kind == 2 ? a.scale[1] : a.scale[0];
+    const uint4* w = norm && x.kind < 2 ? reinterpret_cast<const uint4*>(x.kind == 0 ? a.weight[0] : a.weight[1]) : nullptr;
+    float wt[NV][8];
 #pragma unroll
-  for (int i = 0; i < RH; ++i) {
-    const int row = r0 + i;
-    if (row >= a.rows) break;
-    const int kind = kind_of(row), head = head_of(row, kind);
-    const bool norm = (a.norm >> kind) & 1, turn = turned && kind < 2;
-    if (norm || turn) {   // (else the row goes on bit for bit)
-      float f = 1.0f;
-      if (norm) {
-        if (ss[i] <= 1e38f) {
-          f = rsqrtf(fmaf(ss[i], 1.0f / D, a.eps));
-        } else {   // squares past fp32 (magnitudes near 2^64), infinities, NaN: the row over 2^70
-          constexpr float pre = 8.470329472543003e-22f;
-          f = pre * rsqrtf(warp_sum(row_square_sum<D>(r[i], pre)) * (1.0f / D));
+    for (int j = 0; j < NV; ++j) {
+      if (w) bf16x8_to_f32(__ldg(w + j * 32 + lane), wt[j]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ca[j][e] = wt[j][e] = w ? wt[j][e] + a.offset : 1.0f;
+    }
+    if (turn) {
+#pragma unroll
+      for (int j = 0; j < NR; ++j) {
+        const int v = j * 32 + lane;
+        const bool first = v < a.half8, none = v >= 2 * a.half8;
+        const int o = none ? v : first ? v + a.half8 : v - a.half8;
+        from[j] = o;
+        float cs[8], sn[8], ow[8];
+        turns8(a.steps, none ? 0 : min(v, o), x.pos, cs, sn);
+        if (ROT != kOwnLane && w) bf16x8_to_f32(__ldg(w + o), ow);   // the partner's weights
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float wo = ROT == kOwnLane ? wt[NV - 1 - j][e] : w ? ow[e] + a.offset : 1.0f;
+          cb[j][e] = none ? 0.f : first ? -sn[e] * wo : sn[e] * wo;
+          ca[j][e] = none ? ca[j][e] : ca[j][e] * cs[e];
         }
       }
-      float y[NV][8];
+    }
+  };
+
+  while (true) {
+    RowItem y = x;   // what comes next: its loads go out before this one's arithmetic
+    y.h += RH;
+    const bool another = y.h >= x.h1;
+    if (another) y = item(x.i + nwarps);
+    const bool more = y.i < a.items;
+    if (more) load(y, next);
+    if (fresh) make();
+    fresh = another;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        bf16x8_to_f32(r[i].v[j], y[j]);
-        if (norm) {
+    for (int i = 0; i < RH; ++i) {
+      if (x.h + i >= x.h1) break;
+      if (norm || turn) {   // (else the row goes on bit for bit)
+        float v[NV][8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[j][e] *= f;
-          if (kind < 2 && a.weight[kind]) {
-            float w[8];
-            bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(a.weight[kind]) + j * 32 + lane), w);
+        for (int j = 0; j < NV; ++j) bf16x8_to_f32(r[i].v[j], v[j]);
+        const float f = norm ? row_factor<D>(v, a.eps) : 1.0f;
+        const uint64_t f2 = pack_f32x2(f, f);
+        uint64_t z[NV][4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[j][e] *= w[e] + a.offset;
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            z[j][k] = mul_f32x2(pack_f32x2(v[j][2 * k], v[j][2 * k + 1]), pack_f32x2(ca[j][2 * k], ca[j][2 * k + 1]));
+        if (turn) {
+#pragma unroll
+          for (int j = 0; j < NR; ++j) {
+            float p[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              if constexpr (ROT == kOwnLane) {
+                p[e] = v[NV - 1 - j][e];
+              } else {
+                p[e] = __shfl_sync(0xffffffffu, v[0][e], from[j] & 31);
+                if constexpr (ROT == kAnywhere) {
+                  const float o = __shfl_sync(0xffffffffu, v[NV - 1][e], from[j] & 31);
+                  p[e] = from[j] >= 32 ? o : p[e];
+                }
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              z[j][k] = fma_f32x2(pack_f32x2(p[2 * k], p[2 * k + 1]), pack_f32x2(cb[j][2 * k], cb[j][2 * k + 1]), z[j][k]);
           }
-        }
-      }
-      if (turn) {
-        float z[NV][8];   // the partners
-        if constexpr (FULL && D == 512) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            z[0][e] = y[NV - 1][e];
-            z[NV - 1][e] = y[0][e];
-          }
-        } else if constexpr (FULL) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) z[0][e] = __shfl_xor_sync(0xffffffffu, y[0][e], 16);
-        } else {
-          float4* m = meet + (threadIdx.x >> 5) * (D / 4);
-#pragma unroll
-          for (int j = 0; j < NV; ++j) {
-            m[2 * (j * 32 + lane)] = make_float4(y[j][0], y[j][1], y[j][2], y[j][3]);
-            m[2 * (j * 32 + lane) + 1] = make_float4(y[j][4], y[j][5], y[j][6], y[j][7]);
-          }
-          __syncwarp();
-#pragma unroll
-          for (int j = 0; j < NV; ++j) {
-            const int v = j * 32 + lane, o = part[j] == 0 ? v + a.half8 : part[j] == 1 ? v - a.half8 : v;
-            const float4 lo = m[2 * o], hi = m[2 * o + 1];
-            z[j][0] = lo.x, z[j][1] = lo.y, z[j][2] = lo.z, z[j][3] = lo.w;
-            z[j][4] = hi.x, z[j][5] = hi.y, z[j][6] = hi.z, z[j][7] = hi.w;
-          }
-          __syncwarp();
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-          if (part[j] == 2) continue;
-          const float sign = part[j] == 0 ? -1.0f : 1.0f;
+          uint32_t out[4];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[j][e] = fmaf(y[j][e], cs[j % NC][e], sign * z[j][e] * sn[j % NC][e]);
+          for (int k = 0; k < 4; ++k) {
+            float lo, up;
+            unpack_f32x2(mul_f32x2(z[j][k], f2), lo, up);
+            out[k] = pack_bf16x2(lo, up);
+          }
+          // a vector neither normed nor turned stays as it is, infinities and all
+          if (norm || ROT == kOwnLane || j * 32 + lane < 2 * a.half8) r[i].v[j] = make_uint4(out[0], out[1], out[2], out[3]);
         }
       }
+      if (dst) row_store_bf16<D>(r[i], dst + static_cast<size_t>(x.h + i) * D, lane);
+      if (to < 0) continue;
+      const size_t row = static_cast<size_t>(to) + static_cast<size_t>(x.h + i) * a.page_size;
+      row_store<D, KV>(r[i], slab + row * kRowBytes<D, KV>, KV == FA_KV_BF16 ? nullptr : scale + row, lane);
+    }
+    if (!more) break;
+    x = y;
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-        r[i].v[j] = make_uint4(pack_bf16x2(y[j][0], y[j][1]), pack_bf16x2(y[j][2], y[j][3]), pack_bf16x2(y[j][4], y[j][5]),
-                               pack_bf16x2(y[j][6], y[j][7]));
-    }
-    if (a.dst[kind])
-      row_store_bf16<D>(r[i], a.dst[kind] + (static_cast<size_t>(t) * (kind == 0 ? a.Hq : a.Hkv) + head) * D, lane);
-    if (kind == 0 || slot < 0) continue;   // a negative slot is a padding token
-    const uint32_t page = a.by_page.div(slot), off = slot - page * a.page_size;
-    if (page >= static_cast<uint32_t>(a.num_pages)) {
-      if (lane == 0) atomicOr(a.err, FA_DEV_ERR_SLOT);
-      continue;
-    }
-    const size_t to = (static_cast<size_t>(page) * a.Hkv + head) * a.page_size + off;
-    row_store<D, KV>(r[i], a.slab[kind - 1] + to * kRowBytes<D, KV>, KV == FA_KV_BF16 ? nullptr : a.scale[kind - 1] + to, lane);
+    for (int i = 0; i < RH; ++i) r[i] = next[i];
   }
 }
 
 template <int D, int KV>
 static cudaError_t launch_rows_t(RowsK k, cudaStream_t s) {
-  constexpr int RH = D == 256 ? 8 : 4;
-  const long long all = static_cast<long long>(k.T) * k.rows;
-  // few rows: a warp each, for the shortest path; many: RH a warp
-  const int rh = all <= 64LL * sm_count() ? 1 : RH;
-  const int groups = (k.rows + rh - 1) / rh;
-  const long long warps = static_cast<long long>(k.T) * groups;
-  if (warps >= (1LL << 31) - 8) return cudaErrorInvalidConfiguration;
-  k.by_groups = FastDiv(groups);
-  const int block = rh == 1 && warps < 8LL * sm_count() ? 64 : 256;
-  const dim3 g(static_cast<unsigned>((warps * 32 + block - 1) / block)), b(block);
-  const bool full = k.half8 * 16 == D;
-  if (rh == 1) return full ? launch_pdl(rows_kernel<D, KV, 1, true>, g, b, 0, s, k) : launch_pdl(rows_kernel<D, KV, 1, false>, g, b, 0, s, k);
-  return full ? launch_pdl(rows_kernel<D, KV, RH, true>, g, b, 0, s, k) : launch_pdl(rows_kernel<D, KV, RH, false>, g, b, 0, s, k);
+  constexpr int RH = D == 256 ? 4 : 2;   // rows in flight behind those in work
+  // as many heads an item as leave every resident warp one
+  const long long resident = static_cast<long long>(kRowsWarps) * sm_count();
+  const long long share = (static_cast<long long>(k.T) * k.rows + resident - 1) / resident;
+  k.per_q = k.per_kv = static_cast<int>(std::min<long long>(share, kRowsHeads));
+  k.groups_q = (k.nq + k.per_q - 1) / k.per_q;
+  k.groups_kv = k.rows > k.nq ? (k.Hkv + k.per_kv - 1) / k.per_kv : 0;
+  const long long items = static_cast<long long>(k.T) * (k.groups_q + 2 * k.groups_kv);
+  if (items >= (1LL << 31) - (1 << 20)) return cudaErrorInvalidConfiguration;
+  k.items = static_cast<uint32_t>(items);
+  k.by_T = FastDiv(k.T);
+  constexpr int wpb = kRowsThreads / 32;
+  const dim3 g(static_cast<unsigned>((std::min(items, resident) + wpb - 1) / wpb)), b(kRowsThreads);
+  if (k.half8 <= 16) return launch_pdl(rows_kernel<D, KV, RH, kFirst>, g, b, 0, s, k);
+  if constexpr (D == 512) {
+    if (k.half8 == 32) return launch_pdl(rows_kernel<D, KV, RH, kOwnLane>, g, b, 0, s, k);
+    return launch_pdl(rows_kernel<D, KV, 1, kAnywhere>, g, b, 0, s, k);
+  }
+  return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_rows(const RowsArgs& a, cudaStream_t s) {

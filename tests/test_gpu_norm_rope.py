@@ -184,6 +184,21 @@ def test_infinities_and_nan_stay_in_their_rows():
     assert bool((q[2, 0][~torch.isnan(q[2, 0])] == 0).all())
 
 
+@pytest.mark.parametrize("D,R", [(256, 64), (512, 64), (512, 320)])
+def test_infinities_outside_the_turned_columns(D, R):
+    """Without a norm, a column past R goes on as it is, beside turned ones."""
+    import full_attention_gb300 as fa
+    T, hq, hkv = 40, 2, 1
+    x, pos, _, _ = inputs(T, hq, hkv, D, 4)
+    x[3, 0, R], x[5, 1, D - 1], x[9, 1, R + 3] = float("inf"), -float("inf"), float("nan")
+    how = fa.NormRope(D, freqs(R), norm_q=False, norm_k=False)
+    cache, _ = make(fa, D, hq, hkv)
+    q = torch.empty((T, hq, D), dtype=torch.bfloat16, device="cuda")
+    cache.norm_rope_store(0, how, x[:, :hq], None, None, pos, None, q)
+    assert torch.equal(torch.nan_to_num(q[..., R:], nan=7.0), torch.nan_to_num(x[:, :hq, R:], nan=7.0))
+    assert bool(torch.isfinite(q[..., :R]).all())
+
+
 def test_a_shared_layer_takes_its_queries_alone():
     import full_attention_gb300 as fa
     D, T, hq, hkv = 512, 20, 8, 2
