@@ -163,9 +163,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     }
   }
 
-  // ---- this CTA has read the state; the last one to say so writes it, below
+  // ---- a state changed in place is written, below, by the last CTA to have read it
   __syncthreads();
-  if (tid == 0) last = gridDim.x == 1 || atom_add_acq_rel_gpu(p.state_out + 2, 1) == static_cast<int>(gridDim.x) - 1;
+  if (tid == 0)
+    last = p.state_in != p.state_out ? blockIdx.x == 0
+                                     : gridDim.x == 1 || atom_add_acq_rel_gpu(p.state_out + 2, 1) == static_cast<int>(gridDim.x) - 1;
 
   // ---- the tokens: position, slot, and at a new page's first token its table entry.  Where
   // a warp's next 128 tokens lie in one sequence they share its numbers; otherwise
