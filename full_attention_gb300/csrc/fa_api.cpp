@@ -122,6 +122,10 @@ DecodePlan plan_decode(const fa_cache* c, int layer, int B, int max_seq_len, lon
     const size_t rows = static_cast<size_t>(parts + p.units) * 8 * maps;   // partial slots x heads x maps
     p.off_o = (rows * (fp4 || maps == 2 ? 4 : 2) * sizeof(float) + 255) / 256 * 256;
     p.part_bytes = p.off_o + rows * d.head_dim * sizeof(float);
+    if (maps == 2) {
+      p.off_joins = p.part_bytes;
+      p.part_bytes += static_cast<size_t>(p.ncta) * 2 * sizeof(int32_t);
+    }
   }
   return p;
 }

@@ -252,90 +252,6 @@ __device__ void merge_unit(const DecK& p, int u, const Unit& x, int nh, int head
   named_bar_sync(1, 128);   // the scratch (the score-exchange buffer) is free again
 }
 
-// The same of a unit's two maps (differential attention): the 16 rows are (map m,
-// head h) at 8 m + h, their partials at ml_part [slot][16][4] (base, rounded sum,
-// unrounded sum, 0) and o_part [slot][16][D], and
-//   out_h = O_0h / l_0h - lambda_h O_1h / l_1h.
-// A thread holds the same columns of a head's two rows.  8 threads a row join the
-// (m, l) pairs; wbuf holds 16 x 64 weights, then 16 x (max, 1 / rounded sum, lse).
-template <int D>
-__device__ void merge_unit_diff(const DecK& p, int u, const Unit& x, int nh, int head0, int cf, int cl, float* wbuf) {
-  constexpr int CH = 64;                    // source CTAs per weight chunk
-  constexpr int ITEMS = 16 * (D / 4) / 128; // float4 sums per thread
-  const int tid = threadIdx.x;
-  const int nct = cl - cf + 1;
-  const float4* mlg = reinterpret_cast<const float4*>(p.ml_part);
-  float* Mr = wbuf + 16 * CH;
-  float* Ir = Mr + 16;
-  const int row = tid >> 3, k = tid & 7;
-  float M = -INFINITY, L = 0.f, A = 0.f;
-  for (int c = k; c < nct; c += 8) {
-    const float4 v = __ldcg(mlg + (static_cast<size_t>(cf + c) + u) * 16 + row);
-    if (v.x == -INFINITY) continue;
-    const float Mn = fmaxf(M, v.x), f = ex2(M - Mn), w = ex2(v.x - Mn);
-    L = L * f + v.y * w;
-    A = A * f + v.z * w;
-    M = Mn;
-  }
-#pragma unroll
-  for (int o = 4; o; o >>= 1) {
-    const float Mo = __shfl_xor_sync(0xffffffffu, M, o), Lo = __shfl_xor_sync(0xffffffffu, L, o), Ao = __shfl_xor_sync(0xffffffffu, A, o);
-    const float Mn = fmaxf(M, Mo);
-    const float f = Mn == -INFINITY ? 0.f : ex2(M - Mn), w = Mn == -INFINITY ? 0.f : ex2(Mo - Mn);
-    L = L * f + Lo * w;
-    A = A * f + Ao * w;
-    M = Mn;
-  }
-  if (k == 0) {
-    Mr[row] = M;
-    Ir[row] = L > 0.f ? 1.0f / L : 0.f;
-    if (p.lse && (row & 7) < nh)
-      p.lse[(static_cast<size_t>(x.b) * p.Hq + head0 + (row & 7)) * 2 + (row >> 3)] = (M + __log2f(A)) * 0.69314718055994531f;
-  }
-  float4 acc[ITEMS];
-#pragma unroll
-  for (int i = 0; i < ITEMS; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c0 = 0; c0 < nct; c0 += CH) {
-    const int n = min(CH, nct - c0);
-    named_bar_sync(1, 128);
-    for (int e = tid; e < n * 16; e += 128) {
-      const int c = e >> 4, r = e & 15;
-      wbuf[e] = ((r & 7) < nh) ? ex2(__ldcg(p.ml_part + ((static_cast<size_t>(cf + c0 + c) + u) * 16 + r) * 4) - Mr[r]) : 0.f;
-    }
-    named_bar_sync(1, 128);
-#pragma unroll 2
-    for (int c = 0; c < n; ++c) {
-      const float* src = p.o_part + (static_cast<size_t>(cf + c0 + c) + u) * 16 * D;
-      float4 o[ITEMS];
-#pragma unroll
-      for (int i = 0; i < ITEMS; ++i) {
-        const int idx = tid + i * 128, r = idx / (D / 4), d = (idx % (D / 4)) * 4;
-        o[i] = ((r & 7) < nh) ? __ldcg(reinterpret_cast<const float4*>(src + r * D + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-#pragma unroll
-      for (int i = 0; i < ITEMS; ++i) {
-        const float w = wbuf[c * 16 + (tid + i * 128) / (D / 4)];
-        acc[i].x += w * o[i].x;
-        acc[i].y += w * o[i].y;
-        acc[i].z += w * o[i].z;
-        acc[i].w += w * o[i].w;
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < ITEMS / 2; ++i) {
-    const int idx = tid + i * 128, h = idx / (D / 4), d = (idx % (D / 4)) * 4;
-    if (h >= nh) continue;
-    const float w0 = Ir[h], w1 = -__ldg(p.lambda + head0 + h) * Ir[8 + h];
-    const float4 a = acc[i], b = acc[i + ITEMS / 2];
-    uint2 packed;
-    packed.x = pack_bf16x2(a.x * w0 + b.x * w1, a.y * w0 + b.y * w1);
-    packed.y = pack_bf16x2(a.z * w0 + b.z * w1, a.w * w0 + b.w * w1);
-    *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(x.b) * p.Hq + head0 + h) * D + d) = packed;
-  }
-  named_bar_sync(1, 128);   // the scratch (the score-exchange buffer) is free again
-}
-
 // One CTA of a layer's decode: CTA `cta` of the `grid` CTAs launched for the
 // layer (a launch may hold several layers; see decode_layers_kernel).
 // MAPS = 2: differential attention.  A consumer warp's QK^T columns lie in one half
@@ -370,6 +286,10 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
 
   Share sh;
   if (!cut_share(p, cta, grid, sh)) {
+    if (MAPS == 2 && p.joins && threadIdx.x == 0) {
+      griddep_wait();
+      p.joins[cta] = make_int2(-1, 0);
+    }
     if (sh.ncta == 0 && cta == 0) {   // nothing visible anywhere: only empty outputs to write
       griddep_wait();
       zero_empty_units<D, KV, MAPS>(p, 0, 1, threadIdx.x, blockDim.x);
@@ -511,6 +431,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
 
   // -------------------------------------------------------------- consumers
   griddep_wait();
+  if (MAPS == 2 && p.joins && threadIdx.x == 0) p.joins[cta] = make_int2(-1, 0);   // no unit's second part begins here, so far
   zero_empty_units<D, KV, MAPS>(p, cta, ncta, threadIdx.x, C::NCW * 32);
   const int qk_tile = warp % C::NT;
   const int qk_d0 = (warp / C::NT) * C::QK_COLS;
@@ -852,33 +773,35 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
               reinterpret_cast<float4*>(p.ml_part)[(slot * MAPS + m) * 8 + gid] = make_float4(m_run[m], l_run[m], l_all[m], 0.f);
           }
         }
-        // arrive; the last of the unit's CTAs merges every partial row.  The
-        // barrier orders the CTA's partial writes before thread 0's
-        // release/acquire add, which publishes them and, for the last
-        // arrival, makes the other CTAs' rows visible.
-        named_bar_sync(1, C::NCW * 32);
-        if (threadIdx.x == 0) {
-          const int nct = c_last - c_first + 1;
-          int* counter = p.counters + c_first + 1;
-          const int old = atom_add_acq_rel_gpu(counter, 1);
-          int last = 0;
-          if (old == nct - 1) {
-            last = 1;
-            atomicExch(counter, 0);   // leave the counter zero for the next call
-          } else if (old < 0 || old >= nct) {
-            atomicOr(p.err, FA_DEV_ERR_WORKSPACE);
+        if constexpr (MAPS == 2) {
+          // join_diff_kernel joins the parts; it finds them by the second one's share
+          if (cta == c_first + 1 && threadIdx.x == 0) p.joins[cta] = make_int2(u, c_last);
+        } else {
+          // arrive; the last of the unit's CTAs merges every partial row.  The
+          // barrier orders the CTA's partial writes before thread 0's
+          // release/acquire add, which publishes them and, for the last
+          // arrival, makes the other CTAs' rows visible.
+          named_bar_sync(1, C::NCW * 32);
+          if (threadIdx.x == 0) {
+            const int nct = c_last - c_first + 1;
+            int* counter = p.counters + c_first + 1;
+            const int old = atom_add_acq_rel_gpu(counter, 1);
+            int last = 0;
+            if (old == nct - 1) {
+              last = 1;
+              atomicExch(counter, 0);   // leave the counter zero for the next call
+            } else if (old < 0 || old >= nct) {
+              atomicOr(p.err, FA_DEV_ERR_WORKSPACE);
+            }
+            sh_last = last;
           }
-          sh_last = last;
-        }
-        named_bar_sync(1, C::NCW * 32);
-        if (sh_last) {
-          // the ring is idle once this CTA's last segment is consumed: stage the merge there
-          const bool idle = P + x.n >= s_end;
-          if constexpr (MAPS == 1)
+          named_bar_sync(1, C::NCW * 32);
+          if (sh_last) {
+            // the ring is idle once this CTA's last segment is consumed: stage the merge there
+            const bool idle = P + x.n >= s_end;
             merge_unit<D, C::STAGE_ALL>(p, u, x, nh, head0, c_first, c_last, sx, idle ? smem : nullptr, mbar_merge,
                                          &abort_flag);
-          else
-            merge_unit_diff<D>(p, u, x, nh, head0, c_first, c_last, sx);
+          }
         }
       }
     }
@@ -958,17 +881,92 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s) {
   return launch_decode_t<512, FA_KV_BF16>(a, k, s);
 }
 
+// Differential attention: the parts of units that were cut, joined.  A unit's 16 rows are
+// (map m, head h) at 8 m + h, their partials at ml_part [slot][16][4] (base, rounded
+// sum, unrounded sum, 0) and o_part [slot][16][D], and
+//   out_h = O_0h / l_0h - lambda_h O_1h / l_1h.
+// A block takes 64 columns of the unit whose second part is share blockIdx.x.  (Joined by
+// the unit's last CTA to finish, as the plain kernel's 8 rows are, 38 parts of 32 KB ran
+// through one SM for as long as 58% of the launch took; spread out they cost 3 us.)
+template <int D>
+__global__ void __launch_bounds__(256) join_diff_kernel(const DecK p) {
+  __shared__ float weight[16][65], top[16], inv[16];   // of up to 64 parts at a time
+  __shared__ float4 other[8][16];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int2 job = __ldcg(p.joins + blockIdx.x);
+  if (job.x < 0) return;
+  const int u = job.x, cf = static_cast<int>(blockIdx.x) - 1, n = job.y - cf + 1;
+  const Unit x = unit_of(p, u);
+  const int nh = min(8, p.g - x.c * 8), head0 = x.h * p.g + x.c * 8;
+  const int row = threadIdx.x >> 4, k = threadIdx.x & 15, h = row & 7;
+  const float4* ml = reinterpret_cast<const float4*>(p.ml_part) + (static_cast<size_t>(cf) + u) * 16 + row;   // part c's at 16 c
+  {
+    float m = -INFINITY, l = 0.f, all = 0.f;
+    for (int c = k; c < n; c += 16) {
+      const float4 v = __ldcg(ml + c * 16);
+      if (v.x == -INFINITY) continue;
+      const float mn = fmaxf(m, v.x), f = ex2(m - mn), w = ex2(v.x - mn);
+      l = l * f + v.y * w;
+      all = all * f + v.z * w;
+      m = mn;
+    }
+#pragma unroll
+    for (int o = 8; o; o >>= 1) {
+      const float mo = __shfl_xor_sync(0xffffffffu, m, o), lo = __shfl_xor_sync(0xffffffffu, l, o), ao = __shfl_xor_sync(0xffffffffu, all, o);
+      const float mn = fmaxf(m, mo), f = mn == -INFINITY ? 0.f : ex2(m - mn), w = mn == -INFINITY ? 0.f : ex2(mo - mn);
+      l = l * f + lo * w;
+      all = all * f + ao * w;
+      m = mn;
+    }
+    if (k == 0) {
+      top[row] = m;
+      inv[row] = l > 0.f ? 1.0f / l : 0.f;
+      if (p.lse && blockIdx.y == 0 && h < nh)
+        p.lse[(static_cast<size_t>(x.b) * p.Hq + head0 + h) * 2 + (row >> 3)] = (m + __log2f(all)) * 0.69314718055994531f;
+    }
+  }
+  const float* src = p.o_part + ((static_cast<size_t>(cf) + u) * 16 + row) * D + blockIdx.y * 64 + k * 4;   // part c's at 16 c D
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c0 = 0; c0 < n; c0 += 64) {
+    const int nc = min(64, n - c0);
+    __syncthreads();
+    for (int c = k; c < nc; c += 16) weight[row][c] = ex2(__ldcg(reinterpret_cast<const float*>(ml + (c0 + c) * 16)) - top[row]);
+    __syncthreads();
+    if (h < nh)
+#pragma unroll 8
+      for (int c = 0; c < nc; ++c) {
+        const float4 o = __ldcg(reinterpret_cast<const float4*>(src + static_cast<size_t>(c0 + c) * 16 * D));
+        const float w = weight[row][c];
+        acc.x += w * o.x;
+        acc.y += w * o.y;
+        acc.z += w * o.z;
+        acc.w += w * o.w;
+      }
+  }
+  if (row >= 8) other[h][k] = acc;
+  __syncthreads();
+  if (row >= 8 || h >= nh) return;
+  const float w0 = inv[h], w1 = -__ldg(p.lambda + head0 + h) * inv[8 + h];
+  const float4 b = other[h][k];
+  uint2 packed;
+  packed.x = pack_bf16x2(acc.x * w0 + b.x * w1, acc.y * w0 + b.y * w1);
+  packed.y = pack_bf16x2(acc.z * w0 + b.z * w1, acc.w * w0 + b.w * w1);
+  *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(x.b) * p.Hq + head0 + h) * D + blockIdx.y * 64 + k * 4) = packed;
+}
+
 template <int D, int KV>
 static cudaError_t launch_decode_diff_t(const DecodeArgs& a, const DecK& k, cudaStream_t s) {
   using C = DecCfg<D, KV>;
-  // a warp's QK^T columns within one half of the row; the merge's scratch
+  // a warp's QK^T columns lie within one half of the row
   static_assert((C::NCW / C::NT) % 2 == 0 && C::QK_COLS * (C::NCW / C::NT) == D, "halves by warps");
-  static_assert(C::NCW == 4 && (16 * 64 + 32) * 4 <= C::SX_BYTES, "merge scratch");
   static unsigned int done = 0;
   cudaError_t e = set_smem_once(reinterpret_cast<const void*>(decode_diff_kernel<D, KV>), C::SMEM_ALLOC, &done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(decode_diff_kernel<D, KV>, dim3(a.plan.ncta), dim3(C::NTHR), C::SMEM_ALLOC, s, *a.tm_k, *a.tm_v,
-                    *a.tm_ks, *a.tm_vs, k);
+  e = launch_pdl(decode_diff_kernel<D, KV>, dim3(a.plan.ncta), dim3(C::NTHR), C::SMEM_ALLOC, s, *a.tm_k, *a.tm_v,
+                 *a.tm_ks, *a.tm_vs, k);
+  if (e != cudaSuccess || !k.joins) return e;
+  return launch_pdl(join_diff_kernel<D>, dim3(a.plan.ncta, D / 64), dim3(256), 0, s, k);
 }
 
 cudaError_t launch_decode_diff(const DecodeArgs& a, cudaStream_t s) {

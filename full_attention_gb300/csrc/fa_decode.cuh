@@ -31,6 +31,7 @@ struct DecK {
   int max_seq_len, units, min_tiles, early_metadata;
   int shares;         // fp4: shares the work may be cut into
   const float* lambda;   // differential attention: [Hq]
+  int2* joins;        // differential attention: [CTAs] (unit, its last share) where a unit's second part begins; null: nothing to join
   float scale_log2;   // sm_scale * log2(e)
 };
 
@@ -293,6 +294,7 @@ inline DecK make_deck(const DecodeArgs& a) {
   k.early_metadata = a.early_metadata;
   k.shares = a.plan.ncta;
   k.lambda = a.lambda;
+  if (a.lambda && a.partials) k.joins = reinterpret_cast<int2*>(static_cast<char*>(a.partials) + a.plan.off_joins);
   k.scale_log2 = a.sm_scale * 1.4426950408889634f;
   return k;
 }

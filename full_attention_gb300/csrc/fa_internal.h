@@ -106,6 +106,7 @@ struct DecodePlan {
   int ncta = 0;             // shares the work may be cut into: CTAs launched (fp4: three a CTA)
   int blocks = 0;           // fp4: CTAs launched
   size_t off_o = 0;         // partials: (m, l) rows, then from off_o on the rows of O (bytes)
+  size_t off_joins = 0;     // differential attention: behind the rows of O, a pair of ints a CTA
   size_t part_bytes = 0;    // 0: nothing to join, no workspace needed
   // the workspace of a call of this layer alone: counters, partials
   size_t ws_bytes() const { return part_bytes ? kCounterBytes + part_bytes : 0; }
