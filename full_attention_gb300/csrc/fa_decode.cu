@@ -252,12 +252,330 @@ __device__ void merge_unit(const DecK& p, int u, const Unit& x, int nh, int head
   named_bar_sync(1, 128);   // the scratch (the score-exchange buffer) is free again
 }
 
+// The two maps of differential attention over one segment: tiles [ta, tz) of unit u,
+// whose queries are in qf.  A warp's QK^T columns lie in one half of the row, so its
+// partial scores belong to one map, mp = warp / 2: the pair of warps exchanges them
+// (no MMA is spent on the other half), does that map's softmax, and passes its weights and
+// factors on to the other pair; every warp then accumulates a quarter of the columns of
+// both maps, o[0] its own pair's, o[1] the other's, from each V fragment.  O is rescaled
+// only where a maximum or the V scales' power of two has moved.  Eight contexts of
+// 32k to 131k keys at head_dim 512, 8 query heads: int8 163 us (4.6 TB/s; plain attention 145), bf16 241 us (6.2
+// TB/s; plain 232); each warp doing both maps' softmax, int8 178 us, bound by 1166
+// instructions for 32 keys.  Returns false where a wait ran out.
+template <int D, int KV, int QF, int QW>
+__device__ __forceinline__ bool diff_segment(const DecK& p, const Unit& x, uint8_t* smem, float* sx, uint64_t* full,
+                                             uint64_t* empty, int& gi, int ta, int tz, long long P, int u, int cta, int ncta,
+                                             int kper, int T, int nh, int head0, const uint32_t (&qf)[QF][QW], int* abort_flag) {
+  using C = DecCfg<D, KV>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gid = lane >> 2, tig = lane & 3;
+  const int mp = warp >> 1;
+  const int qk_tile = warp % C::NT, qk_d0 = (warp / C::NT) * C::QK_COLS, pv_d0 = warp * C::PV_COLS;
+  const int qpos = x.L - 1, lo = x.lo;
+  // the exchange buffer: partial scores [warp][key][head]; two buffers of each map's
+  // weights (MMA fragments, a lane's side by side) and factors; at the end its (max, sums)
+  constexpr int PX = C::NT * 64 + 8;   // words of a map's weights and factors
+  float* px = sx + C::NCW * kTile * C::SX_STRIDE;
+  float* ends = px + 4 * PX;           // [map][head][3]
+  static_assert((C::NCW * kTile * C::SX_STRIDE + 4 * PX + 48) * 4 <= C::SX_BYTES, "exchange buffer");
+
+  float o[2][C::PV_MT][4];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int i = 0; i < C::PV_MT; ++i) o[m][i][0] = o[m][i][1] = o[m][i][2] = o[m][i][3] = 0.0f;
+  // l_run: the sum of the weights as the PV MMA takes them; l_all: unrounded, for lse
+  float m_run = -INFINITY, l_run = 0.0f, l_all = 0.0f, sigma = 1.0f;
+
+  for (int tile0 = ta; tile0 < tz; tile0 += C::NT) {
+    const int st = gi % C::NSTAGE;
+    const int ntl = min(C::NT, tz - tile0);
+    const uint8_t* ks = smem + st * C::STAGE_KV;
+    const uint8_t* vs = ks + C::NT * C::TILE_BYTES;
+    const float* scl = reinterpret_cast<const float*>(smem + C::OFF_SC + st * C::SC_BYTES);
+    float* pxb = px + (gi & 1) * 2 * PX;
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(&full[st], (gi / C::NSTAGE) & 1));
+    if (!ok && lane == 0) {
+      *reinterpret_cast<volatile int*>(abort_flag) = 1;
+      atomicOr(p.err, FA_DEV_ERR_TIMEOUT);
+    }
+    // ---- partial S^T over this warp's columns, two accumulator chains
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    float acc1[4] = {0.f, 0.f, 0.f, 0.f};
+    if (ok && qk_tile < ntl) {
+      const uint8_t* kt = ks + qk_tile * C::TILE_BYTES;
+      const int r = (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+      for (int kk = 0; kk < QF; ++kk) {
+        uint32_t a0, a1, a2, a3;
+        if constexpr (!KV) {
+          const int dc = qk_d0 + kk * 16 + (lane >> 4) * 8;
+          ldsm_x4(smem_u32(kt + (dc >> 6) * 2048 + sw128(r, (dc & 63) >> 3)), a0, a1, a2, a3);
+          mma_bf16((kk & 1) ? acc1 : acc, a0, a1, a2, a3, qf[kk][0], qf[kk][1]);
+        } else {
+          const int dc = qk_d0 + kk * 32 + (lane >> 4) * 16;
+          ldsm_x4(smem_u32(kt + (dc >> 7) * 2048 + sw128(r, (dc & 127) >> 4)), a0, a1, a2, a3);
+          mma_f16(acc, codes_to_f16x2<KV, 0, 1>(a0), codes_to_f16x2<KV, 0, 1>(a1), codes_to_f16x2<KV, 2, 3>(a0),
+                  codes_to_f16x2<KV, 2, 3>(a1), qf[kk][0], qf[kk][1]);
+          mma_f16(acc1, codes_to_f16x2<KV, 0, 1>(a2), codes_to_f16x2<KV, 0, 1>(a3), codes_to_f16x2<KV, 2, 3>(a2),
+                  codes_to_f16x2<KV, 2, 3>(a3), qf[kk][QW - 2], qf[kk][QW - 1]);
+        }
+      }
+    }
+    float* sxw = sx + warp * kTile * C::SX_STRIDE;
+    *reinterpret_cast<float2*>(sxw + gid * C::SX_STRIDE + 2 * tig) = make_float2(acc[0] + acc1[0], acc[1] + acc1[1]);
+    *reinterpret_cast<float2*>(sxw + (gid + 8) * C::SX_STRIDE + 2 * tig) = make_float2(acc[2] + acc1[2], acc[3] + acc1[3]);
+    named_bar_sync(2 + mp, 64);
+
+    // ---- this pair's map: scores of head gid, keys {2tig, 2tig+1, 2tig+8, 2tig+9} of each tile
+    const bool edge = ntl < C::NT || tile0 * kTile < lo || (tile0 + C::NT) * kTile - 1 > qpos;   // some key not visible
+    uint32_t pf[C::NT][2];
+    {
+      float s[C::NT][4], vw[C::NT][4];   // vw: 8-bit, the keys' V scales
+#pragma unroll
+      for (int t = 0; t < C::NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = 2 * tig + (e & 1) + (e >> 1) * 8;
+          float v = 0.0f;
+#pragma unroll
+          for (int w = t; w < 2; w += C::NT) v += sx[((2 * mp + w) * kTile + key) * C::SX_STRIDE + gid];
+          float sc = p.scale_log2;
+          if constexpr (KV) {
+            sc *= scl[t * 32 + key];
+            vw[t][e] = scl[(C::NT + t) * 32 + key];
+          }
+          s[t][e] = v * sc;
+        }
+      if (edge) {
+#pragma unroll
+        for (int t = 0; t < C::NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int pos = (tile0 + t) * kTile + 2 * tig + (e & 1) + (e >> 1) * 8;
+            if (t < ntl && pos >= lo && pos <= qpos) continue;
+            s[t][e] = -INFINITY;
+            vw[t][e] = 0.0f;
+          }
+      }
+      float mloc = -INFINITY, vm = 0.0f;
+#pragma unroll
+      for (int t = 0; t < C::NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          mloc = fmaxf(mloc, s[t][e]);
+          if constexpr (KV) vm = fmaxf(vm, vw[t][e]);
+        }
+      mloc = fmaxf(mloc, __shfl_xor_sync(0xffffffffu, mloc, 1));
+      mloc = fmaxf(mloc, __shfl_xor_sync(0xffffffffu, mloc, 2));
+      const float m_new = fmaxf(m_run, mloc);
+      const float alpha = (m_run == -INFINITY) ? 0.0f : ex2(m_run - m_new);
+      float ofac = alpha;
+      if constexpr (KV) {
+        // weights times V scales, over the power of two at or above the step's largest scale, so
+        // that f16 holds them; O is kept over the same power
+        vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
+        vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
+        const uint32_t pw = vm > 0.0f ? (__float_as_uint(vm) + 0x7fffffu) & 0x7f800000u : 0x3f800000u;
+        const float inv = __uint_as_float(0x7f000000u - pw);
+        ofac *= sigma * inv;
+        sigma = __uint_as_float(pw);
+#pragma unroll
+        for (int t = 0; t < C::NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) vw[t][e] *= inv;
+      }
+      float psum = 0.0f, pall = 0.0f;
+#pragma unroll
+      for (int t = 0; t < C::NT; ++t) {
+        float pe[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          pe[e] = ex2(s[t][e] - m_new);
+          pall += pe[e];
+          if constexpr (KV) pe[e] *= vw[t][e];
+        }
+        if constexpr (!KV) {
+          // the denominator sums the bf16-rounded weights the PV MMA uses
+          pf[t][0] = pack_bf16x2(pe[0], pe[1]);
+          pf[t][1] = pack_bf16x2(pe[2], pe[3]);
+          psum += __uint_as_float(pf[t][0] << 16) + __uint_as_float(pf[t][0] & 0xffff0000u) +
+                  __uint_as_float(pf[t][1] << 16) + __uint_as_float(pf[t][1] & 0xffff0000u);
+        } else {
+          pf[t][0] = pack_f16x2(pe[0], pe[1]);
+          pf[t][1] = pack_f16x2(pe[2], pe[3]);
+        }
+      }
+      if constexpr (!KV) l_run = l_run * alpha + psum;
+      l_all = l_all * alpha + pall;
+      m_run = m_new;
+      if (!(warp & 1)) {   // for the other pair (its two warps hold the same)
+        float* mine = pxb + mp * PX;
+#pragma unroll
+        for (int t = 0; t < C::NT; ++t) reinterpret_cast<uint2*>(mine + t * 64)[lane] = make_uint2(pf[t][0], pf[t][1]);
+        if (tig == 0) mine[C::NT * 64 + gid] = ofac;
+      }
+    }
+    named_bar_sync(1, C::NCW * 32);
+    if (*reinterpret_cast<volatile int*>(abort_flag)) return false;
+
+    uint32_t pg[C::NT][2];   // the other map's weights
+    const float* theirs = pxb + (mp ^ 1) * PX;
+#pragma unroll
+    for (int t = 0; t < C::NT; ++t) {
+      const uint2 v = reinterpret_cast<const uint2*>(theirs + t * 64)[lane];
+      pg[t][0] = v.x;
+      pg[t][1] = v.y;
+    }
+    // rescale O: this lane's O columns are heads 2tig and 2tig+1
+    const uint64_t f0 = *reinterpret_cast<const uint64_t*>(pxb + mp * PX + C::NT * 64 + 2 * tig);
+    const uint64_t f1 = *reinterpret_cast<const uint64_t*>(theirs + C::NT * 64 + 2 * tig);
+    constexpr uint64_t kOnes = 0x3f8000003f800000ull;
+    if (__any_sync(0xffffffffu, f0 != kOnes || f1 != kOnes)) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int mt = 0; mt < C::PV_MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            float a, b;
+            unpack_f32x2(mul_f32x2(pack_f32x2(o[m][mt][e], o[m][mt][e + 1]), m ? f1 : f0), a, b);
+            o[m][mt][e] = a;
+            o[m][mt][e + 1] = b;
+          }
+    }
+    if constexpr (KV != FA_KV_INT8) {
+      // masked keys have weight 0, but their V rows may hold anything (NaN included): zero
+      // this warp's columns of those rows before the MMA
+      if (edge) {
+        constexpr int EPU = 16 / C::ELEM;              // elements per 16-byte unit
+        constexpr int UNITS = C::PV_COLS / EPU;        // 16-byte units per row slice
+        constexpr int EPB = 128 / C::ELEM;             // elements per 128-byte column block
+        uint8_t* vz = const_cast<uint8_t*>(vs);
+        for (int t = 0; t < ntl; ++t) {
+          for (int idx = lane; idx < kTile * UNITS; idx += 32) {
+            const int r = idx / UNITS, uu = idx % UNITS;
+            const int pos = (tile0 + t) * kTile + r;
+            if (pos < lo || pos > qpos) {
+              const int dc = pv_d0 + uu * EPU;
+              *reinterpret_cast<uint4*>(vz + t * C::TILE_BYTES + (dc / EPB) * 2048 + sw128(r, (dc % EPB) / EPU)) =
+                  make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+    }
+    // ---- O^T += V^T P^T over this warp's columns, both maps
+#pragma unroll
+    for (int t = 0; t < C::NT; ++t) {
+      if (t >= ntl) break;
+      const uint8_t* vt = vs + t * C::TILE_BYTES;
+      const int r = (lane & 7) + (lane >> 4) * 8;
+      if constexpr (!KV) {
+#pragma unroll
+        for (int mt = 0; mt < C::PV_MT; ++mt) {
+          const int dc = pv_d0 + mt * 16 + ((lane >> 3) & 1) * 8;
+          uint32_t a0, a1, a2, a3;
+          ldsm_x4_t(smem_u32(vt + (dc >> 6) * 2048 + sw128(r, (dc & 63) >> 3)), a0, a1, a2, a3);
+          mma_bf16(o[0][mt], a0, a1, a2, a3, pf[t][0], pf[t][1]);
+          mma_bf16(o[1][mt], a0, a1, a2, a3, pg[t][0], pg[t][1]);
+        }
+      } else {
+#pragma unroll
+        for (int g2 = 0; g2 < C::PV_MT / 2; ++g2) {
+          const int dc = pv_d0 + g2 * 32 + ((lane >> 3) & 1) * 16;
+          uint32_t r0, r1, r2, r3;
+          ldsm_x4_t(smem_u32(vt + (dc >> 7) * 2048 + sw128(r, (dc & 127) >> 4)), r0, r1, r2, r3);
+          const uint32_t e0 = codes_to_f16x2<KV, 0, 2>(r0), e1 = codes_to_f16x2<KV, 0, 2>(r1), e2 = codes_to_f16x2<KV, 0, 2>(r2), e3 = codes_to_f16x2<KV, 0, 2>(r3);
+          mma_f16(o[0][2 * g2], e0, e1, e2, e3, pf[t][0], pf[t][1]);
+          mma_f16(o[1][2 * g2], e0, e1, e2, e3, pg[t][0], pg[t][1]);
+          const uint32_t h0 = codes_to_f16x2<KV, 1, 3>(r0), h1 = codes_to_f16x2<KV, 1, 3>(r1), h2 = codes_to_f16x2<KV, 1, 3>(r2), h3 = codes_to_f16x2<KV, 1, 3>(r3);
+          mma_f16(o[0][2 * g2 + 1], h0, h1, h2, h3, pf[t][0], pf[t][1]);
+          mma_f16(o[1][2 * g2 + 1], h0, h1, h2, h3, pg[t][0], pg[t][1]);
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[st]);
+    ++gi;
+  }
+
+  // -------------------------------------------------------- segment epilogue
+  l_all += __shfl_xor_sync(0xffffffffu, l_all, 1);
+  l_all += __shfl_xor_sync(0xffffffffu, l_all, 2);
+  if constexpr (KV) {
+    l_run = l_all;
+  } else {
+    l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
+    l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
+  }
+  // output column d of C-fragment row (gid + 8 * half) of O^T tile mt
+  auto out_d = [&](int mt, int half) -> int {
+    if constexpr (!KV) return pv_d0 + mt * 16 + gid + 8 * half;
+    else return pv_d0 + (mt >> 1) * 32 + 16 * half + 2 * gid + (mt & 1);
+  };
+  const int hA = 2 * tig, hB = 2 * tig + 1;
+  const int c_first = kper ? u * kper : cta_of(P, ncta, T);
+  const int c_last = kper ? c_first + kper - 1 : cta_of(P + x.n - 1, ncta, T);
+  if (c_first == c_last) {
+    if (!(warp & 1) && tig == 0) {
+      float* e = ends + (mp * 8 + gid) * 3;
+      e[0] = m_run;
+      e[1] = l_run;
+      e[2] = l_all;
+    }
+    named_bar_sync(1, C::NCW * 32);
+    float wA[2], wB[2];   // the weights of o[0] and o[1] in heads hA and hB
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const int map = mp ^ m;
+      const float lA = ends[(map * 8 + hA) * 3 + 1], lB = ends[(map * 8 + hB) * 3 + 1];
+      wA[m] = (lA > 0.f) ? sigma / lA : 0.f;
+      wB[m] = (lB > 0.f) ? sigma / lB : 0.f;
+      if (map == 1) {
+        wA[m] *= hA < nh ? -__ldg(p.lambda + head0 + hA) : 0.f;
+        wB[m] *= hB < nh ? -__ldg(p.lambda + head0 + hB) : 0.f;
+      }
+    }
+#pragma unroll
+    for (int mt = 0; mt < C::PV_MT; ++mt)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int d = out_d(mt, half);
+        if (hA < nh)
+          p.out[(static_cast<size_t>(x.b) * p.Hq + head0 + hA) * D + d] =
+              __float2bfloat16_rn(o[0][mt][2 * half] * wA[0] + o[1][mt][2 * half] * wA[1]);
+        if (hB < nh)
+          p.out[(static_cast<size_t>(x.b) * p.Hq + head0 + hB) * D + d] =
+              __float2bfloat16_rn(o[0][mt][2 * half + 1] * wB[0] + o[1][mt][2 * half + 1] * wB[1]);
+      }
+    if (p.lse && !(warp & 1) && tig == 0 && gid < nh)
+      p.lse[(static_cast<size_t>(x.b) * p.Hq + head0 + gid) * 2 + mp] = (m_run + __log2f(l_all)) * 0.69314718055994531f;
+  } else {
+    // join_diff_kernel joins the parts; it finds them by the second one's share
+    const size_t slot = static_cast<size_t>(cta) + u;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int mt = 0; mt < C::PV_MT; ++mt)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int d = out_d(mt, half);
+          p.o_part[((slot * 2 + (mp ^ m)) * 8 + hA) * D + d] = o[m][mt][2 * half] * sigma;
+          p.o_part[((slot * 2 + (mp ^ m)) * 8 + hB) * D + d] = o[m][mt][2 * half + 1] * sigma;
+        }
+    if (!(warp & 1) && tig == 0)
+      reinterpret_cast<float4*>(p.ml_part)[(slot * 2 + mp) * 8 + gid] = make_float4(m_run, l_run, l_all, 0.f);
+    if (cta == c_first + 1 && threadIdx.x == 0) p.joins[cta] = make_int2(u, c_last);
+  }
+  return true;
+}
+
 // One CTA of a layer's decode: CTA `cta` of the `grid` CTAs launched for the
 // layer (a launch may hold several layers; see decode_layers_kernel).
-// MAPS = 2: differential attention.  A consumer warp's QK^T columns lie in one half
-// of the row, so its partial scores belong to one map: the exchange adds up each
-// map's warps apart, at no cost in MMAs; each lane then holds its head's weights of
-// both maps, and each V fragment feeds two MMAs.
+// MAPS = 2: differential attention (diff_segment).
 template <int D, int KV, int MAPS = 1>
 __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUtensorMap* tm_v,
                                             const CUtensorMap* tm_ks, const CUtensorMap* tm_vs, const DecK& p,
@@ -489,16 +807,16 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
     __syncwarp();
     if (lane == 0) mbar_arrive(qempty);
 
-    // l_run: the sum of the weights as the PV MMA takes them; l_all (MAPS 2): unrounded, for lse
-    float o[MAPS][C::PV_MT][4];
-    float m_run[MAPS], l_run[MAPS], l_all[MAPS], sigma = 1.0f;
-#pragma unroll
-    for (int m = 0; m < MAPS; ++m) {
-      m_run[m] = -INFINITY;
-      l_run[m] = l_all[m] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < C::PV_MT; ++i) o[m][i][0] = o[m][i][1] = o[m][i][2] = o[m][i][3] = 0.0f;
+    if constexpr (MAPS == 2) {
+      if (!diff_segment<D, KV>(p, x, smem, sx, full, empty, gi, ta, tz, P, u, cta, ncta, kper, T, nh, head0, qf, &abort_flag)) break;
+      ++j;
+      P += x.n;
     }
+    if (MAPS == 2) continue;
+    float o[C::PV_MT][4];
+#pragma unroll
+    for (int i = 0; i < C::PV_MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+    float m_run = -INFINITY, l_run = 0.0f, sigma = 1.0f;
 
     for (int tile0 = ta; tile0 < tz; tile0 += C::NT) {
       const int st = gi % C::NSTAGE;
@@ -547,14 +865,31 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
 
       {
         // ---- scores for this lane's head (gid), keys {2tig, 2tig+1, 2tig+8, 2tig+9} of each tile
+        float s[C::NT][4];
         bool valid[C::NT][4];
+        float mloc = -INFINITY;
 #pragma unroll
-        for (int t = 0; t < C::NT; ++t)
+        for (int t = 0; t < C::NT; ++t) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int pos = (tile0 + t) * kTile + 2 * tig + (e & 1) + (e >> 1) * 8;
+            const int key = 2 * tig + (e & 1) + (e >> 1) * 8;
+            float v = 0.0f;
+#pragma unroll
+            for (int w = t; w < C::NCW; w += C::NT) v += sx[((buf * C::NCW + w) * kTile + key) * C::SX_STRIDE + gid];
+            const int pos = (tile0 + t) * kTile + key;
             valid[t][e] = (t < ntl) && pos >= lo && pos <= qpos;
+            float sc = p.scale_log2;
+            if constexpr (KV) sc *= scl[t * 32 + key];
+            s[t][e] = valid[t][e] ? v * sc : -INFINITY;
+            mloc = fmaxf(mloc, s[t][e]);
           }
+        }
+        mloc = fmaxf(mloc, __shfl_xor_sync(0xffffffffu, mloc, 1));
+        mloc = fmaxf(mloc, __shfl_xor_sync(0xffffffffu, mloc, 2));
+        const float m_new = fmaxf(m_run, mloc);
+        const float alpha = (m_run == -INFINITY) ? 0.0f : ex2(m_run - m_new);
+        float psum = 0.0f;
+        uint32_t pf[C::NT][2];
         float vmax = 1.0f, ivm = 1.0f;
         float vsc[C::NT][4];   // 8-bit: this lane's keys' V scales (0 where not visible)
         if constexpr (KV) {
@@ -571,72 +906,46 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
           vmax = vm > 0.0f ? vm : 1.0f;
           ivm = __frcp_rn(vmax);   // one reciprocal per step instead of a division per weight
         }
-        uint32_t pf[MAPS][C::NT][2];
 #pragma unroll
-        for (int m = 0; m < MAPS; ++m) {
-          float s[C::NT][4];
-          float mloc = -INFINITY;
+        for (int t = 0; t < C::NT; ++t) {
+          float pe[4];
 #pragma unroll
-          for (int t = 0; t < C::NT; ++t) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int key = 2 * tig + (e & 1) + (e >> 1) * 8;
-              float v = 0.0f;
-#pragma unroll
-              for (int w = t + m * (C::NCW / MAPS); w < (m + 1) * (C::NCW / MAPS); w += C::NT)
-                v += sx[((buf * C::NCW + w) * kTile + key) * C::SX_STRIDE + gid];
-              float sc = p.scale_log2;
-              if constexpr (KV) sc *= scl[t * 32 + key];
-              s[t][e] = valid[t][e] ? v * sc : -INFINITY;
-              mloc = fmaxf(mloc, s[t][e]);
+          for (int e = 0; e < 4; ++e) {
+            pe[e] = ex2(s[t][e] - m_new);
+            if constexpr (KV) {
+              psum += pe[e];
+              pe[e] *= vsc[t][e] * ivm;
             }
           }
-          mloc = fmaxf(mloc, __shfl_xor_sync(0xffffffffu, mloc, 1));
-          mloc = fmaxf(mloc, __shfl_xor_sync(0xffffffffu, mloc, 2));
-          const float m_new = fmaxf(m_run[m], mloc);
-          const float alpha = (m_run[m] == -INFINITY) ? 0.0f : ex2(m_run[m] - m_new);
-          float psum = 0.0f, pall = 0.0f;
-#pragma unroll
-          for (int t = 0; t < C::NT; ++t) {
-            float pe[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              pe[e] = ex2(s[t][e] - m_new);
-              if constexpr (MAPS == 2 && !KV) pall += pe[e];
-              if constexpr (KV) {
-                psum += pe[e];
-                pe[e] *= vsc[t][e] * ivm;
-              }
-            }
-            if constexpr (!KV) {
-              // the denominator sums the bf16-rounded weights the PV MMA uses, so
-              // the weights of each output row sum to exactly one
-              pf[m][t][0] = pack_bf16x2(pe[0], pe[1]);
-              pf[m][t][1] = pack_bf16x2(pe[2], pe[3]);
-              psum += __uint_as_float(pf[m][t][0] << 16) + __uint_as_float(pf[m][t][0] & 0xffff0000u) +
-                      __uint_as_float(pf[m][t][1] << 16) + __uint_as_float(pf[m][t][1] & 0xffff0000u);
-            } else {
-              pf[m][t][0] = pack_f16x2(pe[0], pe[1]);
-              pf[m][t][1] = pack_f16x2(pe[2], pe[3]);
-            }
-          }
-          l_run[m] = l_run[m] * alpha + psum;
-          if constexpr (MAPS == 2 && !KV) l_all[m] = l_all[m] * alpha + pall;
-          m_run[m] = m_new;
-          float ofac = alpha;
-          if constexpr (KV) ofac = alpha * sigma * ivm;
-          // rescale O: this lane's O columns are heads 2tig and 2tig+1
-          const float fa_ = __shfl_sync(0xffffffffu, ofac, 8 * tig);
-          const float fb_ = __shfl_sync(0xffffffffu, ofac, 8 * tig + 4);
-#pragma unroll
-          for (int mt = 0; mt < C::PV_MT; ++mt) {
-            o[m][mt][0] *= fa_;
-            o[m][mt][1] *= fb_;
-            o[m][mt][2] *= fa_;
-            o[m][mt][3] *= fb_;
+          if constexpr (!KV) {
+            // the denominator sums the bf16-rounded weights the PV MMA uses, so
+            // the weights of each output row sum to exactly one
+            pf[t][0] = pack_bf16x2(pe[0], pe[1]);
+            pf[t][1] = pack_bf16x2(pe[2], pe[3]);
+            psum += __uint_as_float(pf[t][0] << 16) + __uint_as_float(pf[t][0] & 0xffff0000u) +
+                    __uint_as_float(pf[t][1] << 16) + __uint_as_float(pf[t][1] & 0xffff0000u);
+          } else {
+            pf[t][0] = pack_f16x2(pe[0], pe[1]);
+            pf[t][1] = pack_f16x2(pe[2], pe[3]);
           }
         }
-        if constexpr (KV) sigma = vmax;
+        l_run = l_run * alpha + psum;
+        m_run = m_new;
+        float ofac = alpha;
+        if constexpr (KV) {
+          ofac = alpha * sigma * ivm;
+          sigma = vmax;
+        }
+        // rescale O: this lane's O columns are heads 2tig and 2tig+1
+        const float fa_ = __shfl_sync(0xffffffffu, ofac, 8 * tig);
+        const float fb_ = __shfl_sync(0xffffffffu, ofac, 8 * tig + 4);
+#pragma unroll
+        for (int mt = 0; mt < C::PV_MT; ++mt) {
+          o[mt][0] *= fa_;
+          o[mt][1] *= fb_;
+          o[mt][2] *= fa_;
+          o[mt][3] *= fb_;
+        }
 
         if constexpr (KV != FA_KV_INT8) {
           // masked keys have p = 0, but their V rows may hold anything (NaN
@@ -675,8 +984,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
               const int dc = pv_d0 + mt * 16 + ((lane >> 3) & 1) * 8;
               uint32_t a0, a1, a2, a3;
               ldsm_x4_t(smem_u32(vt + (dc >> 6) * 2048 + sw128(r, (dc & 63) >> 3)), a0, a1, a2, a3);
-              #pragma unroll
-              for (int m = 0; m < MAPS; ++m) mma_bf16(o[m][mt], a0, a1, a2, a3, pf[m][t][0], pf[m][t][1]);
+              mma_bf16(o[mt], a0, a1, a2, a3, pf[t][0], pf[t][1]);
             }
           } else {
 #pragma unroll
@@ -684,13 +992,10 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
               const int dc = pv_d0 + gi2 * 32 + ((lane >> 3) & 1) * 16;
               uint32_t r0, r1, r2, r3;
               ldsm_x4_t(smem_u32(vt + (dc >> 7) * 2048 + sw128(r, (dc & 127) >> 4)), r0, r1, r2, r3);
-#pragma unroll
-              for (int m = 0; m < MAPS; ++m) {
-                mma_f16(o[m][2 * gi2], codes_to_f16x2<KV, 0, 2>(r0), codes_to_f16x2<KV, 0, 2>(r1),
-                        codes_to_f16x2<KV, 0, 2>(r2), codes_to_f16x2<KV, 0, 2>(r3), pf[m][t][0], pf[m][t][1]);
-                mma_f16(o[m][2 * gi2 + 1], codes_to_f16x2<KV, 1, 3>(r0), codes_to_f16x2<KV, 1, 3>(r1),
-                        codes_to_f16x2<KV, 1, 3>(r2), codes_to_f16x2<KV, 1, 3>(r3), pf[m][t][0], pf[m][t][1]);
-              }
+              mma_f16(o[2 * gi2], codes_to_f16x2<KV, 0, 2>(r0), codes_to_f16x2<KV, 0, 2>(r1),
+                      codes_to_f16x2<KV, 0, 2>(r2), codes_to_f16x2<KV, 0, 2>(r3), pf[t][0], pf[t][1]);
+              mma_f16(o[2 * gi2 + 1], codes_to_f16x2<KV, 1, 3>(r0), codes_to_f16x2<KV, 1, 3>(r1),
+                      codes_to_f16x2<KV, 1, 3>(r2), codes_to_f16x2<KV, 1, 3>(r3), pf[t][0], pf[t][1]);
             }
           }
         }
@@ -702,21 +1007,11 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
 
     {
       // ------------------------------------------------------ segment epilogue
+      l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
+      l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
       const int hA = 2 * tig, hB = 2 * tig + 1;
-      float lA[MAPS], lB[MAPS];
-#pragma unroll
-      for (int m = 0; m < MAPS; ++m) {
-        l_run[m] += __shfl_xor_sync(0xffffffffu, l_run[m], 1);
-        l_run[m] += __shfl_xor_sync(0xffffffffu, l_run[m], 2);
-        if constexpr (MAPS == 2 && !KV) {
-          l_all[m] += __shfl_xor_sync(0xffffffffu, l_all[m], 1);
-          l_all[m] += __shfl_xor_sync(0xffffffffu, l_all[m], 2);
-        } else {
-          l_all[m] = l_run[m];
-        }
-        lA[m] = __shfl_sync(0xffffffffu, l_run[m], 8 * tig);
-        lB[m] = __shfl_sync(0xffffffffu, l_run[m], 8 * tig + 4);
-      }
+      const float lA = __shfl_sync(0xffffffffu, l_run, 8 * tig);
+      const float lB = __shfl_sync(0xffffffffu, l_run, 8 * tig + 4);
       // output column d of C-fragment row (gid + 8 * half) of O^T tile mt
       auto out_d = [&](int mt, int half) -> int {
         if constexpr (!KV) return pv_d0 + mt * 16 + gid + 8 * half;
@@ -725,83 +1020,56 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
       const int c_first = kper ? u * kper : cta_of(P, ncta, T);
       const int c_last = kper ? c_first + kper - 1 : cta_of(P + x.n - 1, ncta, T);
       if (c_first == c_last) {
-        float iA[MAPS], iB[MAPS];
-#pragma unroll
-        for (int m = 0; m < MAPS; ++m) {
-          iA[m] = (lA[m] > 0.f) ? sigma / lA[m] : 0.f;
-          iB[m] = (lB[m] > 0.f) ? sigma / lB[m] : 0.f;
-        }
-        if constexpr (MAPS == 2) {   // the second map's weight: - lambda
-          iA[MAPS - 1] *= hA < nh ? -__ldg(p.lambda + head0 + hA) : 0.f;
-          iB[MAPS - 1] *= hB < nh ? -__ldg(p.lambda + head0 + hB) : 0.f;
-        }
+        const float iA = (lA > 0.f) ? sigma / lA : 0.f, iB = (lB > 0.f) ? sigma / lB : 0.f;
 #pragma unroll
         for (int mt = 0; mt < C::PV_MT; ++mt)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             const int d = out_d(mt, half);
-            float yA = o[0][mt][2 * half] * iA[0], yB = o[0][mt][2 * half + 1] * iB[0];
-            if constexpr (MAPS == 2) {
-              yA += o[MAPS - 1][mt][2 * half] * iA[MAPS - 1];
-              yB += o[MAPS - 1][mt][2 * half + 1] * iB[MAPS - 1];
-            }
-            if (hA < nh) p.out[(static_cast<size_t>(x.b) * p.Hq + head0 + hA) * D + d] = __float2bfloat16_rn(yA);
-            if (hB < nh) p.out[(static_cast<size_t>(x.b) * p.Hq + head0 + hB) * D + d] = __float2bfloat16_rn(yB);
+            if (hA < nh)
+              p.out[(static_cast<size_t>(x.b) * p.Hq + head0 + hA) * D + d] = __float2bfloat16_rn(o[mt][2 * half] * iA);
+            if (hB < nh)
+              p.out[(static_cast<size_t>(x.b) * p.Hq + head0 + hB) * D + d] =
+                  __float2bfloat16_rn(o[mt][2 * half + 1] * iB);
           }
         if (p.lse && warp == 0 && tig == 0 && hv)
-#pragma unroll
-          for (int m = 0; m < MAPS; ++m)
-            p.lse[(static_cast<size_t>(x.b) * p.Hq + head0 + gid) * MAPS + m] = (m_run[m] + __log2f(l_all[m])) * 0.69314718055994531f;
+          p.lse[static_cast<size_t>(x.b) * p.Hq + head0 + gid] = (m_run + __log2f(l_run)) * 0.69314718055994531f;
       } else {
         const size_t slot = static_cast<size_t>(cta) + u;
 #pragma unroll
-        for (int m = 0; m < MAPS; ++m)
+        for (int mt = 0; mt < C::PV_MT; ++mt)
 #pragma unroll
-          for (int mt = 0; mt < C::PV_MT; ++mt)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const int d = out_d(mt, half);
-              p.o_part[((slot * MAPS + m) * 8 + hA) * D + d] = o[m][mt][2 * half] * sigma;
-              p.o_part[((slot * MAPS + m) * 8 + hB) * D + d] = o[m][mt][2 * half + 1] * sigma;
-            }
-        if (warp == 0 && tig == 0) {
-          if constexpr (MAPS == 1) {
-            reinterpret_cast<float2*>(p.ml_part)[slot * 8 + gid] = make_float2(m_run[0], l_run[0]);
-          } else {
-#pragma unroll
-            for (int m = 0; m < MAPS; ++m)
-              reinterpret_cast<float4*>(p.ml_part)[(slot * MAPS + m) * 8 + gid] = make_float4(m_run[m], l_run[m], l_all[m], 0.f);
+          for (int half = 0; half < 2; ++half) {
+            const int d = out_d(mt, half);
+            p.o_part[(slot * 8 + hA) * D + d] = o[mt][2 * half] * sigma;
+            p.o_part[(slot * 8 + hB) * D + d] = o[mt][2 * half + 1] * sigma;
           }
+        if (warp == 0 && tig == 0)
+          reinterpret_cast<float2*>(p.ml_part)[slot * 8 + gid] = make_float2(m_run, l_run);
+        // arrive; the last of the unit's CTAs merges every partial row.  The
+        // barrier orders the CTA's partial writes before thread 0's
+        // release/acquire add, which publishes them and, for the last
+        // arrival, makes the other CTAs' rows visible.
+        named_bar_sync(1, C::NCW * 32);
+        if (threadIdx.x == 0) {
+          const int nct = c_last - c_first + 1;
+          int* counter = p.counters + c_first + 1;
+          const int old = atom_add_acq_rel_gpu(counter, 1);
+          int last = 0;
+          if (old == nct - 1) {
+            last = 1;
+            atomicExch(counter, 0);   // leave the counter zero for the next call
+          } else if (old < 0 || old >= nct) {
+            atomicOr(p.err, FA_DEV_ERR_WORKSPACE);
+          }
+          sh_last = last;
         }
-        if constexpr (MAPS == 2) {
-          // join_diff_kernel joins the parts; it finds them by the second one's share
-          if (cta == c_first + 1 && threadIdx.x == 0) p.joins[cta] = make_int2(u, c_last);
-        } else {
-          // arrive; the last of the unit's CTAs merges every partial row.  The
-          // barrier orders the CTA's partial writes before thread 0's
-          // release/acquire add, which publishes them and, for the last
-          // arrival, makes the other CTAs' rows visible.
-          named_bar_sync(1, C::NCW * 32);
-          if (threadIdx.x == 0) {
-            const int nct = c_last - c_first + 1;
-            int* counter = p.counters + c_first + 1;
-            const int old = atom_add_acq_rel_gpu(counter, 1);
-            int last = 0;
-            if (old == nct - 1) {
-              last = 1;
-              atomicExch(counter, 0);   // leave the counter zero for the next call
-            } else if (old < 0 || old >= nct) {
-              atomicOr(p.err, FA_DEV_ERR_WORKSPACE);
-            }
-            sh_last = last;
-          }
-          named_bar_sync(1, C::NCW * 32);
-          if (sh_last) {
-            // the ring is idle once this CTA's last segment is consumed: stage the merge there
-            const bool idle = P + x.n >= s_end;
-            merge_unit<D, C::STAGE_ALL>(p, u, x, nh, head0, c_first, c_last, sx, idle ? smem : nullptr, mbar_merge,
-                                         &abort_flag);
-          }
+        named_bar_sync(1, C::NCW * 32);
+        if (sh_last) {
+          // the ring is idle once this CTA's last segment is consumed: stage the merge there
+          const bool idle = P + x.n >= s_end;
+          merge_unit<D, C::STAGE_ALL>(p, u, x, nh, head0, c_first, c_last, sx, idle ? smem : nullptr, mbar_merge,
+                                       &abort_flag);
         }
       }
     }
