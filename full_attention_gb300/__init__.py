@@ -183,12 +183,21 @@ def _desc(d: dict) -> LayerDesc:
                      int(d.get("window", 0)), int(d.get("kv_source", KV_OWN)), float(d["sm_scale"]))
 
 
-_TWO_PI = Fraction(6283185307179586476925286766559005768394338798750211641949889184615, 10 ** 66)
+# 2^192 / (2 pi)
+_TURN = round(Fraction(1 << 192) / Fraction(6283185307179586476925286766559005768394338798750211641949889184615, 10 ** 66))
 
 
 def rope_steps(inv_freq) -> list:
     """fa_norm_rope's steps: each frequency (radians a position) in turns times 2^64, modulo 2^64."""
-    return [round(Fraction(float(f)) * (1 << 64) / _TWO_PI) % (1 << 64) for f in inv_freq]
+    steps = []
+    for f in inv_freq.tolist() if isinstance(inv_freq, torch.Tensor) else inv_freq:
+        f = float(f)
+        if f - f != 0.0:
+            raise FAError(ERR_INVALID_ARG, f"frequency {f}")
+        n, d = f.as_integer_ratio()   # d: a power of two
+        shift = 128 + d.bit_length() - 1
+        steps.append((n * _TURN + (1 << (shift - 1)) >> shift) % (1 << 64))
+    return steps
 
 
 class NormRope:

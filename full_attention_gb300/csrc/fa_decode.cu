@@ -573,6 +573,7 @@ __device__ __forceinline__ bool diff_segment(const DecK& p, const Unit& x, uint8
   return true;
 }
 
+#pragma nv_diag_suppress 128   // "loop is not reachable": with MAPS 2 diff_segment takes the segments
 // One CTA of a layer's decode: CTA `cta` of the `grid` CTAs launched for the
 // layer (a launch may hold several layers; see decode_layers_kernel).
 // MAPS = 2: differential attention (diff_segment).
@@ -1078,6 +1079,8 @@ __device__ __forceinline__ void decode_body(const CUtensorMap* tm_k, const CUten
   }
 consumers_done:;
 }
+
+#pragma nv_diag_default 128
 
 template <int D, int KV>
 __global__ void __launch_bounds__(DecCfg<D, KV>::NTHR, 2)

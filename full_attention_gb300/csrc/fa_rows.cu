@@ -93,20 +93,22 @@ __device__ __forceinline__ float warp_sum(float x) {
 }
 
 // 1 / sqrt(mean(x^2) + eps) of a row.  Where the squares leave fp32 (magnitudes near 2^64,
-// infinities, NaN) the row is divided by 2^70 first.
+// infinities, NaN) the row is multiplied by `small`, 2^-70, first.
 template <int D, int NV>
-__device__ __forceinline__ float row_factor(float (&x)[NV][8], float eps) {
+__device__ __forceinline__ float row_factor(float (&x)[NV][8], float eps, float& small) {
   const float ss = warp_sum(square_sum(x));
   if (ss <= 1e38f) return rsqrtf(fmaf(ss, 1.0f / D, eps));
+  small = 8.470329472543003e-22f;
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[j][e] *= 8.470329472543003e-22f;
+    for (int e = 0; e < 8; ++e) x[j][e] *= small;
   return rsqrtf(warp_sum(square_sum(x)) * (1.0f / D));
 }
 
 // Where a rotated vector's partner is: in its own lane (D = 512, R = D), in a lane's
-// first vector (2 R / 16 <= 32 vectors rotated), or in any.
+// first vector (2 R / 16 <= 32 vectors rotated: exchanged by shuffles), or in any (read
+// again: the row was just loaded, so from L1).
 enum { kOwnLane, kFirst, kAnywhere };
 
 // Cosines and sines of pairs 8 c .. 8 c + 7 at position pos.
@@ -241,10 +243,16 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsWarps * 32 / kRowsThreads)
     for (int i = 0; i < RH; ++i) {
       if (x.h + i >= x.h1) break;
       if (norm || turn) {   // (else the row goes on bit for bit)
-        float v[NV][8];
+        float v[NV][8], small = 1.0f;
+        uint4 o[NR];
+        if (ROT == kAnywhere && turn) {
+#pragma unroll
+          for (int j = 0; j < NR; ++j) o[j] = x.src[(x.h + i) * (D / 8) + from[j] - lane];
+          __syncwarp();   // every lane has read the row (which may be its own output)
+        }
 #pragma unroll
         for (int j = 0; j < NV; ++j) bf16x8_to_f32(r[i].v[j], v[j]);
-        const float f = norm ? row_factor<D>(v, a.eps) : 1.0f;
+        const float f = norm ? row_factor<D>(v, a.eps, small) : 1.0f;
         const uint64_t f2 = pack_f32x2(f, f);
         uint64_t z[NV][4];
 #pragma unroll
@@ -256,17 +264,12 @@ __global__ void __launch_bounds__(kRowsThreads, kRowsWarps * 32 / kRowsThreads)
 #pragma unroll
           for (int j = 0; j < NR; ++j) {
             float p[8];
+            if constexpr (ROT == kAnywhere) bf16x8_to_f32(o[j], p);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              if constexpr (ROT == kOwnLane) {
-                p[e] = v[NV - 1 - j][e];
-              } else {
-                p[e] = __shfl_sync(0xffffffffu, v[0][e], from[j] & 31);
-                if constexpr (ROT == kAnywhere) {
-                  const float o = __shfl_sync(0xffffffffu, v[NV - 1][e], from[j] & 31);
-                  p[e] = from[j] >= 32 ? o : p[e];
-                }
-              }
+              if constexpr (ROT == kOwnLane) p[e] = v[NV - 1 - j][e];
+              if constexpr (ROT == kFirst) p[e] = __shfl_sync(0xffffffffu, v[0][e], from[j] & 31);
+              if constexpr (ROT == kAnywhere) p[e] *= small;
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -316,7 +319,7 @@ static cudaError_t launch_rows_t(RowsK k, cudaStream_t s) {
   if (k.half8 <= 16) return launch_pdl(rows_kernel<D, KV, RH, kFirst>, g, b, 0, s, k);
   if constexpr (D == 512) {
     if (k.half8 == 32) return launch_pdl(rows_kernel<D, KV, RH, kOwnLane>, g, b, 0, s, k);
-    return launch_pdl(rows_kernel<D, KV, 1, kAnywhere>, g, b, 0, s, k);
+    return launch_pdl(rows_kernel<D, KV, 1, kAnywhere>, g, b, 0, s, k);   // (its partners take the room: 83 us, 2 rows with spills 96)
   }
   return cudaErrorInvalidValue;
 }

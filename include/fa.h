@@ -347,8 +347,8 @@ typedef struct {
  * 2 Hkv) * D] is read where it lies; k, v: the same with Hkv rows.  q may be NULL
  * (keys and values alone), k and v both NULL (queries alone).
  * positions: int32 [T], each token's position (any int32; may be NULL where
- * rotary_dim is 0).  All arithmetic is fp32, each
- * row rounded to bf16 once; a row neither normed nor turned goes on bit for bit.
+ * rotary_dim is 0).  All arithmetic is fp32 (a value times its weight has to stay
+ * in its range), each row rounded to bf16 once; a row neither normed nor turned goes on bit for bit.
  * q_out: bf16 [T][Hq][D].  k_out, v_out: bf16 [T][Hkv][D], either may be NULL
  * (extend takes the chunk's rows from them).  An output may be its own input where
  * that is dense; otherwise outputs overlap no input.  slot_mapping: as in fa_kv_store,
