@@ -73,6 +73,12 @@
 // neighbouring lanes, with weights 1 / l_0 and - lambda / l_1.  The zeros double
 // the S products (4 MMAs of 128 x 64 x 64 columns for 3 that count); two S tiles
 // without them would need two O accumulators, twice the tensor memory there is.
+// 4 x 512 tokens over 3584 at head_dim 256, window 1024, 16 query and 8 KV heads, bf16: 119 us
+// (plain attention 69); 2753 tokens of 5 prompts over up to 3814 at 512, 16 and 2 heads: bf16 852 us
+// (plain 475), fp8 1670 (plain 896).  A tile's cycles, bf16 at 256: of 2850 the MMA warp
+// waits 800 for the weighted sum two tiles back, 1000 for K and V to land and 290 for the
+// weights; 8-bit at 512: of 8100, 5000 for converted slots, which copying (1000 cycles a slot) and converting
+// (1250) bound alike.
 // Every wait is bounded; tensor memory is always freed.
 #include <algorithm>
 #include <cfloat>
@@ -1074,11 +1080,22 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
           for (int c4 = 0; c4 < 8; ++c4) {
             const float4 k4 = *reinterpret_cast<const float4*>(ck + 4 * c4);
             const float kk[4] = {k4.x, k4.y, k4.z, k4.w};
+            if constexpr (DIFF) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int c = 4 * c4 + e;
-              const float t = __uint_as_float(sr[c]) * kk[e];
-              sv[c] = (all || (c >= clo && c <= chi)) ? t : -INFINITY;
+              for (int e = 0; e < 4; e += 2)
+                unpack_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(sr[4 * c4 + e]), __uint_as_float(sr[4 * c4 + e + 1])), pack_f32x2(kk[e], kk[e + 1])),
+                             sv[4 * c4 + e], sv[4 * c4 + e + 1]);
+              if (!all)
+#pragma unroll
+                for (int c = 4 * c4; c < 4 * c4 + 4; ++c)
+                  if (c < clo || c > chi) sv[c] = -INFINITY;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int c = 4 * c4 + e;
+                const float t = __uint_as_float(sr[c]) * kk[e];
+                sv[c] = (all || (c >= clo && c <= chi)) ? t : -INFINITY;
+              }
             }
           }
         } else if (__all_sync(0xffffffffu, clo <= 0 && chi >= 31)) {   // all 32 columns visible to the warp's rows
@@ -1135,7 +1152,29 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
       float ps[4] = {0.f, 0.f, 0.f, 0.f}, pe[2] = {0.f, 0.f};
       // a row with no visible key so far has m_run = -inf and only -inf scores: exponent base 0 gives 0
       const float mb = (m_run > -INFINITY) ? m_run - MB_OFF : 0.f;
-      if constexpr (C::Q8) {
+      if constexpr (DIFF) {
+        // pairs of values an instruction, and one sum, of the unrounded weights (a rounded
+        // weight is then off by half a step of itself, not of its sum's too)
+        const uint64_t sc2 = pack_f32x2(sc, sc), mb2 = pack_f32x2(-mb, -mb);
+        uint64_t sum[2] = {0, 0};
+        const float4* cv4 = reinterpret_cast<const float4*>(cvh);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const uint64_t v = pack_f32x2(sv[2 * c], sv[2 * c + 1]);
+          float p0, p1;
+          unpack_f32x2(C::Q8 ? add_f32x2(v, mb2) : fma_f32x2(v, sc2, mb2), p0, p1);
+          uint64_t w = pack_f32x2(ex2(p0), ex2(p1));
+          sum[c & 1] = add_f32x2(sum[c & 1], w);
+          if constexpr (C::Q8) {
+            const float4 k4 = cv4[c >> 1];
+            w = mul_f32x2(w, (c & 1) ? pack_f32x2(k4.z, k4.w) : pack_f32x2(k4.x, k4.y));
+          }
+          unpack_f32x2(w, p0, p1);
+          pk[c] = C::Q8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+        }
+        unpack_f32x2(add_f32x2(sum[0], sum[1]), pe[0], pe[1]);
+        l_run += pe[0] + pe[1];
+      } else if constexpr (C::Q8) {
         // weight q = 2^(score - mb) into the denominator; q x cv, below 2^15
         // (score + log2 cv <= m_run + 8), into the PV MMA as f16
 #pragma unroll
