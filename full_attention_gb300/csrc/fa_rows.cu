@@ -16,17 +16,15 @@
 // are off by 2^-21 at most: an 8192nd of a bf16 rounding of the pair's length.
 //
 // With A_i = w_i cos, B_i = -w_{i+h} sin (i < h; A_{i+h} = w_{i+h} cos, B_{i+h} = w_i sin), made once
-// a token and weight, a value costs z = f (x A + x' B), x' its partner, f the row's 1 / root.
-//
-// With A_i = w_i cos, B_i = -w_{i+h} sin (i < h; A_{i+h} = w_{i+h} cos, B_{i+h} = w_i sin), made once
-// a warp, a value costs z = f (x A + x' B), x' its partner, f the row's 1 / root.
+// an item (below), a value costs z = f (x A + x' B), x' its partner, f the row's 1 / root.
 //
 // A memory pass: each row read once, written once (rows out, slab).  Warps are
-// persistent and independent: each walks items (up to 8 heads of one kind of one
+// persistent and independent: each walks items (up to 16 heads of one kind of one
 // token: its sines serve them all), with the next rows' loads in flight
 // while it works on the ones before.  30011 tokens of 16 + 2 + 2 heads at head_dim 512, bf16:
 // 197 us, 6.25 TB/s of 6.8 (copied without arithmetic 186); 2048 tokens of 16 + 8 + 8 at 256
-// with the rows out: 17.8 us, 4.7 TB/s.  Blocks of their own for each token's heads took 224 and 20 us (their
+// with the rows out: 17.8 us, 4.7 TB/s (there the schedulers issue half of the time, on shuffles and
+// short rows).  Blocks of their own for each token's heads took 224 and 20 us (their
 // loads waited for their sines, and blocks start at one a nanosecond), rows through
 // a ring of shared memory with a copying warp 263 and 18.6.
 #include <algorithm>
