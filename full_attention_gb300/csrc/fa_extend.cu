@@ -73,12 +73,14 @@
 // neighbouring lanes, with weights 1 / l_0 and - lambda / l_1.  The zeros double
 // the S products (4 MMAs of 128 x 64 x 64 columns for 3 that count); two S tiles
 // without them would need two O accumulators, twice the tensor memory there is.
-// 4 x 512 tokens over 3584 at head_dim 256, window 1024, 16 query and 8 KV heads, bf16: 119 us
-// (plain attention 69); 2753 tokens of 5 prompts over up to 3814 at 512, 16 and 2 heads: bf16 852 us
-// (plain 475), fp8 1670 (plain 896).  A tile's cycles, bf16 at 256: of 2850 the MMA warp
+// 4 x 512 tokens over 3584 at head_dim 256, window 1024, 16 query and 8 KV heads, bf16: 120 us
+// (plain attention 69); 2753 tokens of 5 prompts over up to 3814 at 512, 16 and 2 heads: bf16 875 us
+// (plain 475), fp8 1670 (plain 904).  A tile's cycles, bf16 at 256: of 2850 the MMA warp
 // waits 800 for the weighted sum two tiles back, 1000 for K and V to land and 290 for the
-// weights; 8-bit at 512: of 8100, 5000 for converted slots, which copying (1000 cycles a slot) and converting
-// (1250) bound alike.
+// weights; 8-bit at 512: of 8100, 5000 for converted slots, which copying (1000 cycles a slot) and
+// converting (1250) bound alike; a warp a slot and two copying warps took 1790 us and, int8 at 256, 435 for 225.
+// (A denominator of unrounded weights saves 4 us of the 120 and takes the outputs' error
+// from 0.0019 to 0.0024.)
 // Every wait is bounded; tensor memory is always freed.
 #include <algorithm>
 #include <cfloat>
@@ -1153,10 +1155,9 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
       // a row with no visible key so far has m_run = -inf and only -inf scores: exponent base 0 gives 0
       const float mb = (m_run > -INFINITY) ? m_run - MB_OFF : 0.f;
       if constexpr (DIFF) {
-        // pairs of values an instruction, and one sum, of the unrounded weights (a rounded
-        // weight is then off by half a step of itself, not of its sum's too)
+        // pairs of values an instruction
         const uint64_t sc2 = pack_f32x2(sc, sc), mb2 = pack_f32x2(-mb, -mb);
-        uint64_t sum[2] = {0, 0};
+        uint64_t sum[2] = {0, 0}, rounded[2] = {0, 0};
         const float4* cv4 = reinterpret_cast<const float4*>(cvh);
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
@@ -1171,9 +1172,13 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
           }
           unpack_f32x2(w, p0, p1);
           pk[c] = C::Q8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+          // bf16: the denominator sums the rounded weights the PV MMA uses
+          if constexpr (!C::Q8)
+            rounded[c & 1] = add_f32x2(rounded[c & 1], pack_f32x2(__uint_as_float(pk[c] << 16), __uint_as_float(pk[c] & 0xffff0000u)));
         }
         unpack_f32x2(add_f32x2(sum[0], sum[1]), pe[0], pe[1]);
-        l_run += pe[0] + pe[1];
+        unpack_f32x2(add_f32x2(rounded[0], rounded[1]), ps[0], ps[1]);
+        l_run += C::Q8 ? pe[0] + pe[1] : ps[0] + ps[1];
       } else if constexpr (C::Q8) {
         // weight q = 2^(score - mb) into the denominator; q x cv, below 2^15
         // (score + log2 cv <= m_run + 8), into the PV MMA as f16
