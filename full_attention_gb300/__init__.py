@@ -448,7 +448,8 @@ class Cache:
     def extend_workspace_bytes(self, layer: int, batch: int, max_q_len: int, max_len: int) -> int:
         """Bytes of an extend workspace for calls of up to these sizes (max_len: of the
         prefixes, or in multi-token decode of the sequences):
-        fa_extend_workspace_bytes, and on an fp4 cache fa_extend_unpack_bytes more."""
+        fa_extend_workspace_bytes, and on an fp4 cache, or on an 8-bit one for
+        differential extend, fa_extend_unpack_bytes more."""
         self._layer(layer)
         return extend_workspace_bytes() + int(_lib.fa_extend_unpack_bytes(self._h, layer, int(batch), int(max_q_len),
                                                                           int(max_len)))

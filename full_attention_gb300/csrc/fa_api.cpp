@@ -919,27 +919,40 @@ static void set_split(const fa_cache* c, ExtendArgs& a) {
 
 namespace fa {
 // Where the unpacked fp4 rows of an extend or multi-token decode call lie in the
-// workspace: K rows, V rows, block table.  ring 0: nothing to unpack.
+// workspace: K rows, V rows, block table; or the f16 rows of an 8-bit differential
+// extend call: behind them its chunk of `tokens` tokens (K, V) and the rows' scales
+// (K, V).  ring 0: nothing to unpack.
 struct UnpackLayout {
   int ring = 0, table_pages = 0;
-  size_t off_v = 0, off_table = 0, bytes = 0;
+  size_t off_v = 0, off_table = 0, off_kx = 0, off_vx = 0, off_ks = 0, off_vs = 0, bytes = 0;
 };
-static UnpackLayout unpack_layout(const fa_cache* c, int32_t layer, int32_t B, int32_t max_q_len, int32_t max_len) {
+static UnpackLayout unpack_layout(const fa_cache* c, int32_t layer, int32_t B, int32_t max_q_len, int32_t max_len,
+                                  int64_t tokens) {
   UnpackLayout u;
   const fa_layer_desc& d = c->layers[layer].d;
-  if (c->kv_dtype != FA_KV_FP4 || B <= 0 || max_len <= 0 || max_q_len < 0) return u;
+  const bool chunk = c->kv_dtype != FA_KV_FP4;
+  if (c->kv_dtype == FA_KV_BF16 || B <= 0 || max_q_len < 0 || max_len < (chunk ? 0 : 1) || (chunk && max_q_len == 0)) return u;
   // a sliding layer's queries see W - 1 rows before the first of them and (in
   // multi-token decode) their own, from a 16-row boundary on
   const int64_t seen = d.kind == FA_SLIDING ? std::min<int64_t>(max_len, static_cast<int64_t>(d.window) + max_q_len + 15) : max_len;
-  const int64_t ring = (seen + kTile - 1) / kTile * kTile;
+  const int64_t ring = std::max<int64_t>(1, (seen + kTile - 1) / kTile) * kTile;
   const int64_t rows = ring * B * d.num_kv_heads;
   if (rows >= (1LL << 31) || static_cast<int64_t>(B) * d.num_kv_heads > 65535) return u;   // row indices are 32-bit
+  if (chunk && (tokens <= 0 || tokens >= (1LL << 31))) return u;
   u.ring = static_cast<int>(ring);
-  u.table_pages = static_cast<int>((max_len + ring - 1) / ring);
+  u.table_pages = static_cast<int>(std::max<int64_t>(1, (max_len + ring - 1) / ring));
   auto up = [](size_t b) { return (b + 255) / 256 * 256; };
   u.off_v = up(static_cast<size_t>(rows) * d.head_dim * 2);
   u.off_table = 2 * u.off_v;
   u.bytes = u.off_table + up(static_cast<size_t>(B) * u.table_pages * sizeof(int32_t));
+  if (chunk) {
+    const size_t ext = up(static_cast<size_t>(tokens) * d.num_kv_heads * d.head_dim * 2), sc = up(static_cast<size_t>(rows) * 4);
+    u.off_kx = u.bytes;
+    u.off_vx = u.off_kx + ext;
+    u.off_ks = u.off_vx + ext;
+    u.off_vs = u.off_ks + sc;
+    u.bytes = u.off_vs + sc;
+  }
   return u;
 }
 
@@ -960,30 +973,64 @@ static bool unpack_pays(const ExtendArgs& a, int ring) {
   return saved_us > cost_us;
 }
 
+// Whether f16 rows shorten a differential extend call over an 8-bit slab.  Converting
+// costs each job up to 1 us (256) or 2.5 (512) a 64-key tile, less when few SMs work
+// and for int8, and a tile of the chunk, whose bf16 rows take twice the reads, more;
+// the f16 rows cost a launch, 3 bytes a value of the visible rows and 4 of the chunk.
+// Measured, converting against f16 rows (us; sequences x prefix + new tokens, query/KV
+// heads): 512: 8 x 4096 + 4, 8/1 fp8 145 : 105, int8 136 : 105; 16 x 4096 + 4, 8/8 fp8
+// 605 : 571, int8 554 : 574; 8 x 0 + 1000, 16/8 1374 : 802; 1 x 500 + 4, 8/1 43 : 33.
+// 256: 4 x 3584 + 512, window 1024, 16/8 fp8 241 : 174, int8 223 : 173; 16 x 4096 + 16,
+// 8/8 207 : 295; 8 x 4096 + 4, 8/1 92 : 66; 1 x 100 + 30, 4/1 13.5 : 16.4; 2 x 30000 +
+// 64, window 512, 16/8 24 : 28; 1 x 0 + 512, 4/1 29 : 20.
+static bool f16_rows_pay(const ExtendArgs& a, int ring) {
+  const int T = 128 / (2 * a.Hq / a.Hkv);
+  const double jobs = static_cast<double>((a.max_q_len + T - 1) / T) * a.Hkv * (a.D / 256) * a.B;
+  const double fill = std::min(1.0, jobs / sm_count()), waves = std::max(1.0, std::ceil(jobs / sm_count()));
+  const double prefix = a.kind == FA_SLIDING ? std::min(a.window, a.max_prefix_len) : a.max_prefix_len;
+  const double tile_us = (a.D == 512 ? 1.0 + 1.3 * fill : 0.45 + 0.4 * fill) * (a.kv_dtype == FA_KV_FP8 ? 1.2 : 1.0);
+  const double saved_us = waves * (prefix / 64 * tile_us + (a.max_q_len + 64) / 128.0 * (a.D == 512 ? 2.5 : 1.3));
+  const double rows = 3.0 * std::min(ring, a.max_prefix_len) + 4.0 * a.max_q_len;
+  return saved_us > 5.0 + rows * a.B * a.Hkv * a.D * 2 / 5e6;
+}
+
 // fp4 with room in the workspace: unpack what the call can see and point its
-// arguments at the bf16 rows (maps are written to tm).  Leaves `a` as it is
-// where the call converts codes itself.
+// arguments at the bf16 rows (maps are written to tm); differential extend over an
+// 8-bit slab: at f16 rows, the chunk's too.  Leaves `a` as it is where the call
+// converts codes itself.
 static fa_status unpack_for_extend(const fa_cache* c, int32_t layer, ExtendArgs& a, CUtensorMap (&tm)[2], cudaStream_t stream) {
   const Layer& L = c->layers[layer];
-  const UnpackLayout ul = unpack_layout(c, layer, a.B, a.max_q_len, a.max_prefix_len);
-  if (ul.ring == 0 || ul.bytes > c->unpack_bytes || !unpack_pays(a, ul.ring)) return FA_OK;
+  const bool chunk = c->kv_dtype != FA_KV_FP4;
+  if (chunk && !a.lambda) return FA_OK;   // plain attention over 8-bit slabs converts
+  const UnpackLayout ul = unpack_layout(c, layer, a.B, a.max_q_len, a.max_prefix_len, a.num_tokens);
+  if (ul.ring == 0 || ul.bytes > c->unpack_bytes || !(chunk ? f16_rows_pay(a, ul.ring) : unpack_pays(a, ul.ring))) return FA_OK;
   char* ws = static_cast<char*>(c->unpack_ws);
   const UnpackArgs u{a.keys_in_pages ? a.seq_lens : a.prefix_lens, a.qo_indptr, a.block_table,
                      a.k_slab, a.v_slab, a.k_scale, a.v_scale, ws, ws + ul.off_v,
-                     reinterpret_cast<int32_t*>(ws + ul.off_table), a.B, a.Hkv, a.D, a.kind == FA_SLIDING ? a.window : 0,
+                     reinterpret_cast<int32_t*>(ws + ul.off_table), reinterpret_cast<float*>(ws + ul.off_ks),
+                     reinterpret_cast<float*>(ws + ul.off_vs), a.k_ext, a.v_ext, ws + ul.off_kx, ws + ul.off_vx,
+                     c->kv_dtype, a.num_tokens, a.B, a.Hkv, a.D, a.kind == FA_SLIDING ? a.window : 0,
                      a.page_size, a.num_pages, a.max_pages_per_seq, a.max_prefix_len, a.max_q_len, a.early_metadata,
                      a.keys_in_pages, ul.ring, ul.table_pages, a.err};
   const uint64_t rows = static_cast<uint64_t>(a.B) * L.d.num_kv_heads * ul.ring;
   fa_status st;
   if ((st = encode_slab_map(&tm[0], u.k, a.D, FA_KV_BF16, rows))) return st;
   if ((st = encode_slab_map(&tm[1], u.v, a.D, FA_KV_BF16, rows))) return st;
+  if (chunk) {   // (the maps move 16-bit values as they are)
+    if ((st = encode_ext_map(&a.tm_kx, u.kx, a.num_tokens, a.Hkv, a.D))) return st;
+    if ((st = encode_ext_map(&a.tm_vx, u.vx, a.num_tokens, a.Hkv, a.D))) return st;
+    a.k_ext = u.kx;
+    a.v_ext = u.vx;
+    a.k_scale = u.ks;
+    a.v_scale = u.vs;
+  }
   const cudaError_t ce = launch_unpack(u, stream);
   if (ce != cudaSuccess) return fail(FA_ERR_CUDA, "unpack launch: %s", cudaGetErrorString(ce));
   a.k_slab = u.k;
   a.v_slab = u.v;
   a.tm_k = &tm[0];
   a.tm_v = &tm[1];
-  a.kv_dtype = FA_KV_BF16;
+  a.kv_dtype = chunk ? kRowsF16 : FA_KV_BF16;
   a.page_size = ul.ring;
   a.num_pages = a.B;
   a.block_table = u.table;
@@ -995,7 +1042,7 @@ static fa_status unpack_for_extend(const fa_cache* c, int32_t layer, ExtendArgs&
 
 size_t fa_extend_unpack_bytes(const fa_cache* c, int32_t layer, int32_t B, int32_t max_q_len, int32_t max_len) {
   if (check_layer(c, layer) != FA_OK) return 0;
-  return unpack_layout(c, layer, B, max_q_len, max_len).bytes;
+  return unpack_layout(c, layer, B, max_q_len, max_len, static_cast<int64_t>(B) * max_q_len).bytes;
 }
 
 size_t fa_extend_workspace_bytes(void) { return ext_split_layout(ext_split_cap()).bytes; }

@@ -75,10 +75,15 @@
 // without them would need two O accumulators, twice the tensor memory there is.
 // 4 x 512 tokens over 3584 at head_dim 256, window 1024, 16 query and 8 KV heads, bf16: 120 us
 // (plain attention 69); 2753 tokens of 5 prompts over up to 3814 at 512, 16 and 2 heads: bf16 875 us
-// (plain 475), fp8 1670 (plain 904).  A tile's cycles, bf16 at 256: of 2850 the MMA warp
+// (plain 475), fp8 converting 1670 (plain 904).  A tile's cycles, bf16 at 256: of 2850 the MMA warp
 // waits 800 for the weighted sum two tiles back, 1000 for K and V to land and 290 for the
-// weights; 8-bit at 512: of 8100, 5000 for converted slots, which copying (1000 cycles a slot) and
+// weights; converting at 512: of 8100, 5000 for converted slots, which copying (1000 cycles a slot) and
 // converting (1250) bound alike; a warp a slot and two copying warps took 1790 us and, int8 at 256, 435 for 225.
+// So with room in the workspace the 8-bit codes and the chunk become f16 rows first
+// (kRowsF16, fa_unpack.cu): slots are filled as in bf16, the fourteenth warp reads the
+// scales, a tile ahead, and nothing else, everything behind the slots is the 8-bit path: 1050 us,
+// 17 of them unpacking; at 256, 4 x 512 tokens, fp8 241 to 174 us.  (Scales by a warp that fills
+// slots: 1143 and 202.)
 // (A denominator of unrounded weights saves 4 us of the 120 and takes the outputs' error
 // from 0.0019 to 0.0024.)
 // Every wait is bounded; tensor memory is always freed.
@@ -118,6 +123,8 @@ struct ExtCfg {
   // 64 K scales x softmax scale, 64 V scales, and per half of the keys the
   // largest log2 V scale
   static constexpr bool Q8 = KV != FA_KV_BF16;
+  static constexpr bool F16 = KV == kRowsF16;   // rows of sequence b: page b, a ring
+  static constexpr bool CONV = Q8 && !F16;      // slots are converted in place
   static constexpr int SCL_R = 8;
   static constexpr int SCL_TILE = 3 * 64 * 4;
   static constexpr int SCL_BYTES = Q8 ? SCL_R * SCL_TILE : 0;
@@ -143,7 +150,7 @@ struct ExtCfg {
   static constexpr int W_MMA = NPW;             // the MMA warp; the softmax warps follow it
   static constexpr int NSMX = 8;                // softmax warps: two per tensor-memory lane quarter
   // 8-bit slabs: one more warp, the loader, issues every slot's TMA copies
-  // (the producer warps convert what lands); an SM sub-partition then holds
+  // (the producer warps convert what lands; over f16 rows they copy, and it reads scales); an SM sub-partition then holds
   // 4 warps at most, so the register budget (128) is unchanged
   static constexpr int W_LOAD = NPW + 1 + NSMX;
   static constexpr int NTHR = (NPW + 1 + NSMX + (Q8 ? 1 : 0)) * 32;
@@ -418,7 +425,7 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
     if (pos < x.Pk) {
       const int pg = pos / p.page_size;
       off0 = pos - pg * p.page_size;
-      pid0 = ld_nc_early(p.block_table + static_cast<size_t>(x.b) * p.max_pages_per_seq + pg);
+      pid0 = C::F16 ? x.b : ld_nc_early(p.block_table + static_cast<size_t>(x.b) * p.max_pages_per_seq + pg);
     }
   }
 
@@ -440,11 +447,11 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
       mbar_init(q_free, C::NSMX);
     } else if (lane <= C::NSLOT) {
       const int i = lane - 1;
-      // bf16: the filling warp's lane 0 expect_tx + 32 lane arrivals; 8-bit:
-      // one arrival per converting warp
-      mbar_init(&full[i], C::Q8 ? C::NPW : 33);
+      // bf16 and f16 rows: the filling warp's lane 0 expect_tx + 32 lane arrivals;
+      // codes: one arrival per converting warp
+      mbar_init(&full[i], C::CONV ? C::NPW : 33);
       mbar_init(&empty[i], 1);
-      if constexpr (C::Q8) mbar_init(&land[i], 32);   // the loader warp's 32 lanes
+      if constexpr (C::CONV) mbar_init(&land[i], 32);   // the loader warp's 32 lanes
     } else if (C::Q8 && lane >= 16 && lane < 16 + C::SCL_R) {
       mbar_init(&sc_full[lane - 16], 32);        // the 32 lanes of producer warp 0
       mbar_init(&sc_empty[lane - 16], C::NSMX);  // one arrival per softmax warp
@@ -510,7 +517,7 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
         if (pos < x.Pk) {
           const int q = pos / p.page_size;
           r.off = pos - q * p.page_size;
-          r.pid = ld_nc_early(bt + q);
+          r.pid = C::F16 ? x.b : ld_nc_early(bt + q);
         }
       }
       return r;
@@ -654,7 +661,7 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
     };
     // one slot: column blocks blk0 .. blk0 + CPS - 1 (8 KB each)
     auto emit = [&](const TileSrc& ts, int blk0, bool is_v) {
-      if constexpr (C::Q8) {
+      if constexpr (C::CONV) {
         // the loader copies every slot once it is empty (so copies run as far
         // ahead as the ring allows); the producer warps convert it together
         const int sl = e % C::NSLOT;
@@ -773,6 +780,22 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
             }
             if (any_cp) cp_async_mbar_arrive(&full[sl]);
             else if (lane == 0) mbar_arrive_n(&full[sl], 32);
+          } else if (C::Q8 && ts.lim < 64) {
+            // the chunk's last rows out of the workspace, where others' rows or
+            // older data (NaN for all this launch knows) lie behind them: zeros
+            const uint8_t* base = is_v ? p.v_ext : p.k_ext;
+            if (lane == 0) mbar_arrive_expect_tx(&full[sl], 0);
+#pragma unroll
+            for (int h = 0; h < C::CPS; ++h)
+#pragma unroll 4
+              for (int i = 0; i < 16; ++i) {
+                const int r = (lane >> 3) + 4 * i, tok = ts.tok0 + r;
+                const bool v = r < ts.lim && tok >= 0 && tok < p.num_tokens;
+                const uint8_t* src =
+                    base + (v ? ((static_cast<size_t>(tok) * p.Hkv + x.h) * D + (blk0 + h) * 64) * 2 + (lane & 7) * 16 : 0);
+                cp_async16_zfill(dst + h * C::CHUNK + sw128(r, lane & 7), src, v, pol);
+              }
+            cp_async_mbar_arrive(&full[sl]);
           } else {
             if (lane == 0) {
               mbar_arrive_expect_tx(&full[sl], C::SLOT);
@@ -795,6 +818,8 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
     // the softmax of tile t or later before writing tile t's scales; and
     // before it waits for the softmax of tile t - SCL_R it converts every
     // slot it still holds, so that softmax never waits on this warp.
+    // (f16 rows: the warp that copies codes elsewhere does this instead, in a loop of
+    // its own; its wait for a scale slot holds up no other warp's slots.)
     float sk0 = 0.f, sk1 = 0.f, sv0 = 0.f, sv1 = 0.f;   // keys lane and lane + 32
     // key r of the tile lies in row group r / 16, whose slab row is row0
     auto scale_pair = [&](const TileSrc& ts, int r, int row0, float& k, float& v) {
@@ -802,11 +827,12 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
       if (ts.prefix) {
         if (row0 >= 0 && r < ts.lim && r >= ts.wlim) {
           const int row = row0 + (r & 15);
-          k = __ldg(p.k_scale + row) * p.scale_log2;
-          v = __ldg(p.v_scale + row);
+          // (f16 rows: the kernel before wrote them, perhaps while this one was starting)
+          k = C::CONV ? __ldg(p.k_scale + row) * p.scale_log2 : __ldcg(p.k_scale + row);
+          v = C::CONV ? __ldg(p.v_scale + row) : __ldcg(p.v_scale + row);
         }
       } else if (r < ts.lim) {
-        k = p.scale_log2;
+        k = C::CONV ? p.scale_log2 : 1.0f;
         v = 1.0f;
       }
     };
@@ -817,8 +843,8 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
       ok = __all_sync(0xffffffffu, w) && ok;
       if (!ok) return;
       float* dst = scl + s * (C::SCL_TILE / 4);
-      dst[lane] = sk0;
-      dst[lane + 32] = sk1;
+      dst[lane] = C::CONV ? sk0 : sk0 * p.scale_log2;   // (f16 rows: read a tile ahead, not waited for there)
+      dst[lane + 32] = C::CONV ? sk1 : sk1 * p.scale_log2;
       dst[64 + lane] = sv0;
       dst[96 + lane] = sv1;
       // the largest log2 V scale of each half's 32 keys: it only places the
@@ -836,19 +862,35 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
     };
     PageRef pid_next{pid0, off0};   // load_pid(0), read above
     TileSrc src_cur{}, src_prev{};
-    for (int t = 0; ok && t <= nt; ++t) {
+    const bool scales_only = C::F16 && pw == C::NPW;
+    if constexpr (C::F16) {
+      if (scales_only) {
+        const bool hi = lane >= 16;
+        float k0 = 0.f, k1 = 0.f, v0 = 0.f, v1 = 0.f;
+        for (int t = 0; ok && t <= nt; ++t) {
+          sk0 = k0, sk1 = k1, sv0 = v0, sv1 = v1;
+          if (t < nt) {
+            const TileSrc ts = tile_src(t, t == 0 ? pid_next : load_pid(t));
+            scale_pair(ts, lane, hi ? ts.row0[1] : ts.row0[0], k0, v0);
+            scale_pair(ts, lane + 32, hi ? ts.row0[3] : ts.row0[2], k1, v1);
+          }
+          if (t > 0) write_scales(t - 1);
+        }
+      }
+    }
+    for (int t = 0; ok && t <= nt && !scales_only; ++t) {
       if (t < nt) {
         const PageRef pid = pid_next;
         pid_next = load_pid(t + 1);   // a tile ahead
         src_cur = tile_src(t, pid);
-        if constexpr (C::Q8)
+        if constexpr (C::CONV)
           if (pw == 0) {
             const bool hi = lane >= 16;
             scale_pair(src_cur, lane, hi ? src_cur.row0[1] : src_cur.row0[0], sk0, sv0);
             scale_pair(src_cur, lane + 32, hi ? src_cur.row0[3] : src_cur.row0[2], sk1, sv1);
           }
         for (int kb = 0; ok && kb < C::KB; kb += C::CPS) emit(src_cur, kb, false);
-        if constexpr (C::Q8)
+        if constexpr (C::CONV)
           if (pw == 0 && ok) write_scales(t);
       }
       if (t >= 1)
@@ -859,10 +901,10 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
     // drain: no copy may still be landing when the CTA exits (8-bit slabs:
     // the loader waits for its copies, the converting warps issued none)
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (lane == 0 && (!C::Q8 || pw == C::NPW)) {
+    if (lane == 0 && (!C::CONV || pw == C::NPW)) {
       for (int i = max(0, e - C::NSLOT); i < e; ++i)
-        if ((C::Q8 || i % C::NPW == pw) &&
-            !mbar_wait(C::Q8 ? &land[i % C::NSLOT] : &full[i % C::NSLOT], (i / C::NSLOT) & 1))
+        if ((C::CONV || i % C::NPW == pw) &&
+            !mbar_wait(C::CONV ? &land[i % C::NSLOT] : &full[i % C::NSLOT], (i / C::NSLOT) & 1))
           atomicOr(p.err, FA_DEV_ERR_TIMEOUT);
     }
     if (threadIdx.x == 0 && !(mbar_wait(q_full, 0) && mbar_wait(qst_full, 0))) atomicOr(p.err, FA_DEV_ERR_TIMEOUT);
@@ -1453,6 +1495,9 @@ cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t s) {
   }
   auto run = [&](auto diff) {
     constexpr bool X = decltype(diff)::value;
+    if constexpr (X)
+      if (a.kv_dtype == kRowsF16)
+        return a.D == 256 ? launch_extend_t<256, kRowsF16, X>(a, k, s) : launch_extend_t<512, kRowsF16, X>(a, k, s);
     if (a.kv_dtype == FA_KV_INT8)
       return a.D == 256 ? launch_extend_t<256, FA_KV_INT8, X>(a, k, s) : launch_extend_t<512, FA_KV_INT8, X>(a, k, s);
     if (a.kv_dtype == FA_KV_FP8)

@@ -289,7 +289,12 @@ struct ExtendArgs {
 };
 cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t s);
 
-// The fp4 rows of an extend or multi-token decode call as bf16 (fa_unpack.cu).
+// ExtendArgs::kv_dtype of rows that launch_unpack wrote from 8-bit codes: f16 codes
+// and the keys' scales, the chunk in f16 too.
+constexpr int32_t kRowsF16 = 16;
+
+// The fp4 rows of an extend or multi-token decode call as bf16, or the 8-bit
+// codes and the chunk of a differential extend call as f16 (fa_unpack.cu).
 struct UnpackArgs {
   const int32_t* lens;        // prefix lengths, or (stored) sequence lengths
   const int32_t* qo_indptr;
@@ -298,9 +303,18 @@ struct UnpackArgs {
   const void* v_slab;
   const float* k_scale;
   const float* v_scale;
-  void* k;          // [B][Hkv][ring][D] bf16
+  void* k;          // [B][Hkv][ring][D] bf16, or f16
   void* v;
   int32_t* table;   // [B][table_pages]
+  // 8-bit: the rows' scales [B][Hkv][ring], and the chunk, [num_tokens][Hkv][D] bf16
+  // in, f16 out
+  float* ks;
+  float* vs;
+  const void* k_ext;
+  const void* v_ext;
+  void* kx;
+  void* vx;
+  int kv_dtype, num_tokens;
   int B, Hkv, D, window, page_size, num_pages, max_pages_per_seq, max_len, max_q_len, early_metadata;
   int stored;   // multi-token decode: the queries are the sequences' last tokens
   int ring, table_pages;

@@ -14,7 +14,15 @@
 // of 16): position pos lies in row (b * Hkv + h) * ring + pos % ring.  To the
 // extend kernel that is a slab of pages of `ring` rows whose block table says b
 // for every page of sequence b; the table is written here too.
+//
+// Differential extend over an 8-bit slab is paced by the same conversion (2753
+// tokens of 5 prompts over up to 3814 keys at 512, 16 and 2 heads, fp8: 1670 us converting, 1050 over f16 rows, 17 of them here).  A
+// code is exact in f16, the operands' type there, and its row's scale goes to the
+// scores and weights; so this kernel writes codes as f16, their scales beside them,
+// and the chunk's rows as f16 with the range's checks: operands equal in every bit to
+// those of the converting path, 3 bytes a value of the prefix and 4 of the chunk.
 #include <algorithm>
+#include <type_traits>
 
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
@@ -24,8 +32,26 @@ namespace fa {
 
 constexpr long long kMaxBlocks = 16384;
 
-template <int D>
+// 8-bit: the row's codes as f16, and its scale.
+template <int D, int KV>
+__device__ __forceinline__ void raw_to_f16(const RawRow<D, KV>& r, __half* dst, float* scale, int lane) {
+#pragma unroll
+  for (int i = 0; i < RawRow<D, KV>::NV; ++i) {
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t two = r.c[i][k >> 1] >> (16 * (k & 1));
+      if constexpr (KV == FA_KV_FP8) o[k] = e4m3x2_to_f16x2(two & 0xffffu);
+      else o[k] = pack_f16x2(static_cast<float>(static_cast<int8_t>(two)), static_cast<float>(static_cast<int8_t>(two >> 8)));
+    }
+    reinterpret_cast<uint4*>(dst)[i * 32 + lane] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+  if (lane == 0) *scale = r.s;
+}
+
+template <int D, int KV>
 __global__ void __launch_bounds__(256, 6) unpack_kernel(UnpackArgs a) {
+  constexpr bool F4 = KV == FA_KV_FP4;
   constexpr int R = D == 256 ? 8 : 4;   // rows a warp moves at a time, K and V alternating
   if (!a.early_metadata) griddep_wait();
   griddep_launch_dependents();
@@ -53,22 +79,56 @@ __global__ void __launch_bounds__(256, 6) unpack_kernel(UnpackArgs a) {
     const size_t src = there ? (static_cast<size_t>(pid) * a.Hkv + h) * a.page_size + (pos0 - pg * a.page_size) : 0;
     const size_t dst = (static_cast<size_t>(b) * a.Hkv + h) * a.ring + (pos0 - a.by_ring.div(pos0) * a.ring);
     griddep_wait();
-    RawRow<D, FA_KV_FP4> raw[R];
+    RawRow<D, KV> raw[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       if (there && pos0 + i / 2 < last) {
         const size_t r = src + i / 2;
-        raw_load<D, FA_KV_FP4>(raw[i], static_cast<const uint8_t*>((i & 1) ? a.v_slab : a.k_slab) + r * kRowBytes<D, FA_KV_FP4>,
-                               ((i & 1) ? a.v_scale : a.k_scale) + r, lane);
+        raw_load<D, KV>(raw[i], static_cast<const uint8_t*>((i & 1) ? a.v_slab : a.k_slab) + r * kRowBytes<D, KV>,
+                        ((i & 1) ? a.v_scale : a.k_scale) + r, lane);
       } else {
-        raw[i] = RawRow<D, FA_KV_FP4>{};
+        raw[i] = RawRow<D, KV>{};
       }
     }
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       if (pos0 + i / 2 >= last) continue;
-      raw_to_bf16<D, FA_KV_FP4>(raw[i], static_cast<__nv_bfloat16*>((i & 1) ? a.v : a.k) + (dst + i / 2) * D, lane);
+      const size_t d = dst + i / 2;
+      if constexpr (F4) raw_to_bf16<D, KV>(raw[i], static_cast<__nv_bfloat16*>((i & 1) ? a.v : a.k) + d * D, lane);
+      else raw_to_f16<D, KV>(raw[i], static_cast<__half*>((i & 1) ? a.v : a.k) + d * D, ((i & 1) ? a.vs : a.ks) + d, lane);
     }
+  }
+  if constexpr (!F4) {
+    // the sequence's chunk rows; values that f16 cannot hold saturate and are reported
+    griddep_wait();
+    const int qo0 = __ldg(a.qo_indptr + b);
+    uint32_t big = 0;
+    for (int t0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * (R / 2); t0 < fresh; t0 += static_cast<int>(step)) {
+      RowRegs<D> row[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int t = qo0 + t0 + i / 2;
+        if (t0 + i / 2 < fresh && t >= 0 && t < a.num_tokens)
+          row_load(row[i], static_cast<const __nv_bfloat16*>((i & 1) ? a.v_ext : a.k_ext) + (static_cast<size_t>(t) * a.Hkv + h) * D, lane);
+      }
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int t = qo0 + t0 + i / 2;
+        if (t0 + i / 2 >= fresh || t < 0 || t >= a.num_tokens) continue;
+        uint4* out = reinterpret_cast<uint4*>(static_cast<__half*>((i & 1) ? a.vx : a.kx) + (static_cast<size_t>(t) * a.Hkv + h) * D);
+#pragma unroll
+        for (int c = 0; c < RowRegs<D>::NV; ++c) {
+          uint32_t w[4] = {row[i].v[c].x, row[i].v[c].y, row[i].v[c].z, row[i].v[c].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            big |= bf16x2_past_f16(w[k]);
+            w[k] = pack_f16x2_sat(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+          }
+          out[c * 32 + lane] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+    if (__any_sync(0xffffffffu, big != 0) && lane == 0) atomicOr(a.err, FA_DEV_ERR_RANGE);
   }
   griddep_wait();   // the grid ends only after the kernel before it
 }
@@ -78,7 +138,7 @@ cudaError_t launch_unpack(const UnpackArgs& args, cudaStream_t s) {
   a.by_page = FastDiv(a.page_size);
   a.by_ring = FastDiv(a.ring);
   const int per_block = 8 * (a.D == 256 ? 4 : 2);   // positions
-  const int span = a.ring < a.max_len ? a.ring : a.max_len;
+  const int span = std::max(std::min(a.ring, a.max_len), a.kv_dtype == FA_KV_FP4 ? 1 : a.max_q_len);
   const long long gy = static_cast<long long>(a.B) * a.Hkv;
   if (gy > 65535) return cudaErrorInvalidConfiguration;   // the caller takes the direct path
   // the bound may be far above the lengths, and blocks that find nothing cost their
@@ -87,7 +147,13 @@ cudaError_t launch_unpack(const UnpackArgs& args, cudaStream_t s) {
   // cost 64 prefixes of 4096 rows 538 us for 529); converting in the kernel 93
   const long long most = std::max(1LL, (kMaxBlocks + gy - 1) / gy);
   const dim3 g(static_cast<unsigned>(std::min<long long>((span + per_block - 1) / per_block, most)), static_cast<unsigned>(gy)), b(256);
-  return a.D == 256 ? launch_pdl(unpack_kernel<256>, g, b, 0, s, a) : launch_pdl(unpack_kernel<512>, g, b, 0, s, a);
+  auto run = [&](auto kv) {
+    constexpr int KV = decltype(kv)::value;
+    return a.D == 256 ? launch_pdl(unpack_kernel<256, KV>, g, b, 0, s, a) : launch_pdl(unpack_kernel<512, KV>, g, b, 0, s, a);
+  };
+  if (a.kv_dtype == FA_KV_INT8) return run(std::integral_constant<int, FA_KV_INT8>{});
+  if (a.kv_dtype == FA_KV_FP8) return run(std::integral_constant<int, FA_KV_FP8>{});
+  return run(std::integral_constant<int, FA_KV_FP4>{});
 }
 
 }  // namespace fa

@@ -214,7 +214,8 @@ FA_API size_t fa_extend_workspace_bytes(void);
  * the cache that use it must run in stream order (one stream, or streams
  * ordered by events): concurrent calls would share its slots.  On an fp4
  * cache the bytes past fa_extend_workspace_bytes() take the unpacked prefix
- * (fa_extend_unpack_bytes).  Zeroes its
+ * (fa_extend_unpack_bytes), on an 8-bit cache the f16 rows of differential
+ * extend.  Zeroes its
  * arrival counters (synchronous); each launch leaves them zero.  A launch
  * splits when the wave is at most half full and its length bounds promise
  * 8 key tiles (512 keys) or more per job.  NULL unbinds.  Errors: FA_ERR_INVALID_ARG
@@ -236,7 +237,10 @@ FA_API fa_status fa_cache_bind_extend_workspace(fa_cache* cache, void* workspace
  * a call unpacks goes by its sizes, the bounds and the room, not by the data.
  * A call that needs
  * more room than the workspace has, or has none bound, converts the codes
- * inside the kernel.  0 in the other formats.  Host only. */
+ * inside the kernel.  On an 8-bit cache the room serves differential extend alone
+ * (fa_paged_extend_diff_attn; max_q_len then counts too): codes and chunk become
+ * f16 rows first where that is faster, with the same results bit for bit.  A call with
+ * num_tokens above B * max_q_len needs more.  0 on a bf16 cache.  Host only. */
 FA_API size_t fa_extend_unpack_bytes(const fa_cache* cache, int32_t layer, int32_t B, int32_t max_q_len,
                                      int32_t max_len);
 
@@ -634,7 +638,8 @@ FA_API fa_status fa_paged_extend_attn(fa_cache* cache, int32_t layer, const void
 /* Differential attention (fa_paged_decode_diff_attn) of a chunk of new tokens over a
  * paged prefix: arguments, layers, masks, ranges and errors as in
  * fa_paged_extend_attn, lambda and lse (float [N][Hq][2]) as above.  Every slab
- * format; 2 * Hq / Hkv must divide 128. */
+ * format; 2 * Hq / Hkv must divide 128.  Over an 8-bit slab a workspace with
+ * fa_extend_unpack_bytes of room makes long chunks faster (by a third). */
 FA_API fa_status fa_paged_extend_diff_attn(fa_cache* cache, int32_t layer, const void* q, const float* lambda,
                                            const void* k_ext, const void* v_ext, const int32_t* qo_indptr,
                                            const int32_t* prefix_lens, const int32_t* block_table,

@@ -103,6 +103,98 @@ def test_extend(D, hq, hkv, ps, window, prefix, new, split, kv):
     c.check(*c.extend())
 
 
+@pytest.mark.parametrize("kv", [W.KV_INT8, W.KV_FP8])
+@pytest.mark.parametrize("D,hq,hkv,ps,window,prefix,new", EXTEND + [
+    (256, 16, 8, 16, 1024, [3584, 1, 0, 1500], [512, 300, 64, 0]), (512, 16, 2, 32, 0, [0, 2100, 3814, 16], [400, 1, 513, 1000]),
+    (512, 8, 1, 64, 0, [0, 0, 0], [700, 63, 65])])
+def test_extend_over_f16_rows_is_the_same(D, hq, hkv, ps, window, prefix, new, kv):
+    """With room in the workspace the codes and the chunk become f16 rows before the
+    kernel: the same operands, so the same bits; nothing of what lay in the room, of
+    another sequence's chunk or of rows that nobody sees gets into a result."""
+    c = DiffCase(D, hq, hkv, ps, prefix, kv, window, new, seed=D + hq + len(new))
+    fa = c.fa
+    base = fa.extend_workspace_bytes()
+    full = c.cache.extend_workspace_bytes(c.layer, c.B, max(new), max(prefix))
+    assert full > base
+    ws = torch.full((full,), 0xFF, dtype=torch.uint8, device="cuda")
+    res = []
+    for n in (base, full, full - 256 * 64):   # (the last has not the room)
+        ws[base:] = 0xFF
+        c.cache.bind_extend_workspace(ws[:n])
+        c.out.fill_(float("nan")), c.lse.fill_(float("nan"))
+        res.append([t.clone() for t in c.extend()])
+    c.check(*res[0])
+    for out, lse in res[1:]:
+        assert torch.equal(out, res[0][0]) and torch.equal(lse, res[0][1])
+
+
+@pytest.mark.parametrize("kv", [W.KV_INT8, W.KV_FP8])
+@pytest.mark.parametrize("D", [256, 512])
+def test_f16_rows_keep_sequences_apart(D, kv):
+    """Sequences of NaN in rows and chunk beside others; a page that is none; a chunk
+    beyond f16's range: as without the workspace, and reported."""
+    c = DiffCase(D, 16, 2, 16, [700, 200, 900], kv, 0, [330, 70, 280], seed=D)
+    fa = c.fa
+    ws = fa.workspace(c.cache.extend_workspace_bytes(0, c.B, 330, 900))
+    c.cache.bind_extend_workspace(ws)
+    want = [t.clone() for t in c.extend()]
+    c.check(*want)
+    page = c.bt[1, : 200 // 16].long()
+    keep = [t[page].clone() for t in c.slabs[2:]], c.k_ext.clone(), c.v_ext.clone()
+    for t in c.slabs[2:]:
+        t[page] = float("nan")
+    c.v_ext[330:400] = float("nan")
+    got = c.extend()
+    assert c.cache.device_error() == fa.DEV_ERR_RANGE
+    for a, b in zip(got, want):
+        assert torch.equal(a[:330], b[:330]) and torch.equal(a[400:], b[400:])
+    c.v_ext.copy_(keep[2])
+    for t, k in zip(c.slabs[2:], keep[0]):
+        t[page] = k
+    bt = c.bt.clone()
+    results = []
+    for n in (fa.extend_workspace_bytes(), ws.numel()):
+        c.cache.bind_extend_workspace(ws[:n])
+        c.bt = bt.clone()
+        c.bt[0, 3] = c.cache.num_pages
+        c.k_ext[5] = 1e5
+        results.append([t.clone() for t in c.extend()])
+        assert c.cache.device_error() == fa.DEV_ERR_PAGE | fa.DEV_ERR_RANGE
+        c.bt, c.k_ext = bt, keep[1].clone()
+    for a, b in zip(*results):   # bits: scores beyond the softmax's range may leave NaN
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+def test_f16_rows_in_a_graph_and_between_other_calls():
+    """One workspace: calls of other sizes, layers and plain attention between, and a replay."""
+    import full_attention_gb300 as fa
+    a = DiffCase(512, 8, 2, 16, [800, 90], W.KV_FP8, 0, [260, 300], seed=1)
+    b = DiffCase(256, 8, 4, 32, [1500, 0, 70], W.KV_INT8, 200, [64, 130, 1], seed=2)
+    ws = fa.workspace(max(c.cache.extend_workspace_bytes(0, c.B, max(c.new), max(c.lens)) for c in (a, b)))
+    want = [[t.clone() for t in c.extend()] for c in (a, b)]
+    for c in (a, b):
+        c.cache.bind_extend_workspace(ws)
+    for c, w in zip((a, b, a, b), want * 2):
+        c.out.zero_(), c.lse.zero_()
+        got = c.extend()
+        assert all(torch.equal(x, y) for x, y in zip(got, w))
+    plain = torch.empty_like(a.out)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        a.extend()
+        b.extend()
+        a.cache.extend(0, a.q, a.k_ext, a.v_ext, a.indptr, a.lens_dev, a.bt, 300, 800, plain)
+    for _ in range(3):
+        for c in (a, b):
+            c.out.zero_(), c.lse.zero_()
+        ws[fa.extend_workspace_bytes():] = 0xFF
+        g.replay()
+        for c, w in zip((a, b), want):
+            assert torch.equal(c.out, w[0]) and torch.equal(c.lse, w[1])
+    assert a.cache.device_error() == b.cache.device_error() == 0
+
+
 def _fp4(D, hq, hkv, ps, window, prefix, new):
     import full_attention_gb300 as fa
     c = DiffCase(D, hq, hkv, ps, prefix, W.KV_BF16, window, new, seed=D + hq + len(new))
