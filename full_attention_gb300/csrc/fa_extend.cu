@@ -780,9 +780,9 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
             }
             if (any_cp) cp_async_mbar_arrive(&full[sl]);
             else if (lane == 0) mbar_arrive_n(&full[sl], 32);
-          } else if (C::Q8 && ts.lim < 64) {
-            // the chunk's last rows out of the workspace, where others' rows or
-            // older data (NaN for all this launch knows) lie behind them: zeros
+          } else if ((C::Q8 || DIFF) && ts.lim < 64) {
+            // behind the chunk's last rows lie another sequence's, a padded batch's or, in
+            // the workspace, older data, NaN for all this launch knows: zeros
             const uint8_t* base = is_v ? p.v_ext : p.k_ext;
             if (lane == 0) mbar_arrive_expect_tx(&full[sl], 0);
 #pragma unroll
@@ -1051,7 +1051,7 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
         if constexpr (C::Q8) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            qbig |= bf16x2_past_f16(w[i]);
+            qbig |= DIFF && !row_ok ? 0u : bf16x2_past_f16(w[i]);   // (a padded batch's rows are not reported)
             w[i] = pack_f16x2_sat(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
           }
         }

@@ -92,3 +92,22 @@ def test_the_workspace_holds_both_maps(fa):
         plain, both = c.decode_workspace_bytes(0, b, n), c.decode_diff_workspace_bytes(0, b, n)
         assert plain > 0 and both - fa.DECODE_COUNTER_BYTES >= 2 * (plain - fa.DECODE_COUNTER_BYTES) - 4096
     assert c.decode_diff_workspace_bytes(0, 0, 10) == c.decode_diff_workspace_bytes(3, 1, 10) == 0
+
+
+@pytest.mark.parametrize("kv,each", [(0, None), (1, 4), (2, 4)])
+def test_room_for_f16_rows(fa, kv, each):
+    """8-bit: K and V rows of what the queries see and of the chunk, a scale a row, a table."""
+    lays = [dict(kind=fa.FULL, head_dim=512, num_q_heads=8, num_kv_heads=2, window=0, kv_source=fa.KV_OWN, sm_scale=0.1),
+            dict(kind=fa.SLIDING, head_dim=256, num_q_heads=8, num_kv_heads=1, window=100, kv_source=fa.KV_OWN, sm_scale=0.1)]
+    c = fa.Cache(lays, 8, 16, kv)
+    room = lambda *a: int(fa._lib.fa_extend_unpack_bytes(c._h, *a))
+    up = lambda n: (n + 255) // 256 * 256
+    if each is None:
+        assert room(0, 2, 150, 300) == room(1, 2, 150, 300) == 0
+        return
+    full = 2 * (2 * 2 * 304 * 512 * 2) + 256 + 2 * (2 * 150 * 2 * 512 * 2) + 2 * up(2 * 2 * 304 * each)
+    assert room(0, 2, 150, 300) == full
+    slid = 2 * (2 * 272 * 256 * 2) + 256 + 2 * (2 * 150 * 256 * 2) + 2 * up(2 * 272 * each)   # 100 + 150 + 15 rows at most
+    assert room(1, 2, 150, 300) == slid
+    assert room(0, 2, 150, 0) == 2 * (2 * 2 * 16 * 512 * 2) + 256 + 2 * (2 * 150 * 2 * 512 * 2) + 2 * up(2 * 2 * 16 * each)
+    assert room(0, 2, 0, 300) == room(0, 0, 150, 300) == room(0, 1, -1, 300) == room(0, 70000, 1, 1) == 0

@@ -195,6 +195,34 @@ def test_f16_rows_in_a_graph_and_between_other_calls():
     assert a.cache.device_error() == b.cache.device_error() == 0
 
 
+@pytest.mark.parametrize("kv", FORMATS)
+@pytest.mark.parametrize("D", [256, 512])
+@pytest.mark.parametrize("early", [False, True])
+def test_shared_layers_padded_batches_and_plain_calls(kv, D, early):
+    """A layer that reads its source; token rows behind the last sequence, NaN, get into
+    no result or report and their outputs stay; in 8 bits with and without f16 rows, and
+    plain attention with the same workspace is as without."""
+    c = DiffCase(D, 16, 2, 64, [1200, 0, 640], kv, 0, [200, 170, 33], seed=9, shared=True, early=early)
+    fa, N, more = c.fa, 403, 61
+    pad = lambda t, x: torch.cat((t, torch.full((more,) + t.shape[1:], x, dtype=t.dtype, device="cuda")))
+    q, k, v = (pad(t, float("nan")) for t in (c.q, c.k_ext, c.v_ext))
+    ws = fa.workspace(c.cache.extend_workspace_bytes(1, c.B, 200, 1200))
+    base = fa.extend_workspace_bytes()
+    got, plain = [], []
+    for n in (base, ws.numel()):
+        c.cache.bind_extend_workspace(ws[:n])
+        out, lse = pad(c.out, 7.0), pad(c.lse, 7.0)
+        c.cache.extend_diff(1, q, c.lam, k, v, c.indptr, c.lens_dev, c.bt, 200, 1200, out, lse)
+        got.append((out, lse))
+        c.check(out[:N], lse[:N])
+        out = pad(c.out, 7.0)
+        c.cache.extend(1, pad(c.q, 0.0), pad(c.k_ext, 0.0), pad(c.v_ext, 0.0), c.indptr, c.lens_dev, c.bt, 200, 1200, out)
+        plain.append(out)
+    for (a, b) in zip(*got):
+        assert torch.equal(a, b) and bool((a[N:] == 7.0).all())
+    assert torch.equal(*plain) and bool((plain[0][N:] == 7.0).all())
+
+
 def _fp4(D, hq, hkv, ps, window, prefix, new):
     import full_attention_gb300 as fa
     c = DiffCase(D, hq, hkv, ps, prefix, W.KV_BF16, window, new, seed=D + hq + len(new))
