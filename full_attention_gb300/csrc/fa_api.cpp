@@ -615,7 +615,8 @@ fa_status fa_plan_step(fa_cache* c, int32_t kind, const int32_t* new_lens, int32
   if (!c) return fail(FA_ERR_INVALID_ARG, "cache is NULL");
   if (kind != FA_FULL && kind != FA_SLIDING) return fail(FA_ERR_INVALID_ARG, "kind %d", kind);
   if (B < 1 || B > FA_MAX_STEP_BATCH) return fail(FA_ERR_INVALID_ARG, "B must be in [1, %d]", FA_MAX_STEP_BATCH);
-  if (num_tokens < 0 || num_tokens == INT32_MAX) return fail(FA_ERR_INVALID_ARG, "num_tokens must be in [0, 2^31 - 2]");
+  // (the kernel counts runs of 128 tokens in 32 bits, up to the end of the last run)
+  if (num_tokens < 0 || num_tokens > (1LL << 31) - 256) return fail(FA_ERR_INVALID_ARG, "num_tokens must be in [0, 2^31 - 256]");
   if (max_pages_per_seq < 1 || static_cast<int64_t>(max_pages_per_seq) * c->page_size >= (1LL << 31) - 256)
     return fail(FA_ERR_INVALID_ARG, "max_pages_per_seq * page_size must be positive and below 2^31 - 256");
   if (!new_lens || !state || !state_out || !free_pages || !block_table || !qo_indptr || !prefix_lens ||

@@ -414,7 +414,8 @@ FA_API fa_status fa_norm_rope_store(fa_cache* cache, int32_t layer, const fa_nor
  * where a sequence outgrows max_pages_per_seq or the new tokens num_tokens,
  * FA_DEV_ERR_WORKSPACE for a state that no step leaves.  A ring or table entry
  * outside the pool sets FA_DEV_ERR_PAGE and its tokens' slots to -1.
- * 1 <= B <= FA_MAX_STEP_BATCH; max_pages_per_seq * page_size below 2^31 - 256.
+ * 1 <= B <= FA_MAX_STEP_BATCH; max_pages_per_seq * page_size below 2^31 - 256;
+ * num_tokens at most 2^31 - 256.
  * Calls on one state run in stream order.  A cache with FA_FLAG_EARLY_METADATA: the call
  * launched right behind this one must not be one that reads its arrays before it
  * has finished; fa_norm_rope_store and fa_plan_step do not. */
