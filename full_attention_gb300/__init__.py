@@ -76,6 +76,7 @@ def _load() -> ctypes.CDLL:
         "fa_decode_workspace_bytes": (sz, [vp, i32, i32, i32]),
         "fa_extend_workspace_bytes": (sz, []),
         "fa_extend_unpack_bytes": (sz, [vp, i32, i32, i32, i32]),
+        "fa_extend_diff_unpack_bytes": (sz, [vp, i32, i32, i32, i32]),
         "fa_cache_bind_extend_workspace": (i32, [vp, vp, sz]),
         "fa_paged_decode_attn": (i32, [vp, i32, vp, vp, i32, vp, i32, i32, vp, vp, vp, sz, vp]),
         "fa_paged_decode_store_attn": (i32, [vp, i32, vp, vp, vp, vp, vp, i32, vp, i32, i32, vp, vp, vp, sz, vp]),
@@ -448,11 +449,21 @@ class Cache:
     def extend_workspace_bytes(self, layer: int, batch: int, max_q_len: int, max_len: int) -> int:
         """Bytes of an extend workspace for calls of up to these sizes (max_len: of the
         prefixes, or in multi-token decode of the sequences):
-        fa_extend_workspace_bytes, and on an fp4 cache, or on an 8-bit one for
-        differential extend, fa_extend_unpack_bytes more."""
+        fa_extend_workspace_bytes, and on an fp4 cache fa_extend_unpack_bytes more.  (On an
+        8-bit cache that is 128 MiB at most, which only differential extend uses: see
+        extend_diff_workspace_bytes.)"""
         self._layer(layer)
         return extend_workspace_bytes() + int(_lib.fa_extend_unpack_bytes(self._h, layer, int(batch), int(max_q_len),
                                                                           int(max_len)))
+
+    def extend_diff_workspace_bytes(self, layer: int, batch: int, max_q_len: int, max_len: int) -> int:
+        """Bytes of an extend workspace with which differential extend calls of up to these
+        sizes over an fp4 or 8-bit cache are fastest (fa_extend_diff_unpack_bytes more than
+        fa_extend_workspace_bytes; f16 rows of what the queries see can be gigabytes).  It
+        serves the other calls too."""
+        self._layer(layer)
+        return extend_workspace_bytes() + int(_lib.fa_extend_diff_unpack_bytes(self._h, layer, int(batch), int(max_q_len),
+                                                                               int(max_len)))
 
     def bind_extend_workspace(self, workspace) -> None:
         """fa_cache_bind_extend_workspace: let extend and multi-token decode

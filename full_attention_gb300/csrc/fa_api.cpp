@@ -1042,6 +1042,11 @@ static fa_status unpack_for_extend(const fa_cache* c, int32_t layer, ExtendArgs&
 }  // namespace fa
 
 size_t fa_extend_unpack_bytes(const fa_cache* c, int32_t layer, int32_t B, int32_t max_q_len, int32_t max_len) {
+  const size_t n = fa_extend_diff_unpack_bytes(c, layer, B, max_q_len, max_len);
+  return n > FA_F16_ROWS_UNASKED_BYTES && c->kv_dtype != FA_KV_FP4 ? 0 : n;
+}
+
+size_t fa_extend_diff_unpack_bytes(const fa_cache* c, int32_t layer, int32_t B, int32_t max_q_len, int32_t max_len) {
   if (check_layer(c, layer) != FA_OK) return 0;
   return unpack_layout(c, layer, B, max_q_len, max_len, static_cast<int64_t>(B) * max_q_len).bytes;
 }

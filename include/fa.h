@@ -215,7 +215,7 @@ FA_API size_t fa_extend_workspace_bytes(void);
  * ordered by events): concurrent calls would share its slots.  On an fp4
  * cache the bytes past fa_extend_workspace_bytes() take the unpacked prefix
  * (fa_extend_unpack_bytes), on an 8-bit cache the f16 rows of differential
- * extend.  Zeroes its
+ * extend (fa_extend_diff_unpack_bytes).  Zeroes its
  * arrival counters (synchronous); each launch leaves them zero.  A launch
  * splits when the wave is at most half full and its length bounds promise
  * 8 key tiles (512 keys) or more per job.  NULL unbinds.  Errors: FA_ERR_INVALID_ARG
@@ -237,12 +237,21 @@ FA_API fa_status fa_cache_bind_extend_workspace(fa_cache* cache, void* workspace
  * a call unpacks goes by its sizes, the bounds and the room, not by the data.
  * A call that needs
  * more room than the workspace has, or has none bound, converts the codes
- * inside the kernel.  On an 8-bit cache the room serves differential extend alone
- * (fa_paged_extend_diff_attn; max_q_len then counts too): codes and chunk become
- * f16 rows first where that is faster, with the same results bit for bit.  A call with
- * num_tokens above B * max_q_len needs more.  0 on a bf16 cache.  Host only. */
+ * inside the kernel.  0 on a bf16 cache.  On an 8-bit cache no call but differential
+ * extend uses any of it: there this is fa_extend_diff_unpack_bytes where that is
+ * FA_F16_ROWS_UNASKED_BYTES or less, and 0 where it is more, so that a caller of the
+ * others is not asked for gigabytes that nothing reads.  Host only. */
+#define FA_F16_ROWS_UNASKED_BYTES (128u << 20)
 FA_API size_t fa_extend_unpack_bytes(const fa_cache* cache, int32_t layer, int32_t B, int32_t max_q_len,
                                      int32_t max_len);
+
+/* The same for differential extend (fa_paged_extend_diff_attn), of any size.  fp4:
+ * fa_extend_unpack_bytes.  8-bit: codes and chunk become f16 rows first where that is
+ * faster and the workspace has this room, with the same results bit for bit (prefix rows
+ * and chunk rows, B * max_q_len of them, K and V, a scale a row, a block table; a call with
+ * num_tokens above B * max_q_len needs more).  0 on a bf16 cache.  Host only. */
+FA_API size_t fa_extend_diff_unpack_bytes(const fa_cache* cache, int32_t layer, int32_t B, int32_t max_q_len,
+                                          int32_t max_len);
 
 /* Give the sliding layers' slabs a page pool of their own (the pages' window
  * pool: "FreeToken PR #898", description, the window slots come from one
@@ -640,7 +649,7 @@ FA_API fa_status fa_paged_extend_attn(fa_cache* cache, int32_t layer, const void
  * paged prefix: arguments, layers, masks, ranges and errors as in
  * fa_paged_extend_attn, lambda and lse (float [N][Hq][2]) as above.  Every slab
  * format; 2 * Hq / Hkv must divide 128.  Over an 8-bit slab a workspace with
- * fa_extend_unpack_bytes of room makes long chunks faster (by a third). */
+ * fa_extend_diff_unpack_bytes of room makes long chunks faster (by a third). */
 FA_API fa_status fa_paged_extend_diff_attn(fa_cache* cache, int32_t layer, const void* q, const float* lambda,
                                            const void* k_ext, const void* v_ext, const int32_t* qo_indptr,
                                            const int32_t* prefix_lens, const int32_t* block_table,
