@@ -299,7 +299,7 @@ def _prepare_diff(st, case, g):
         if new is None:
             st["ws"] = fa.workspace(st["cache"].decode_diff_workspace_bytes(0, B, st["max_len"]))
         else:
-            st["ws"] = fa.workspace(st["cache"].extend_workspace_bytes(0, B, st["max_new"], st["max_prefix"]))
+            st["ws"] = fa.workspace(st["cache"].extend_diff_workspace_bytes(0, B, st["max_new"], st["max_prefix"]))
             st["cache"].bind_extend_workspace(st["ws"])
     return st
 
