@@ -593,6 +593,7 @@ class PageTable:
             raise FAError(ERR_INVALID_ARG, f"block_table must have two dimensions, not {block_table.dim()}")
         self.cache, self.kind = cache, int(kind)
         self.block_table, self.free_pages, self.state = block_table, free_pages, state
+        self._last = state, state   # what the last step read and wrote
 
     @property
     def batch(self) -> int:
@@ -600,12 +601,17 @@ class PageTable:
 
     @property
     def seq_lens(self):
-        """The sequences' lengths after the last step, as decode reads them (a view of the state)."""
-        return self.state[4: 4 + self.batch]
+        """The sequences' lengths after the last step, as decode reads them: a view of the state
+        that it wrote (its state_out, where it was given one), or of `state` where
+        that was replaced since."""
+        read, wrote = self._last
+        return (wrote if self.state is read else self.state)[4: 4 + self.batch]
 
     def step(self, new_lens, qo_indptr, prefix_lens, positions, slot_mapping, state_out=None, stream=None) -> None:
         """One step: new_lens[b] tokens join sequence b (negative: it ends); the outputs
-        are filled for the calls of the step."""
+        are filled for the calls of the step.  With state_out the state after it goes there and
+        `state` stays, so that the step can be made again; to go on from it, copy state_out
+        into `state` or assign it."""
         bt, c, dev, i32 = self.block_table, self.cache, _device(), torch.int32
         B, cols = bt.shape
         N = slot_mapping.numel()
@@ -622,6 +628,7 @@ class PageTable:
         _check(_lib.fa_plan_step(c._h, self.kind, _p(new_lens), B, _p(self.state), _p(self.state if state_out is None else state_out),
                                  _p(self.free_pages), _p(bt), cols, _p(qo_indptr), _p(prefix_lens), _p(positions),
                                  _p(slot_mapping), N, _s(stream)))
+        self._last = self.state, self.state if state_out is None else state_out
 
 
 def device_error(stream=None) -> int:

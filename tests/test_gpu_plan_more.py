@@ -1,0 +1,66 @@
+"""Step plans: where the lengths are after a step into another state."""
+import pytest
+import torch
+
+import workloads as W
+from test_gpu_plan import FULL, Model, buffers, i32, make
+
+pytestmark = pytest.mark.gpu
+
+
+def test_lengths_follow_the_state_that_the_last_step_wrote():
+    """seq_lens is what decode of the step reads: with state_out, too, the new tokens are in it."""
+    import full_attention_gb300 as fa
+    B, ps, N = 3, 16, 64
+    cache = make(fa, FULL, 30, ps)
+    table, model = cache.page_table(FULL, B, 8), Model(B, 30, ps, 8, 0)
+    assert table.seq_lens.tolist() == [0] * B
+    out, spare = buffers(B, N), torch.zeros_like(table.state)
+
+    def step(new, **kw):
+        model.step(new, N)
+        table.step(i32(new), *out, **kw)
+        assert cache.device_error() == 0 and table.seq_lens.tolist() == model.len
+
+    step([5, 0, 20])
+    step([1, 17, 1], state_out=spare)
+    table.step(i32([1, 17, 1]), *out, state_out=spare)      # made again: the same lengths
+    assert table.seq_lens.tolist() == model.len and table.state[4: 4 + B].tolist() == [5, 0, 20]
+    table.state.copy_(spare)                                  # going on by a copy ...
+    assert table.seq_lens.tolist() == model.len
+    step([1, 1, -1])
+    step([2, 1, 9], state_out=spare)
+    table.state, spare = spare, table.state                   # ... or by taking the other buffer's place
+    assert table.seq_lens.tolist() == model.len
+    spare.zero_()
+    step([1, 1, 1], state_out=spare)
+    table.state.copy_(spare)
+    step([1, 1, 1])
+    assert table.state.tolist() == model.state()
+    snapshot = table.state.clone()
+    step([1, 0, 3])
+    table.state = snapshot                                    # an earlier state put back
+    assert table.seq_lens.tolist() == snapshot[4: 4 + B].tolist()
+
+
+def test_a_decode_after_a_step_into_another_state_sees_the_new_token():
+    """A captured step into another state and the decode behind it, fed by table.seq_lens."""
+    import full_attention_gb300 as fa
+    cache = fa.Cache([W.layer(FULL, 256, 2, 1)], 8, 16)
+    for t in cache.allocate("cuda")[0][:2]:
+        t.zero_()
+    table = cache.page_table(FULL, 1, 4)
+    out, spare = buffers(1, 1), torch.zeros_like(table.state)
+    q = torch.zeros(1, 2, 256, dtype=torch.bfloat16, device="cuda")
+    att, lse = torch.empty_like(q), torch.empty(1, 2, device="cuda")
+    one = i32([1])
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        table.step(one, *out, state_out=spare)
+        cache.decode(0, q, table.block_table, table.seq_lens, 64, att, lse, fa.workspace(cache.decode_workspace_bytes(0, 1, 64)))
+    for n in range(1, 4):
+        graph.replay()
+        assert torch.allclose(lse, torch.full_like(lse, float(n)).log())   # n keys of score 0
+        table.state.copy_(spare)
+    assert cache.device_error() == 0
