@@ -145,7 +145,7 @@ def _need(what, t, dtype, dev, rows=None, per=1):
     type, not dense, or (rows not None) neither rows * per elements nor more
     rows of per elements than `rows`."""
     if t is None:
-        raise FAError(ERR_INVALID_ARG, f"{what} must be non-NULL")
+        _missing(what)
     if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
         raise FAError(ERR_INVALID_ARG, f"{what} must be a dense {dtype} tensor on the current CUDA device, not "
                                        f"{t.dtype}, strides {tuple(t.stride())}, on {t.device}")
@@ -153,6 +153,11 @@ def _need(what, t, dtype, dev, rows=None, per=1):
         return
     if t.dim() == 0 or t.shape[0] < rows or t.numel() != t.shape[0] * per:
         raise FAError(ERR_INVALID_ARG, f"{what}, of shape {tuple(t.shape)}, must hold {rows} rows of {per} elements")
+
+
+def _missing(what) -> None:
+    """Refuse a call without a tensor whose shape is needed before it is checked."""
+    raise FAError(ERR_INVALID_ARG, f"{what} must be non-NULL")
 
 
 def _token_stride(what, t, T, heads, D, dev) -> int:
@@ -366,6 +371,8 @@ class Cache:
         [T][Hkv][D] (slices of one projection's rows are taken as they lie), and the
         store of k and v at slot_mapping (None: not stored), in one launch."""
         d, dev = self._layer(layer), _device()
+        if how is None:
+            _missing("how")
         D, hq, hkv = d["head_dim"], d["num_q_heads"], d["num_kv_heads"]
         if how.head_dim != D:
             raise FAError(ERR_INVALID_ARG, f"how is for head_dim {how.head_dim}, layer {layer} has {D}")
@@ -412,6 +419,8 @@ class Cache:
 
     def _decode_args(self, layer: int, q, block_table, seq_lens, out, lse) -> None:
         """fp4 caches and differential attention: refuse tensors the decode kernel would misread."""
+        if q is None or block_table is None:
+            _missing("q" if q is None else "block_table")
         d, B, dev = self._layer(layer), q.shape[0], _device()
         row = d["num_q_heads"] * d["head_dim"]
         _need("q", q, torch.bfloat16, dev, B, row)
@@ -515,8 +524,9 @@ class Cache:
         """fa_paged_decode_diff_attn: differential attention of one new token per
         sequence, lam (fp32) a number for each query head; with k_new, v_new and
         slot_mapping the current rows are stored first, as by decode_store."""
-        d, B = self._layer(layer), q.shape[0]
+        d = self._layer(layer)
         self._decode_args(layer, q, block_table, seq_lens, out, None)
+        B = q.shape[0]
         _need("lam", lam, torch.float32, _device(), d["num_q_heads"])
         if lse is not None:
             _need("lse", lse, torch.float32, _device(), B, 2 * d["num_q_heads"])
@@ -531,6 +541,8 @@ class Cache:
 
     def _extend_args(self, layer: int, q, indptr, lens, block_table, out, lse, k_ext=None, v_ext=None) -> None:
         """fp4 caches and differential attention: refuse tensors the extend kernel would misread."""
+        if q is None or lens is None:
+            _missing("q" if q is None else "lengths")
         d, N, B, dev = self._layer(layer), q.shape[0], lens.numel(), _device()
         row = d["num_q_heads"] * d["head_dim"]
         _need("q", q, torch.bfloat16, dev, N, row)
@@ -569,9 +581,8 @@ class Cache:
                     max_prefix_len: int, out, lse=None, stream=None) -> None:
         """fa_paged_extend_diff_attn: differential attention of a chunk over its prefix."""
         d = self._layer(layer)
-        for name, t in (("k_ext", k_ext), ("v_ext", v_ext)):
-            if t is None:
-                raise FAError(ERR_INVALID_ARG, f"{name} must be non-NULL")
+        if k_ext is None or v_ext is None:
+            _missing("k_ext" if k_ext is None else "v_ext")
         self._extend_args(layer, q, qo_indptr, prefix_lens, block_table, out, None, k_ext, v_ext)
         _need("lam", lam, torch.float32, _device(), d["num_q_heads"])
         if lse is not None:
@@ -589,6 +600,8 @@ class PageTable:
     every step changes.  Cache.page_table makes one."""
 
     def __init__(self, cache: Cache, kind: int, block_table, free_pages, state):
+        if block_table is None:
+            _missing("block_table")
         if block_table.dim() != 2:
             raise FAError(ERR_INVALID_ARG, f"block_table must have two dimensions, not {block_table.dim()}")
         self.cache, self.kind = cache, int(kind)
@@ -612,6 +625,8 @@ class PageTable:
         are filled for the calls of the step.  With state_out the state after it goes there and
         `state` stays, so that the step can be made again; to go on from it, copy state_out
         into `state` or assign it."""
+        if slot_mapping is None:
+            _missing("slot_mapping")
         bt, c, dev, i32 = self.block_table, self.cache, _device(), torch.int32
         B, cols = bt.shape
         N = slot_mapping.numel()
