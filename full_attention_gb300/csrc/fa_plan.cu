@@ -99,9 +99,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int head = p.state_in[0], count = p.state_in[1];
+  // (the third word counts arrivals where several CTAs change a state in place)
+  auto counted = [&] { return p.state_in == p.state_out && gridDim.x > 1; };
+  unsigned bad = (p.state_in[3] | (counted() ? 0 : p.state_in[2])) != 0 ? FA_DEV_ERR_WORKSPACE : 0;
 
   Sums run{0, 0, 0};
-  unsigned bad = 0;
   for (int base = 0; base < p.B; base += kPlanThreads) {
     const int b = base + tid;
     Sums mine{0, 0, 0};
@@ -159,18 +161,25 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   if (!bad && run.gone > 0) {
     const int warps = gridDim.x * (kPlanThreads / 32);
     for (int b = blockIdx.x * (kPlanThreads / 32) + warp; b < p.B; b += warps) {
-      const int n = (b + 1 < p.B ? gone[b + 1] : static_cast<int>(run.gone)) - gone[b];
+      int n = (b + 1 < p.B ? gone[b + 1] : static_cast<int>(run.gone)) - gone[b];
       if (n == 0) continue;
-      const int32_t* row = p.table + static_cast<size_t>(b) * p.max_pages + p.state_in[4 + p.B + b];
+      const int first = p.state_in[4 + p.B + b];
+      n = min(n, p.max_pages - first);   // (a state whose third word was not 0 may have been written meanwhile)
+      const int32_t* row = p.table + static_cast<size_t>(b) * p.max_pages + first;
       for (int i = lane; i < n; i += 32) p.ring[in_ring(head + count + gone[b] + i)] = row[i];
     }
   }
 
   // ---- a state changed in place is written, below, by the last CTA to have read it
   __syncthreads();
-  if (tid == 0)
-    last = p.state_in != p.state_out ? blockIdx.x == 0
-                                     : gridDim.x == 1 || atom_add_acq_rel_gpu(p.state_out + 2, 1) == static_cast<int>(gridDim.x) - 1;
+  if (tid == 0) {
+    last = blockIdx.x == 0;
+    if (counted()) {
+      const int before = atom_add_acq_rel_gpu(p.state_out + 2, 1);
+      last = before == static_cast<int>(gridDim.x) - 1;
+      if (before < 0 || before >= static_cast<int>(gridDim.x)) atomicOr(p.err, FA_DEV_ERR_WORKSPACE);   // it did not start at 0
+    }
+  }
 
   // ---- the tokens: position, slot, and at a new page's first token its table entry.  Where
   // a warp's next 128 tokens lie in one sequence they share its numbers; otherwise

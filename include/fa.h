@@ -421,7 +421,8 @@ FA_API fa_status fa_norm_rope_store(fa_cache* cache, int32_t layer, const fa_nor
  * tokens (offsets 0, slots -1, prefix_lens the lengths): FA_DEV_ERR_POOL where free
  * pages are too few (those that this step gives up do not count), FA_DEV_ERR_BOUND
  * where a sequence outgrows max_pages_per_seq or the new tokens num_tokens,
- * FA_DEV_ERR_WORKSPACE for a state that no step leaves.  A ring or table entry
+ * FA_DEV_ERR_WORKSPACE for a state that no step leaves (where its third word is not 0,
+ * ring and table may have changed all the same).  A ring or table entry
  * outside the pool sets FA_DEV_ERR_PAGE and its tokens' slots to -1.
  * 1 <= B <= FA_MAX_STEP_BATCH; max_pages_per_seq * page_size below 2^31 - 256;
  * num_tokens at most 2^31 - 256.

@@ -1,4 +1,5 @@
-"""Step plans: where the lengths are after a step into another state."""
+"""Step plans: the lengths after a step into another state, and states that no step leaves."""
+
 import pytest
 import torch
 
@@ -53,14 +54,45 @@ def test_a_decode_after_a_step_into_another_state_sees_the_new_token():
     out, spare = buffers(1, 1), torch.zeros_like(table.state)
     q = torch.zeros(1, 2, 256, dtype=torch.bfloat16, device="cuda")
     att, lse = torch.empty_like(q), torch.empty(1, 2, device="cuda")
-    one = i32([1])
+    one, ws = i32([1]), fa.workspace(cache.decode_workspace_bytes(0, 1, 64))
     graph = torch.cuda.CUDAGraph()
     torch.cuda.synchronize()
     with torch.cuda.graph(graph):
         table.step(one, *out, state_out=spare)
-        cache.decode(0, q, table.block_table, table.seq_lens, 64, att, lse, fa.workspace(cache.decode_workspace_bytes(0, 1, 64)))
+        cache.decode(0, q, table.block_table, table.seq_lens, 64, att, lse, ws)
     for n in range(1, 4):
         graph.replay()
         assert torch.allclose(lse, torch.full_like(lse, float(n)).log())   # n keys of score 0
         table.state.copy_(spare)
     assert cache.device_error() == 0
+
+
+@pytest.mark.parametrize("N", [64, 30000])   # one CTA, and several
+def test_the_states_words_of_0(N):
+    """A state whose third or fourth word is not 0 is one that no step leaves."""
+    import full_attention_gb300 as fa
+    B, ps = 4, 16
+    cache = make(fa, FULL, 2 * (N // ps + B), ps)
+    table, model = cache.page_table(FULL, B, N // ps + 2), Model(B, cache.num_pages, ps, N // ps + 2, 0)
+    out, spare = buffers(B, N), torch.zeros_like(table.state)
+    new = [N // 4 - 1, 0, N // 2, 7]
+    model.step(new, N)
+    table.step(i32(new), *out)
+    assert cache.device_error() == 0
+    for into in (None, spare):
+        for at, value in ((3, 1), (3, -5), (2, 1000), (2, -1000)):
+            table.state[at] = value
+            odd = table.state.clone()
+            table.step(i32([1, 1, -1, 1]), *out, state_out=into)
+            assert cache.device_error() == fa.DEV_ERR_WORKSPACE
+            if at == 3 or into is not None or N == 64:   # else: CTAs count their arrivals there
+                assert out[0].tolist() == [0] * (B + 1) and out[3].tolist() == [-1] * N
+                assert table.free_pages.tolist() == model.ring and table.block_table.tolist() == model.table
+                if at == 3 or into is not None:
+                    assert torch.equal(table.state, odd)
+            table.state.copy_(i32(model.state()))
+            table.free_pages.copy_(i32(model.ring)), table.block_table.copy_(i32(model.table))
+    want = model.step([1, 1, -1, 1], N)
+    table.step(i32([1, 1, -1, 1]), *out)
+    assert cache.device_error() == 0
+    assert [t.tolist() for t in out] == list(want) and table.state.tolist() == model.state()
