@@ -1,4 +1,6 @@
-"""Step plans: the lengths after a step into another state, and states that no step leaves."""
+"""Step plans: the lengths after a step into another state, states that no step leaves, and
+runs of more tokens than a warp takes at once."""
+import random
 
 import pytest
 import torch
@@ -96,3 +98,36 @@ def test_the_states_words_of_0(N):
     table.step(i32([1, 1, -1, 1]), *out)
     assert cache.device_error() == 0
     assert [t.tolist() for t in out] == list(want) and table.state.tolist() == model.state()
+
+
+@pytest.mark.parametrize("window", [0, 1000])
+def test_more_tokens_than_one_run_a_warp(window):
+    """Enough tokens for every warp to take several runs of 128: long and short prompts,
+    sequences without new tokens and ended ones in between, a prompt longer than a warp's
+    share, and padding that begins inside a run; in place and into another state."""
+    import full_attention_gb300 as fa
+    B, ps, most, seed = 300, 64, 120_000, window
+    r = random.Random(seed)
+    kind = W.SLIDING if window else FULL
+    cols = 2 * most // ps + 2
+    cache = make(fa, kind, 60_000, ps, window)
+    table, model = cache.page_table(kind, B, cols), Model(B, 60_000, ps, cols, window)
+    spare = torch.zeros_like(table.state)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for step in range(3):
+        new = [r.choice((0, 0, 1, 1, 3, 127, 128, 130, r.randint(1, 30_000), r.randint(1, 30_000)) + ((-1,) if step else ())) for _ in range(B)]
+        new[40 + step] = most // 2 + step          # longer than a warp's share
+        new[100: 180] = [1] * 40 + [0] * 40        # many short ones in a run, and none
+        N = sum(max(n, 0) for n in new) + 250_001 + 13 * step
+        assert N > 2 * 128 * 16 * sms
+        want = model.step(new, N)
+        into = spare if step == 1 else None
+        out = buffers(B, N)
+        table.step(i32(new), *out, state_out=into)
+        assert cache.device_error() == 0 and want is not None
+        for t, w in zip(out, want):
+            assert t.tolist() == w
+        assert table.free_pages.tolist() == model.ring and table.block_table.tolist() == model.table
+        if into is not None:
+            table.state.copy_(into)
+        assert table.state.tolist() == model.state()
