@@ -73,7 +73,7 @@
 // neighbouring lanes, with weights 1 / l_0 and - lambda / l_1.  The zeros double
 // the S products (4 MMAs of 128 x 64 x 64 columns for 3 that count); two S tiles
 // without them would need two O accumulators, twice the tensor memory there is.
-// 4 x 512 tokens over 3584 at head_dim 256, window 1024, 16 query and 8 KV heads, bf16: 120 us
+// 4 x 512 tokens over 3584 at head_dim 256, window 1024, 16 query and 8 KV heads, bf16: 121 us
 // (plain attention 69); 2753 tokens of 5 prompts over up to 3814 at 512, 16 and 2 heads: bf16 875 us
 // (plain 475), fp8 converting 1670 (plain 904).  A tile's cycles, bf16 at 256: of 2850 the MMA warp
 // waits 800 for the weighted sum two tiles back, 1000 for K and V to land and 290 for the
@@ -84,7 +84,7 @@
 // scales, a tile ahead, and nothing else, everything behind the slots is the 8-bit path: 1050 us,
 // 17 of them unpacking; at 256, 4 x 512 tokens, fp8 241 to 174 us.  (Scales by a warp that fills
 // slots: 1143 and 202.)
-// (A denominator of unrounded weights saves 4 us of the 120 and takes the outputs' error
+// (A denominator of unrounded weights saves 4 us of those 121 and takes the outputs' error
 // from 0.0019 to 0.0024.)
 // Every wait is bounded; tensor memory is always freed.
 #include <algorithm>
@@ -786,7 +786,7 @@ __global__ void __launch_bounds__(ExtCfg<D, KV>::NTHR, 1)
             const uint8_t* base = is_v ? p.v_ext : p.k_ext;
             if (lane == 0) mbar_arrive_expect_tx(&full[sl], 0);
             // (once a sequence: what its length costs the loop around it decides, bf16 4 x 512 at 256
-            // and ragged fp8 at 512: all unrolled 126 and 1043 us, rolled 125 and 1071, this 123 and 1047)
+            // and ragged fp8 at 512: all unrolled 126 and 1043 us, rolled 125 and 1071, this 121 to 123 and 1047)
 #pragma unroll 1
             for (int h = 0; h < C::CPS; ++h)
 #pragma unroll 4

@@ -18,8 +18,10 @@
 // apart in a ring that holds every page), so only the state waits until every CTA has
 // read it: the last to arrive writes it, and the state read and the one written may be the same.
 // 64 sequences of one token 3.2 us, 128 in a window's pool 4.2, 512 prompts (2.1 million
-// tokens) 13 us, 1.3 TB/s: of those 6 are the launch, the sums and 17 MB written, the rest the
-// lookups' latency, seven times in a row a warp (more CTAs repeat the sums and take longer: 17 us for twice as many).
+// tokens) 13 us, 1.3 TB/s: of those 6 are the launch, the sums and 17 MB written (2 million rows
+// of padding alone take 6.0), the rest the lookups: 126 instructions a token, as each lane looks
+// its tokens up alone, at 2.1 instructions a cycle (of 4) between their loads.  More CTAs repeat the
+// sums and take longer: 17 us for twice as many.
 #include <algorithm>
 
 #include "fa_internal.h"
